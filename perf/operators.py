@@ -231,7 +231,7 @@ def _quantize(s):
     block, (r, c) = s["case"]["block"], s["X"].shape
     x = _blocks(s["X"].float(), block)
     top = x.abs().amax((1, 3), keepdim=True).clamp(min=LEAST)
-    codes = (x * (TOP / top)).clamp(-TOP, TOP).view(-1, x.shape[2] * x.shape[3])[:r, :c]
+    codes = (x * torch.div(torch.full_like(top, TOP), top)).clamp(-TOP, TOP).view(-1, x.shape[2] * x.shape[3])[:r, :c]
     scales = (top / TOP)[:, 0, :, 0]
     if block == "cols":
         codes, scales = torch.nn.functional.pad(codes.t(), (0, -r % 16)), scales.t()
