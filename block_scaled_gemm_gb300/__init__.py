@@ -29,7 +29,8 @@ __all__ = [
     "mxgemm_set_profile_events", "mxgemm_get_launch_count", "mxgemm_run_noalloc", "mxgemm_run_host",
     "mxgemm_quantize", "IN_F32", "IN_BF16", "EXPORTED_SYMBOLS", "Gemm", "OPT_SCALE_LAYOUT", "OPT_ELEMENT_LAYOUT", "OPT_B_MAJOR", "B_K_BY_N", "B_N_BY_K", "ELEMS_BYTE", "ELEMS_PACKED",
     "SCALES_ROW_MAJOR", "SCALES_PACKED", "mxgemm_scale_bytes", "mxgemm_noalloc_get_status",
-    "mxgemm_noalloc_set_option",
+    "mxgemm_noalloc_set_option", "mxgemm_run_block128", "mxgemm_quantize_block128", "BLOCK_ROWS", "BLOCK_COLS",
+    "BLOCK_TILES", "Cache", "mxgemm_cache_append", "mxgemm_cache_attention",
 ]
 
 OUT_F32 = 0
@@ -54,6 +55,11 @@ ELEMS_PACKED = 1
 SCALES_ROW_MAJOR = 0
 SCALES_PACKED = 1
 
+# blocks of mxgemm_quantize_block128 (mxgemm_block_t)
+BLOCK_ROWS = 0
+BLOCK_COLS = 1
+BLOCK_TILES = 2
+
 # element formats (mxgemm_format_t); one element per byte, sub-byte codes in
 # the low bits
 FMT_E4M3 = 0
@@ -76,10 +82,18 @@ EXPORTED_SYMBOLS = (
     "mxgemm_get_device_status", "mxgemm_status_string", "mxgemm_set_profile_events",
     "mxgemm_get_launch_count", "mxgemm_run_noalloc", "mxgemm_run_host", "mxgemm_quantize",
     "mxgemm_quantize_sr", "mxgemm_quantize_ex", "mxgemm_scale_bytes", "mxgemm_noalloc_get_status",
-    "mxgemm_noalloc_set_option",
+    "mxgemm_noalloc_set_option", "mxgemm_run_block128", "mxgemm_quantize_block128",
+    "mxgemm_cache_append", "mxgemm_cache_attention",
 )
 
 _lib = None
+
+
+class _CacheStruct(ctypes.Structure):
+    """mxgemm_cache_t"""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("K_scale", ctypes.c_void_p),
+                ("V_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class MxgemmError(RuntimeError):
@@ -133,6 +147,15 @@ def library():
         lib.mxgemm_noalloc_get_status.restype = i32
         lib.mxgemm_noalloc_set_option.argtypes = [i32, i64]
         lib.mxgemm_noalloc_set_option.restype = i32
+        lib.mxgemm_run_block128.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i32, vp, i32, i32, vp]
+        lib.mxgemm_run_block128.restype = i32
+        lib.mxgemm_quantize_block128.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+        lib.mxgemm_quantize_block128.restype = i32
+        lib.mxgemm_cache_append.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, i32, vp]
+        lib.mxgemm_cache_append.restype = i32
+        lib.mxgemm_cache_attention.argtypes = [vp, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64,
+                                               ctypes.c_float, i32, i64, i64, vp, vp, vp]
+        lib.mxgemm_cache_attention.restype = i32
         lib.mxgemm_status_string.argtypes = [i32]
         lib.mxgemm_status_string.restype = ctypes.c_char_p
         _lib = lib
@@ -264,6 +287,121 @@ def mxgemm_noalloc_set_option(option: int, value: int) -> None:
     """Process-wide option of mxgemm_run_noalloc (OPT_WAIT_TIMEOUT_NS or
     OPT_TEST_STALL_PRODUCER)."""
     _check(library().mxgemm_noalloc_set_option(int(option), int(value)), "mxgemm_noalloc_set_option")
+
+
+def mxgemm_run_block128(h, M, N, K, A, A_scale, B, B_scale, C, use_acc=0, out_dtype=OUT_F32,
+                        b_block=128, stream=None, check: bool = True) -> int:
+    """C (+)= A.B with one float32 scale per block of 128 along K: A M x K with
+    scales M x ceil(K/128); B N x K or K x N as the handle's OPT_B_MAJOR says,
+    with a scale per 128 x 128 block (b_block=128) or per column and block of
+    128 (b_block=1), laid out as B is (see include/mxgemm.h)."""
+    st = library().mxgemm_run_block128(h, int(M), int(N), int(K), _ptr(A), _ptr(A_scale), _ptr(B),
+                                       _ptr(B_scale), int(b_block), _ptr(C), int(bool(use_acc)),
+                                       int(out_dtype), _stream(stream))
+    if check:
+        _check(st, "mxgemm_run_block128")
+    return st
+
+
+def mxgemm_quantize_block128(X, R, C, codes, scales, block=BLOCK_ROWS, x_dtype=None, stream=None,
+                             check: bool = True) -> int:
+    """Quantize the R x C device matrix X (float32 or bfloat16) into E4M3 codes
+    with one float32 scale per block: BLOCK_ROWS 1 x 128 (codes R x C, scales
+    R x ceil(C/128)), BLOCK_COLS 128 x 1 stored transposed (codes
+    C x round_up(R, 16), scales C x ceil(R/128)), BLOCK_TILES 128 x 128 (codes
+    R x C, scales ceil(R/128) x ceil(C/128))."""
+    if x_dtype is None:
+        import torch
+        x_dtype = IN_BF16 if getattr(X, "dtype", None) == torch.bfloat16 else IN_F32
+    st = library().mxgemm_quantize_block128(_ptr(X), int(x_dtype), int(R), int(C), int(block),
+                                            _ptr(codes), _ptr(scales), _stream(stream))
+    if check:
+        _check(st, "mxgemm_quantize_block128")
+    return st
+
+
+class Cache:
+    """An 8-bit key/value cache: uint8 tensors K and V (pages x kv heads x page
+    size x head dim) and float32 tensors of their scales (pages x kv heads)."""
+
+    def __init__(self, K, V, K_scale, V_scale):
+        if K.dim() != 4 or K.shape != V.shape or K_scale.shape != K.shape[:2] or V_scale.shape != K.shape[:2]:
+            raise ValueError("K and V: pages x kv heads x page size x head dim, scales: pages x kv heads")
+        for t, size in ((K, 1), (V, 1), (K_scale, 4), (V_scale, 4)):
+            if not t.is_contiguous() or t.element_size() != size:
+                raise ValueError("a cache is dense, with 8-bit codes and float32 scales")
+        self.K, self.V, self.K_scale, self.V_scale = K, V, K_scale, V_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = K.shape
+        self._c = _CacheStruct(K.data_ptr(), V.data_ptr(), K_scale.data_ptr(), V_scale.data_ptr(),
+                               self.num_pages, self.page_size, self.kv_heads, self.head_dim)
+        self._ref = ctypes.byref(self._c)
+
+
+def _token_pitch(t, name):
+    """Elements from token to token of a (tokens, heads, head dim) tensor whose tokens are dense."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: tokens x heads x head dim, each token dense")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _batch(page_table, kv_len, q_start):
+    """The pointers of a batch's page table, lengths and row starts."""
+    for t, name in ((page_table, "page_table"), (kv_len, "kv_len"), (q_start, "q_start")):
+        if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()):
+            raise ValueError(f"{name}: a dense int32 tensor")
+    batch = page_table.shape[0]
+    if page_table.dim() != 2 or kv_len.numel() != batch or (q_start is not None and q_start.numel() != batch + 1):
+        raise ValueError("page_table: batch x pages, kv_len: batch, q_start: batch + 1")
+    return _ptr(page_table), _ptr(kv_len), _ptr(q_start)
+
+
+def mxgemm_cache_append(h, cache: Cache, page_table, kv_len, new_K, new_V, q_start=None, stream=None,
+                        check: bool = True) -> int:
+    """Append new keys and values (tokens x kv heads x head dim, float32 or
+    bfloat16; slices of a projection's output will do) to the sequences of a
+    cache.  page_table: batch x pages int32; kv_len: lengths with the new
+    tokens; q_start: batch + 1 row starts, None for one token each."""
+    import torch
+    pitch = _token_pitch(new_K, "new_K")
+    if new_V.shape != new_K.shape or new_V.dtype != new_K.dtype or _token_pitch(new_V, "new_V") != pitch:
+        raise ValueError("new_V is laid out as new_K is")
+    if new_K.shape[1:] != (cache.kv_heads, cache.head_dim):
+        raise ValueError("new_K: tokens x kv heads x head dim")
+    if new_K.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("new_K: float32 or bfloat16")
+    table, lens, starts = _batch(page_table, kv_len, q_start)
+    st = library().mxgemm_cache_append(
+        h, cache._ref, page_table.shape[0], table, page_table.shape[1], lens, starts, new_K.shape[0],
+        _ptr(new_K), _ptr(new_V), pitch, IN_BF16 if new_K.dtype == torch.bfloat16 else IN_F32, _stream(stream))
+    if check:
+        _check(st, "mxgemm_cache_append")
+    return st
+
+
+def mxgemm_cache_attention(h, cache: Cache, page_table, kv_len, Q, O, q_start=None, scale=None,
+                           causal=True, window=0, sinks=0, lse=None, stream=None,
+                           check: bool = True) -> int:
+    """Attention of Q (tokens x heads x head dim bfloat16) over a cache into O
+    (the same shape, dense) and, where given, lse (tokens x heads float32).
+    page_table, kv_len and q_start as for mxgemm_cache_append; scale defaults
+    to 1 / sqrt(head dim); window = 0 is no window."""
+    import torch
+    pitch = _token_pitch(Q, "Q")
+    if Q.dtype != torch.bfloat16 or O.dtype != torch.bfloat16 or O.shape != Q.shape or not O.is_contiguous():
+        raise ValueError("Q and O: bfloat16 of one shape, O dense")
+    if Q.shape[2] != cache.head_dim:
+        raise ValueError("Q: tokens x heads x head dim")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != Q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse: a dense float32 tensor, tokens x heads")
+    table, lens, starts = _batch(page_table, kv_len, q_start)
+    st = library().mxgemm_cache_attention(
+        h, cache._ref, page_table.shape[0], Q.shape[1], table, page_table.shape[1], lens, starts,
+        Q.shape[0], _ptr(Q), pitch,
+        cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
+        int(sinks), _ptr(O), _ptr(lse), _stream(stream))
+    if check:
+        _check(st, "mxgemm_cache_attention")
+    return st
 
 
 def mxgemm_set_option(h, option: int, value: int) -> None:

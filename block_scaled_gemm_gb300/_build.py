@@ -18,8 +18,10 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 SRC_DIR = PKG / "csrc"
 # translation units: the C interface with the tiled kernel (B given K x N),
-# the tiled kernel's variants for B given N x K, and the skinny-problem kernel
-UNITS = [SRC_DIR / "mxgemm.cu", SRC_DIR / "tiled_kmajor.cu", SRC_DIR / "swapab.cu"]
+# the tiled kernel's variants for B given N x K, the skinny-problem kernel, the
+# product with block-128 scales, and the 8-bit key/value cache
+UNITS = [SRC_DIR / "mxgemm.cu", SRC_DIR / "tiled_kmajor.cu", SRC_DIR / "swapab.cu",
+         SRC_DIR / "block128.cu", SRC_DIR / "cache.cu"]
 OBJ_DIR = PKG / "_build"
 HEADER = ROOT / "include" / "mxgemm.h"
 LIB = PKG / "libmxgemm.so"
@@ -42,7 +44,7 @@ def nvcc_path() -> str:
 
 
 def _sources():
-    return [HEADER] + sorted(SRC_DIR.glob("*.cu")) + sorted(SRC_DIR.glob("*.cuh"))
+    return [HEADER] + sorted(SRC_DIR.glob("*.cu")) + sorted(SRC_DIR.glob("*.cuh")) + sorted(SRC_DIR.glob("*.h"))
 
 
 def needs_build() -> bool:

@@ -1,0 +1,145 @@
+// cache.cu -- the 8-bit key/value cache: argument checks and launches of
+// mxgemm_cache_append and mxgemm_cache_attention.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "cache_append.cuh"
+#include "cache_attention.cuh"
+#include "context.h"
+#include "mxgemm.h"
+
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+constexpr int64_t kLim = int64_t(1) << 31;
+
+// The checks that both entry points share; fills the kernels' views.
+int cache_args(const mxg::HandleView &v, const mxgemm_cache_t *c, int64_t batch, const int32_t *table,
+               int64_t table_pitch, const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
+               mxg::CacheView *cv, mxg::BatchView *bv) {
+  if (!c || batch < 0 || batch >= (1 << 20) || tokens < 0 || tokens >= kLim || table_pitch < 0)
+    return MXGEMM_ERR_INVALID_VALUE;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return MXGEMM_ERR_INVALID_VALUE;
+  if (c->head_dim != 64 && c->head_dim != 128) return MXGEMM_ERR_INVALID_VALUE;
+  if (c->kv_heads < 1 || c->kv_heads > 65535 || c->num_pages < 0 || c->num_pages >= kLim)
+    return MXGEMM_ERR_INVALID_VALUE;
+  if (table_pitch * c->page_size >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+  if (!q_start && tokens != batch) return MXGEMM_ERR_INVALID_VALUE;
+  if (batch == 0 || tokens == 0) return MXGEMM_OK;
+  if (!kv_len || (table_pitch > 0 && !table)) return MXGEMM_ERR_INVALID_VALUE;
+  if (c->num_pages > 0 && (!c->K || !c->V || !c->K_scale || !c->V_scale)) return MXGEMM_ERR_INVALID_VALUE;
+  if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->K_scale, 4) || !aligned(c->V_scale, 4) ||
+      !aligned(table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4))
+    return MXGEMM_ERR_MISALIGNED;
+  for (const void *p : {static_cast<const void *>(c->K), static_cast<const void *>(c->V),
+                        static_cast<const void *>(c->K_scale), static_cast<const void *>(c->V_scale),
+                        static_cast<const void *>(table), static_cast<const void *>(kv_len),
+                        static_cast<const void *>(q_start)})
+    if (p && !mxg::pointer_on_device(p, v.device)) return MXGEMM_ERR_INVALID_VALUE;
+  cv->K = static_cast<uint8_t *>(c->K);
+  cv->V = static_cast<uint8_t *>(c->V);
+  cv->K_scale = c->K_scale;
+  cv->V_scale = c->V_scale;
+  cv->num_pages = c->num_pages;
+  cv->page_size = c->page_size;
+  cv->page_log2 = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  cv->kv_heads = c->kv_heads;
+  bv->batch = static_cast<int>(batch);
+  bv->table = table;
+  bv->table_pitch = table_pitch;
+  bv->kv_len = kv_len;
+  bv->q_start = q_start;
+  bv->tokens = tokens;
+  bv->status = v.status;
+  return MXGEMM_OK;
+}
+
+int launched(const mxg::HandleView &v) {
+  if (cudaGetLastError() != cudaSuccess) return MXGEMM_ERR_CUDA;
+  ++*v.launches;
+  return MXGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
+                                   const int32_t *page_table, int64_t table_pitch,
+                                   const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
+                                   const void *new_K, const void *new_V, int64_t pitch, int x_dtype,
+                                   mxgemm_stream_t stream_) {
+  if (!h) return MXGEMM_ERR_INVALID_VALUE;
+  const mxg::HandleView v = mxg::handle_view(h);
+  mxg::CurrentDevice g(v.device);
+  mxg::AppendParams p;
+  if (int st = cache_args(v, cache, batch, page_table, table_pitch, kv_len, q_start, tokens, &p.c, &p.b))
+    return st;
+  if (x_dtype != MXGEMM_IN_F32 && x_dtype != MXGEMM_IN_BF16) return MXGEMM_ERR_INVALID_VALUE;
+  if (pitch < static_cast<int64_t>(cache->kv_heads) * cache->head_dim) return MXGEMM_ERR_INVALID_VALUE;
+  if (batch == 0 || tokens == 0) return MXGEMM_OK;
+  if (!new_K || !new_V) return MXGEMM_ERR_INVALID_VALUE;
+  const size_t al = x_dtype == MXGEMM_IN_F32 ? 32 : 16;
+  if (!aligned(new_K, al) || !aligned(new_V, al) || pitch % 8 != 0) return MXGEMM_ERR_MISALIGNED;
+  if (!mxg::pointer_on_device(new_K, v.device) || !mxg::pointer_on_device(new_V, v.device))
+    return MXGEMM_ERR_INVALID_VALUE;
+  p.newK = new_K;
+  p.newV = new_V;
+  p.pitch = pitch;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const dim3 grid(static_cast<unsigned>((tokens >> p.c.page_log2) + 2 * batch),
+                  static_cast<unsigned>(cache->kv_heads), 2);
+  const bool f32 = x_dtype == MXGEMM_IN_F32;
+  if (cache->head_dim == 128) {
+    if (f32) mxg::cache_append_kernel<float, 128><<<grid, 128, 0, stream>>>(p);
+    else mxg::cache_append_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
+  } else {
+    if (f32) mxg::cache_append_kernel<float, 64><<<grid, 128, 0, stream>>>(p);
+    else mxg::cache_append_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
+  }
+  return launched(v);
+}
+
+extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
+                                      int64_t heads, const int32_t *page_table, int64_t table_pitch,
+                                      const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
+                                      const void *Q, int64_t q_pitch, float scale, int causal,
+                                      int64_t window, int64_t sinks, void *O, float *lse,
+                                      mxgemm_stream_t stream_) {
+  if (!h) return MXGEMM_ERR_INVALID_VALUE;
+  const mxg::HandleView v = mxg::handle_view(h);
+  mxg::CurrentDevice g(v.device);
+  mxg::AttnParams p;
+  if (int st = cache_args(v, cache, batch, page_table, table_pitch, kv_len, q_start, tokens, &p.c, &p.b))
+    return st;
+  if (heads < 1 || heads >= (1 << 16) || heads % cache->kv_heads != 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (q_pitch < heads * cache->head_dim || !std::isfinite(scale)) return MXGEMM_ERR_INVALID_VALUE;
+  if ((causal != 0 && causal != 1) || window < 0 || sinks < 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (batch == 0 || tokens == 0) return MXGEMM_OK;
+  if (!Q || !O) return MXGEMM_ERR_INVALID_VALUE;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(lse, 4) || q_pitch % 8 != 0)
+    return MXGEMM_ERR_MISALIGNED;
+  if (!mxg::pointer_on_device(Q, v.device) || !mxg::pointer_on_device(O, v.device) ||
+      (lse && !mxg::pointer_on_device(lse, v.device)))
+    return MXGEMM_ERR_INVALID_VALUE;
+  p.Q = static_cast<const __nv_bfloat16 *>(Q);
+  p.q_pitch = q_pitch;
+  p.heads = static_cast<int>(heads);
+  p.group = static_cast<int>(heads / cache->kv_heads);
+  p.scale = scale;
+  p.causal = causal;
+  p.window = window;
+  p.sinks = sinks;
+  p.O = static_cast<__nv_bfloat16 *>(O);
+  p.lse = lse;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const unsigned grid = static_cast<unsigned>(cdiv(tokens * heads, 4));
+  if (cache->head_dim == 128) mxg::cache_attention_kernel<128><<<grid, 128, 0, stream>>>(p);
+  else mxg::cache_attention_kernel<64><<<grid, 128, 0, stream>>>(p);
+  return launched(v);
+}

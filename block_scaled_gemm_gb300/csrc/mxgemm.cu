@@ -18,6 +18,7 @@
 #include <new>
 
 #include "mxgemm.h"
+#include "context.h"
 #include "mxgemm_kernel.cuh"
 #include "prepass.cuh"
 #include "quantize.cuh"
@@ -104,6 +105,7 @@ struct mxgemm_ctx {
   // creation; each launch writes and waits for its own epoch (never 0)
   unsigned *flags = nullptr;
   unsigned epoch = 0;
+  unsigned *counters = nullptr;  // mxg::kCounters words, zero between launches
   Workspace ws;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   long long timeout_ns = 2000000000LL;
@@ -127,18 +129,7 @@ struct mxgemm_ctx {
 
 namespace {
 
-struct DeviceGuard {
-  int prev = -1;
-  bool changed = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) {
-      changed = cudaSetDevice(dev) == cudaSuccess;
-    }
-  }
-  ~DeviceGuard() {
-    if (changed) cudaSetDevice(prev);
-  }
-};
+using DeviceGuard = mxg::CurrentDevice;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
@@ -614,14 +605,17 @@ int mxgemm_create(mxgemm_handle_t *out, int device) {
     return MXGEMM_ERR_CUDA;
   }
   // a flag slot per epilogue warp of every CTA a grid can have
+  // (and, behind them, the counters of split attention work)
   const size_t flag_bytes = static_cast<size_t>(h->sm_count) * mxg::Cfg<1>::EPI_WARPS * sizeof(unsigned);
-  if (cudaMalloc(&h->flags, flag_bytes) != cudaSuccess) {
+  const size_t counter_bytes = mxg::kCounters * sizeof(unsigned);
+  if (cudaMalloc(&h->flags, flag_bytes + counter_bytes) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->d_status);
     delete h;
     return MXGEMM_ERR_OUT_OF_MEMORY;
   }
-  if (cudaMemset(h->flags, 0, flag_bytes) != cudaSuccess) {
+  h->counters = h->flags + flag_bytes / sizeof(unsigned);
+  if (cudaMemset(h->flags, 0, flag_bytes + counter_bytes) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->flags);
     cudaFree(h->d_status);
@@ -883,6 +877,25 @@ int mxgemm_destroy(mxgemm_handle_t h) {
 }
 
 }  // extern "C"
+
+namespace mxg {
+
+HandleView handle_view(mxgemm_handle_t h) {
+  return HandleView{h->device,   h->sm_count,    h->d_status, static_cast<unsigned long long>(h->timeout_ns),
+                    h->stall_producer, h->a_fmt, h->b_fmt,    h->b_major,
+                    &h->launches, h->prof_before, h->prof_after, h->encode,
+                    h->counters};
+}
+
+int handle_workspace(mxgemm_handle_t h, size_t bytes, cudaStream_t stream, uint8_t **ptr) {
+  const int st = ensure_workspace(h, bytes, stream);
+  *ptr = h->ws.ptr;
+  return st;
+}
+
+bool pointer_on_device(const void *p, int device) { return on_device(p, device); }
+
+}  // namespace mxg
 
 // ===========================================================================
 // mxgemm_quantize: MX quantization of a real matrix on the GPU.

@@ -43,6 +43,9 @@
  * mxgemm_noalloc_set_option), mxgemm_quantize and mxgemm_quantize_sr
  * (FP32/BF16 -> E4M3 codes and E8M0 scales on the GPU, rounding to nearest
  * or stochastically), plus handle, option, status and timing helpers.
+ * For 8-bit layers with coarser scales: mxgemm_run_block128 (the product with
+ * one FP32 scale per block of 128), mxgemm_quantize_block128 (its operands),
+ * and the 8-bit key/value cache: mxgemm_cache_append, mxgemm_cache_attention.
  */
 #ifndef MXGEMM_H_
 #define MXGEMM_H_
@@ -373,6 +376,144 @@ int mxgemm_noalloc_get_status(mxgemm_stream_t stream, int *status_out, int *deta
  * MXGEMM_OPT_TEST_STALL_PRODUCER (default 0), as for mxgemm_set_option;
  * other options are MXGEMM_ERR_INVALID_VALUE.  Applies to later calls. */
 int mxgemm_noalloc_set_option(int option, int64_t value);
+
+/* ------------------------------------------------------------------------
+ * 8-bit layers with one FP32 scale per block of 128.
+ * ------------------------------------------------------------------------ */
+
+/* The product with coarse scales, on `stream`:
+ *
+ *   C[m,n] (+)= sum over K blocks kb of 128:
+ *                 A_scale[m,kb] * B_scale[n / b_block, kb]
+ *                 * sum over k in kb of A[m,k] * B[n,k]
+ *
+ * The sums are formed in FP32: each block's products in the tensor cores,
+ * the scaled blocks added in registers.
+ *   M, N, K : each in [0, 2^31); K % 16 == 0 (a last block of fewer than 128
+ *             is a block of its own).  M == 0 or N == 0 is a no-op; K == 0
+ *             sets C to 0 (use_acc = 0) or leaves it unchanged.
+ *   A       : M x K element codes, K contiguous.
+ *   A_scale : M x ceil(K/128) float.
+ *   B       : with MXGEMM_OPT_B_MAJOR = MXGEMM_B_N_BY_K N x K, K contiguous (a
+ *             linear layer's weight: the forward product); with
+ *             MXGEMM_B_K_BY_N (the default) K x N, N contiguous, and then
+ *             N % 16 == 0 (the same weight as it lies, contracted over its
+ *             rows: the gradient of the layer's input).
+ *   b_block : columns of the product that share a scale of B: 128, or 1 (the
+ *             gradient of a weight, where both operands have their scales
+ *             along the contracted tokens).
+ *   B_scale : float, laid out as B is: ceil(N/b_block) x ceil(K/128) for
+ *             MXGEMM_B_N_BY_K, ceil(K/128) x ceil(N/b_block) for
+ *             MXGEMM_B_K_BY_N.
+ *   C       : M x N, out_dtype; use_acc as for mxgemm_run.
+ * A, B and C 16-byte aligned, the scales 4-byte (MXGEMM_ERR_MISALIGNED).
+ * MXGEMM_OPT_A_FORMAT and MXGEMM_OPT_B_FORMAT may be E4M3 or E5M2 (others:
+ * MXGEMM_ERR_INVALID_VALUE); the wait limit, the stall hook, the profile
+ * events and the launch count apply, the other options do not.  C must not
+ * overlap the operands.  Errors as for mxgemm_run. */
+int mxgemm_run_block128(mxgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *A,
+                        const float *A_scale, const void *B, const float *B_scale, int b_block,
+                        void *C, int use_acc, int out_dtype, mxgemm_stream_t stream);
+
+/* Blocks of mxgemm_quantize_block128. */
+typedef enum {
+  MXGEMM_BLOCK_ROWS = 0,  /* 1 x 128: activations (A); codes R x C, scales R x ceil(C/128) */
+  MXGEMM_BLOCK_COLS = 1,  /* 128 x 1, stored transposed, so that the blocks run along the
+                             rows of the result: codes C x round_up(R, 16) (the added
+                             columns are code 0), scales C x ceil(R/128).  Both operands of
+                             a weight's gradient, with K = round_up(R, 16). */
+  MXGEMM_BLOCK_TILES = 2  /* 128 x 128: weights; codes R x C, scales ceil(R/128) x ceil(C/128) */
+} mxgemm_block_t;
+
+/* Operands of mxgemm_run_block128 from a dense row-major R x C matrix X
+ * (MXGEMM_IN_F32 or MXGEMM_IN_BF16), on `stream`.  Per block, in FP32:
+ *   top   = max(largest |x|, 2^-100)
+ *   scale = top / 448
+ *   code  = nearest E4M3 value to clamp(x * (448 / top), +-448), ties to even.
+ * R in [0, 2^31), C in [0, 2^31) a multiple of 16.  X and codes 16-byte
+ * aligned, scales 4-byte.  X must hold finite values.  Needs no handle and
+ * allocates nothing; errors as for mxgemm_quantize. */
+int mxgemm_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t C, int block,
+                             void *codes, float *scales, mxgemm_stream_t stream);
+
+/* A key/value cache held in pages of E4M3 codes, with one FP32 scale for each
+ * page and key/value head (value = code * scale).  The caller owns the device
+ * memory; the struct is read during the call only.
+ *   K, V             : num_pages x kv_heads x page_size x head_dim codes,
+ *                      16-byte aligned
+ *   K_scale, V_scale : num_pages x kv_heads float, positive and finite
+ *   page_size        : 16, 32, 64 or 128;  head_dim : 64 or 128.
+ * Which pages a sequence has, in order, is row b of a page table: batch rows
+ * of int32, table_pitch entries apart; entries past a sequence's last page
+ * are not read.  A page number outside [0, num_pages) or a length that is
+ * negative or does not fit the table is not followed: what it names counts as
+ * absent, and MXGEMM_ERR_INVALID_VALUE is recorded in the handle's device
+ * status word. */
+typedef struct {
+  void *K;
+  void *V;
+  float *K_scale;
+  float *V_scale;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+} mxgemm_cache_t;
+
+/* Append tokens to the sequences of a cache, on `stream`.
+ *   page_table : batch x table_pitch int32 (above)
+ *   kv_len     : batch int32, each sequence's length WITH the new tokens (the
+ *                array that mxgemm_cache_attention takes next)
+ *   q_start    : batch + 1 int32, ascending from 0 to `tokens`: sequence b's
+ *                new tokens are rows q_start[b] .. q_start[b+1] - 1.  NULL: one
+ *                token each (tokens == batch).
+ *   new_K, new_V : tokens rows of kv_heads x head_dim values, `pitch`
+ *                elements from row to row (slices of a projection's output);
+ *                x_dtype as for mxgemm_quantize.  Finite.
+ * Token i of a sequence's n goes to position kv_len - n + i.  Of each page
+ * that new tokens touch and each head, for K and V alike:
+ *   need  = max(2^-64, the least power of two >= (largest new |x|) / 448)
+ *   scale = need where the new tokens begin the page, else max(old scale, need)
+ *   codes of the new tokens: nearest E4M3 value to clamp(x / scale, +-448);
+ *   codes that the page held before, when the scale grew: nearest E4M3 value
+ *   to code * (old scale / scale) (exact for old scales that are powers of two,
+ *   but for values that fall below E4M3's normal range).
+ * Pages that two sequences share must not be appended to.  All device
+ * pointers; K, V of the cache 16-byte aligned, new_K and new_V aligned to, and
+ * pitch a multiple of, 8 elements (MXGEMM_ERR_MISALIGNED). */
+int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
+                        const int32_t *page_table, int64_t table_pitch, const int32_t *kv_len,
+                        const int32_t *q_start, int64_t tokens, const void *new_K,
+                        const void *new_V, int64_t pitch, int x_dtype, mxgemm_stream_t stream);
+
+/* Attention of `tokens` query tokens over the cache, on `stream`:
+ *
+ *   O[t,h] = sum_j p_j V[j],  p = softmax over the visible j of scale * Q[t,h] . K[j]
+ *   lse[t,h] = log of the sum of exp(scale * Q[t,h] . K[j])   (natural)
+ *
+ * Query token i of sequence b's n stands at position p = kv_len[b] - n + i of
+ * its sequence.  Key j (0 <= j < kv_len[b]) is visible when j <= p (causal = 1;
+ * with causal = 0 every key is) and, when window > 0, p - j < window or
+ * j < sinks (a sliding window, with the first `sinks` tokens always visible).
+ * A query that sees no key gets O = 0 and lse = -inf.  Head h reads key/value
+ * head h / (heads / kv_heads); heads is a multiple of kv_heads.
+ *   Q : tokens rows of heads x head_dim bfloat16, q_pitch elements apart;
+ *   O : tokens x heads x head_dim bfloat16, dense;  lse : tokens x heads
+ *   float, or NULL.
+ *   page_table, kv_len, q_start : as for mxgemm_cache_append.
+ *   scale : finite.  window, sinks >= 0.
+ * Sums and softmax statistics are FP32; the codes enter the products exactly,
+ * the weights p rounded to FP16.  Places past a sequence's end and absent
+ * pages may hold anything, NaN codes included.  The split of the work, and so
+ * the order of the sums, depends on the lengths and sizes alone: equal calls
+ * give equal bits.  Q and O 16-byte aligned, q_pitch % 8 == 0
+ * (MXGEMM_ERR_MISALIGNED).  The handle's workspace holds partial results. */
+int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
+                           int64_t heads, const int32_t *page_table, int64_t table_pitch,
+                           const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
+                           const void *Q, int64_t q_pitch, float scale, int causal,
+                           int64_t window, int64_t sinks, void *O, float *lse,
+                           mxgemm_stream_t stream);
 
 /* Static description of a status code. */
 const char *mxgemm_status_string(int status);
