@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "block128_kernel.cuh"
 #include "context.h"
@@ -34,6 +35,136 @@ int launch_quantize128(const T *x, int64_t R, int64_t C, int block, uint8_t *cd,
     mxg::quantize128_tiles_kernel<T><<<grid, 512, 0, stream>>>(x, R, C, cd, sc);
   }
   return cudaGetLastError() == cudaSuccess ? MXGEMM_OK : MXGEMM_ERR_CUDA;
+}
+
+// 2-D tensor map of bytes (or of C's elements), 128-byte swizzle: dims
+// {inner, outer}, row pitch in bytes, box.
+int encode(const mxg::HandleView &v, CUtensorMap *tm, CUtensorMapDataType dt, const void *base, int64_t inner,
+           int64_t outer, int64_t pitch, uint32_t box_inner, uint32_t box_outer) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return v.encode(tm, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MXGEMM_OK
+             : MXGEMM_ERR_CUDA;
+}
+
+// A launch with clusters of `cluster` CTAs along x.
+template <typename... Params, typename... Args>
+int launch_cluster(void (*kern)(Params...), int grid, int threads, int smem, int cluster, cudaStream_t stream,
+                   const Args &...args) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  return MXGEMM_OK;
+}
+
+// M > 128: CTA pairs on 256 x 256 tiles, one pair per two SMs.
+int run_pair(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, bool bf16,
+             int variant, cudaStream_t stream) {
+  CUtensorMap tA, tB, tC;
+  std::memset(&tC, 0, sizeof(tC));
+  const int eb = bf16 ? 2 : 4;
+  p.idesc_fmt = mxg::fmt_bits(v.a_fmt, v.b_fmt);
+  p.m_tiles = static_cast<int>(cdiv(p.M, 256));
+  p.n_tiles = static_cast<int>(cdiv(p.N, 256));
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  if (tiles >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+  p.tiles = static_cast<int>(tiles);
+  p.tma_store = !p.use_acc && static_cast<int64_t>(p.N) * eb % 16 == 0;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (encode(v, &tA, u8, A, p.K, p.M, p.K, 128, 128) ||
+      (nk ? encode(v, &tB, u8, B, p.K, p.N, p.K, 128, 128) : encode(v, &tB, u8, B, p.N, p.K, p.N, 128, 128)) ||
+      (p.tma_store && encode(v, &tC, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                             p.C, p.N, p.M, static_cast<int64_t>(p.N) * eb, bf16 ? 64 : 32, 32)))
+    return MXGEMM_ERR_CUDA;
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, v.sm_count / 2));
+  switch (variant) {
+#define MXG_PAIR(V)                                                                                     \
+  case V:                                                                                               \
+    return launch_cluster(mxg::b128_pair_kernel<V>, grid, mxg::PairCfg<V>::THREADS,                     \
+                          mxg::PairCfg<V>::SMEM_BYTES, 2, stream, tA, tB, tC, p);
+    MXG_PAIR(0)
+    MXG_PAIR(1)
+    MXG_PAIR(2)
+    MXG_PAIR(3)
+    MXG_PAIR(4)
+    MXG_PAIR(5)
+    MXG_PAIR(6)
+    MXG_PAIR(7)
+#undef MXG_PAIR
+    default:
+      return MXGEMM_ERR_INVALID_VALUE;
+  }
+}
+
+template <int NT>
+int run_skinny_nt(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, int variant,
+                  cudaStream_t stream) {
+  using S = mxg::SkinnyCfg<NT>;
+  p.nm = (p.M + 15) / 16 * 16;
+  // the MMA's A operand is B and its B operand A
+  p.idesc_fmt = mxg::fmt_bits(v.b_fmt, v.a_fmt);
+  // enough CTAs for the SMs where the column blocks alone are too few, within
+  // one cluster, four K blocks each at least
+  const int64_t blocks = cdiv(p.N, 128);
+  int64_t splits = std::max<int64_t>(1, v.sm_count / blocks);
+  splits = std::min<int64_t>(splits, S::MAX_SPLITS);
+  splits = std::min<int64_t>(splits, std::max(1, p.kb / 4));
+  p.splits = static_cast<int>(splits);
+  CUtensorMap tA, tB;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (encode(v, &tA, u8, A, p.K, p.M, p.K, 128, static_cast<uint32_t>(p.nm)) ||
+      (nk ? encode(v, &tB, u8, B, p.K, p.N, p.K, 128, 128) : encode(v, &tB, u8, B, p.N, p.K, p.N, 128, 128)))
+    return MXGEMM_ERR_CUDA;
+  const int grid = static_cast<int>(blocks * splits);
+  switch (variant) {
+#define MXG_SKINNY(V)                                                                              \
+  case V:                                                                                          \
+    return launch_cluster(mxg::b128_skinny_kernel<NT, V>, grid, S::THREADS, S::SMEM_BYTES,         \
+                          p.splits, stream, tB, tA, p);
+    MXG_SKINNY(0)
+    MXG_SKINNY(1)
+    MXG_SKINNY(2)
+    MXG_SKINNY(3)
+    MXG_SKINNY(4)
+    MXG_SKINNY(5)
+    MXG_SKINNY(6)
+    MXG_SKINNY(7)
+#undef MXG_SKINNY
+    default:
+      return MXGEMM_ERR_INVALID_VALUE;
+  }
+}
+
+// M <= 128: transposed, the kernel for M rounded up to 16, 32, 64 or 128.
+int run_skinny(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, int variant,
+               cudaStream_t stream) {
+  if (p.M <= 16) return run_skinny_nt<16>(v, p, A, B, nk, variant, stream);
+  if (p.M <= 32) return run_skinny_nt<32>(v, p, A, B, nk, variant, stream);
+  if (p.M <= 64) return run_skinny_nt<64>(v, p, A, B, nk, variant, stream);
+  return run_skinny_nt<128>(v, p, A, B, nk, variant, stream);
 }
 
 }  // namespace
@@ -73,7 +204,8 @@ extern "C" int mxgemm_run_block128(mxgemm_handle_t h, int64_t M, int64_t N, int6
   if (!h) return MXGEMM_ERR_INVALID_VALUE;
   const mxg::HandleView v = mxg::handle_view(h);
   const bool nk = v.b_major == MXGEMM_B_N_BY_K;
-  if (M < 0 || N < 0 || K < 0 || M >= kLim || N >= kLim || K >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+  // (sizes rounded up to whole tiles stay below 2^31)
+  if (M < 0 || N < 0 || K < 0 || M > kLim - 512 || N > kLim - 512 || K > kLim - 512) return MXGEMM_ERR_INVALID_VALUE;
   if (K % 16 != 0 || (!nk && N % 16 != 0)) return MXGEMM_ERR_INVALID_VALUE;
   if (b_block != 1 && b_block != 128) return MXGEMM_ERR_INVALID_VALUE;
   if (out_dtype != MXGEMM_OUT_F32 && out_dtype != MXGEMM_OUT_BF16) return MXGEMM_ERR_INVALID_VALUE;
@@ -101,31 +233,30 @@ extern "C" int mxgemm_run_block128(mxgemm_handle_t h, int64_t M, int64_t N, int6
     return MXGEMM_ERR_INVALID_VALUE;
 
   mxg::B128Params p;
-  p.M = M;
-  p.N = N;
-  p.K = K;
-  p.kb = cdiv(K, 128);
-  p.A = static_cast<const uint8_t *>(A);
-  p.B = static_cast<const uint8_t *>(B);
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.kb = static_cast<int>(cdiv(K, 128));
   p.a_scale = A_scale;
   p.b_scale = B_scale;
+  p.bs_cols = cdiv(N, b_block);
+  p.bs_n = nk ? p.kb : 1;
+  p.bs_k = nk ? 1 : p.bs_cols;
   p.C = C;
-  p.b_pitch_k = nk ? 1 : N;
-  p.b_pitch_n = nk ? K : 1;
-  p.bs_pitch_k = nk ? 1 : cdiv(N, b_block);
-  p.bs_pitch_n = nk ? p.kb : 1;
-  p.b_block = b_block;
   p.use_acc = use_acc;
-  p.out_bf16 = out_dtype == MXGEMM_OUT_BF16;
-  p.a_e5m2 = v.a_fmt == MXGEMM_FMT_E5M2;
-  p.b_e5m2 = v.b_fmt == MXGEMM_FMT_E5M2;
+  p.status = v.status;
+  p.timeout_ns = v.timeout_ns;
+  p.stall_producer = v.stall_producer;
+  const bool bf16 = out_dtype == MXGEMM_OUT_BF16;
+  const int variant = (bf16 ? mxg::kB128Bf16 : 0) | (nk ? mxg::kB128KMajor : 0) | (b_block == 1 ? mxg::kB128Cols : 0);
   if (v.prof_before && cudaEventRecord(v.prof_before, stream) != cudaSuccess) {
     cudaGetLastError();
     return MXGEMM_ERR_CUDA;
   }
-  const int64_t mt = cdiv(M, 64), nt = cdiv(N, 64);
-  mxg::block128_kernel<<<static_cast<unsigned>(mt * nt), 256, 0, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return MXGEMM_ERR_CUDA;
+  const int st = M <= 128 ? run_skinny(v, p, A, B, nk, variant, stream)
+                          : run_pair(v, p, A, B, nk, bf16, variant, stream);
+  if (st != MXGEMM_OK) return st;
   ++*v.launches;
   if (v.prof_after && cudaEventRecord(v.prof_after, stream) != cudaSuccess) {
     cudaGetLastError();

@@ -1,73 +1,732 @@
-// block128_kernel.cuh -- C (+)= sum over K blocks of 128 of
-// A_scale * B_scale * (A block . B block), the products of a block summed
-// unscaled in FP32 and the scaled blocks added in FP32.
+// block128_kernel.cuh -- the product with one FP32 scale per block of 128 on
+// sm_103a:
 //
-// 64 x 64 tiles, 256 threads of 4 x 4 results, operands decoded to FP32 in
-// shared memory 16 K values at a time.
+//   C[m,n] (+)= sum over K blocks kb of  sA[m,kb] * sB[n,kb] * P_kb[m,n],
+//   P_kb[m,n] = sum over the 128 k of block kb of A[m,k] B[n,k]
+//
+// The tensor cores form each P_kb unscaled (tcgen05.mma.kind::f8f6f4, 8-bit
+// operands, FP32 accumulator in TMEM, cleared for every block), and the
+// epilogue warps read it from TMEM and add it, scaled, to FP32 sums that stay
+// in registers for the whole of K: FP32 scales cannot enter the MMA, whose
+// own block scales are powers of two.  So per K block of a 128 x 256 tile an
+// SM has 512 cycles of MMA, and beside them 128 KB to read from TMEM and
+// 32768 multiply-adds, two per instruction (fma.rn.f32x2): two accumulators
+// in TMEM, and the MMA of one block runs while the other is being added.
+//
+// Two kernels:
+//   b128_pair_kernel    M > 128: CTA pairs (cta_group::2), 256 x 256 tiles,
+//                       each CTA with 128 rows of A and 128 columns of B a
+//                       K block: 32 KB of operands per 512 cycles and SM.
+//   b128_skinny_kernel  M <= 128: transposed, 128 columns of B on the MMA's
+//                       128-row side and the rows of A as its N, K split over
+//                       a cluster; bound by reading B once.
+//
+// Waits are bounded as in the other kernels: one that runs out records
+// MXGEMM_ERR_TIMEOUT, the roles drain and return.
 #pragma once
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cstdint>
+
+#include "mxgemm_kernel.cuh"
+#include "ptx.cuh"
 
 namespace mxg {
 
 struct B128Params {
-  int64_t M, N, K, kb;
-  const uint8_t *A, *B;
-  const float *a_scale, *b_scale;
+  int M, N, K;
+  int kb;          // ceil(K / 128)
+  const float *a_scale;  // M x kb
+  const float *b_scale;
+  int64_t bs_n, bs_k;  // entries of B_scale from one block of columns (of K) to the next
+  int64_t bs_cols;     // blocks of columns
   void *C;
-  int64_t b_pitch_k, b_pitch_n;    // elements of B from one k (n) to the next
-  int64_t bs_pitch_k, bs_pitch_n;  // entries of B_scale
-  int b_block;
-  int use_acc, out_bf16;
-  int a_e5m2, b_e5m2;
+  int use_acc;
+  uint32_t idesc_fmt;
+  int *status;
+  unsigned long long timeout_ns;
+  int stall_producer;
+  // pairs
+  int m_tiles, n_tiles, tiles;
+  int tma_store;  // C's rows are multiples of 16 bytes and nothing is added
+  // skinny
+  int nm;      // M rounded up to 16
+  int splits;  // CTAs of a cluster that share a column block's K
 };
 
-__device__ __forceinline__ float fp8_value(uint8_t c, int e5m2) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, e5m2 ? __NV_E5M2 : __NV_E4M3)));
+// Instruction descriptor of kind::f8f6f4: FP32 accumulator, M x N; the
+// operands' formats are OR-ed in, and the transpose bit of an operand whose
+// M (N) dimension is the contiguous one.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
 }
 
-__global__ void __launch_bounds__(256) block128_kernel(const B128Params p) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int64_t tiles_n = (p.N + 63) / 64;
-  const int64_t m0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t b = 0; b < p.kb; ++b) {
-    float part[4][4] = {};
-    const int64_t ke = min(p.K, (b + 1) * 128);
-    for (int64_t k0 = b * 128; k0 < ke; k0 += 16) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < 1024; i += 256) {
-        const int r = i >> 4, k = i & 15;
-        sa[k][r] = m0 + r < p.M ? fp8_value(p.A[(m0 + r) * p.K + k0 + k], p.a_e5m2) : 0.f;
-        sb[k][r] = n0 + r < p.N ? fp8_value(p.B[(n0 + r) * p.b_pitch_n + (k0 + k) * p.b_pitch_k], p.b_e5m2) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 16; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) part[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Wait for this thread's tcgen05.ld results in r: the registers are named so
+// that no use of them moves above the wait.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Two FP32 values in a 64-bit register pair, and arithmetic on both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+constexpr int kB128Bf16 = 1;    // BF16 output (else FP32)
+constexpr int kB128KMajor = 2;  // B given N x K (else K x N)
+constexpr int kB128Cols = 4;    // a scale of B for each column (else for 128)
+
+template <int V>
+struct PairCfg {
+  static constexpr int STAGES = 6;
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // per CTA
+  static constexpr uint32_t STAGE_TX = 2 * (A_BYTES + B_BYTES);   // both CTAs
+  static constexpr int OFF_A = 0;
+  static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+  // 4 KB for each epilogue warp: pieces of C on their way out and, with a scale
+  // for each column, [2 groups][4 K blocks][128 columns] of them before that
+  static constexpr int OFF_STG = OFF_B + STAGES * B_BYTES;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * 4096;
+  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;  // full, empty, acc_full[2], acc_empty[2], final
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int THREADS = 32 * (4 + EPI_WARPS);
+  // registers a thread: at launch, then of the load and MMA warps' group and
+  // of the epilogue's two (3 x 168 = 56 + 2 x 224: the block's own)
+  static constexpr int REGS_MAIN = 56, REGS_EPI = 224;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+// Warp roles (per CTA, 384 threads): warp 0 loads, warp 1 of the pair's first
+// CTA issues the MMAs (and allocates TMEM in both), warps 2 and 3 idle, warps
+// 4-11 are the epilogue: warp w has TMEM lanes 32 (w % 4) .. +31, rows of its
+// CTA's half tile, and 128 of the tile's 256 columns, one row and 128 sums a
+// thread.  The first four warps give registers to the others.
+template <int V>
+__global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
+    b128_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC, const B128Params p) {
+  using C = PairCfg<V>;
+  constexpr bool kBF16 = (V & kB128Bf16) != 0, kKM = (V & kB128KMajor) != 0, kCols = (V & kB128Cols) != 0;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  const uint32_t bar_full = base + C::OFF_BAR;
+  const uint32_t bar_empty = bar_full + 8 * C::STAGES;
+  const uint32_t bar_acc_full = bar_empty + 8 * C::STAGES;
+  const uint32_t bar_acc_empty = bar_acc_full + 16;
+  const uint32_t bar_final = bar_acc_empty + 16;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);
+  volatile int *never = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 8);  // never raised
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (m < p.M && n < p.N)
-          acc[i][j] += part[i][j] * (p.a_scale[m * p.kb + b] *
-                                     p.b_scale[n / p.b_block * p.bs_pitch_n + b * p.bs_pitch_k]);
-      }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_acc_full + 8 * b, 1);
+      mbar_init(bar_acc_empty + 8 * b, 2 * C::EPI_WARPS);
+    }
+    mbar_init(bar_final, 1);
+    *abort_flag = 0;
+    *never = 0;
+    fence_mbar_init();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= p.M || n >= p.N) continue;
-      if (p.out_bf16) {
-        __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.C) + m * p.N + n;
-        *c = __float2bfloat16_rn(acc[i][j] + (p.use_acc ? __bfloat162float(*c) : 0.f));
-      } else {
-        float *c = static_cast<float *>(p.C) + m * p.N + n;
-        *c = acc[i][j] + (p.use_acc ? *c : 0.f);
+  if (warp == 1) {
+    tmem_alloc<2>(smem_u32(tmem_slot), 512);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+  const WaitCtl wn{p.status, never, p.timeout_ns};
+  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+  const int kb = p.kb;
+
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_MAIN));
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one() != 0;
+    int st = 0;
+    uint32_t ph = 0;
+    long long issued = 0;
+    bool ok = !p.stall_producer;
+    for (int t = unit; ok && t < p.tiles; t += units) {
+      int mt, nt;
+      tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
+      const int row = mt * 256 + 128 * static_cast<int>(rank), col = nt * 256 + 128 * static_cast<int>(rank);
+      for (int ks = 0; ks < kb; ++ks) {
+        if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * st, ph ^ 1u, wc, 0x01 | (st << 8)))) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, C::STAGE_TX);
+          const uint32_t fb = mapa_shared(bar_full + 8 * st, 0);
+          tma_load_2d_pair(base + C::OFF_A + st * C::A_BYTES, &tmA, ks * 128, row, fb);
+          if constexpr (kKM) tma_load_2d_pair(base + C::OFF_B + st * C::B_BYTES, &tmB, ks * 128, col, fb);
+          else tma_load_2d_pair(base + C::OFF_B + st * C::B_BYTES, &tmB, col, ks * 128, fb);
+        }
+        __syncwarp();
+        ++issued;
+        if (++st == C::STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
     }
+    // Before the CTA may finish: every fill's MMA has released its stage; and
+    // where a wait gave up, the fills that are still on their way land (the
+    // full barriers are the first CTA's).
+    bool clean = true;
+    const int n = static_cast<int>(issued < C::STAGES ? issued : C::STAGES);
+    for (int i = 0; i < n; ++i) {
+      const int s = (st + C::STAGES - n + i) % C::STAGES;
+      const uint32_t par = (s < st ? ph : ph ^ 1u);  // parity of that stage's last fill
+      if (clean)
+        clean = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * s, par, wc, 0x11 | (s << 8)));
+      if (!clean && rank == 0) wait_phase<false>(bar_full + 8 * s, par, wn, 0x11 | (s << 8));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0) {
+      const bool leader = elect_one() != 0;
+      int st = 0;
+      uint32_t ph = 0, it = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_f8(256, 256, false, !kKM) | p.idesc_fmt;
+      for (int t = unit; ok && t < p.tiles; t += units) {
+        for (int ks = 0; ks < kb; ++ks, ++it) {
+          const uint32_t buf = it & 1u;
+          ok = __all_sync(0xFFFFFFFFu, wait_phase<true>(bar_acc_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, wc, 0x02)) &&
+               __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_full + 8 * st, ph, wc, 0x03 | (st << 8)));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t sA = base + C::OFF_A + st * C::A_BYTES, sB = base + C::OFF_B + st * C::B_BYTES;
+            // A (and a K-major B): 128-byte swizzle, 8-row groups 1 KB apart,
+            // 32 bytes per K = 32; an N-major B: 32 K rows (4 KB) per K = 32
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f8<2>(tmem + 256 * buf, smem_desc(sA + 32 * k, 0, 1024, 2),
+                        kKM ? smem_desc(sB + 32 * k, 0, 1024, 2) : smem_desc(sB + 4096 * k, 16384, 1024, 2),
+                        idesc, k != 0);
+            tc_commit_pair(bar_empty + 8 * st, 0x3);
+            tc_commit_pair(bar_acc_full + 8 * buf, 0x3);
+          }
+          __syncwarp();
+          if (++st == C::STAGES) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (leader) tc_commit_pair(bar_final, 0x1);
+      __syncwarp();
+      wait_phase<false>(bar_final, 0, wn, 0x04);
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
+    const int w = warp - 4, q = warp & 3, half = w >> 2;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
+    const uint32_t stg = base + C::OFF_STG + w * 4096;
+    float *cs = reinterpret_cast<float *>(sm + C::OFF_STG + w * 4096);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = unit; ok && t < p.tiles; t += units) {
+      int mt, nt;
+      tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
+      const int row0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
+      const int col0 = nt * 256 + 128 * half;
+      // this thread's row of A_scale, and its half's block of B_scale (or its
+      // four columns, lane + 32 c); in the ragged tile rows and columns past
+      // the edge repeat the last
+      const float *as = p.a_scale + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * kb;
+      constexpr int kNb = kCols ? 4 : 1;
+      const float *bs[kNb];
+#pragma unroll
+      for (int c = 0; c < kNb; ++c)
+        bs[c] = p.b_scale + min(kCols ? static_cast<int64_t>(col0 + lane + 32 * c) : static_cast<int64_t>(col0 >> 7),
+                                p.bs_cols - 1) * p.bs_n;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      // scales of the current group of four K blocks (s) and of the next one,
+      // loaded while the current one is added
+      float s[4], na[4], nb[4][kNb];
+      auto fetch = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = min(4 * g + j, kb - 1);
+          na[j] = __ldg(as + k);
+#pragma unroll
+          for (int c = 0; c < kNb; ++c) nb[j][c] = __ldg(bs[c] + k * p.bs_k);
+        }
+      };
+      fetch(0);
+      if constexpr (kCols) {  // the last tile's pieces of C have left the buffer
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+      }
+      for (int ks = 0; ks < kb; ++ks, ++it) {
+        if ((ks & 3) == 0) {
+          const int g = ks >> 2;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kCols) {
+              s[j] = na[j];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) cs[((g & 1) * 4 + j) * 128 + lane + 32 * c] = nb[j][c];
+            } else {
+              s[j] = na[j] * nb[j][0];
+            }
+          }
+          if constexpr (kCols) __syncwarp();
+          fetch(g + 1);
+        }
+        const uint32_t buf = it & 1u;
+        ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_full + 8 * buf, (it >> 1) & 1u, wc, 0x05));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t s2 = pack2(s[0], s[0]);
+        s[0] = s[1];
+        s[1] = s[2];
+        s[2] = s[3];
+        const float4 *c4 = reinterpret_cast<const float4 *>(cs + (((ks >> 2) & 1) * 4 + (ks & 3)) * 128);
+        uint32_t v[2][16];
+        const uint32_t ta = lane_addr + 256 * buf;
+        tmem_ld_32x32b_x16(ta, v[0]);
+        tmem_ld_wait16(v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c < 7) tmem_ld_32x32b_x16(ta + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint64_t x = pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
+            if constexpr (kCols) {
+              const float4 f = c4[4 * c + (i >> 1)];
+              x = mul2(x, (i & 1) ? pack2(f.z, f.w) : pack2(f.x, f.y));
+            }
+            acc[8 * c + i] = fma2(x, s2, acc[8 * c + i]);
+          }
+          if (c < 7) tmem_ld_wait16(v[(c + 1) & 1]);
+          if (c == 6) {  // the accumulator has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(bar_acc_empty + 8 * buf, 0);
+          }
+        }
+      }
+      if (!ok) break;
+      // C: rows row0 .. +31, columns col0 .. +127, in pieces of 128 bytes a
+      // row through this warp's 4 KB (16-byte units swizzled by the row)
+      if (row0 >= p.M || col0 >= p.N) continue;
+      const uint32_t mine = stg + lane * 128;
+      if (p.tma_store) {
+        constexpr int kCol = kBF16 ? 64 : 32;
+#pragma unroll
+        for (int c = 0; c < 128 / kCol; ++c) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a, b;
+              if constexpr (kBF16) {
+                unpack2(acc[c * 32 + 4 * j + e], a, b);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                o[e] = *reinterpret_cast<const uint32_t *>(&h);
+              } else {
+                unpack2(acc[c * 16 + 2 * j + (e >> 1)], a, b);
+                o[e] = __float_as_uint((e & 1) ? b : a);
+              }
+            }
+            st_shared_v4(mine + ((j ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && col0 + c * kCol < p.N) {
+            tma_store_2d(&tmC, stg, col0 + c * kCol, row0);
+            bulk_commit_group();
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float a, b, d, e;
+            unpack2(acc[c * 16 + 2 * j], a, b);
+            unpack2(acc[c * 16 + 2 * j + 1], d, e);
+            st_shared_v4(mine + ((j ^ (lane & 7)) << 4), __float_as_uint(a), __float_as_uint(b),
+                         __float_as_uint(d), __float_as_uint(e));
+          }
+          __syncwarp();
+          const int col = col0 + c * 32 + lane;
+          const int rows = min(32, p.M - row0);
+          const float *from = reinterpret_cast<const float *>(sm + (stg - base));
+          if (col < p.N)
+            for (int r = 0; r < rows; ++r) {
+              float x = from[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+              const int64_t at = static_cast<int64_t>(row0 + r) * p.N + col;
+              if constexpr (kBF16) {
+                __nv_bfloat16 *cp = static_cast<__nv_bfloat16 *>(p.C) + at;
+                if (p.use_acc) x += __bfloat162float(*cp);
+                *cp = __float2bfloat16_rn(x);
+              } else {
+                float *cp = static_cast<float *>(p.C) + at;
+                if (p.use_acc) x += *cp;
+                *cp = x;
+              }
+            }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// M <= 128: C^T[n, m] for 128 columns n of B and the rows m of A.
+template <int NT>
+struct SkinnyCfg {
+  static constexpr int BT_BYTES = 128 * 128;  // 128 columns of B
+  static constexpr int AT_BYTES = NT * 128;   // up to NT rows of A
+  static constexpr int STAGES = NT <= 16 ? 11 : NT <= 32 ? 10 : NT <= 64 ? 8 : 6;
+  static constexpr int BUFS = 4;  // accumulators
+  static constexpr int OFF_BT = 0;
+  static constexpr int OFF_AT = OFF_BT + STAGES * BT_BYTES;
+  // scales of A, for each epilogue warp [2 groups][4 K blocks][NT]
+  static constexpr int OFF_CS = OFF_AT + STAGES * AT_BYTES;
+  static constexpr int OFF_BAR = OFF_CS + 4 * 2 * 4 * NT * 4;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr uint32_t TM_COLS = NT * BUFS < 32 ? 32 : NT * BUFS;
+  static constexpr int THREADS = 6 * 32;
+  // the cluster reduction reuses the ring: NT x 128 sums of each other CTA
+  static constexpr int MAX_SPLITS = OFF_CS / (NT * 128 * 4) + 1 < 8 ? OFF_CS / (NT * 128 * 4) + 1 : 8;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(AT_BYTES % 1024 == 0 && OFF_CS % 16 == 0, "operand alignment");
+};
+
+template <int NT, int V>
+__global__ void __launch_bounds__(SkinnyCfg<NT>::THREADS, 1)
+    b128_skinny_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
+                       const B128Params p) {
+  using S = SkinnyCfg<NT>;
+  constexpr bool kBF16 = (V & kB128Bf16) != 0, kKM = (V & kB128KMajor) != 0, kCols = (V & kB128Cols) != 0;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = p.splits;
+  const int split = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int n0 = static_cast<int>(blockIdx.x) / splits * 128;
+  const int k_beg = static_cast<int>(static_cast<long long>(split) * p.kb / splits);
+  const int k_end = static_cast<int>(static_cast<long long>(split + 1) * p.kb / splits);
+
+  const uint32_t bar_full = base + S::OFF_BAR;
+  const uint32_t bar_empty = bar_full + 8 * S::STAGES;
+  const uint32_t bar_acc_full = bar_empty + 8 * S::STAGES;
+  const uint32_t bar_acc_empty = bar_acc_full + 8 * S::BUFS;
+  const uint32_t bar_final = bar_acc_empty + 8 * S::BUFS;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 4);
+  volatile int *never = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 8);  // never raised
+  const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+  const WaitCtl wn{p.status, never, p.timeout_ns};
+
+  auto load_step = [&](int st, int ks) {
+    const uint32_t fb = bar_full + 8 * st;
+    mbar_arrive_expect_tx(fb, S::BT_BYTES + p.nm * 128);
+    if constexpr (kKM) tma_load_2d(base + S::OFF_BT + st * S::BT_BYTES, &tmB, ks * 128, n0, fb);
+    else tma_load_2d(base + S::OFF_BT + st * S::BT_BYTES, &tmB, n0, ks * 128, fb);
+    tma_load_2d(base + S::OFF_AT + st * S::AT_BYTES, &tmA, ks * 128, 0, fb);
+  };
+  // the first ring round goes out before the rest of the set-up
+  const int n_early = p.stall_producer ? 0 : min(S::STAGES, k_end - k_beg);
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmA);
+      for (int s = 0; s < S::STAGES; ++s) {
+        mbar_init(bar_full + 8 * s, 1);
+        mbar_init(bar_empty + 8 * s, 1);
+      }
+      for (int b = 0; b < S::BUFS; ++b) {
+        mbar_init(bar_acc_full + 8 * b, 1);
+        mbar_init(bar_acc_empty + 8 * b, 4);
+      }
+      mbar_init(bar_final, 1);
+      *abort_flag = 0;
+      *never = 0;
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane < n_early) load_step(lane, k_beg + lane);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_u32(tmem_slot), S::TM_COLS);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  float acc[NT];  // epilogue: this lane's column of C, one sum per row
+  bool have = false;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one() != 0;
+    int st = n_early == S::STAGES ? 0 : n_early;
+    uint32_t ph = n_early == S::STAGES ? 1u : 0u;
+    int issued = n_early;
+    for (int ks = k_beg + n_early; ks < k_end && !p.stall_producer; ++ks) {
+      if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * st, ph ^ 1u, wc, 0x01 | (st << 8)))) break;
+      if (leader) load_step(st, ks);
+      __syncwarp();
+      ++issued;
+      if (++st == S::STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    // every fill has been consumed (or, after a wait that gave up, has
+    // landed) before the CTA may finish or reuse the ring
+    bool clean = true;
+    const int n = min(issued, S::STAGES);
+    for (int i = 0; i < n; ++i) {
+      const int s = (st + S::STAGES - n + i) % S::STAGES;
+      const uint32_t par = s < st ? ph : ph ^ 1u;
+      if (clean)
+        clean = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * s, par, wc, 0x11 | (s << 8)));
+      if (!clean) wait_phase<false>(bar_full + 8 * s, par, wn, 0x11 | (s << 8));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one() != 0;
+    const uint32_t idesc = idesc_f8(128, p.nm, !kKM, false) | p.idesc_fmt;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < k_end - k_beg; ++i) {
+      const int buf = i % S::BUFS;
+      if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_empty + 8 * buf, ((i / S::BUFS) & 1) ^ 1u, wc, 0x02)) ||
+          !__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_full + 8 * st, ph, wc, 0x03 | (st << 8))))
+        break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t sB = base + S::OFF_BT + st * S::BT_BYTES, sA = base + S::OFF_AT + st * S::AT_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f8<1>(tmem + NT * buf,
+                    kKM ? smem_desc(sB + 32 * k, 0, 1024, 2) : smem_desc(sB + 4096 * k, 16384, 1024, 2),
+                    smem_desc(sA + 32 * k, 0, 1024, 2), idesc, k != 0);
+        tc_commit(bar_empty + 8 * st);
+        tc_commit(bar_acc_full + 8 * buf);
+      }
+      __syncwarp();
+      if (++st == S::STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    if (leader) tc_commit(bar_final);
+    __syncwarp();
+    wait_phase<false>(bar_final, 0, wn, 0x04);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const int col = n0 + 32 * q + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float *cs = reinterpret_cast<float *>(sm + S::OFF_CS) + q * 8 * NT;
+    const float *bs = p.b_scale + (kCols ? min(static_cast<int64_t>(col), p.bs_cols - 1)
+                                         : static_cast<int64_t>(n0 >> 7)) * p.bs_n;
+#pragma unroll
+    for (int m = 0; m < NT; ++m) acc[m] = 0.f;
+    // scales, a group of four K blocks ahead: B's of this lane (s, nb), and
+    // A's 4 x NT, NT / 8 of them by each lane, through the warp's shared memory
+    constexpr int kPer = NT / 8;
+    float s[4], nb[4], na[kPer];
+    auto fetch = [&](int g) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) nb[j] = __ldg(bs + min(k_beg + 4 * g + j, k_end - 1) * p.bs_k);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = lane + 32 * j, k = min(k_beg + 4 * g + i / NT, k_end - 1), m = i % NT;
+        na[j] = m < p.M ? __ldg(p.a_scale + static_cast<int64_t>(m) * p.kb + k) : 0.f;
+      }
+    };
+    fetch(0);
+    have = true;
+    for (int i = 0; i < k_end - k_beg; ++i) {
+      if ((i & 3) == 0) {
+        const int g = i >> 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = nb[j];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          cs[(g & 1) * 4 * NT + lane + 32 * j] = na[j];
+        __syncwarp();
+        fetch(g + 1);
+      }
+      const int buf = i % S::BUFS;
+      have = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_full + 8 * buf, (i / S::BUFS) & 1, wc, 0x05));
+      if (!have) break;
+      tc_fence_after();
+      const float sb = s[0];
+      s[0] = s[1];
+      s[1] = s[2];
+      s[2] = s[3];
+      const float4 *c4 = reinterpret_cast<const float4 *>(cs + ((i >> 2) & 1) * 4 * NT + (i & 3) * NT);
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(lane_addr + NT * buf + 16 * c, v);
+        tmem_ld_wait16(v);
+        if (c == NT / 16 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acc_empty + 8 * buf);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 f = c4[4 * c + e];
+          acc[16 * c + 4 * e + 0] += __uint_as_float(v[4 * e + 0]) * (f.x * sb);
+          acc[16 * c + 4 * e + 1] += __uint_as_float(v[4 * e + 1]) * (f.y * sb);
+          acc[16 * c + 4 * e + 2] += __uint_as_float(v[4 * e + 2]) * (f.z * sb);
+          acc[16 * c + 4 * e + 3] += __uint_as_float(v[4 * e + 3]) * (f.w * sb);
+        }
+      }
+    }
+  }
+
+  // K split: the other CTAs of the cluster put their sums into the first one's
+  // ring, which adds them in rank order.  (First barrier: all main loops are
+  // done, the ring is free; second: the sums have been written.)
+  const bool epi = warp >= 2;
+  const int n = 32 * (warp & 3) + lane;
+  if (splits > 1) {
+    cluster_sync();
+    if (epi && split > 0) {
+      const uint32_t dst = mapa_shared(base, 0) + static_cast<uint32_t>(((split - 1) * (NT / 4)) * 128 + n) * 16;
+#pragma unroll
+      for (int j = 0; j < NT / 4; ++j)
+        st_cluster_v4(dst + j * 2048, __float_as_uint(acc[4 * j]), __float_as_uint(acc[4 * j + 1]),
+                      __float_as_uint(acc[4 * j + 2]), __float_as_uint(acc[4 * j + 3]));
+    }
+    cluster_sync();
+    if (epi && split == 0 && have) {
+      for (int r = 1; r < splits; ++r) {
+        const uint32_t src = base + static_cast<uint32_t>(((r - 1) * (NT / 4)) * 128 + n) * 16;
+#pragma unroll
+        for (int j = 0; j < NT / 4; ++j) {
+          const uint4 o = ld_shared_v4(src + j * 2048);
+          acc[4 * j + 0] += __uint_as_float(o.x);
+          acc[4 * j + 1] += __uint_as_float(o.y);
+          acc[4 * j + 2] += __uint_as_float(o.z);
+          acc[4 * j + 3] += __uint_as_float(o.w);
+        }
+      }
+    }
+  }
+  // a row of C is 32 consecutive columns of a warp's lanes
+  if (epi && split == 0 && have && n0 + n < p.N) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      if (m < p.M) {
+        const int64_t at = static_cast<int64_t>(m) * p.N + n0 + n;
+        float x = acc[m];
+        if constexpr (kBF16) {
+          __nv_bfloat16 *cp = static_cast<__nv_bfloat16 *>(p.C) + at;
+          if (p.use_acc) x += __bfloat162float(*cp);
+          *cp = __float2bfloat16_rn(x);
+        } else {
+          float *cp = static_cast<float *>(p.C) + at;
+          if (p.use_acc) x += *cp;
+          *cp = x;
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<1>(tmem, S::TM_COLS);
 }
 
 }  // namespace mxg

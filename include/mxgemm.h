@@ -389,7 +389,7 @@ int mxgemm_noalloc_set_option(int option, int64_t value);
  *
  * The sums are formed in FP32: each block's products in the tensor cores,
  * the scaled blocks added in registers.
- *   M, N, K : each in [0, 2^31); K % 16 == 0 (a last block of fewer than 128
+ *   M, N, K : each in [0, 2^31 - 512]; K % 16 == 0 (a last block of fewer than 128
  *             is a block of its own).  M == 0 or N == 0 is a no-op; K == 0
  *             sets C to 0 (use_acc = 0) or leaves it unchanged.
  *   A       : M x K element codes, K contiguous.
