@@ -10,8 +10,8 @@
 // in registers for the whole of K: FP32 scales cannot enter the MMA, whose
 // own block scales are powers of two.  So per K block of a 128 x 256 tile an
 // SM has 512 cycles of MMA, and beside them 128 KB to read from TMEM and
-// 32768 multiply-adds, two per instruction (fma.rn.f32x2): two accumulators
-// in TMEM, and the MMA of one block runs while the other is being added.
+// 32768 multiply-adds (256 cycles; two per instruction, fma.rn.f32x2, measured
+// slower: 400 cycles against 329 with the TMEM reads): two accumulators in TMEM, and the MMA of one block runs while the other is being added.
 //
 // Two kernels:
 //   b128_pair_kernel    M > 128: CTA pairs (cta_group::2), 256 x 256 tiles,
@@ -89,29 +89,13 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
-// Two FP32 values in a 64-bit register pair, and arithmetic on both.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
+// Four bytes from global to shared memory, and this thread's arrive on a
+// barrier once its copies so far have landed.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 constexpr int kB128Bf16 = 1;    // BF16 output (else FP32)
@@ -120,31 +104,44 @@ constexpr int kB128Cols = 4;    // a scale of B for each column (else for 128)
 
 template <int V>
 struct PairCfg {
-  static constexpr int STAGES = 6;
+  static constexpr bool COLS = (V & kB128Cols) != 0;
+  static constexpr int STAGES = 5;
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // per CTA
   static constexpr uint32_t STAGE_TX = 2 * (A_BYTES + B_BYTES);   // both CTAs
+  static constexpr int EPI_WARPS = 8;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
-  // 4 KB for each epilogue warp: pieces of C on their way out and, with a scale
-  // for each column, [2 groups][4 K blocks][128 columns] of them before that
-  static constexpr int OFF_STG = OFF_B + STAGES * B_BYTES;
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * 4096;
-  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;  // full, empty, acc_full[2], acc_empty[2], final
+  static constexpr int OFF_STG = OFF_B + STAGES * B_BYTES;  // 4 KB for each epilogue warp: C on its way out
+  // scales of eight K blocks, two slots: [K block][132] of the CTA's 128 rows,
+  // and [K block][260] of the tile's 256 columns (or [K block][4] of its two
+  // blocks); the odd pitches keep the transposing copies free of bank conflicts
+  static constexpr int KB = 8;
+  static constexpr int AS_PITCH = 132, BS_PITCH = COLS ? 260 : 4;
+  static constexpr int SLOT_BYTES = KB * (AS_PITCH + BS_PITCH) * 4;
+  static constexpr int OFF_SC = OFF_STG + EPI_WARPS * 4096;
+  static constexpr int OFF_BAR = OFF_SC + 2 * SLOT_BYTES;
+  // full, empty, acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], final
+  static constexpr int NUM_BARS = 2 * STAGES + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
-  // registers a thread: at launch, then of the load and MMA warps' group and
-  // of the epilogue's two (3 x 168 = 56 + 2 x 224: the block's own)
+  // registers a thread: 168 at launch, then of the first four warps and of the
+  // epilogue's eight (3 x 168 = 56 + 2 x 224: the block's own)
   static constexpr int REGS_MAIN = 56, REGS_EPI = 224;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(OFF_SC % 16 == 0 && SLOT_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
 // Warp roles (per CTA, 384 threads): warp 0 loads, warp 1 of the pair's first
-// CTA issues the MMAs (and allocates TMEM in both), warps 2 and 3 idle, warps
-// 4-11 are the epilogue: warp w has TMEM lanes 32 (w % 4) .. +31, rows of its
-// CTA's half tile, and 128 of the tile's 256 columns, one row and 128 sums a
-// thread.  The first four warps give registers to the others.
+// CTA issues the MMAs (and allocates TMEM in both), warp 2 brings the scales
+// (with a scale for each column, those by warp 3), warps 4-11 are the
+// epilogue: warp w has TMEM lanes 32 (w % 4) .. +31, rows of its CTA's half
+// tile, and 128 of the tile's 256 columns, one row and 128 sums a thread.  The
+// first four warps give registers to the others.
+// Scales come through shared memory because a warp's load of its 32 rows'
+// scales of one K block touches 32 lines: read by the epilogue warps
+// themselves they held up every K block (8192 x 28672 x 8192: 1784 us; with
+// one line for all rows, for comparison, 1533 us).
 template <int V>
 __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     b128_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -162,7 +159,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
   const uint32_t bar_empty = bar_full + 8 * C::STAGES;
   const uint32_t bar_acc_full = bar_empty + 8 * C::STAGES;
   const uint32_t bar_acc_empty = bar_acc_full + 16;
-  const uint32_t bar_final = bar_acc_empty + 16;
+  const uint32_t bar_sc_full = bar_acc_empty + 16;
+  const uint32_t bar_sc_empty = bar_sc_full + 16;
+  const uint32_t bar_final = bar_sc_empty + 16;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);
   volatile int *never = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 8);  // never raised
@@ -177,6 +176,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_acc_full + 8 * b, 1);
       mbar_init(bar_acc_empty + 8 * b, 2 * C::EPI_WARPS);
+      mbar_init(bar_sc_full + 8 * b, C::COLS ? 64 : 32);  // lanes of the warps that copy
+      mbar_init(bar_sc_empty + 8 * b, C::EPI_WARPS);
     }
     mbar_init(bar_final, 1);
     *abort_flag = 0;
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       for (int t = unit; ok && t < p.tiles; t += units) {
         for (int ks = 0; ks < kb; ++ks, ++it) {
           const uint32_t buf = it & 1u;
-          ok = __all_sync(0xFFFFFFFFu, wait_phase<true>(bar_acc_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, wc, 0x02)) &&
+          ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, wc, 0x02)) &&
                __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_full + 8 * st, ph, wc, 0x03 | (st << 8)));
           if (!ok) break;
           tc_fence_after();
@@ -279,6 +280,49 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       __syncwarp();
       wait_phase<false>(bar_final, 0, wn, 0x04);
     }
+  } else if (warp == 2 || kCols) {
+    // ------------------------------------------------------------ scales
+    const bool cols = warp == 3;  // the columns' scales, else the rows'
+    uint32_t n = 0;               // groups of eight K blocks so far
+    bool ok = true;
+    for (int t = unit; ok && t < p.tiles; t += units) {
+      int mt, nt;
+      tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
+      const int row0 = mt * 256 + 128 * static_cast<int>(rank);
+      for (int k0 = 0; k0 < kb; k0 += C::KB, ++n) {
+        const uint32_t slot = n & 1u;
+        ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_empty + 8 * slot, ((n >> 1) & 1u) ^ 1u, wc, 0x09));
+        if (!ok) break;
+        const uint32_t as = base + C::OFF_SC + slot * C::SLOT_BYTES, bs = as + C::KB * C::AS_PITCH * 4;
+        // (rows, columns and K blocks past the edge repeat the last)
+        if (!cols) {
+          const int j = lane & 7, k = min(k0 + j, kb - 1);
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            cp_async4(as + (j * C::AS_PITCH + r) * 4, p.a_scale + static_cast<int64_t>(min(row0 + r, p.M - 1)) * kb + k);
+          }
+          if (!kCols && lane < 16)
+            cp_async4(bs + (j * C::BS_PITCH + (lane >> 3)) * 4,
+                      p.b_scale + min(static_cast<int64_t>(2 * nt + (lane >> 3)), p.bs_cols - 1) * p.bs_n + k * p.bs_k);
+        } else if constexpr (kKM) {
+          const int j = lane & 7, k = min(k0 + j, kb - 1);
+#pragma unroll 8
+          for (int i = 0; i < 64; ++i) {
+            const int c = 4 * i + (lane >> 3);
+            cp_async4(bs + (j * C::BS_PITCH + c) * 4, p.b_scale + min(static_cast<int64_t>(nt * 256 + c), p.bs_cols - 1) * p.bs_n + k);
+          }
+        } else {
+#pragma unroll 8
+          for (int i = 0; i < 64; ++i) {
+            const int j = i >> 3, k = min(k0 + j, kb - 1), c = 32 * (i & 7) + lane;
+            cp_async4(bs + (j * C::BS_PITCH + c) * 4, p.b_scale + min(static_cast<int64_t>(nt * 256 + c), p.bs_cols - 1) + k * p.bs_k);
+          }
+        }
+        cp_async_arrive(bar_sc_full + 8 * slot);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -286,69 +330,31 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     const int w = warp - 4, q = warp & 3, half = w >> 2;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
     const uint32_t stg = base + C::OFF_STG + w * 4096;
-    float *cs = reinterpret_cast<float *>(sm + C::OFF_STG + w * 4096);
-    uint32_t it = 0;
+    uint32_t it = 0, n = 0;
     bool ok = true;
     for (int t = unit; ok && t < p.tiles; t += units) {
       int mt, nt;
       tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
       const int row0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const int col0 = nt * 256 + 128 * half;
-      // this thread's row of A_scale, and its half's block of B_scale (or its
-      // four columns, lane + 32 c); in the ragged tile rows and columns past
-      // the edge repeat the last
-      const float *as = p.a_scale + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * kb;
-      constexpr int kNb = kCols ? 4 : 1;
-      const float *bs[kNb];
+      float acc[128];
 #pragma unroll
-      for (int c = 0; c < kNb; ++c)
-        bs[c] = p.b_scale + min(kCols ? static_cast<int64_t>(col0 + lane + 32 * c) : static_cast<int64_t>(col0 >> 7),
-                                p.bs_cols - 1) * p.bs_n;
-      uint64_t acc[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      // scales of the current group of four K blocks (s) and of the next one,
-      // loaded while the current one is added
-      float s[4], na[4], nb[4][kNb];
-      auto fetch = [&](int g) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = min(4 * g + j, kb - 1);
-          na[j] = __ldg(as + k);
-#pragma unroll
-          for (int c = 0; c < kNb; ++c) nb[j][c] = __ldg(bs[c] + k * p.bs_k);
-        }
-      };
-      fetch(0);
-      if constexpr (kCols) {  // the last tile's pieces of C have left the buffer
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
-      }
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       for (int ks = 0; ks < kb; ++ks, ++it) {
-        if ((ks & 3) == 0) {
-          const int g = ks >> 2;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (kCols) {
-              s[j] = na[j];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) cs[((g & 1) * 4 + j) * 128 + lane + 32 * c] = nb[j][c];
-            } else {
-              s[j] = na[j] * nb[j][0];
-            }
-          }
-          if constexpr (kCols) __syncwarp();
-          fetch(g + 1);
+        const uint32_t slot = n & 1u;
+        if ((ks & (C::KB - 1)) == 0) {
+          ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * slot, (n >> 1) & 1u, wc, 0x0A));
+          if (!ok) break;
         }
+        const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC + slot * C::SLOT_BYTES);
+        const float *bc = sc + C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH;
+        float s = sc[(ks & (C::KB - 1)) * C::AS_PITCH + 32 * q + lane];
+        if constexpr (!kCols) s *= bc[half];
+        const float4 *c4 = reinterpret_cast<const float4 *>(bc + 128 * half);
         const uint32_t buf = it & 1u;
         ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_full + 8 * buf, (it >> 1) & 1u, wc, 0x05));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t s2 = pack2(s[0], s[0]);
-        s[0] = s[1];
-        s[1] = s[2];
-        s[2] = s[3];
-        const float4 *c4 = reinterpret_cast<const float4 *>(cs + (((ks >> 2) & 1) * 4 + (ks & 3)) * 128);
         uint32_t v[2][16];
         const uint32_t ta = lane_addr + 256 * buf;
         tmem_ld_32x32b_x16(ta, v[0]);
@@ -357,13 +363,13 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         for (int c = 0; c < 8; ++c) {
           if (c < 7) tmem_ld_32x32b_x16(ta + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint64_t x = pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
+          for (int i = 0; i < 16; ++i) {
+            float x = __uint_as_float(v[c & 1][i]);
             if constexpr (kCols) {
-              const float4 f = c4[4 * c + (i >> 1)];
-              x = mul2(x, (i & 1) ? pack2(f.z, f.w) : pack2(f.x, f.y));
+              const float4 f = c4[4 * c + (i >> 2)];
+              x *= (i & 3) == 0 ? f.x : (i & 3) == 1 ? f.y : (i & 3) == 2 ? f.z : f.w;
             }
-            acc[8 * c + i] = fma2(x, s2, acc[8 * c + i]);
+            acc[16 * c + i] = fmaf(x, s, acc[16 * c + i]);
           }
           if (c < 7) tmem_ld_wait16(v[(c + 1) & 1]);
           if (c == 6) {  // the accumulator has been read
@@ -371,6 +377,11 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(bar_acc_empty + 8 * buf, 0);
           }
+        }
+        if ((ks & (C::KB - 1)) == C::KB - 1 || ks == kb - 1) {  // and the group's scales
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_sc_empty + 8 * slot);
+          ++n;
         }
       }
       if (!ok) break;
@@ -389,14 +400,11 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float a, b;
               if constexpr (kBF16) {
-                unpack2(acc[c * 32 + 4 * j + e], a, b);
-                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[64 * c + 8 * j + 2 * e], acc[64 * c + 8 * j + 2 * e + 1]);
                 o[e] = *reinterpret_cast<const uint32_t *>(&h);
               } else {
-                unpack2(acc[c * 16 + 2 * j + (e >> 1)], a, b);
-                o[e] = __float_as_uint((e & 1) ? b : a);
+                o[e] = __float_as_uint(acc[32 * c + 4 * j + e]);
               }
             }
             st_shared_v4(mine + ((j ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -413,13 +421,10 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         for (int c = 0; c < 4; ++c) {
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float a, b, d, e;
-            unpack2(acc[c * 16 + 2 * j], a, b);
-            unpack2(acc[c * 16 + 2 * j + 1], d, e);
-            st_shared_v4(mine + ((j ^ (lane & 7)) << 4), __float_as_uint(a), __float_as_uint(b),
-                         __float_as_uint(d), __float_as_uint(e));
-          }
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(mine + ((j ^ (lane & 7)) << 4), __float_as_uint(acc[32 * c + 4 * j]),
+                         __float_as_uint(acc[32 * c + 4 * j + 1]), __float_as_uint(acc[32 * c + 4 * j + 2]),
+                         __float_as_uint(acc[32 * c + 4 * j + 3]));
           __syncwarp();
           const int col = col0 + c * 32 + lane;
           const int rows = min(32, p.M - row0);
