@@ -89,6 +89,13 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_ld_waitN(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // Four bytes from global to shared memory, and this thread's arrive on a
 // barrier once its copies so far have landed.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
@@ -244,39 +251,46 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // One thread runs the whole loop.  What comes between the epilogue's
+    // release of an accumulator and the next MMA into it is on the critical
+    // path of two accumulators (release, MMA 560 cycles, read, release), and
+    // this warp shares its issue slots with two busy epilogue warps: so the
+    // operands' barrier is waited for first, and the descriptors are ready.
     if (rank == 0) {
-      const bool leader = elect_one() != 0;
-      int st = 0;
-      uint32_t ph = 0, it = 0;
-      bool ok = true;
-      const uint32_t idesc = idesc_f8(256, 256, false, !kKM) | p.idesc_fmt;
-      for (int t = unit; ok && t < p.tiles; t += units) {
-        for (int ks = 0; ks < kb; ++ks, ++it) {
-          const uint32_t buf = it & 1u;
-          ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, wc, 0x02)) &&
-               __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_full + 8 * st, ph, wc, 0x03 | (st << 8)));
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const uint32_t sA = base + C::OFF_A + st * C::A_BYTES, sB = base + C::OFF_B + st * C::B_BYTES;
-            // A (and a K-major B): 128-byte swizzle, 8-row groups 1 KB apart,
-            // 32 bytes per K = 32; an N-major B: 32 K rows (4 KB) per K = 32
+      if (elect_one()) {
+        int st = 0;
+        uint32_t ph = 0, it = 0;
+        bool ok = true;
+        const uint32_t idesc = idesc_f8(256, 256, false, !kKM) | p.idesc_fmt;
+        // A (and a K-major B): 128-byte swizzle, 8-row groups 1 KB apart, 32
+        // bytes per K = 32; an N-major B: 32 K rows (4 KB) per K = 32
+        const uint64_t dA = smem_desc(base + C::OFF_A, 0, 1024, 2);
+        const uint64_t dB = smem_desc(base + C::OFF_B, kKM ? 0 : 16384, 1024, 2);
+        constexpr uint32_t kBStep = (kKM ? 32 : 4096) >> 4;
+        for (int t = unit; ok && t < p.tiles; t += units) {
+          for (int ks = 0; ks < kb; ++ks, ++it) {
+            const uint32_t buf = it & 1u;
+            ok = wait_phase<false>(bar_full + 8 * st, ph, wc, 0x03 | (st << 8));
+            if (!ok) break;
+            const uint64_t a = dA + static_cast<uint32_t>(st * (C::A_BYTES >> 4));
+            const uint64_t b = dB + static_cast<uint32_t>(st * (C::B_BYTES >> 4));
+            // only tcgen05.ld of the accumulator must come before: cluster-scope
+            // acquire is not needed for that
+            ok = wait_phase<false>(bar_acc_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, wc, 0x02);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f8<2>(tmem + 256 * buf, smem_desc(sA + 32 * k, 0, 1024, 2),
-                        kKM ? smem_desc(sB + 32 * k, 0, 1024, 2) : smem_desc(sB + 4096 * k, 16384, 1024, 2),
-                        idesc, k != 0);
-            tc_commit_pair(bar_empty + 8 * st, 0x3);
+            for (int k = 0; k < 4; ++k) mma_f8<2>(tmem + 256 * buf, a + 2 * k, b + kBStep * k, idesc, k != 0);
             tc_commit_pair(bar_acc_full + 8 * buf, 0x3);
-          }
-          __syncwarp();
-          if (++st == C::STAGES) {
-            st = 0;
-            ph ^= 1u;
+            tc_commit_pair(bar_empty + 8 * st, 0x3);
+            if (++st == C::STAGES) {
+              st = 0;
+              ph ^= 1u;
+            }
           }
         }
+        tc_commit_pair(bar_final, 0x1);
       }
-      if (leader) tc_commit_pair(bar_final, 0x1);
       __syncwarp();
       wait_phase<false>(bar_final, 0, wn, 0x04);
     }
@@ -357,11 +371,10 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         tc_fence_after();
         uint32_t v[2][16];
         const uint32_t ta = lane_addr + 256 * buf;
-        tmem_ld_32x32b_x16(ta, v[0]);
-        tmem_ld_wait16(v[0]);
+        tmem_ld_32x32b_x16(ta, v[0]); tmem_ld_waitN(v[0]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          if (c < 7) tmem_ld_32x32b_x16(ta + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c < 7) { tmem_ld_32x32b_x16(ta + 16 * (c + 1), v[(c + 1) & 1]); }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x = __uint_as_float(v[c & 1][i]);
@@ -371,8 +384,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             }
             acc[16 * c + i] = fmaf(x, s, acc[16 * c + i]);
           }
-          if (c < 7) tmem_ld_wait16(v[(c + 1) & 1]);
-          if (c == 6) {  // the accumulator has been read
+          if (c < 7) tmem_ld_waitN(v[(c + 1) & 1]);
+          if (c == 6) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(bar_acc_empty + 8 * buf, 0);

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "cache_append.cuh"
 #include "cache_attention.cuh"
@@ -14,7 +15,6 @@
 
 namespace {
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 constexpr int64_t kLim = int64_t(1) << 31;
@@ -30,7 +30,9 @@ int cache_args(const mxg::HandleView &v, const mxgemm_cache_t *c, int64_t batch,
   if (c->head_dim != 64 && c->head_dim != 128) return MXGEMM_ERR_INVALID_VALUE;
   if (c->kv_heads < 1 || c->kv_heads > 65535 || c->num_pages < 0 || c->num_pages >= kLim)
     return MXGEMM_ERR_INVALID_VALUE;
-  if (table_pitch * c->page_size >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+  if (table_pitch >= kLim || table_pitch * c->page_size >= kLim ||
+      c->num_pages * c->kv_heads >= kLim / c->page_size)
+    return MXGEMM_ERR_INVALID_VALUE;
   if (!q_start && tokens != batch) return MXGEMM_ERR_INVALID_VALUE;
   if (batch == 0 || tokens == 0) return MXGEMM_OK;
   if (!kv_len || (table_pitch > 0 && !table)) return MXGEMM_ERR_INVALID_VALUE;
@@ -64,6 +66,45 @@ int cache_args(const mxg::HandleView &v, const mxgemm_cache_t *c, int64_t batch,
 int launched(const mxg::HandleView &v) {
   if (cudaGetLastError() != cudaSuccess) return MXGEMM_ERR_CUDA;
   ++*v.launches;
+  return MXGEMM_OK;
+}
+
+// Tensor map of a cache's codes as rows of head_dim bytes.
+int encode_rows(const mxg::HandleView &v, CUtensorMap *tm, const void *base, int64_t rows, int d, int box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return v.encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MXGEMM_OK
+             : MXGEMM_ERR_CUDA;
+}
+
+template <int D, int NT>
+int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+  using S = mxg::DecodeCfg<D, NT>;
+  const int grid = std::min(2 * v.sm_count, mxg::kCounters);
+  uint8_t *ws = nullptr;
+  if (int st = mxg::handle_workspace(h, static_cast<size_t>(grid) * 2 * S::PARTIAL * sizeof(float), stream, &ws))
+    return st;
+  p.partials = reinterpret_cast<float *>(ws);
+  // (a cache of no pages: the maps are not used)
+  CUtensorMap tK, tV;
+  std::memset(&tK, 0, sizeof(tK));
+  std::memset(&tV, 0, sizeof(tV));
+  const int64_t rows = p.c.num_pages * p.c.kv_heads * p.c.page_size;
+  const int box = std::min(p.c.page_size, 32);
+  if (rows > 0 && (encode_rows(v, &tK, p.c.K, rows, D, box) || encode_rows(v, &tV, p.c.V, rows, D, box)))
+    return MXGEMM_ERR_CUDA;
+  if (cudaFuncSetAttribute(mxg::cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           S::SMEM_BYTES) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  mxg::cache_decode_kernel<D, NT><<<grid, 128, S::SMEM_BYTES, stream>>>(tK, tV, p);
   return MXGEMM_OK;
 }
 
@@ -138,8 +179,13 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   p.O = static_cast<__nv_bfloat16 *>(O);
   p.lse = lse;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const unsigned grid = static_cast<unsigned>(cdiv(tokens * heads, 4));
-  if (cache->head_dim == 128) mxg::cache_attention_kernel<128><<<grid, 128, 0, stream>>>(p);
-  else mxg::cache_attention_kernel<64><<<grid, 128, 0, stream>>>(p);
+  p.counters = v.counters;
+  p.timeout_ns = v.timeout_ns;
+  // rows (query tokens x heads of a group) of an ordinary sequence: one or two
+  // of the MMA's eight
+  const bool two = tokens * p.group > 8 * batch;
+  const int st = cache->head_dim == 128 ? (two ? run_decode<128, 2>(h, v, p, stream) : run_decode<128, 1>(h, v, p, stream))
+                                        : (two ? run_decode<64, 2>(h, v, p, stream) : run_decode<64, 1>(h, v, p, stream));
+  if (st != MXGEMM_OK) return st;
   return launched(v);
 }

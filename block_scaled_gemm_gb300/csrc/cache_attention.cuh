@@ -1,9 +1,31 @@
-// cache_attention.cuh -- attention over the 8-bit key/value cache.
+// cache_attention.cuh -- attention over the 8-bit key/value cache for few
+// query rows (single tokens, short runs): bound by reading the codes once.
 //
-// One warp per (query token, head); the keys in order, with the running
-// maximum and sum of the softmax.
+//   x_j = scale * q . k_j,  k_j = ks * K_j,  v_j = vs * V_j   (ks, vs per page)
+//   o = sum_j e^(x_j) v_j / sum_j e^(x_j)
+//
+// A page's vs goes into the exponent: with w_j = 2^(x_j log2 e + log2 vs - m),
+// m the running maximum of that exponent,
+//   o = (sum_j w_j V_j) / (sum_j w_j / vs_j):
+// the weights that meet the codes in the tensor cores are at most 2^8 and the
+// largest is near 1 whatever the pages' scales are, so FP16 (11 bits) holds
+// them, and V's codes, E4M3, are exact in FP16.  So are K's, and Q's BF16 after
+// its row is divided by a power of two; sums are FP32.
+//
+// Transposed: S^T = K Q^T and O^T = V^T P^T with mma.m16n8k16, so that 8
+// query rows (the heads of a group) fill the MMA's narrow side and K and V,
+// converted in registers, its 16-row side.  One warp takes tiles of 32 keys:
+// TMA brings each page's rows, swizzled, into the warp's own ring of shared
+// memory; no other warp waits for it.  Running maximum, sum and O stay in
+// the warp until the end of its run.
+//
+// Work: an item is one sequence, key/value head and ROWS query rows; all
+// items' tiles, laid end to end, are cut into equal ranges, one per CTA.  An
+// item that spans CTAs leaves FP32 partials in the workspace and the CTA that
+// arrives last adds them, in order: the result does not depend on timing.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "cache_common.cuh"
 
@@ -20,51 +42,616 @@ struct AttnParams {
   int64_t window, sinks;
   __nv_bfloat16 *O;
   float *lse;
+  float *partials;     // two slots per CTA
+  unsigned *counters;  // one per CTA, zero between launches
+  unsigned long long timeout_ns;
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) cache_attention_kernel(const AttnParams p) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= p.b.tokens * p.heads) return;
-  const int64_t t = w / p.heads;
-  const int h = static_cast<int>(w % p.heads), kv = h / p.group;
-  auto f = [&](int b) -> int64_t { return p.b.q_start ? p.b.q_start[b] : b; };
-  const int b = warp_find(p.b.batch, f, t);
-  const Sequence s = load_sequence(p.b, p.c, b);
-  const int64_t pos = static_cast<int64_t>(s.len) - s.n + (t - s.first);
-  float q[kPer], o[kPer];
-  for (int e = 0; e < kPer; ++e) {
-    q[e] = __bfloat162float(p.Q[t * p.q_pitch + static_cast<int64_t>(h) * D + lane * kPer + e]) * p.scale;
-    o[e] = 0.f;
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two E4M3 codes (the low or the high half of w) as FP16.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async4_cache(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100, for 1 / vs
+
+// Which keys of a sequence any of its queries sees, as tiles of 32: `ns` tiles
+// of first tokens from key 0, then the tiles from tile `lo` on, `tiles` in all
+// (one at least, so that a sequence without keys still has its zeros written).
+struct KeyTiles {
+  int ns, lo, tiles;
+  int end;       // keys >= end are seen by no query
+  int win_lo;    // keys < win_lo are seen only as first tokens
+};
+
+__device__ __forceinline__ KeyTiles key_tiles(const AttnParams &p, const Sequence &s) {
+  KeyTiles k;
+  const int64_t first = static_cast<int64_t>(s.len) - s.n;  // position of the first query
+  k.end = s.n > 0 ? s.len : 0;  // (the last query stands at len - 1)
+  int64_t lo = 0;
+  if (p.window > 0) lo = max(static_cast<int64_t>(0), first - p.window + 1);
+  k.win_lo = static_cast<int>(min(lo, static_cast<int64_t>(k.end)));
+  k.lo = k.win_lo >> 5;
+  k.ns = static_cast<int>(min((min(p.sinks, static_cast<int64_t>(k.win_lo)) + 31) >> 5, static_cast<int64_t>(k.lo)));
+  k.tiles = max(1, k.ns + ((k.end + 31) >> 5) - k.lo);
+  return k;
+}
+
+// Items of sequence s: row tiles x key/value heads.
+__device__ __forceinline__ int64_t item_count(const AttnParams &p, const Sequence &s, int rows) {
+  return (static_cast<int64_t>(s.n) * p.group + rows - 1) / rows * p.c.kv_heads;
+}
+
+// Position in the flat order of tiles: a sequence, and in it an item.
+struct Cursor {
+  int b;
+  Sequence s;
+  KeyTiles k;
+  int64_t beg;    // the item's first tile
+  int64_t items;  // of the sequence
+  int64_t item;
+  int h;          // the item's key/value head
+
+  // the item of tile x, in sequence b_ whose tiles begin at `base`
+  __device__ void start(const AttnParams &p, int rows, int b_, int64_t base, int64_t x) {
+    b = b_;
+    enter(p, rows);
+    item = (x - base) / k.tiles;
+    beg = base + item * k.tiles;
+    h = static_cast<int>(item % p.c.kv_heads);
   }
-  float m = -INFINITY, l = 0.f;
-  const int64_t last = p.causal ? min(static_cast<int64_t>(s.len), pos + 1) : s.len;
-  int page = -1, pg = -1;
-  for (int64_t j = 0; j < last; ++j) {
-    if (p.window > 0 && pos - j >= p.window && j >= p.sinks) continue;
-    if (static_cast<int>(j >> p.c.page_log2) != page) {
-      page = static_cast<int>(j >> p.c.page_log2);
-      pg = load_page(p.b, p.c, b, page);
+  // forward to the item of tile x (below the total)
+  __device__ void to(const AttnParams &p, int rows, int64_t x) {
+    while (x >= beg + k.tiles) {
+      beg += k.tiles;
+      if (++item == items) {
+        do {
+          ++b;
+          enter(p, rows);
+        } while (items == 0);
+        item = 0;
+        h = 0;
+      } else if (++h == p.c.kv_heads) {
+        h = 0;
+      }
     }
-    if (pg < 0) continue;
-    const int64_t cell = static_cast<int64_t>(pg) * p.c.kv_heads + kv;
-    const int64_t at = (cell * p.c.page_size + (j & (p.c.page_size - 1))) * D + lane * kPer;
-    float x = 0.f;
-    for (int e = 0; e < kPer; ++e)
-      x += q[e] * __half2float(__half(__nv_cvt_fp8_to_halfraw(p.c.K[at + e], __NV_E4M3)));
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-    x *= p.c.K_scale[cell];
-    const float mn = fmaxf(m, x), c = __expf(m - mn), e0 = __expf(x - mn), vs = p.c.V_scale[cell];
-    l = l * c + e0;
-    for (int e = 0; e < kPer; ++e)
-      o[e] = o[e] * c + e0 * vs * __half2float(__half(__nv_cvt_fp8_to_halfraw(p.c.V[at + e], __NV_E4M3)));
-    m = mn;
   }
-  for (int e = 0; e < kPer; ++e)
-    p.O[(t * p.heads + h) * D + lane * kPer + e] = __float2bfloat16_rn(l > 0.f ? o[e] / l : 0.f);
-  if (p.lse && lane == 0) p.lse[t * p.heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  __device__ void enter(const AttnParams &p, int rows) {
+    s = load_sequence(p.b, p.c, b);
+    k = key_tiles(p, s);
+    items = item_count(p, s, rows);
+  }
+  // first key of tile x of the item
+  __device__ int key(int64_t x) const {
+    const int tile = static_cast<int>(x - beg);
+    return (tile < k.ns ? tile : k.lo + tile - k.ns) * 32;
+  }
+};
+
+// The sequence that tile x (below the total) belongs to, and where its tiles
+// begin: by a whole warp, 32 sequences at a time.
+__device__ __forceinline__ int find_sequence(const AttnParams &p, int rows, int64_t x, int64_t *base) {
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    int64_t mine = 0;
+    if (b0 + lane < p.b.batch) {
+      const Sequence s = load_sequence(p.b, p.c, b0 + lane);
+      mine = item_count(p, s, rows) * key_tiles(p, s).tiles;
+    }
+    int64_t upto = mine;  // of this sequence and those before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > x);
+    if (past) {
+      const int i = __ffs(past) - 1;
+      *base = before + __shfl_sync(0xFFFFFFFFu, upto - mine, i);
+      return b0 + i;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+}
+
+template <int D, int NT>
+struct DecodeCfg {
+  static constexpr int ROWS = 8 * NT;  // query rows of an item
+  static constexpr int WARPS = 4;
+  static constexpr int TILE = 32;
+  static constexpr int STAGE = 2 * TILE * D;              // K, then V
+  static constexpr int STAGES = 3 * 128 / D;              // of each warp
+  static constexpr int OFF_MERGE = WARPS * STAGES * STAGE;  // [warp][8 rows][64] floats
+  static constexpr int OFF_ML = OFF_MERGE + WARPS * 8 * 64 * 4;  // m and l: [2][warp][ROWS]
+  static constexpr int OFF_SC = OFF_ML + 2 * WARPS * ROWS * 4;   // [warp][stage][K, V][2 pages] scales
+  static constexpr int OFF_PG = OFF_SC + WARPS * STAGES * 16;    // [warp][stage][2] whether the page is there
+  static constexpr int OFF_BAR = OFF_PG + WARPS * STAGES * 8;
+  static constexpr int OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+  static constexpr int PARTIAL = ROWS * (D + 2);  // floats of a partial: O, m, l
+  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(128, 2)
+    cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const AttnParams p) {
+  using S = DecodeCfg<D, NT>;
+  constexpr int ROWS = S::ROWS, STAGES = S::STAGES, KW = D / 16;  // 32-bit words of a K row per thread
+  constexpr int MT = D / 16;                                      // 16-row tiles of O^T
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = base + warp * STAGES * S::STAGE;
+  const uint32_t bars = base + S::OFF_BAR + warp * STAGES * 8;
+  float *sc = reinterpret_cast<float *>(sm + S::OFF_SC) + warp * STAGES * 4;
+  int *pg_ok = reinterpret_cast<int *>(sm + S::OFF_PG) + warp * STAGES * 2;
+  float *merge = reinterpret_cast<float *>(sm + S::OFF_MERGE);
+  float *ml = reinterpret_cast<float *>(sm + S::OFF_ML);
+  int64_t *total_at = reinterpret_cast<int64_t *>(sm + S::OFF_MISC);
+  int *last_at = reinterpret_cast<int *>(sm + S::OFF_MISC + 40);
+
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 33);  // the bytes' arrive, and the lanes' copies
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  // all tiles, and this CTA's range of them: ranges of at least four tiles
+  int64_t mine = 0;
+  for (int b = threadIdx.x; b < p.b.batch; b += 128) {
+    const Sequence s = load_sequence(p.b, p.c, b);
+    mine += item_count(p, s, ROWS) * key_tiles(p, s).tiles;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+  if (lane == 0) total_at[warp] = mine;
+  __syncthreads();
+  const int64_t total = total_at[0] + total_at[1] + total_at[2] + total_at[3];
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 3) / 4);
+  if (blockIdx.x >= ctas) return;
+  auto first_tile = [&](int64_t u) { return u * total / ctas; };
+  auto cta_of = [&](int64_t x) { return ((x + 1) * ctas - 1) / total; };  // the CTA whose range holds tile x
+  const int64_t x0 = first_tile(blockIdx.x), x1 = first_tile(blockIdx.x + 1);
+
+  const int lg = p.c.page_log2, per = lg == 4 ? 2 : 1;  // pages of a tile
+  const uint32_t box_bytes = (lg == 4 ? 16 : 32) * D;
+  // ------------------------------------------------------------ loads
+  int64_t base_b;
+  const int b0 = find_sequence(p, ROWS, x0, &base_b);
+  Cursor at, in;  // of the item being computed, and of the next tile to load
+  at.start(p, ROWS, b0, base_b, x0);
+  in = at;
+  auto issue = [&](int64_t x, int st) {
+    in.to(p, ROWS, x);
+    const int h = in.h, key0 = in.key(x);
+    int pg = -1;
+    if (lane < per && key0 + 16 * lane < in.k.end) pg = load_page(p.b, p.c, in.b, (key0 + 16 * lane) >> lg);
+    const uint32_t bar = bars + 8 * st;
+    const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
+    if (lane < per) {
+      pg_ok[2 * st + lane] = pg >= 0;
+      const int64_t cell = static_cast<int64_t>(pg) * p.c.kv_heads + h;
+      if (pg >= 0) {
+        cp_async4_cache(smem_u32(sc + 4 * st + lane), p.c.K_scale + cell);
+        cp_async4_cache(smem_u32(sc + 4 * st + 2 + lane), p.c.V_scale + cell);
+      }
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * box_bytes * __popc(there));
+    __syncwarp();
+    if (pg >= 0) {
+      const int row = (pg * p.c.kv_heads + h) * p.c.page_size + (key0 & (p.c.page_size - 1));
+      const uint32_t dst = ring + st * S::STAGE + lane * 16 * D;
+      tma_load_2d(dst, &tmK, 0, row, bar);
+      tma_load_2d(dst + 32 * D, &tmV, 0, row, bar);
+    }
+  };
+  // bounded wait (whole warp): the loads of this stage have landed
+  auto wait_stage = [&](int st, uint32_t ph) -> bool {
+    bool ok = mbar_try_wait(bars + 8 * st, ph);
+    if (!ok) {
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t i = 1; !(ok = mbar_try_wait(bars + 8 * st, ph)); ++i)
+        if ((i & 31u) == 0 && globaltimer_ns() - t0 > p.timeout_ns) {
+          if (atomicCAS(p.b.status, 0, 6) == 0) atomicExch(p.b.status + 1, 0x31);
+          break;
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+  };
+  int64_t px = x0 + warp;  // next tile to load
+  int pst = 0;
+  for (int i = 0; i < STAGES && px < x1; ++i, px += 4) {
+    issue(px, pst);
+    pst = pst + 1 == STAGES ? 0 : pst + 1;
+  }
+
+  // ------------------------------------------------------------ items
+  int64_t x = x0 + warp;  // this warp's next tile
+  int st = 0;
+  uint32_t ph = 0;
+  bool alive = true;
+  for (int64_t seg = x0; seg < x1;) {
+    at.to(p, ROWS, seg);
+    const int64_t item_beg = at.beg, item_end = item_beg + at.k.tiles;
+    const int64_t seg_end = min(item_end, x1);
+    const int h = at.h;
+    const int row0 = static_cast<int>(at.item / p.c.kv_heads) * ROWS;  // row = token * group + head of the group
+    const int rows = min(ROWS, at.s.n * p.group - row0);
+    const int pos0 = at.s.len - at.s.n;
+
+    // Q: thread (g, t) holds row g of each 8, d = (D/4) t .. + D/4 - 1, in the
+    // order of K's words; rows past the last are zero
+    uint32_t q[NT][KW][2];
+    float cq[NT][2];  // logits of this lane's columns 2t, 2t+1: S * cq
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + g;
+      uint4 w[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int tok = (row0 + r) / p.group, hd = h * p.group + (row0 + r) % p.group;
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + static_cast<int64_t>(at.s.first + tok) * p.q_pitch +
+                                                           static_cast<int64_t>(hd) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[i] = src[i];
+      }
+      const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      // the row over 2^e, |q| < 2 (2^e of its largest; 1 for a row of zeros)
+      const int e = top > 0.f ? min(max((__float_as_int(top) >> 23) - 127, -126), 126) : 0;
+      const float inv = __int_as_float((127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < KW; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t b = u[2 * i + c];
+          q[n][i][c] = half2_of(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv);
+        }
+      const float c = p.scale * 1.44269504088896340736f * __int_as_float((127 + e) << 23);
+      cq[n][0] = __shfl_sync(0xFFFFFFFFu, c, 8 * t);
+      cq[n][1] = __shfl_sync(0xFFFFFFFFu, c, 8 * t + 4);
+    }
+    // positions of this lane's columns, and of all rows
+    int pos[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) pos[n][c] = pos0 + (row0 + min(8 * n + 2 * t + c, rows - 1)) / p.group;
+    const int pos_lo = pos0 + row0 / p.group, pos_hi = pos0 + (row0 + rows - 1) / p.group;
+
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    for (; x < seg_end; x += 4) {
+      const int key0 = at.key(x);
+      if (alive) alive = wait_stage(st, ph);
+      const uint32_t kb = ring + st * S::STAGE, vb = kb + 32 * D;
+      // S^T: keys 16 mt + g (+ 8) x rows
+      float s[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t k0[KW], k1[KW];
+#pragma unroll
+        for (int c = 0; c < KW / 4; ++c) {
+          const int ra = 16 * mt + g, rb = ra + 8, ch = (KW / 4) * t + c;  // 16-byte chunk of the row
+          const uint4 a = ld_shared_v4(kb + ra * D + ((ch ^ (D == 128 ? ra & 7 : (ra >> 1) & 3)) << 4));
+          const uint4 b = ld_shared_v4(kb + rb * D + ((ch ^ (D == 128 ? rb & 7 : (rb >> 1) & 3)) << 4));
+          k0[4 * c] = a.x; k0[4 * c + 1] = a.y; k0[4 * c + 2] = a.z; k0[4 * c + 3] = a.w;
+          k1[4 * c] = b.x; k1[4 * c + 1] = b.y; k1[4 * c + 2] = b.z; k1[4 * c + 3] = b.w;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][n][j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          const uint32_t a0 = e4m3_lo(k0[i]), a1 = e4m3_lo(k1[i]), a2 = e4m3_hi(k0[i]), a3 = e4m3_hi(k1[i]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(s[mt][n], a0, a1, a2, a3, q[n][i][0], q[n][i][1]);
+        }
+      }
+      // exponents; ivs = 1 / vs
+      const bool ok0 = pg_ok[2 * st] != 0, ok1 = per == 2 ? pg_ok[2 * st + 1] != 0 : ok0;
+      float ivs[2];
+      const int jlast = key0 + 31;
+      const bool whole = ok0 && ok1 && jlast < at.k.end && (!p.causal || jlast <= pos_lo) &&
+                         (p.window == 0 || pos_hi - key0 < p.window || jlast < p.sinks);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float ks = sc[4 * st + (per == 2 ? mt : 0)], vs = sc[4 * st + 2 + (per == 2 ? mt : 0)];
+        const float v1 = fmaxf(vs, kScaleFloor), lv = lg2(v1);
+        ivs[mt] = __frcp_rn(v1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][n][j] = fmaf(s[mt][n][j], cq[n][j & 1] * ks, lv);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int key = key0 + 16 * mt + g + 8 * (j >> 1), ps = pos[n][j & 1];
+              const bool seen = (mt ? ok1 : ok0) && key < at.k.end && (!p.causal || key <= ps) &&
+                                (p.window == 0 || ps - key < p.window || key < p.sinks);
+              if (!seen) s[mt][n][j] = -INFINITY;
+            }
+      }
+      // running maximum, moved only when it grows by 2^8
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float top[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[c] = fmaxf(fmaxf(s[0][n][c], s[0][n][c + 2]), fmaxf(s[1][n][c], s[1][n][c + 2]));
+          top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
+          top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
+          top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] + 8.f || top[1] > m[n][1] + 8.f)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float mn = fmaxf(m[n][c], top[c]);
+            const float f = mn == -INFINITY ? 1.f : ex2(m[n][c] - mn);
+            m[n][c] = mn;
+            l[n][c] *= f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[n][i][c] *= f;
+              o[n][i][c + 2] *= f;
+            }
+          }
+        }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const float w0 = ex2(s[mt][n][0] - m0), w1 = ex2(s[mt][n][1] - m1);
+          const float w2 = ex2(s[mt][n][2] - m0), w3 = ex2(s[mt][n][3] - m1);
+          l[n][0] = fmaf(w0 + w2, ivs[mt], l[n][0]);
+          l[n][1] = fmaf(w1 + w3, ivs[mt], l[n][1]);
+          pb[mt][n][0] = transpose8x8(half2_of(w0, w1));
+          pb[mt][n][1] = transpose8x8(half2_of(w2, w3));
+        }
+      }
+      // O^T += V^T P^T: thread (g, t) has keys 2t, 2t+1, 2t+8, 2t+9 of each 16 and
+      // d = (D/8) g .. + D/8 - 1
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * mt + 2 * t + (i & 1) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 a = ld_shared_v4(vb + r * D + ((g ^ (r & 7)) << 4));
+            v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+          } else {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(v[i][0]), "=r"(v[i][1])
+                         : "r"(vb + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1))
+                         : "memory");
+          }
+          if (!whole) {
+            // codes of keys that no row sees may be anything: 0 * NaN is NaN
+            const int key = key0 + r;
+            const bool used = (mt ? ok1 : ok0) && key < at.k.end && (key >= at.k.win_lo || key < p.sinks);
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) v[i][w] = used ? v[i][w] : 0u;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t a = __byte_perm(v[0][w], v[1][w], 0x5140), b = __byte_perm(v[2][w], v[3][w], 0x5140);
+          const uint32_t c = __byte_perm(v[0][w], v[1][w], 0x7362), d = __byte_perm(v[2][w], v[3][w], 0x7362);
+          const uint32_t a0 = e4m3_lo(a), a1 = e4m3_hi(a), a2 = e4m3_lo(b), a3 = e4m3_hi(b);
+          const uint32_t c0 = e4m3_lo(c), c1 = e4m3_hi(c), c2 = e4m3_lo(d), c3 = e4m3_hi(d);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[n][2 * w], a0, a1, a2, a3, pb[mt][n][0], pb[mt][n][1]);
+            mma_f16(o[n][2 * w + 1], c0, c1, c2, c3, pb[mt][n][0], pb[mt][n][1]);
+          }
+        }
+      }
+      // this stage's reads come before the next load into it
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (alive && px < x1) issue(px, st);
+      px += 4;
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+
+    // ---------------------------------------------------------- the CTA's result
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
+        l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
+        l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
+        if (g == 0) {
+          ml[warp * ROWS + 8 * n + 2 * t + c] = m[n][c];
+          ml[(4 + warp) * ROWS + 8 * n + 2 * t + c] = l[n][c];
+        }
+      }
+    __syncthreads();
+    const bool split = item_beg < x0 || item_end > x1;
+    const int64_t u0 = split ? cta_of(item_beg) : 0, u1 = split ? cta_of(item_end - 1) : 0;
+    float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (blockIdx.x == u0)) * S::PARTIAL;
+    const int hr = threadIdx.x >> 4, hd = threadIdx.x & 15;  // output: row of 8, four of 64 d
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // this warp's sums over the maximum of the four
+      float f[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * n + 2 * t + c;
+        const float top = fmaxf(fmaxf(ml[r], ml[ROWS + r]), fmaxf(ml[2 * ROWS + r], ml[3 * ROWS + r]));
+        f[c] = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - top);
+      }
+      const int r = 8 * n + hr;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w * ROWS + r]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (ml[w * ROWS + r] != -INFINITY) sum += ml[(4 + w) * ROWS + r] * ex2(ml[w * ROWS + r] - top);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        __syncthreads();
+        // d = (D/8) g + 2 i (+ 1): the lanes whose d lie in this 64
+        if (D == 64 || (g >> 2) == e) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+              *reinterpret_cast<float2 *>(merge + (warp * 8 + 2 * t + c) * 64 + ((D / 8) * g + 2 * i) % 64) =
+                  make_float2(o[n][i][c] * f[c], o[n][i][c + 2] * f[c]);
+        }
+        __syncthreads();
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 b = *reinterpret_cast<const float4 *>(merge + (w * 8 + hr) * 64 + 4 * hd);
+          a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        }
+        const int d = 64 * e + 4 * hd;
+        if (split) {
+          *reinterpret_cast<float4 *>(part + r * D + d) = a;
+        } else if (r < rows) {
+          const float k = sum == 0.f ? 0.f : 1.f / sum;
+          const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * k, a.y * k), hi = __floats2bfloat162_rn(a.z * k, a.w * k);
+          *reinterpret_cast<uint2 *>(p.O + (static_cast<int64_t>(tok) * p.heads + head) * D + d) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        }
+      }
+      if (hd == 0) {
+        if (split) {
+          part[ROWS * D + r] = top;
+          part[ROWS * D + ROWS + r] = sum;
+        } else if (r < rows && p.lse) {
+          const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
+          p.lse[static_cast<int64_t>(tok) * p.heads + head] =
+              sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.69314718055994530942f;
+        }
+      }
+    }
+    // ---------------------------------------------------------- split items
+    if (split) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0)
+        *last_at = atomicAdd(p.counters + u0, 1u) == static_cast<unsigned>(u1 - u0);
+      __syncthreads();
+      if (*last_at) {
+        if (threadIdx.x == 0) p.counters[u0] = 0;  // for the next launch
+        __threadfence();
+        for (int rr = hr; rr < rows; rr += 8) {
+          auto slot = [&](int64_t u) { return p.partials + (2 * u + (u == u0)) * S::PARTIAL; };
+          float top = -INFINITY, sum = 0.f;
+          for (int64_t u = u0; u <= u1; ++u) top = fmaxf(top, __ldcg(slot(u) + ROWS * D + rr));
+          float4 a[D / 64];
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int64_t u = u0; u <= u1; ++u) {
+            const float mu = __ldcg(slot(u) + ROWS * D + rr);
+            const float k = mu == -INFINITY ? 0.f : ex2(mu - top);
+            sum = fmaf(__ldcg(slot(u) + ROWS * D + ROWS + rr), k, sum);
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+              const float4 b = __ldcg(reinterpret_cast<const float4 *>(slot(u) + rr * D + 64 * e + 4 * hd));
+              a[e].x = fmaf(b.x, k, a[e].x); a[e].y = fmaf(b.y, k, a[e].y);
+              a[e].z = fmaf(b.z, k, a[e].z); a[e].w = fmaf(b.w, k, a[e].w);
+            }
+          }
+          const float k = sum == 0.f ? 0.f : 1.f / sum;
+          const int tok = at.s.first + (row0 + rr) / p.group, head = h * p.group + (row0 + rr) % p.group;
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(a[e].x * k, a[e].y * k), hi = __floats2bfloat162_rn(a[e].z * k, a[e].w * k);
+            *reinterpret_cast<uint2 *>(p.O + (static_cast<int64_t>(tok) * p.heads + head) * D + 64 * e + 4 * hd) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+          }
+          if (hd == 0 && p.lse)
+            p.lse[static_cast<int64_t>(tok) * p.heads + head] =
+                sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.69314718055994530942f;
+        }
+      }
+    }
+    __syncthreads();  // ml and merge are free for the next item
+    seg = seg_end;
+  }
+  // after a wait that gave up: loads still on their way land first
+  for (int i = 0; !alive && i < STAGES; ++i) {
+    wait_stage(st, ph);
+    if (++st == STAGES) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
 }
 
 }  // namespace mxg
