@@ -10,6 +10,7 @@
 
 #include "cache_append.cuh"
 #include "cache_attention.cuh"
+#include "cache_prompt.cuh"
 #include "context.h"
 #include "mxgemm.h"
 
@@ -69,18 +70,48 @@ int launched(const mxg::HandleView &v) {
   return MXGEMM_OK;
 }
 
-// Tensor map of a cache's codes as rows of head_dim bytes.
-int encode_rows(const mxg::HandleView &v, CUtensorMap *tm, const void *base, int64_t rows, int d, int box_rows) {
+// Tensor map of a cache's codes as rows of head_dim bytes, swizzled or not.
+int encode_rows(const mxg::HandleView &v, CUtensorMap *tm, const void *base, int64_t rows, int d, int box_rows,
+                bool swizzle) {
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   return v.encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  !swizzle   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                  : d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                             : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? MXGEMM_OK
              : MXGEMM_ERR_CUDA;
+}
+
+int encode_cache(const mxg::HandleView &v, const mxg::CacheView &c, int d, int box_rows, bool swizzle,
+                 CUtensorMap *tK, CUtensorMap *tV) {
+  // (a cache of no pages: the maps are not used)
+  std::memset(tK, 0, sizeof(*tK));
+  std::memset(tV, 0, sizeof(*tV));
+  const int64_t rows = c.num_pages * c.kv_heads * c.page_size;
+  if (rows > 0 && (encode_rows(v, tK, c.K, rows, d, box_rows, swizzle) ||
+                   encode_rows(v, tV, c.V, rows, d, box_rows, swizzle)))
+    return MXGEMM_ERR_CUDA;
+  return MXGEMM_OK;
+}
+
+// Many query rows: one CTA for each 256 of a sequence and key/value head.
+template <int D>
+int run_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t ctas, cudaStream_t stream) {
+  using S = mxg::PromptCfg<D>;
+  CUtensorMap tK, tV;
+  if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
+  if (cudaFuncSetAttribute(mxg::cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           S::SMEM_BYTES) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  mxg::cache_prompt_kernel<D><<<static_cast<unsigned>(ctas), S::THREADS, S::SMEM_BYTES, stream>>>(tK, tV, p);
+  return MXGEMM_OK;
 }
 
 template <int D, int NT>
@@ -91,14 +122,8 @@ int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   if (int st = mxg::handle_workspace(h, static_cast<size_t>(grid) * 2 * S::PARTIAL * sizeof(float), stream, &ws))
     return st;
   p.partials = reinterpret_cast<float *>(ws);
-  // (a cache of no pages: the maps are not used)
   CUtensorMap tK, tV;
-  std::memset(&tK, 0, sizeof(tK));
-  std::memset(&tV, 0, sizeof(tV));
-  const int64_t rows = p.c.num_pages * p.c.kv_heads * p.c.page_size;
-  const int box = std::min(p.c.page_size, 32);
-  if (rows > 0 && (encode_rows(v, &tK, p.c.K, rows, D, box) || encode_rows(v, &tV, p.c.V, rows, D, box)))
-    return MXGEMM_ERR_CUDA;
+  if (int st = encode_cache(v, p.c, D, std::min(p.c.page_size, 32), true, &tK, &tV)) return st;
   if (cudaFuncSetAttribute(mxg::cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            S::SMEM_BYTES) != cudaSuccess) {
     cudaGetLastError();
@@ -181,11 +206,18 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.counters = v.counters;
   p.timeout_ns = v.timeout_ns;
-  // rows (query tokens x heads of a group) of an ordinary sequence: one or two
-  // of the MMA's eight
-  const bool two = tokens * p.group > 8 * batch;
-  const int st = cache->head_dim == 128 ? (two ? run_decode<128, 2>(h, v, p, stream) : run_decode<128, 1>(h, v, p, stream))
-                                        : (two ? run_decode<64, 2>(h, v, p, stream) : run_decode<64, 1>(h, v, p, stream));
+  // Rows (query tokens x heads of a group) of an ordinary sequence decide: many
+  // go to the tensor cores by 256, where they make CTAs enough; few to the
+  // kernel whose items are 8 or 16 rows.
+  const int64_t ctas = (tokens * p.group / mxg::PromptCfg<128>::ROWS + batch) * p.c.kv_heads;
+  int st;
+  if (tokens * p.group >= 64 * batch && ctas >= 16 && ctas < kLim) {
+    st = cache->head_dim == 128 ? run_prompt<128>(v, p, ctas, stream) : run_prompt<64>(v, p, ctas, stream);
+  } else {
+    const bool two = tokens * p.group > 8 * batch;
+    st = cache->head_dim == 128 ? (two ? run_decode<128, 2>(h, v, p, stream) : run_decode<128, 1>(h, v, p, stream))
+                                : (two ? run_decode<64, 2>(h, v, p, stream) : run_decode<64, 1>(h, v, p, stream));
+  }
   if (st != MXGEMM_OK) return st;
   return launched(v);
 }

@@ -138,6 +138,37 @@ def test_several_tokens(h, lens, news, kv, group, d, page, causal, window, sinks
     check(m, q, news, O, L, causal=causal, window=window, sinks=sinks)
 
 
+PROMPTS = [  # as PROMPT, with rows enough for whole tiles of the tensor cores
+    ([300, 129], [130, 129], 8, 8, 128, 64), ([1100], [1100], 4, 4, 128, 64), ([257, 700, 500], [129, 300, 333], 6, 2, 64, 16),
+    ([900, 64, 2], [300, 64, 2], 8, 7, 128, 32), ([513, 512, 511], [513, 200, 511], 8, 1, 128, 128), ([400], [257], 16, 3, 64, 128),
+    ([0, 1500, 40], [9, 700, 31], 8, 4, 128, 16),
+]
+
+
+@pytest.mark.parametrize("lens,news,kv,group,d,page", PROMPTS)
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (False, 0, 0), (True, 33, 5), (True, 200, 130), (False, 50, 2)])
+def test_prompts(h, lens, news, kv, group, d, page, causal, window, sinks):
+    m = Made(lens, kv, d, page, seed=sum(lens))
+    q = queries(m, sum(news), kv * group)
+    O, L = attend(h, m, q, news, causal=causal, window=window, sinks=sinks)
+    check(m, q, news, O, L, causal=causal, window=window, sinks=sinks)
+    again, L2 = attend(h, m, q, news, causal=causal, window=window, sinks=sinks)
+    assert torch.equal(O, again) and torch.equal(L, L2)
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
+
+
+@pytest.mark.parametrize("f,scale", [(2.0 ** 20, 0.08), (2.0 ** -40, 0.08), (1.0, -0.1)])
+def test_prompts_with_wide_scales(h, f, scale):
+    """Page scales over 2^30, queries past FP16's range, a negative scale."""
+    m = Made([300, 250], 8, 128, 16, scales=(-30, 0))
+    m.sK.fill_(2.0 ** -8)
+    m.table[0][3], m.table[1][0] = -1, m.pages
+    q = (queries(m, 300, 32).float() * f).bfloat16()
+    O, L = attend(h, m, q, [200, 100], scale=scale / f)
+    check(m, q, [200, 100], O, L, scale=scale / f)
+    assert mx.mxgemm_get_device_status(h)[0] == mx.ERR_INVALID_VALUE
+
+
 def test_long_sequence_is_split(h):
     m = Made([20011, 64], 1, 128, 64)
     q = queries(m, 2, 8)
