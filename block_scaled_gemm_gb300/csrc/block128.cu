@@ -20,19 +20,34 @@ inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t
 
 constexpr int64_t kLim = int64_t(1) << 31;
 
+// Row (tile) blocks past a grid's y limit go to further launches.
+constexpr int64_t kGridY = 65535;
+
 template <typename T>
-int launch_quantize128(const T *x, int64_t R, int64_t C, int block, uint8_t *cd, float *sc, int sms,
-                       cudaStream_t stream) {
+int launch_quantize128(const T *x, int64_t R, int64_t C, int block, uint8_t *cd, float *sc, cudaStream_t stream) {
+  const int64_t kb = cdiv(C, 128), rb = cdiv(R, 128);
   if (block == MXGEMM_BLOCK_ROWS) {
-    const int64_t kb = cdiv(C, 128);
-    const int grid = static_cast<int>(std::min<int64_t>(cdiv(R * kb, 8), int64_t(sms) * 8));
-    mxg::quantize128_rows_kernel<T><<<grid, 256, 0, stream>>>(x, R, C, kb, cd, sc);
-  } else if (block == MXGEMM_BLOCK_COLS) {
-    const dim3 grid(static_cast<unsigned>(cdiv(C, 128)), static_cast<unsigned>(cdiv(R, 128)));
-    mxg::quantize128_cols_kernel<T><<<grid, 128, 0, stream>>>(x, R, C, cdiv(R, 16) * 16, cd, sc);
+    const int64_t blocks = R * kb;
+    // four groups of blocks a warp: FP32 holds twice BF16's registers
+    constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
+    const int64_t grid = cdiv(blocks, 8 * 4 * kUnroll);
+    if (grid >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+    if (C % 128 == 0)
+      mxg::quantize128_rows_kernel<T, false, kUnroll><<<static_cast<unsigned>(grid), 256, 0, stream>>>(x, C, kb, blocks, cd, sc);
+    else
+      mxg::quantize128_rows_kernel<T, true, kUnroll><<<static_cast<unsigned>(grid), 256, 0, stream>>>(x, C, kb, blocks, cd, sc);
   } else {
-    const dim3 grid(static_cast<unsigned>(cdiv(C, 128)), static_cast<unsigned>(cdiv(R, 128)));
-    mxg::quantize128_tiles_kernel<T><<<grid, 512, 0, stream>>>(x, R, C, cd, sc);
+    const int64_t pitch = cdiv(R, 16) * 16;
+    for (int64_t y = 0; y < rb; y += kGridY) {
+      const unsigned gy = static_cast<unsigned>(std::min(kGridY, rb - y));
+      const T *xr = x + y * 128 * C;
+      if (block == MXGEMM_BLOCK_COLS)
+        mxg::quantize128_cols_kernel<T><<<dim3(static_cast<unsigned>(cdiv(C, 64)), gy), 256, 0, stream>>>(
+            xr, R - y * 128, C, pitch, y * 128, rb, cd, sc + y);
+      else
+        mxg::quantize128_tiles_kernel<T><<<dim3(static_cast<unsigned>(kb), gy), 512, 0, stream>>>(
+            xr, R - y * 128, C, cd + y * 128 * C, sc + y * kb);
+    }
   }
   return cudaGetLastError() == cudaSuccess ? MXGEMM_OK : MXGEMM_ERR_CUDA;
 }
@@ -178,7 +193,7 @@ extern "C" int mxgemm_quantize_block128(const void *X, int x_dtype, int64_t R, i
   if (R == 0 || C == 0) return MXGEMM_OK;
   if (!X || !codes || !scales) return MXGEMM_ERR_INVALID_VALUE;
   if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MXGEMM_ERR_MISALIGNED;
-  int dev = 0, sms = 0;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return MXGEMM_ERR_CUDA;
@@ -186,15 +201,11 @@ extern "C" int mxgemm_quantize_block128(const void *X, int x_dtype, int64_t R, i
   if (!mxg::pointer_on_device(X, dev) || !mxg::pointer_on_device(codes, dev) ||
       !mxg::pointer_on_device(scales, dev))
     return MXGEMM_ERR_INVALID_VALUE;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return MXGEMM_ERR_CUDA;
-  }
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   uint8_t *cd = static_cast<uint8_t *>(codes);
   if (x_dtype == MXGEMM_IN_F32)
-    return launch_quantize128(static_cast<const float *>(X), R, C, block, cd, scales, sms, stream);
-  return launch_quantize128(static_cast<const __nv_bfloat16 *>(X), R, C, block, cd, scales, sms, stream);
+    return launch_quantize128(static_cast<const float *>(X), R, C, block, cd, scales, stream);
+  return launch_quantize128(static_cast<const __nv_bfloat16 *>(X), R, C, block, cd, scales, stream);
 }
 
 extern "C" int mxgemm_run_block128(mxgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *A,

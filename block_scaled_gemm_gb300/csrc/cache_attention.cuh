@@ -227,25 +227,23 @@ __global__ void __launch_bounds__(128, 2)
   int *pg_ok = reinterpret_cast<int *>(sm + S::OFF_PG) + warp * STAGES * 2;
   float *merge = reinterpret_cast<float *>(sm + S::OFF_MERGE);
   float *ml = reinterpret_cast<float *>(sm + S::OFF_ML);
-  int64_t *total_at = reinterpret_cast<int64_t *>(sm + S::OFF_MISC);
-  int *last_at = reinterpret_cast<int *>(sm + S::OFF_MISC + 40);
+  int *last_at = reinterpret_cast<int *>(sm + S::OFF_MISC);
 
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 33);  // the bytes' arrive, and the lanes' copies
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  // all tiles, and this CTA's range of them: ranges of at least four tiles
-  int64_t mine = 0;
-  for (int b = threadIdx.x; b < p.b.batch; b += 128) {
+  __syncwarp();
+  // all tiles (each warp counts for itself), and this CTA's range of them:
+  // ranges of four tiles at least
+  int64_t total = 0;
+  for (int b = lane; b < p.b.batch; b += 32) {
     const Sequence s = load_sequence(p.b, p.c, b);
-    mine += item_count(p, s, ROWS) * key_tiles(p, s).tiles;
+    total += item_count(p, s, ROWS) * key_tiles(p, s).tiles;
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  if (lane == 0) total_at[warp] = mine;
-  __syncthreads();
-  const int64_t total = total_at[0] + total_at[1] + total_at[2] + total_at[3];
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 3) / 4);
   if (blockIdx.x >= ctas) return;
   auto first_tile = [&](int64_t u) { return u * total / ctas; };
@@ -608,25 +606,38 @@ __global__ void __launch_bounds__(128, 2)
       if (*last_at) {
         if (threadIdx.x == 0) p.counters[u0] = 0;  // for the next launch
         __threadfence();
-        for (int rr = hr; rr < rows; rr += 8) {
-          auto slot = [&](int64_t u) { return p.partials + (2 * u + (u == u0)) * S::PARTIAL; };
+        auto slot = [&](int64_t u) { return p.partials + (2 * u + (u == u0)) * S::PARTIAL; };
+        // 16 threads a row; they take the contributors' m and l 16 at a time
+        for (int rr = hr; rr < ROWS; rr += 8) {
           float top = -INFINITY, sum = 0.f;
-          for (int64_t u = u0; u <= u1; ++u) top = fmaxf(top, __ldcg(slot(u) + ROWS * D + rr));
+          for (int64_t u = u0 + hd; u <= u1; u += 16) top = fmaxf(top, __ldcg(slot(u) + ROWS * D + rr));
+#pragma unroll
+          for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
           float4 a[D / 64];
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int64_t u = u0; u <= u1; ++u) {
-            const float mu = __ldcg(slot(u) + ROWS * D + rr);
-            const float k = mu == -INFINITY ? 0.f : ex2(mu - top);
-            sum = fmaf(__ldcg(slot(u) + ROWS * D + ROWS + rr), k, sum);
+          for (int64_t v = u0; v <= u1; v += 16) {
+            float kv = 0.f;
+            if (v + hd <= u1) {
+              const float mu = __ldcg(slot(v + hd) + ROWS * D + rr);
+              kv = mu == -INFINITY ? 0.f : ex2(mu - top);
+              sum = fmaf(__ldcg(slot(v + hd) + ROWS * D + ROWS + rr), kv, sum);
+            }
+#pragma unroll 8
+            for (int i = 0; i < 16; ++i) {
+              const float k = __shfl_sync(0xFFFFFFFFu, kv, (lane & 16) + i);
+              const float *from = slot(min(v + i, u1)) + rr * D + 4 * hd;
 #pragma unroll
-            for (int e = 0; e < D / 64; ++e) {
-              const float4 b = __ldcg(reinterpret_cast<const float4 *>(slot(u) + rr * D + 64 * e + 4 * hd));
-              a[e].x = fmaf(b.x, k, a[e].x); a[e].y = fmaf(b.y, k, a[e].y);
-              a[e].z = fmaf(b.z, k, a[e].z); a[e].w = fmaf(b.w, k, a[e].w);
+              for (int e = 0; e < D / 64; ++e) {
+                const float4 b = __ldcg(reinterpret_cast<const float4 *>(from + 64 * e));
+                a[e].x = fmaf(b.x, k, a[e].x); a[e].y = fmaf(b.y, k, a[e].y);
+                a[e].z = fmaf(b.z, k, a[e].z); a[e].w = fmaf(b.w, k, a[e].w);
+              }
             }
           }
+#pragma unroll
+          for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+          if (rr >= rows) continue;
           const float k = sum == 0.f ? 0.f : 1.f / sum;
           const int tok = at.s.first + (row0 + rr) / p.group, head = h * p.group + (row0 + rr) % p.group;
 #pragma unroll

@@ -84,6 +84,20 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The n lowest bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
+// Least factor of S in an exponent: keeps a hidden key's -inf times it -inf
+// where scale * ks underflows or is 0.
+constexpr float kTinyFactor = 1.1754943508222875080e-38f;  // 2^-126
+
 template <int D>
 __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     cache_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -284,44 +298,46 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     const int q = tid % kCh8, r0 = tid / kCh8;
     // a row's chunk q (16 codes) is units 2q, 2q + 1 of 16 bytes of its FP16 row
     const int first = D == 128 && q >= 4 ? 1 : 0;  // the order that keeps the stores free of bank conflicts
-    auto convert = [&](uint32_t from, uint32_t to, int key0, uint32_t there, bool is_v) {
-#pragma unroll
-      for (int it = 0; it < kIter; ++it) {
-        const int r = r0 + it * (128 / kCh8);
-        uint4 w = ld_shared_v4(from + r * D + q * 16);
-        // V's codes of keys that no row sees may be anything: 0 * NaN is NaN
-        if (is_v) {
-          const int key = key0 + r;
-          if (!((there >> (r >> 4)) & 1u) || key >= end || (key < win_lo && key >= p.sinks)) w = make_uint4(0, 0, 0, 0);
-        }
-        const uint32_t dst = to + (q >> 2) * 16384 + r * 128;
-        const int u = 2 * (q & 3);
-        uint32_t x[8] = {e4m3_lo(w.x), e4m3_hi(w.x), e4m3_lo(w.y), e4m3_hi(w.y),
-                         e4m3_lo(w.z), e4m3_hi(w.z), e4m3_lo(w.w), e4m3_hi(w.w)};
-        const uint32_t d0 = dst + (((u + first) ^ (r & 7)) << 4), d1 = dst + (((u + 1 - first) ^ (r & 7)) << 4);
-        st_shared_v4(d0, first ? x[4] : x[0], first ? x[5] : x[1], first ? x[6] : x[2], first ? x[7] : x[3]);
-        st_shared_v4(d1, first ? x[0] : x[4], first ? x[1] : x[5], first ? x[2] : x[6], first ? x[3] : x[7]);
-      }
-      fence_proxy_async_smem();  // the MMAs read what was written, and the next load overwrites what was read
-      __syncwarp();
-    };
     for (int j = 0; j < tiles; ++j) {
-      const int buf = j & 1;
-      const uint32_t par = ((j >> 1) & 1) ^ 1;
-      const int key0 = tile_key(j);
-      if (!wait(k8_full, j & 1, 0x49) || !wait(k_empty + 8 * buf, par, 0x4A)) break;
-      const uint32_t there = groups[j & 3];
-      convert(base + S::OFF_K8, base + S::OFF_K + buf * S::TILE16, key0, there, false);
-      if (lane == 0) {
-        mbar_arrive(k_full + 8 * buf);
-        mbar_arrive(k8_empty);
+      const int buf = j & 1, key0 = tile_key(j);
+      bool ok = true;
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {  // K, then V
+        const uint32_t full8 = v ? v8_full : k8_full, empty8 = v ? v8_empty : k8_empty;
+        const uint32_t full = (v ? v_full : k_full) + 8 * buf, empty = (v ? v_empty : k_empty) + 8 * buf;
+        ok = wait(full8, j & 1, 0x49 + 2 * v) && wait(empty, ((j >> 1) & 1) ^ 1, 0x4A + 2 * v);
+        if (!ok) break;
+        const uint32_t there = groups[j & 3];
+        const uint32_t from = base + (v ? S::OFF_V8 : S::OFF_K8) + r0 * D + q * 16;
+        const uint32_t to = base + (v ? S::OFF_V : S::OFF_K) + buf * S::TILE16 + (q >> 2) * 16384 + r0 * 128;
+        // (rows 8 and more apart have one swizzle: 128 / kCh8 is 16 or 32)
+        const int u = 2 * (q & 3);
+        const uint32_t d0 = to + (((u + first) ^ (r0 & 7)) << 4), d1 = to + (((u + 1 - first) ^ (r0 & 7)) << 4);
+        // V's codes of keys that no row sees may be anything: 0 * NaN is NaN
+        const bool mask = v && (there != 0xFFu || key0 + 128 > end || (key0 < win_lo && key0 + 128 > p.sinks));
+#pragma unroll 4
+        for (int it = 0; it < kIter; ++it) {
+          constexpr int kStep = 128 / kCh8;
+          uint4 w = ld_shared_v4(from + it * kStep * D);
+          if (mask) {
+            const int r = r0 + it * kStep, key = key0 + r;
+            if (!((there >> (r >> 4)) & 1u) || key >= end || (key < win_lo && key >= p.sinks)) w = make_uint4(0, 0, 0, 0);
+          }
+          if (first) {
+            uint32_t x = w.x, y = w.y;
+            w.x = w.z; w.y = w.w; w.z = x; w.w = y;
+          }
+          st_shared_v4(d0 + it * kStep * 128, e4m3_lo(w.x), e4m3_hi(w.x), e4m3_lo(w.y), e4m3_hi(w.y));
+          st_shared_v4(d1 + it * kStep * 128, e4m3_lo(w.z), e4m3_hi(w.z), e4m3_lo(w.w), e4m3_hi(w.w));
+        }
+        fence_proxy_async_smem();  // the MMAs read what was written, and the next load overwrites what was read
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full);
+          mbar_arrive(empty8);
+        }
       }
-      if (!wait(v8_full, j & 1, 0x4B) || !wait(v_empty + 8 * buf, par, 0x4C)) break;
-      convert(base + S::OFF_V8, base + S::OFF_V + buf * S::TILE16, key0, there, true);
-      if (lane == 0) {
-        mbar_arrive(v_full + 8 * buf);
-        mbar_arrive(v8_empty);
-      }
+      if (!ok) break;
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -347,8 +363,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int c = 0; c < D / 2; ++c)
           top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[c] << 16)), fabsf(__uint_as_float(u[c] & 0xFFFF0000u))));
         const int e = top > 0.f ? min(max((__float_as_int(top) >> 23) - 127, -126), 126) : 0;
-        const float inv = __int_as_float((127 - e) << 23);
-        cq = p.scale * 1.44269504088896340736f * __int_as_float((127 + e) << 23);
+        // (a negative scale's sign goes to Q: the exponents' factors are positive)
+        const float inv = copysignf(__int_as_float((127 - e) << 23), p.scale);
+        cq = fabsf(p.scale) * 1.44269504088896340736f * __int_as_float((127 + e) << 23);
         const int rr = 32 * qd + lane;
         const uint32_t dst = base + S::OFF_Q + i * S::TILE16 + rr * 128;
 #pragma unroll
@@ -383,32 +400,34 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_done(v[c]);
         const uint32_t there = groups[j & 3];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float k = cq * sc[c], a = sc[8 + c];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint32_t &x = v[c >> 1][16 * (c & 1) + e];
-            x = __float_as_uint(fmaf(__uint_as_float(x), k, a));
-          }
-        }
         const int jlast = key0 + 127;
         const bool whole = there == 0xFFu && jlast < end && (!p.causal || jlast <= pos_min) &&
                            (p.window == 0 || pos_max - key0 < p.window || jlast < p.sinks);
         if (!whole) {
           // columns [from, upto) and [0, sink) of the tile are seen
           const int upto = min(p.causal ? min(end, pos + 1) : end, s.len) - key0;
-          const int from = p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(-1), min(static_cast<int64_t>(128), pos - p.window + 1 - key0)));
+          const int from = p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(128), pos - p.window + 1 - key0)));
           const int sink = p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(0), min(p.sinks - key0, static_cast<int64_t>(128))));
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const bool seen = ((there >> (c >> 4)) & 1u) && c < upto && (c >= from || c < sink);
-            if (!seen) v[c >> 5][c & 31] = 0xFF800000u;  // -inf
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t seen = low_bits(upto - 32 * c) & (~low_bits(from - 32 * c) | low_bits(sink - 32 * c)) &
+                                  (((there >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((there >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((seen >> e) & 1u)) v[c][e] = 0xFF800000u;  // -inf
           }
         }
+        // exponents of group c: S * k + a, k > 0: their maximum is the one of S's
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; ++c) top = fmaxf(top, __uint_as_float(v[c >> 5][c & 31]));
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t *x = v[c >> 1] + 16 * (c & 1);
+          float g = __uint_as_float(x[0]);
+#pragma unroll
+          for (int e = 1; e < 15; e += 2) g = max3(g, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          g = fmaxf(g, __uint_as_float(x[15]));
+          top = fmaxf(top, fmaf(g, fmaxf(cq * sc[c], kTinyFactor), sc[8 + c]));
+        }
         const bool grow = top > m + 8.f;
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float mn = grow ? top : m;
@@ -437,13 +456,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
+            const float k = fmaxf(cq * sc[2 * c + hf], kTinyFactor), a = sc[8 + 2 * c + hf] - ms;
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float a = ex2(__uint_as_float(v[c][16 * hf + 2 * e]) - ms);
-              const float bb = ex2(__uint_as_float(v[c][16 * hf + 2 * e + 1]) - ms);
-              sum += a + bb;
-              pk[8 * hf + e] = half2_of(a, bb);
+              const float w0 = ex2(fmaf(__uint_as_float(v[c][16 * hf + 2 * e]), k, a));
+              const float w1 = ex2(fmaf(__uint_as_float(v[c][16 * hf + 2 * e + 1]), k, a));
+              sum += w0 + w1;
+              pk[8 * hf + e] = half2_of(w0, w1);
             }
             l = fmaf(sum, sc[16 + 2 * c + hf], l);
           }
