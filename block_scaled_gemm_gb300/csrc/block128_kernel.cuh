@@ -126,9 +126,10 @@ struct PairCfg {
   static constexpr int AS_PITCH = 132, BS_PITCH = COLS ? 260 : 4;
   static constexpr int SLOT_BYTES = KB * (AS_PITCH + BS_PITCH) * 4;
   static constexpr int OFF_SC = OFF_STG + EPI_WARPS * 4096;
-  static constexpr int OFF_BAR = OFF_SC + 2 * SLOT_BYTES;
+  static constexpr int OFF_BAR = OFF_SC + 2 * SLOT_BYTES;  // (accumulators' pairs 16-byte aligned)
   // full, empty, acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], final
   static constexpr int NUM_BARS = 2 * STAGES + 8 + 1;
+  static_assert((OFF_BAR + 16 * STAGES) % 16 == 0, "barrier pairs");
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
@@ -342,9 +343,12 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
     const int w = warp - 4, q = warp & 3, half = w >> 2;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
     const uint32_t stg = base + C::OFF_STG + w * 4096;
-    uint32_t it = 0, n = 0;
+    // accumulator and barrier of the block to come: the two of each alternate
+    uint32_t acc_at = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
+    uint32_t full_at = bar_acc_full, full_ph = 0;
+    uint32_t empty_at = mapa_shared(bar_acc_empty, 0);  // of the pair's first CTA
+    uint32_t n = 0;  // groups of eight K blocks so far
     bool ok = true;
     for (int t = unit; ok && t < p.tiles; t += units) {
       int mt, nt;
@@ -354,27 +358,30 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      for (int ks = 0; ks < kb; ++ks, ++it) {
-        const uint32_t slot = n & 1u;
-        if ((ks & (C::KB - 1)) == 0) {
-          ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * slot, (n >> 1) & 1u, wc, 0x0A));
-          if (!ok) break;
-        }
-        const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC + slot * C::SLOT_BYTES);
-        const float *bc = sc + C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH;
-        float s = sc[(ks & (C::KB - 1)) * C::AS_PITCH + 32 * q + lane];
-        if constexpr (!kCols) s *= bc[half];
-        const float4 *c4 = reinterpret_cast<const float4 *>(bc + 128 * half);
-        const uint32_t buf = it & 1u;
-        ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_full + 8 * buf, (it >> 1) & 1u, wc, 0x05));
+      // this row's scale of the block to come (with its 128 columns', where they
+      // share one), read a block ahead, and the columns' of the current block
+      float s;
+      const float *sc;
+      auto scale_at = [&](int ks) {
+        sc = reinterpret_cast<const float *>(sm + C::OFF_SC + (n & 1u) * C::SLOT_BYTES);
+        s = sc[(ks & (C::KB - 1)) * C::AS_PITCH + 32 * q + lane];
+        if constexpr (!kCols) s *= sc[C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH + half];
+      };
+      ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));
+      if (!ok) break;
+      scale_at(0);
+#pragma unroll 1
+      for (int ks = 0; ks < kb; ++ks) {
+        ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(full_at, full_ph, wc, 0x05));
         if (!ok) break;
         tc_fence_after();
+        const float4 *c4 = reinterpret_cast<const float4 *>(sc + C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH + 128 * half);
         uint32_t v[2][16];
-        const uint32_t ta = lane_addr + 256 * buf;
-        tmem_ld_32x32b_x16(ta, v[0]); tmem_ld_waitN(v[0]);
+        tmem_ld_32x32b_x16(acc_at, v[0]);
+        tmem_ld_waitN(v[0]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          if (c < 7) { tmem_ld_32x32b_x16(ta + 16 * (c + 1), v[(c + 1) & 1]); }
+          if (c < 7) tmem_ld_32x32b_x16(acc_at + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x = __uint_as_float(v[c & 1][i]);
@@ -385,17 +392,27 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             acc[16 * c + i] = fmaf(x, s, acc[16 * c + i]);
           }
           if (c < 7) tmem_ld_waitN(v[(c + 1) & 1]);
-          if (c == 6) {
+          if (c == 6) {  // the accumulator has been read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(bar_acc_empty + 8 * buf, 0);
+            if (lane == 0)
+              asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(empty_at) : "memory");
           }
         }
-        if ((ks & (C::KB - 1)) == C::KB - 1 || ks == kb - 1) {  // and the group's scales
+        // the other accumulator and its barriers
+        acc_at ^= 256u;
+        full_ph ^= (full_at >> 3) & 1u;
+        full_at ^= 8u;
+        empty_at ^= 8u;
+        if (ks + 1 == kb || ((ks + 1) & (C::KB - 1)) == 0) {  // the group's scales have been read
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_sc_empty + 8 * slot);
+          if (lane == 0) mbar_arrive(bar_sc_empty + 8 * (n & 1u));
           ++n;
+          if (ks + 1 == kb) break;
+          ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));
+          if (!ok) break;
         }
+        scale_at(ks + 1);
       }
       if (!ok) break;
       // C: rows row0 .. +31, columns col0 .. +127, in pieces of 128 bytes a
