@@ -80,20 +80,25 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
 
 // Wait for this thread's tcgen05.ld results in r: the registers are named so
 // that no use of them moves above the wait.
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_ld_waitN(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// 16 lanes x 32 columns as the fragments of an 8 x 8 grid: of each eight
+// columns, thread (g, t) = (lane / 4, lane % 4) gets columns 2t, 2t + 1 of lanes
+// g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // Four bytes from global to shared memory, and this thread's arrive on a
@@ -103,6 +108,32 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait by a whole warp; the first probe, which mostly succeeds, is
+// apart from the loop with its clock reads (8192 x 28672 x 8192 BF16: 1311 ->
+// 1285 us).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl &w, int detail) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, wait_phase<false>(bar, parity, w, detail));
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 
 constexpr int kB128Bf16 = 1;    // BF16 output (else FP32)
@@ -358,41 +389,67 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      // this row's scale of the block to come (with its 128 columns', where they
-      // share one), read a block ahead, and the columns' of the current block
-      float s;
+      // Scales of the block to come, read a block ahead.  With one scale of B
+      // for 128 columns a thread has one row, and s its scale times theirs.
+      // With a scale for each column a thread has a fragment, four rows (lane / 4
+      // + 8 i, scales s) and 32 columns, so that it reads 32 columns' scales for
+      // each block and not 128.
+      constexpr int kRows = kCols ? 4 : 1;
+      float s[kRows];
       const float *sc;
       auto scale_at = [&](int ks) {
         sc = reinterpret_cast<const float *>(sm + C::OFF_SC + (n & 1u) * C::SLOT_BYTES);
-        s = sc[(ks & (C::KB - 1)) * C::AS_PITCH + 32 * q + lane];
-        if constexpr (!kCols) s *= sc[C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH + half];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          s[i] = sc[(ks & (C::KB - 1)) * C::AS_PITCH + 32 * q + (kCols ? (lane >> 2) + 8 * i : lane)];
+        sc += C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH;
+        if constexpr (!kCols) s[0] *= sc[half];
       };
       ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));
       if (!ok) break;
       scale_at(0);
 #pragma unroll 1
       for (int ks = 0; ks < kb; ++ks) {
-        ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(full_at, full_ph, wc, 0x05));
+        ok = warp_wait(full_at, full_ph, wc, 0x05);
         if (!ok) break;
         tc_fence_after();
-        const float4 *c4 = reinterpret_cast<const float4 *>(sc + C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH + 128 * half);
-        uint32_t v[2][16];
-        tmem_ld_32x32b_x16(acc_at, v[0]);
+        uint32_t v[2][32];
+        auto load = [&](int c, uint32_t (&r)[32]) {  // columns 32 c .. +31
+          if constexpr (kCols) {
+            tmem_ld_16x256b_x4(acc_at + 32 * c, r);
+            tmem_ld_16x256b_x4(acc_at + 32 * c + (16u << 16), r + 16);
+          } else {
+            tmem_ld_32x32b_x32(acc_at + 32 * c, r);
+          }
+        };
+        load(0, v[0]);
         tmem_ld_waitN(v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c < 7) tmem_ld_32x32b_x16(acc_at + 16 * (c + 1), v[(c + 1) & 1]);
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) load(c + 1, v[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x = __uint_as_float(v[c & 1][i]);
-            if constexpr (kCols) {
-              const float4 f = c4[4 * c + (i >> 2)];
-              x *= (i & 3) == 0 ? f.x : (i & 3) == 1 ? f.y : (i & 3) == 2 ? f.z : f.w;
+          for (int i = 0; i < 8; ++i) {
+            float2 f = make_float2(1.f, 1.f);
+            if constexpr (kCols) f = *reinterpret_cast<const float2 *>(sc + 128 * half + 32 * c + 8 * (i & 3) + 2 * (lane & 3));
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const float x = __uint_as_float(v[c & 1][4 * i + j]), y = __uint_as_float(v[c & 1][4 * i + j + 1]);
+              float &a = acc[32 * c + 4 * i + j], &b = acc[32 * c + 4 * i + j + 1];
+              if constexpr (kCols) {
+                // two at a time: half the instructions of two FP32 operations a
+                // value (137 -> 125 us); slower where there is one (1293 -> 1389 us)
+                const float k = s[2 * (i >> 2) + (j >> 1)];
+                const float2 r = fma2(mul2(make_float2(x, y), f), make_float2(k, k), make_float2(a, b));
+                a = r.x;
+                b = r.y;
+              } else {
+                a = fmaf(x, s[0], a);
+                b = fmaf(y, s[0], b);
+              }
             }
-            acc[16 * c + i] = fmaf(x, s, acc[16 * c + i]);
           }
-          if (c < 7) tmem_ld_waitN(v[(c + 1) & 1]);
-          if (c == 6) {  // the accumulator has been read
+          if (c < 3) tmem_ld_waitN(v[(c + 1) & 1]);
+          if (c == 2) {  // the accumulator has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -418,27 +475,60 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       // C: rows row0 .. +31, columns col0 .. +127, in pieces of 128 bytes a
       // row through this warp's 4 KB (16-byte units swizzled by the row)
       if (row0 >= p.M || col0 >= p.N) continue;
-      const uint32_t mine = stg + lane * 128;
+      // piece c: columns 32 c .. +31 in FP32, or 64 c .. +63 in BF16
+      auto stage_f32 = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float *a = acc + 32 * c + 4 * j;
+          if constexpr (kCols) {
+            // i = j: rows 16 (i / 4) + lane / 4 (+ 8), columns 8 (i % 4) + 2 (lane % 4), + 1
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = 16 * (j >> 2) + 8 * h + (lane >> 2), u = 2 * (j & 3) + ((lane >> 1) & 1);
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(stg + r * 128 + ((u ^ (r & 7)) << 4) + 8 * (lane & 1)),
+                           "r"(__float_as_uint(a[2 * h])), "r"(__float_as_uint(a[2 * h + 1]))
+                           : "memory");
+            }
+          } else {
+            st_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(a[0]), __float_as_uint(a[1]),
+                         __float_as_uint(a[2]), __float_as_uint(a[3]));
+          }
+        }
+      };
+      auto stage_bf16 = [&](int c) {
+        auto two = [](float a, float b) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+          return *reinterpret_cast<const uint32_t *>(&h);
+        };
+        if constexpr (kCols) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float *a = acc + 64 * c + 4 * j;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = 16 * ((j >> 2) & 1) + 8 * h + (lane >> 2), u = 4 * (j >> 3) + (j & 3);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(stg + r * 128 + ((u ^ (r & 7)) << 4) + 4 * (lane & 3)),
+                           "r"(two(a[2 * h], a[2 * h + 1]))
+                           : "memory");
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float *a = acc + 64 * c + 8 * j;
+            st_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4), two(a[0], a[1]), two(a[2], a[3]), two(a[4], a[5]),
+                         two(a[6], a[7]));
+          }
+        }
+      };
       if (p.tma_store) {
         constexpr int kCol = kBF16 ? 64 : 32;
 #pragma unroll
         for (int c = 0; c < 128 / kCol; ++c) {
           if (lane == 0) bulk_wait_read_all();
           __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (kBF16) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[64 * c + 8 * j + 2 * e], acc[64 * c + 8 * j + 2 * e + 1]);
-                o[e] = *reinterpret_cast<const uint32_t *>(&h);
-              } else {
-                o[e] = __float_as_uint(acc[32 * c + 4 * j + e]);
-              }
-            }
-            st_shared_v4(mine + ((j ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
-          }
+          if constexpr (kBF16) stage_bf16(c);
+          else stage_f32(c);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && col0 + c * kCol < p.N) {
@@ -450,11 +540,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared_v4(mine + ((j ^ (lane & 7)) << 4), __float_as_uint(acc[32 * c + 4 * j]),
-                         __float_as_uint(acc[32 * c + 4 * j + 1]), __float_as_uint(acc[32 * c + 4 * j + 2]),
-                         __float_as_uint(acc[32 * c + 4 * j + 3]));
+          stage_f32(c);
           __syncwarp();
           const int col = col0 + c * 32 + lane;
           const int rows = min(32, p.M - row0);
@@ -689,7 +775,7 @@ __global__ void __launch_bounds__(SkinnyCfg<NT>::THREADS, 1)
       for (int c = 0; c < NT / 16; ++c) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(lane_addr + NT * buf + 16 * c, v);
-        tmem_ld_wait16(v);
+        tmem_ld_waitN(v);
         if (c == NT / 16 - 1) {
           tc_fence_before();
           __syncwarp();
