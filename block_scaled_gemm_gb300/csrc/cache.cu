@@ -117,7 +117,7 @@ int run_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t ctas, cudaS
 template <int D, int NT>
 int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::DecodeCfg<D, NT>;
-  const int grid = std::min(2 * v.sm_count, mxg::kCounters);
+  const int grid = std::min(S::CTAS * v.sm_count, mxg::kCounters);
   uint8_t *ws = nullptr;
   if (int st = mxg::handle_workspace(h, static_cast<size_t>(grid) * 2 * S::PARTIAL * sizeof(float), stream, &ws))
     return st;

@@ -115,7 +115,13 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttnParams &p, const Sequenc
 
 // Items of sequence s: row tiles x key/value heads.
 __device__ __forceinline__ int64_t item_count(const AttnParams &p, const Sequence &s, int rows) {
-  return (static_cast<int64_t>(s.n) * p.group + rows - 1) / rows * p.c.kv_heads;
+  return ((static_cast<int64_t>(s.n) * p.group + rows - 1) >> (rows == 8 ? 3 : 4)) * p.c.kv_heads;
+}
+
+// a / b for a >= 0, b > 0: in 32 bits where both fit, as they mostly do.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // Position in the flat order of tiles: a sequence, and in it an item.
@@ -132,9 +138,9 @@ struct Cursor {
   __device__ void start(const AttnParams &p, int rows, int b_, int64_t base, int64_t x) {
     b = b_;
     enter(p, rows);
-    item = (x - base) / k.tiles;
+    item = quotient(x - base, k.tiles);
     beg = base + item * k.tiles;
-    h = static_cast<int>(item % p.c.kv_heads);
+    h = static_cast<int>(item - quotient(item, p.c.kv_heads) * p.c.kv_heads);
   }
   // forward to the item of tile x (below the total)
   __device__ void to(const AttnParams &p, int rows, int64_t x) {
@@ -164,31 +170,20 @@ struct Cursor {
   }
 };
 
-// The sequence that tile x (below the total) belongs to, and where its tiles
-// begin: by a whole warp, 32 sequences at a time.
-__device__ __forceinline__ int find_sequence(const AttnParams &p, int rows, int64_t x, int64_t *base) {
+// Tiles of sequence b (none past the batch).
+__device__ __forceinline__ int64_t sequence_tiles(const AttnParams &p, int rows, int b) {
+  if (b >= p.b.batch) return 0;
+  const Sequence s = load_sequence(p.b, p.c, b);
+  return item_count(p, s, rows) * key_tiles(p, s).tiles;
+}
+__device__ __forceinline__ int64_t warp_prefix(int64_t v) {  // inclusive
   const int lane = threadIdx.x & 31;
-  int64_t before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    int64_t mine = 0;
-    if (b0 + lane < p.b.batch) {
-      const Sequence s = load_sequence(p.b, p.c, b0 + lane);
-      mine = item_count(p, s, rows) * key_tiles(p, s).tiles;
-    }
-    int64_t upto = mine;  // of this sequence and those before it
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > x);
-    if (past) {
-      const int i = __ffs(past) - 1;
-      *base = before + __shfl_sync(0xFFFFFFFFu, upto - mine, i);
-      return b0 + i;
-    }
-    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
   }
+  return v;
 }
 
 template <int D, int NT>
@@ -197,7 +192,11 @@ struct DecodeCfg {
   static constexpr int WARPS = 4;
   static constexpr int TILE = 32;
   static constexpr int STAGE = 2 * TILE * D;              // K, then V
-  static constexpr int STAGES = 3 * 128 / D;              // of each warp
+  // CTAs of an SM: three where the registers allow it (the warps' chains of
+  // dependent instructions bound them, more warps hide them), with two tiles of
+  // 8 KB in flight for each warp, else two with three
+  static constexpr int CTAS = NT == 1 ? 3 : 2;
+  static constexpr int STAGES = (CTAS == 3 ? 2 : 3) * 128 / D;
   static constexpr int OFF_MERGE = WARPS * STAGES * STAGE;  // [warp][8 rows][64] floats
   static constexpr int OFF_ML = OFF_MERGE + WARPS * 8 * 64 * 4;  // m and l: [2][warp][ROWS]
   static constexpr int OFF_SC = OFF_ML + 2 * WARPS * ROWS * 4;   // [warp][stage][K, V][2 pages] scales
@@ -206,11 +205,11 @@ struct DecodeCfg {
   static constexpr int OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
   static constexpr int PARTIAL = ROWS * (D + 2);  // floats of a partial: O, m, l
-  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const AttnParams p) {
   using S = DecodeCfg<D, NT>;
@@ -235,26 +234,37 @@ __global__ void __launch_bounds__(128, 2)
     fence_proxy_async_smem();
   }
   __syncwarp();
-  // all tiles (each warp counts for itself), and this CTA's range of them:
-  // ranges of four tiles at least
-  int64_t total = 0;
-  for (int b = lane; b < p.b.batch; b += 32) {
-    const Sequence s = load_sequence(p.b, p.c, b);
-    total += item_count(p, s, ROWS) * key_tiles(p, s).tiles;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  // All tiles (each warp counts for itself, 32 sequences at a time), and this
+  // CTA's range of them: ranges of four tiles at least.
+  const int64_t mine = sequence_tiles(p, ROWS, lane), upto = warp_prefix(mine);  // the first 32 sequences
+  int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  for (int b = 32; b < p.b.batch; b += 32)
+    total += __shfl_sync(0xFFFFFFFFu, warp_prefix(sequence_tiles(p, ROWS, b + lane)), 31);
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 3) / 4);
   if (blockIdx.x >= ctas) return;
-  auto first_tile = [&](int64_t u) { return u * total / ctas; };
-  auto cta_of = [&](int64_t x) { return ((x + 1) * ctas - 1) / total; };  // the CTA whose range holds tile x
+  auto first_tile = [&](int64_t u) { return quotient(u * total, ctas); };
+  auto cta_of = [&](int64_t x) { return quotient((x + 1) * ctas - 1, total); };  // the CTA whose range holds tile x
   const int64_t x0 = first_tile(blockIdx.x), x1 = first_tile(blockIdx.x + 1);
+  // the sequence of tile x0, and where its tiles begin
+  int b0 = 0;
+  int64_t base_b = 0;
+  {
+    int64_t m = mine, u = upto;
+    uint32_t past;
+    while (!(past = __ballot_sync(0xFFFFFFFFu, base_b + u > x0))) {
+      base_b += __shfl_sync(0xFFFFFFFFu, u, 31);
+      b0 += 32;
+      m = sequence_tiles(p, ROWS, b0 + lane);
+      u = warp_prefix(m);
+    }
+    const int i = __ffs(past) - 1;
+    base_b += __shfl_sync(0xFFFFFFFFu, u - m, i);
+    b0 += i;
+  }
 
   const int lg = p.c.page_log2, per = lg == 4 ? 2 : 1;  // pages of a tile
   const uint32_t box_bytes = (lg == 4 ? 16 : 32) * D;
   // ------------------------------------------------------------ loads
-  int64_t base_b;
-  const int b0 = find_sequence(p, ROWS, x0, &base_b);
   Cursor at, in;  // of the item being computed, and of the next tile to load
   at.start(p, ROWS, b0, base_b, x0);
   in = at;
@@ -283,6 +293,23 @@ __global__ void __launch_bounds__(128, 2)
       tma_load_2d(dst + 32 * D, &tmV, 0, row, bar);
     }
   };
+  // Q of the item at `at`, as it lies: thread (g, t) has rows g of each 8,
+  // d = (D/4) t .. + D/4 - 1; rows past the last are zero
+  uint4 qraw[NT][D / 32];
+  auto load_q = [&]() {
+    const int row0 = static_cast<int>(quotient(at.item, p.c.kv_heads)) * ROWS;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool live = r < at.s.n * p.group;
+      const int tok = r / p.group, hd = at.h * p.group + r % p.group;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + static_cast<int64_t>(at.s.first + tok) * p.q_pitch +
+                                                         static_cast<int64_t>(hd) * D + t * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) qraw[n][i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load_q();
   // bounded wait (whole warp): the loads of this stage have landed
   auto wait_stage = [&](int st, uint32_t ph) -> bool {
     bool ok = mbar_try_wait(bars + 8 * st, ph);
@@ -309,31 +336,19 @@ __global__ void __launch_bounds__(128, 2)
   uint32_t ph = 0;
   bool alive = true;
   for (int64_t seg = x0; seg < x1;) {
-    at.to(p, ROWS, seg);
     const int64_t item_beg = at.beg, item_end = item_beg + at.k.tiles;
     const int64_t seg_end = min(item_end, x1);
     const int h = at.h;
-    const int row0 = static_cast<int>(at.item / p.c.kv_heads) * ROWS;  // row = token * group + head of the group
+    const int row0 = static_cast<int>(quotient(at.item, p.c.kv_heads)) * ROWS;  // row = token * group + head of the group
     const int rows = min(ROWS, at.s.n * p.group - row0);
     const int pos0 = at.s.len - at.s.n;
 
-    // Q: thread (g, t) holds row g of each 8, d = (D/4) t .. + D/4 - 1, in the
-    // order of K's words; rows past the last are zero
+    // Q in the order of K's words
     uint32_t q[NT][KW][2];
     float cq[NT][2];  // logits of this lane's columns 2t, 2t+1: S * cq
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + g;
-      uint4 w[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int tok = (row0 + r) / p.group, hd = h * p.group + (row0 + r) % p.group;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + static_cast<int64_t>(at.s.first + tok) * p.q_pitch +
-                                                           static_cast<int64_t>(hd) * D + t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) w[i] = src[i];
-      }
+      const uint4 (&w)[D / 32] = qraw[n];
       const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
       float top = 0.f;
 #pragma unroll
@@ -378,30 +393,42 @@ __global__ void __launch_bounds__(128, 2)
       const int key0 = at.key(x);
       if (alive) alive = wait_stage(st, ph);
       const uint32_t kb = ring + st * S::STAGE, vb = kb + 32 * D;
-      // S^T: keys 16 mt + g (+ 8) x rows
-      float s[2][NT][4];
+      // S^T: keys 16 mt + g (+ 8) x rows; two sums for the halves of D, so that
+      // chains of dependent MMAs are half as long
+      float s[2][NT][4], s1[2][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t k0[KW], k1[KW];
-#pragma unroll
-        for (int c = 0; c < KW / 4; ++c) {
-          const int ra = 16 * mt + g, rb = ra + 8, ch = (KW / 4) * t + c;  // 16-byte chunk of the row
-          const uint4 a = ld_shared_v4(kb + ra * D + ((ch ^ (D == 128 ? ra & 7 : (ra >> 1) & 3)) << 4));
-          const uint4 b = ld_shared_v4(kb + rb * D + ((ch ^ (D == 128 ? rb & 7 : (rb >> 1) & 3)) << 4));
-          k0[4 * c] = a.x; k0[4 * c + 1] = a.y; k0[4 * c + 2] = a.z; k0[4 * c + 3] = a.w;
-          k1[4 * c] = b.x; k1[4 * c + 1] = b.y; k1[4 * c + 2] = b.z; k1[4 * c + 3] = b.w;
-        }
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[mt][n][j] = 0.f;
+          for (int j = 0; j < 4; ++j) s[mt][n][j] = s1[mt][n][j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          const uint32_t a0 = e4m3_lo(k0[i]), a1 = e4m3_lo(k1[i]), a2 = e4m3_hi(k0[i]), a3 = e4m3_hi(k1[i]);
+      for (int c = 0; c < KW / 4; ++c) {
+        uint4 k0[2], k1[2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(s[mt][n], a0, a1, a2, a3, q[n][i][0], q[n][i][1]);
+        for (int mt = 0; mt < 2; ++mt) {
+          const int ra = 16 * mt + g, rb = ra + 8, ch = (KW / 4) * t + c;  // 16-byte chunk of the row
+          k0[mt] = ld_shared_v4(kb + ra * D + ((ch ^ (D == 128 ? ra & 7 : (ra >> 1) & 3)) << 4));
+          k1[mt] = ld_shared_v4(kb + rb * D + ((ch ^ (D == 128 ? rb & 7 : (rb >> 1) & 3)) << 4));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            const uint32_t a = i == 0 ? k0[mt].x : i == 1 ? k0[mt].y : i == 2 ? k0[mt].z : k0[mt].w;
+            const uint32_t b = i == 0 ? k1[mt].x : i == 1 ? k1[mt].y : i == 2 ? k1[mt].z : k1[mt].w;
+            const uint32_t a0 = e4m3_lo(a), a1 = e4m3_lo(b), a2 = e4m3_hi(a), a3 = e4m3_hi(b);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16((i & 1) ? s1[mt][n] : s[mt][n], a0, a1, a2, a3, q[n][4 * c + i][0], q[n][4 * c + i][1]);
+          }
       }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][n][j] += s1[mt][n][j];
       // exponents; ivs = 1 / vs
       const bool ok0 = pg_ok[2 * st] != 0, ok1 = per == 2 ? pg_ok[2 * st + 1] != 0 : ok0;
       float ivs[2];
@@ -652,8 +679,12 @@ __global__ void __launch_bounds__(128, 2)
         }
       }
     }
-    __syncthreads();  // ml and merge are free for the next item
     seg = seg_end;
+    if (seg < x1) {
+      at.to(p, ROWS, seg);
+      load_q();
+    }
+    __syncthreads();  // ml and merge are free for the next item
   }
   // after a wait that gave up: loads still on their way land first
   for (int i = 0; !alive && i < STAGES; ++i) {
