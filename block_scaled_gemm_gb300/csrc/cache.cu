@@ -70,6 +70,24 @@ int launched(const mxg::HandleView &v) {
   return MXGEMM_OK;
 }
 
+// Passes over a page's rows: of 128 threads, eight values each.
+template <typename T, int D, int LG>
+void launch_append_page(const mxg::AppendParams &p, dim3 grid, cudaStream_t stream) {
+  constexpr int kRows = 128 / (D / 8), kAll = ((1 << LG) + kRows - 1) / kRows;
+  if (p.b.q_start) mxg::cache_append_kernel<T, D, LG, kAll><<<grid, 128, 0, stream>>>(p);
+  else mxg::cache_append_kernel<T, D, LG, 1><<<grid, 128, 0, stream>>>(p);  // one token
+}
+
+template <typename T, int D>
+void launch_append(const mxg::AppendParams &p, dim3 grid, cudaStream_t stream) {
+  switch (p.c.page_log2) {
+    case 4: launch_append_page<T, D, 4>(p, grid, stream); break;
+    case 5: launch_append_page<T, D, 5>(p, grid, stream); break;
+    case 6: launch_append_page<T, D, 6>(p, grid, stream); break;
+    default: launch_append_page<T, D, 7>(p, grid, stream); break;
+  }
+}
+
 // Tensor map of a cache's codes as rows of head_dim bytes, swizzled or not.
 int encode_rows(const mxg::HandleView &v, CUtensorMap *tm, const void *base, int64_t rows, int d, int box_rows,
                 bool swizzle) {
@@ -158,15 +176,15 @@ extern "C" int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cach
   p.newV = new_V;
   p.pitch = pitch;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const dim3 grid(static_cast<unsigned>((tokens >> p.c.page_log2) + 2 * batch),
-                  static_cast<unsigned>(cache->kv_heads), 2);
+  const int64_t items = q_start ? (tokens >> p.c.page_log2) + 2 * batch : batch;
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(cache->kv_heads), 2);
   const bool f32 = x_dtype == MXGEMM_IN_F32;
   if (cache->head_dim == 128) {
-    if (f32) mxg::cache_append_kernel<float, 128><<<grid, 128, 0, stream>>>(p);
-    else mxg::cache_append_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
+    if (f32) launch_append<float, 128>(p, grid, stream);
+    else launch_append<__nv_bfloat16, 128>(p, grid, stream);
   } else {
-    if (f32) mxg::cache_append_kernel<float, 64><<<grid, 128, 0, stream>>>(p);
-    else mxg::cache_append_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
+    if (f32) launch_append<float, 64>(p, grid, stream);
+    else launch_append<__nv_bfloat16, 64>(p, grid, stream);
   }
   return launched(v);
 }

@@ -3,9 +3,9 @@
 // Of each page that new tokens touch, each head and each of K and V:
 //   need  = max(2^-64, least power of two >= amax(new) / 448)
 //   scale = the new tokens begin the page ? need : max(old, need)
-//   codes = E4M3(clamp(x / scale)), and where the scale grew, the page's
+//   codes = E4M3(clamp(x * (1 / scale))), and where the scale grew, the page's
 //           earlier codes E4M3(code * (old / scale)).
-// Powers of two: x / scale is exact, and so is an earlier code's move to a
+// Powers of two: x * (1 / scale) is exact, and so is an earlier code's move to a
 // larger scale unless it falls below E4M3's normal range.
 //
 // One block of threads per (page, head, K or V).  The pages that a batch
@@ -15,6 +15,7 @@
 // whose number names no page ends at once.
 #pragma once
 #include "cache_common.cuh"
+#include "quantize128.cuh"
 
 namespace mxg {
 
@@ -32,18 +33,16 @@ __device__ __forceinline__ float cache_need(float amax) {
   return amax > 0.f ? fmaxf(__int_as_float(mx_scale_of(amax) << 23), kCacheLeast) : kCacheLeast;
 }
 
-template <typename T, int D>
+template <typename T, int D, int LG, int PASSES>
 __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p) {
-  constexpr int kVec = 8, kPer = D / kVec, kRows = 128 / kPer;  // threads of a row, rows of a pass
+  // threads of a row, rows of a pass
+  constexpr int lg = LG, ps = 1 << LG, kPer = D / 8, kRows = 128 / kPer;
   __shared__ float part[4];
-  const int ps = p.c.page_size, lg = p.c.page_log2;
   const int64_t item = blockIdx.x;
   const int head = blockIdx.y;
-  auto f = [&](int b) -> int64_t {
-    const int64_t q = p.b.q_start ? p.b.q_start[b] : b;
-    return (q >> lg) + 2 * static_cast<int64_t>(b);
-  };
-  const int b = warp_find(p.b.batch, f, item);
+  // (one token each: one page each)
+  auto f = [&](int b) -> int64_t { return p.b.q_start ? (p.b.q_start[b] >> lg) + 2 * static_cast<int64_t>(b) : b; };
+  const int b = p.b.q_start ? warp_find(p.b.batch, f, item) : static_cast<int>(item);
   const Sequence s = load_sequence(p.b, p.c, b);
   if (s.n == 0) return;
   const int start = s.len - s.n;  // position of the first new token
@@ -64,48 +63,36 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
   float *scale_at = (isV ? p.c.V_scale : p.c.K_scale) + cell;
   const T *x = static_cast<const T *>(isV ? p.newV : p.newK) +
                static_cast<int64_t>(s.first + p0 - start) * p.pitch + static_cast<int64_t>(head) * D;
-  const int col = (threadIdx.x % kPer) * kVec, row0 = threadIdx.x / kPer;
+  const int col = (threadIdx.x % kPer) * 8, row0 = threadIdx.x / kPer;  // new rows: lo + row0, + kRows, ...
 
-  auto load = [&](int r, float(&v)[8]) {
-    const T *src = x + static_cast<int64_t>(r) * p.pitch + col;
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = reinterpret_cast<const float4 *>(src)[0], c = reinterpret_cast<const float4 *>(src)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4 *>(src);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  // all loads before the first use; the values stay in registers until the
+  // scale is known
+  Eight<T> v[PASSES];
+  const float old = lo > 0 ? *scale_at : 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(w[e] << 16);
-        v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    }
-  };
-
-  float amax = 0.f;
-  for (int r = lo + row0; r < hi; r += kRows) {
-    float v[8];
-    load(r, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  for (int i = 0; i < PASSES; ++i) {
+    const int r = lo + row0 + i * kRows;
+    if (r < hi) v[i].load(x + static_cast<int64_t>(r) * p.pitch + col);
+    else v[i].zero();
   }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) amax = fmaxf(amax, v[i].top());
+#pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-  const float old = lo > 0 ? *scale_at : 0.f;
   __syncthreads();
-  amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-  const float need = cache_need(amax);
-  const float scale = fmaxf(old, need);
-  if (threadIdx.x == 0) *scale_at = scale;
-  for (int r = lo + row0; r < hi; r += kRows) {
-    float v[8];
-    load(r, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __fdiv_rn(v[e], scale);
-    *reinterpret_cast<uint2 *>(codes + r * D + col) =
-        make_uint2(mx_e4m3x2(v[0], v[1]) | (mx_e4m3x2(v[2], v[3]) << 16),
-                   mx_e4m3x2(v[4], v[5]) | (mx_e4m3x2(v[6], v[7]) << 16));
+  for (int w = 0; w < 4; ++w) amax = fmaxf(amax, part[w]);
+  const float scale = fmaxf(old, cache_need(amax));
+  const float inv = __frcp_rn(scale);
+  if (threadIdx.x == 0) *scale_at = scale;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int r = lo + row0 + i * kRows;
+    if (r < hi) {
+      *reinterpret_cast<uint2 *>(codes + r * D + col) = v[i].codes(inv);
+    }
   }
   if (lo > 0 && scale > old) {
     const float ratio = __fdiv_rn(old, scale);

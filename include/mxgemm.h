@@ -474,7 +474,8 @@ typedef struct {
  * that new tokens touch and each head, for K and V alike:
  *   need  = max(2^-64, the least power of two >= (largest new |x|) / 448)
  *   scale = need where the new tokens begin the page, else max(old scale, need)
- *   codes of the new tokens: nearest E4M3 value to clamp(x / scale, +-448);
+ *   codes of the new tokens: nearest E4M3 value to clamp(x * (1 / scale), +-448),
+ *   the reciprocal in FP32 (exact for powers of two);
  *   codes that the page held before, when the scale grew: nearest E4M3 value
  *   to code * (old scale / scale) (exact for old scales that are powers of two,
  *   but for values that fall below E4M3's normal range).
