@@ -27,8 +27,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
-#include "mxgemm_kernel.cuh"
-#include "ptx.cuh"
+#include "tmem_util.cuh"
 
 namespace mxg {
 
@@ -78,15 +77,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
-// Wait for this thread's tcgen05.ld results in r: the registers are named so
-// that no use of them moves above the wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld_waitN(uint32_t (&r)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 // 16 lanes x 32 columns as the fragments of an 8 x 8 grid: of each eight
 // columns, thread (g, t) = (lane / 4, lane % 4) gets columns 2t, 2t + 1 of lanes
 // g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
@@ -108,32 +98,6 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Bounded wait by a whole warp; the first probe, which mostly succeeds, is
-// apart from the loop with its clock reads (8192 x 28672 x 8192 BF16: 1311 ->
-// 1285 us).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl &w, int detail) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xFFFFFFFFu, wait_phase<false>(bar, parity, w, detail));
-}
-
-// Two FP32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
 }
 
 constexpr int kB128Bf16 = 1;    // BF16 output (else FP32)
@@ -423,7 +387,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
           }
         };
         load(0, v[0]);
-        tmem_ld_waitN(v[0]);
+        tmem_ld_done(v[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c < 3) load(c + 1, v[(c + 1) & 1]);
@@ -448,7 +412,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
               }
             }
           }
-          if (c < 3) tmem_ld_waitN(v[(c + 1) & 1]);
+          if (c < 3) tmem_ld_done(v[(c + 1) & 1]);
           if (c == 2) {  // the accumulator has been read
             tc_fence_before();
             __syncwarp();
@@ -775,7 +739,7 @@ __global__ void __launch_bounds__(SkinnyCfg<NT>::THREADS, 1)
       for (int c = 0; c < NT / 16; ++c) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(lane_addr + NT * buf + 16 * c, v);
-        tmem_ld_waitN(v);
+        tmem_ld_done(v);
         if (c == NT / 16 - 1) {
           tc_fence_before();
           __syncwarp();

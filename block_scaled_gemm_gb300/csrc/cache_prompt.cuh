@@ -22,7 +22,7 @@
 // 8-11 and 12-15 the softmax of the two Q tiles.
 #pragma once
 #include "cache_attention.cuh"
-#include "mxgemm_kernel.cuh"
+#include "tmem_util.cuh"
 
 namespace mxg {
 
@@ -40,7 +40,7 @@ struct PromptCfg {
   static constexpr int OFF_SC = OFF_V8 + TILE8;  // [4 tiles][ks, log2 vs, 1/vs][8 groups of 16 keys]
   static constexpr int OFF_PG = OFF_SC + 4 * 3 * 8 * 4;  // [4 tiles] bit mask of the groups that are there
   static constexpr int OFF_BAR = OFF_PG + 16;
-  static constexpr int NUM_BARS = 2 + 2 + 2 * 4 + 2 * 4 + 2;
+  static constexpr int NUM_BARS = 4 + 2 * 4 + 2 + 4 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 512;
@@ -76,14 +76,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// The results of tcgen05.ld are in r: no use of them moves above the wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -139,8 +131,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const uint32_t bars = base + S::OFF_BAR;
   const uint32_t k8_full = bars, v8_full = bars + 8, k8_empty = bars + 16, v8_empty = bars + 24;
   const uint32_t k_full = bars + 32, v_full = bars + 48, k_empty = bars + 64, v_empty = bars + 80;  // two each
-  const uint32_t s_full = bars + 96, p_full = bars + 112, o_done = bars + 128, q_full = bars + 144;  // two each
-  const uint32_t bar_final = bars + 160;
+  const uint32_t s_full = bars + 96, p_full = bars + 112;  // one and two (P's halves) for each Q tile
+  const uint32_t o_done = bars + 144, q_full = bars + 160;  // one for each Q tile
+  const uint32_t bar_final = bars + 176;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 4);
   volatile int *never = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 8);  // never raised
@@ -158,6 +151,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
+      mbar_init(p_full + 16 + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
       mbar_init(q_full + 8 * i, 4);
     }
@@ -260,16 +254,20 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int j = 0; ok && j < tiles; ++j) {
           const int buf = j & 1;
           for (int i = 0; i < nq; ++i) {
-            ok = (i || w1(v_full + 8 * buf, (j >> 1) & 1, 0x46)) && w1(p_full + 8 * i, j & 1, 0x47);
-            if (!ok) break;
-            tc_fence_after();
+            ok = i || w1(v_full + 8 * buf, (j >> 1) & 1, 0x46);
             // P: 8 columns per K = 16 keys; V: N-major, chunks of 64 d 16 KB
             // apart, 16 keys 2 KB apart
             const uint32_t v = base + S::OFF_V + buf * S::TILE16;
+            for (int hf = 0; hf < 2; ++hf) {  // P of 64 keys, then of the others
+              ok = ok && w1(p_full + 16 * i + 8 * hf, j & 1, 0x47);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              mma_f16_ts(tmem + S::TM_O + 128 * i, tmem + S::TM_S + 128 * i + 8 * c, smem_desc(v + 2048 * c, 16384, 1024, 2),
-                         kIdO, j != 0 || c != 0);
+              for (int c = 0; c < 4; ++c)
+                mma_f16_ts(tmem + S::TM_O + 128 * i, tmem + S::TM_S + 128 * i + 32 * hf + 8 * c,
+                           smem_desc(v + 8192 * hf + 2048 * c, 16384, 1024, 2), kIdO, j != 0 || hf != 0 || c != 0);
+            }
+            if (!ok) break;
             tc_commit(o_done + 8 * i);
             if (i == nq - 1) tc_commit(v_empty + 8 * buf);
             if (j + 1 < tiles) {
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       bool ok = true;
       for (int j = 0; j < tiles; ++j) {
         const int key0 = tile_key(j);
-        ok = wait(s_full + 8 * i, j & 1, 0x4D);
+        ok = warp_wait(s_full + 8 * i, j & 1, wc, 0x4D);
         if (!ok) break;
         tc_fence_after();
         const float *sc = scales + (j & 3) * 24;
@@ -457,22 +455,25 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float k = fmaxf(cq * sc[2 * c + hf], kTinyFactor), a = sc[8 + 2 * c + hf] - ms;
-            float sum = 0.f;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float w0 = ex2(fmaf(__uint_as_float(v[c][16 * hf + 2 * e]), k, a));
-              const float w1 = ex2(fmaf(__uint_as_float(v[c][16 * hf + 2 * e + 1]), k, a));
-              sum += w0 + w1;
-              pk[8 * hf + e] = half2_of(w0, w1);
+              const float2 x = fma2(make_float2(__uint_as_float(v[c][16 * hf + 2 * e]), __uint_as_float(v[c][16 * hf + 2 * e + 1])),
+                                    make_float2(k, k), make_float2(a, a));
+              const float2 w = make_float2(ex2(x.x), ex2(x.y));
+              sum = add2(sum, w);
+              pk[8 * hf + e] = half2_of(w.x, w.y);
             }
-            l = fmaf(sum, sc[16 + 2 * c + hf], l);
+            l = fmaf(sum.x + sum.y, sc[16 + 2 * c + hf], l);
           }
           tmem_st_x16(ts + 16 * c, pk);
+          if (c & 1) {  // 64 keys: their MMAs may begin
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 16 * i + 8 * (c >> 1));
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * i);
       }
       if (ok) ok = wait(o_done + 8 * i, (tiles - 1) & 1, 0x4F);
       if (ok) {
