@@ -297,3 +297,70 @@ def test_past_32_bits(handles):
     rows = torch.tensor([0, 65535, 65536, 69998, 69999])
     ref, mag = plain64.product(plain64.value(a[rows]), sa[rows], plain64.value(b), sb, 128)
     check(C[rows.to(DEV)].cpu(), ref, mag, "bf16")
+
+
+@pytest.mark.parametrize("m,b_block", [(16, 128), (300, 128), (300, 1)])
+def test_a_stalled_producer_ends_in_a_status(m, b_block):
+    """No loads: every wait runs out, the kernel returns, the handle stays usable."""
+    h = mx.mxgemm_create(0)
+    try:
+        mx.mxgemm_set_option(h, mx.OPT_B_MAJOR, mx.B_N_BY_K)
+        a, sa, b, sb = operands(m, 300, 400, b_block, 1)
+        dev = [t.to(DEV) for t in (a, sa, b, sb)]
+        C = torch.zeros(m, 300, device=DEV)
+        mx.mxgemm_set_option(h, mx.OPT_WAIT_TIMEOUT_NS, 50_000_000)
+        mx.mxgemm_set_option(h, mx.OPT_TEST_STALL_PRODUCER, 1)
+        mx.mxgemm_run_block128(h, m, 300, 400, *dev, C, b_block=b_block)
+        assert mx.mxgemm_get_device_status(h)[0] == mx.ERR_TIMEOUT
+        mx.mxgemm_set_option(h, mx.OPT_TEST_STALL_PRODUCER, 0)
+        mx.mxgemm_set_option(h, mx.OPT_WAIT_TIMEOUT_NS, 2_000_000_000)
+        ref, mag = plain64.product(plain64.value(a), sa, plain64.value(b), sb, b_block)
+        check(run(h, True, a, sa, b, sb, b_block), ref, mag, "f32")
+    finally:
+        mx.mxgemm_destroy(h)
+
+
+def test_profile_events_and_launch_count(handles):
+    a, sa, b, sb = (t.to(DEV) for t in operands(40, 256, 256, 128, 1))
+    C = torch.empty(40, 256, device=DEV)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for e in ev:
+        e.record()
+    h = handles[True]
+    n = mx.mxgemm_get_launch_count(h)
+    mx.mxgemm_set_profile_events(h, *ev)
+    try:
+        mx.mxgemm_run_block128(h, 40, 256, 256, a, sa, b, sb, C)
+    finally:
+        mx.mxgemm_set_profile_events(h, None, None)
+    torch.cuda.synchronize()
+    assert mx.mxgemm_get_launch_count(h) == n + 1 and ev[0].elapsed_time(ev[1]) > 0
+
+
+def test_captured_in_a_graph(handles):
+    """The product and its quantizer hold no host state: captured once, replayed on new inputs."""
+    T, I, O = 300, 272, 400
+    g = torch.Generator().manual_seed(4)
+    x, w = torch.randn(T, I, generator=g).to(DEV), torch.randn(O, I, generator=g).to(DEV)
+    xc, xs = torch.empty(T, I, dtype=torch.uint8, device=DEV), torch.empty(T, 3, device=DEV)
+    wc, ws = torch.empty(O, I, dtype=torch.uint8, device=DEV), torch.empty(4, 3, device=DEV)
+    C = torch.empty(T, O, device=DEV)
+
+    def step():
+        s = torch.cuda.current_stream()
+        mx.mxgemm_quantize_block128(x, T, I, xc, xs, stream=s)
+        mx.mxgemm_quantize_block128(w, O, I, wc, ws, block=mx.BLOCK_TILES, stream=s)
+        mx.mxgemm_run_block128(handles[True], T, O, I, xc, xs, wc, ws, C, stream=s)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x.copy_(torch.randn(T, I, generator=g))
+    step()
+    want = C.clone()
+    C.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(C, want)
