@@ -17,6 +17,7 @@ The operation is the scaled product documented as ``tlx.async_dot_scaled``
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 from . import _build
@@ -89,11 +90,8 @@ EXPORTED_SYMBOLS = (
 _lib = None
 
 
-class _CacheStruct(ctypes.Structure):
-    """mxgemm_cache_t"""
-    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("K_scale", ctypes.c_void_p),
-                ("V_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
-                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+# mxgemm_cache_t
+_CACHE_STRUCT = struct.Struct("PPPPqiii4x")
 
 
 class MxgemmError(RuntimeError):
@@ -151,9 +149,9 @@ def library():
         lib.mxgemm_run_block128.restype = i32
         lib.mxgemm_quantize_block128.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
         lib.mxgemm_quantize_block128.restype = i32
-        lib.mxgemm_cache_append.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, i32, vp]
+        lib.mxgemm_cache_append.argtypes = [vp, ctypes.c_char_p, i64, vp, i64, vp, vp, i64, vp, vp, i64, i32, vp]
         lib.mxgemm_cache_append.restype = i32
-        lib.mxgemm_cache_attention.argtypes = [vp, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64,
+        lib.mxgemm_cache_attention.argtypes = [vp, ctypes.c_char_p, i64, i64, vp, i64, vp, vp, i64, vp, i64,
                                                ctypes.c_float, i32, i64, i64, vp, vp, vp]
         lib.mxgemm_cache_attention.restype = i32
         lib.mxgemm_status_string.argtypes = [i32]
@@ -325,34 +323,35 @@ class Cache:
     size x head dim) and float32 tensors of their scales (pages x kv heads)."""
 
     def __init__(self, K, V, K_scale, V_scale):
-        if K.dim() != 4 or K.shape != V.shape or K_scale.shape != K.shape[:2] or V_scale.shape != K.shape[:2]:
+        shape, dims = K.shape, K_scale.shape
+        if len(shape) != 4 or V.shape != shape or dims != shape[:2] or V_scale.shape != dims:
             raise ValueError("K and V: pages x kv heads x page size x head dim, scales: pages x kv heads")
-        for t, size in ((K, 1), (V, 1), (K_scale, 4), (V_scale, 4)):
-            if not t.is_contiguous() or t.element_size() != size:
-                raise ValueError("a cache is dense, with 8-bit codes and float32 scales")
+        if not (K.element_size() == V.element_size() == 1 and K_scale.element_size() == V_scale.element_size() == 4
+                and K.is_contiguous() and V.is_contiguous() and K_scale.is_contiguous() and V_scale.is_contiguous()):
+            raise ValueError("a cache is dense, with 8-bit codes and float32 scales")
         self.K, self.V, self.K_scale, self.V_scale = K, V, K_scale, V_scale
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim = K.shape
-        self._c = _CacheStruct(K.data_ptr(), V.data_ptr(), K_scale.data_ptr(), V_scale.data_ptr(),
-                               self.num_pages, self.page_size, self.kv_heads, self.head_dim)
-        self._ref = ctypes.byref(self._c)
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self._c = _CACHE_STRUCT.pack(K.data_ptr(), V.data_ptr(), K_scale.data_ptr(), V_scale.data_ptr(),
+                                     self.num_pages, self.page_size, self.kv_heads, self.head_dim)
 
 
-def _token_pitch(t, name):
+def _token_pitch(shape, stride, name):
     """Elements from token to token of a (tokens, heads, head dim) tensor whose tokens are dense."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{name}: tokens x heads x head dim, each token dense")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _batch(page_table, kv_len, q_start):
-    """The pointers of a batch's page table, lengths and row starts."""
-    for t, name in ((page_table, "page_table"), (kv_len, "kv_len"), (q_start, "q_start")):
-        if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()):
-            raise ValueError(f"{name}: a dense int32 tensor")
-    batch = page_table.shape[0]
-    if page_table.dim() != 2 or kv_len.numel() != batch or (q_start is not None and q_start.numel() != batch + 1):
+    """A batch's size, its table's width, and the pointers of its page table, lengths and row starts."""
+    for t in (page_table, kv_len) if q_start is None else (page_table, kv_len, q_start):
+        if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+            raise ValueError("page_table, kv_len and q_start: dense int32 tensors")
+    shape = page_table.shape
+    if len(shape) != 2 or kv_len.numel() != shape[0] or (q_start is not None and q_start.numel() != shape[0] + 1):
         raise ValueError("page_table: batch x pages, kv_len: batch, q_start: batch + 1")
-    return _ptr(page_table), _ptr(kv_len), _ptr(q_start)
+    return (shape[0], shape[1], page_table.data_ptr(), kv_len.data_ptr(),
+            None if q_start is None else q_start.data_ptr())
 
 
 def mxgemm_cache_append(h, cache: Cache, page_table, kv_len, new_K, new_V, q_start=None, stream=None,
@@ -362,17 +361,19 @@ def mxgemm_cache_append(h, cache: Cache, page_table, kv_len, new_K, new_V, q_sta
     cache.  page_table: batch x pages int32; kv_len: lengths with the new
     tokens; q_start: batch + 1 row starts, None for one token each."""
     import torch
-    pitch = _token_pitch(new_K, "new_K")
-    if new_V.shape != new_K.shape or new_V.dtype != new_K.dtype or _token_pitch(new_V, "new_V") != pitch:
+    shape, stride, dtype = new_K.shape, new_K.stride(), new_K.dtype
+    pitch = _token_pitch(shape, stride, "new_K")
+    if new_V.shape != shape or new_V.dtype != dtype or (new_V.stride() != stride and
+                                                        _token_pitch(shape, new_V.stride(), "new_V") != pitch):
         raise ValueError("new_V is laid out as new_K is")
-    if new_K.shape[1:] != (cache.kv_heads, cache.head_dim):
+    if shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
         raise ValueError("new_K: tokens x kv heads x head dim")
-    if new_K.dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("new_K: float32 or bfloat16")
-    table, lens, starts = _batch(page_table, kv_len, q_start)
-    st = library().mxgemm_cache_append(
-        h, cache._ref, page_table.shape[0], table, page_table.shape[1], lens, starts, new_K.shape[0],
-        _ptr(new_K), _ptr(new_V), pitch, IN_BF16 if new_K.dtype == torch.bfloat16 else IN_F32, _stream(stream))
+    batch, width, table, lens, starts = _batch(page_table, kv_len, q_start)
+    st = library().mxgemm_cache_append(h, cache._c, batch, table, width, lens, starts, shape[0], new_K.data_ptr(),
+                                       new_V.data_ptr(), pitch, IN_BF16 if dtype is torch.bfloat16 else IN_F32,
+                                       _stream(stream))
     if check:
         _check(st, "mxgemm_cache_append")
     return st
@@ -386,19 +387,19 @@ def mxgemm_cache_attention(h, cache: Cache, page_table, kv_len, Q, O, q_start=No
     page_table, kv_len and q_start as for mxgemm_cache_append; scale defaults
     to 1 / sqrt(head dim); window = 0 is no window."""
     import torch
-    pitch = _token_pitch(Q, "Q")
-    if Q.dtype != torch.bfloat16 or O.dtype != torch.bfloat16 or O.shape != Q.shape or not O.is_contiguous():
+    shape = Q.shape
+    pitch = _token_pitch(shape, Q.stride(), "Q")
+    if Q.dtype is not torch.bfloat16 or O.dtype is not torch.bfloat16 or O.shape != shape or not O.is_contiguous():
         raise ValueError("Q and O: bfloat16 of one shape, O dense")
-    if Q.shape[2] != cache.head_dim:
+    if shape[2] != cache.head_dim:
         raise ValueError("Q: tokens x heads x head dim")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != Q.shape[:2] or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse: a dense float32 tensor, tokens x heads")
-    table, lens, starts = _batch(page_table, kv_len, q_start)
+    batch, width, table, lens, starts = _batch(page_table, kv_len, q_start)
     st = library().mxgemm_cache_attention(
-        h, cache._ref, page_table.shape[0], Q.shape[1], table, page_table.shape[1], lens, starts,
-        Q.shape[0], _ptr(Q), pitch,
-        cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
-        int(sinks), _ptr(O), _ptr(lse), _stream(stream))
+        h, cache._c, batch, shape[1], table, width, lens, starts, shape[0], Q.data_ptr(), pitch,
+        shape[2] ** -0.5 if scale is None else scale, 1 if causal else 0, window, sinks, O.data_ptr(),
+        None if lse is None else lse.data_ptr(), _stream(stream))
     if check:
         _check(st, "mxgemm_cache_attention")
     return st
