@@ -10,6 +10,7 @@
 
 #include "block128_kernel.cuh"
 #include "context.h"
+#include "launch.h"
 #include "mxgemm.h"
 #include "quantize128.cuh"
 
@@ -32,24 +33,23 @@ int launch_quantize128(const T *x, int64_t R, int64_t C, int block, uint8_t *cd,
     constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
     const int64_t grid = cdiv(blocks, 8 * 4 * kUnroll);
     if (grid >= kLim) return MXGEMM_ERR_INVALID_VALUE;
-    if (C % 128 == 0)
-      mxg::quantize128_rows_kernel<T, false, kUnroll><<<static_cast<unsigned>(grid), 256, 0, stream>>>(x, C, kb, blocks, cd, sc);
-    else
-      mxg::quantize128_rows_kernel<T, true, kUnroll><<<static_cast<unsigned>(grid), 256, 0, stream>>>(x, C, kb, blocks, cd, sc);
-  } else {
-    const int64_t pitch = cdiv(R, 16) * 16;
-    for (int64_t y = 0; y < rb; y += kGridY) {
-      const unsigned gy = static_cast<unsigned>(std::min(kGridY, rb - y));
-      const T *xr = x + y * 128 * C;
-      if (block == MXGEMM_BLOCK_COLS)
-        mxg::quantize128_cols_kernel<T><<<dim3(static_cast<unsigned>(cdiv(C, 64)), gy), 256, 0, stream>>>(
-            xr, R - y * 128, C, pitch, y * 128, rb, cd, sc + y);
-      else
-        mxg::quantize128_tiles_kernel<T><<<dim3(static_cast<unsigned>(kb), gy), 512, 0, stream>>>(
-            xr, R - y * 128, C, cd + y * 128 * C, sc + y * kb);
-    }
+    return mxg::launch(C % 128 == 0 ? mxg::quantize128_rows_kernel<T, false, kUnroll>
+                                    : mxg::quantize128_rows_kernel<T, true, kUnroll>,
+                       dim3(static_cast<unsigned>(grid)), 256, 0, 1, stream, x, C, kb, blocks, cd, sc);
   }
-  return cudaGetLastError() == cudaSuccess ? MXGEMM_OK : MXGEMM_ERR_CUDA;
+  const int64_t pitch = cdiv(R, 16) * 16;
+  for (int64_t y = 0; y < rb; y += kGridY) {
+    const unsigned gy = static_cast<unsigned>(std::min(kGridY, rb - y));
+    const T *xr = x + y * 128 * C;
+    const int st =
+        block == MXGEMM_BLOCK_COLS
+            ? mxg::launch(mxg::quantize128_cols_kernel<T>, dim3(static_cast<unsigned>(cdiv(C, 64)), gy), 256, 0, 1,
+                          stream, xr, R - y * 128, C, pitch, y * 128, rb, cd, sc + y)
+            : mxg::launch(mxg::quantize128_tiles_kernel<T>, dim3(static_cast<unsigned>(kb), gy), 512, 0, 1, stream, xr,
+                          R - y * 128, C, cd + y * 128 * C, sc + y * kb);
+    if (st != MXGEMM_OK) return st;
+  }
+  return MXGEMM_OK;
 }
 
 // 2-D tensor map of bytes (or of C's elements), 128-byte swizzle: dims
@@ -65,34 +65,6 @@ int encode(const mxg::HandleView &v, CUtensorMap *tm, CUtensorMapDataType dt, co
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? MXGEMM_OK
              : MXGEMM_ERR_CUDA;
-}
-
-// A launch with clusters of `cluster` CTAs along x.
-template <typename... Params, typename... Args>
-int launch_cluster(void (*kern)(Params...), int grid, int threads, int smem, int cluster, cudaStream_t stream,
-                   const Args &...args) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-    cudaGetLastError();
-    return MXGEMM_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return MXGEMM_ERR_CUDA;
-  }
-  return MXGEMM_OK;
 }
 
 // M > 128: CTA pairs on 256 x 256 tiles, one pair per two SMs.
@@ -118,8 +90,8 @@ int run_pair(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const 
   switch (variant) {
 #define MXG_PAIR(V)                                                                                     \
   case V:                                                                                               \
-    return launch_cluster(mxg::b128_pair_kernel<V>, grid, mxg::PairCfg<V>::THREADS,                     \
-                          mxg::PairCfg<V>::SMEM_BYTES, 2, stream, tA, tB, tC, p);
+    return mxg::launch(mxg::b128_pair_kernel<V>, dim3(grid), mxg::PairCfg<V>::THREADS,                  \
+                       mxg::PairCfg<V>::SMEM_BYTES, 2, stream, tA, tB, tC, p);
     MXG_PAIR(0)
     MXG_PAIR(1)
     MXG_PAIR(2)
@@ -157,8 +129,8 @@ int run_skinny_nt(const mxg::HandleView &v, mxg::B128Params &p, const void *A, c
   switch (variant) {
 #define MXG_SKINNY(V)                                                                              \
   case V:                                                                                          \
-    return launch_cluster(mxg::b128_skinny_kernel<NT, V>, grid, S::THREADS, S::SMEM_BYTES,         \
-                          p.splits, stream, tB, tA, p);
+    return mxg::launch(mxg::b128_skinny_kernel<NT, V>, dim3(grid), S::THREADS, S::SMEM_BYTES,      \
+                       p.splits, stream, tB, tA, p);
     MXG_SKINNY(0)
     MXG_SKINNY(1)
     MXG_SKINNY(2)

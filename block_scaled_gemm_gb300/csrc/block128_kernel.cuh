@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();  // the next kernel's set-up may begin
+  griddep_wait();               // no global memory before the kernel before has ended
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
   const WaitCtl wn{p.status, never, p.timeout_ns};
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
@@ -618,6 +620,8 @@ __global__ void __launch_bounds__(SkinnyCfg<NT>::THREADS, 1)
       fence_proxy_async_smem();
     }
     __syncwarp();
+    griddep_launch_dependents();  // the next kernel's set-up may begin
+    griddep_wait();               // no global memory before the kernel before has ended
     if (lane < n_early) load_step(lane, k_beg + lane);
   }
   if (warp == 1) {
@@ -628,6 +632,7 @@ __global__ void __launch_bounds__(SkinnyCfg<NT>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_wait();
 
   float acc[NT];  // epilogue: this lane's column of C, one sum per row
   bool have = false;

@@ -12,6 +12,7 @@
 #include "cache_attention.cuh"
 #include "cache_prompt.cuh"
 #include "context.h"
+#include "launch.h"
 #include "mxgemm.h"
 
 namespace {
@@ -64,27 +65,22 @@ int cache_args(const mxg::HandleView &v, const mxgemm_cache_t *c, int64_t batch,
   return MXGEMM_OK;
 }
 
-int launched(const mxg::HandleView &v) {
-  if (cudaGetLastError() != cudaSuccess) return MXGEMM_ERR_CUDA;
-  ++*v.launches;
-  return MXGEMM_OK;
-}
-
 // Passes over a page's rows: of 128 threads, eight values each.
 template <typename T, int D, int LG>
-void launch_append_page(const mxg::AppendParams &p, dim3 grid, cudaStream_t stream) {
+int launch_append_page(const mxg::AppendParams &p, dim3 grid, cudaStream_t stream) {
   constexpr int kRows = 128 / (D / 8), kAll = ((1 << LG) + kRows - 1) / kRows;
-  if (p.b.q_start) mxg::cache_append_kernel<T, D, LG, kAll><<<grid, 128, 0, stream>>>(p);
-  else mxg::cache_append_kernel<T, D, LG, 1><<<grid, 128, 0, stream>>>(p);  // one token
+  return mxg::launch(p.b.q_start ? mxg::cache_append_kernel<T, D, LG, kAll>
+                                 : mxg::cache_append_kernel<T, D, LG, 1>,  // one token
+                     grid, 128, 0, 1, stream, p);
 }
 
 template <typename T, int D>
-void launch_append(const mxg::AppendParams &p, dim3 grid, cudaStream_t stream) {
+int launch_append(const mxg::AppendParams &p, dim3 grid, cudaStream_t stream) {
   switch (p.c.page_log2) {
-    case 4: launch_append_page<T, D, 4>(p, grid, stream); break;
-    case 5: launch_append_page<T, D, 5>(p, grid, stream); break;
-    case 6: launch_append_page<T, D, 6>(p, grid, stream); break;
-    default: launch_append_page<T, D, 7>(p, grid, stream); break;
+    case 4: return launch_append_page<T, D, 4>(p, grid, stream);
+    case 5: return launch_append_page<T, D, 5>(p, grid, stream);
+    case 6: return launch_append_page<T, D, 6>(p, grid, stream);
+    default: return launch_append_page<T, D, 7>(p, grid, stream);
   }
 }
 
@@ -123,13 +119,8 @@ int run_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t ctas, cudaS
   using S = mxg::PromptCfg<D>;
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
-  if (cudaFuncSetAttribute(mxg::cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           S::SMEM_BYTES) != cudaSuccess) {
-    cudaGetLastError();
-    return MXGEMM_ERR_CUDA;
-  }
-  mxg::cache_prompt_kernel<D><<<static_cast<unsigned>(ctas), S::THREADS, S::SMEM_BYTES, stream>>>(tK, tV, p);
-  return MXGEMM_OK;
+  return mxg::launch(mxg::cache_prompt_kernel<D>, dim3(static_cast<unsigned>(ctas)), S::THREADS, S::SMEM_BYTES, 1, stream,
+                     tK, tV, p);
 }
 
 template <int D, int NT>
@@ -142,13 +133,8 @@ int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   p.partials = reinterpret_cast<float *>(ws);
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, std::min(p.c.page_size, 32), true, &tK, &tV)) return st;
-  if (cudaFuncSetAttribute(mxg::cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           S::SMEM_BYTES) != cudaSuccess) {
-    cudaGetLastError();
-    return MXGEMM_ERR_CUDA;
-  }
-  mxg::cache_decode_kernel<D, NT><<<grid, 128, S::SMEM_BYTES, stream>>>(tK, tV, p);
-  return MXGEMM_OK;
+  return mxg::launch(mxg::cache_decode_kernel<D, NT>, dim3(static_cast<unsigned>(grid)), 128, S::SMEM_BYTES, 1, stream, tK,
+                     tV, p);
 }
 
 }  // namespace
@@ -179,14 +165,12 @@ extern "C" int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cach
   const int64_t items = q_start ? (tokens >> p.c.page_log2) + 2 * batch : batch;
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(cache->kv_heads), 2);
   const bool f32 = x_dtype == MXGEMM_IN_F32;
-  if (cache->head_dim == 128) {
-    if (f32) launch_append<float, 128>(p, grid, stream);
-    else launch_append<__nv_bfloat16, 128>(p, grid, stream);
-  } else {
-    if (f32) launch_append<float, 64>(p, grid, stream);
-    else launch_append<__nv_bfloat16, 64>(p, grid, stream);
-  }
-  return launched(v);
+  const int st = cache->head_dim == 128
+                     ? (f32 ? launch_append<float, 128>(p, grid, stream) : launch_append<__nv_bfloat16, 128>(p, grid, stream))
+                     : (f32 ? launch_append<float, 64>(p, grid, stream) : launch_append<__nv_bfloat16, 64>(p, grid, stream));
+  if (st != MXGEMM_OK) return st;
+  ++*v.launches;
+  return MXGEMM_OK;
 }
 
 extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
@@ -237,5 +221,6 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
                                 : (two ? run_decode<64, 2>(h, v, p, stream) : run_decode<64, 1>(h, v, p, stream));
   }
   if (st != MXGEMM_OK) return st;
-  return launched(v);
+  ++*v.launches;
+  return MXGEMM_OK;
 }

@@ -38,6 +38,8 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
   // threads of a row, rows of a pass
   constexpr int lg = LG, ps = 1 << LG, kPer = D / 8, kRows = 128 / kPer;
   __shared__ float part[4];
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t item = blockIdx.x;
   const int head = blockIdx.y;
   // (one token each: one page each)

@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     fence_proxy_async_smem();
   }
   __syncwarp();
+  griddep_launch_dependents();
+  griddep_wait();
   // All tiles (each warp counts for itself, 32 sequences at a time), and this
   // CTA's range of them: ranges of four tiles at least.
   const int64_t mine = sequence_tiles(p, ROWS, lane), upto = warp_prefix(mine);  // the first 32 sequences

@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   uint8_t *sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  griddep_launch_dependents();
+  griddep_wait();
   // ------------------------------------------------------------ this CTA's rows
   // Sequence b's row tiles are numbered from f(b) = floor(q_start group / 256) + b
   // (room for all of them); the last tiles, which see most keys, come first.

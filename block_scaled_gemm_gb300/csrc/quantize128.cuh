@@ -56,6 +56,8 @@ template <typename T, bool RAGGED, int UNROLL>
 __global__ void __launch_bounds__(256)
     quantize128_rows_kernel(const T *__restrict__ X, int64_t C, int64_t kb, int64_t blocks,
                             uint8_t *__restrict__ codes, float *__restrict__ scales) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t first = warp * (4 * UNROLL) + (lane >> 3);
@@ -105,6 +107,8 @@ __global__ void __launch_bounds__(256)
   constexpr int kPitch = 33;  // words of a column (odd: the transposing accesses are spread over the banks)
   __shared__ float tops[8][64];
   __shared__ uint32_t tile[64 * kPitch];
+  griddep_launch_dependents();
+  griddep_wait();
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, warp = threadIdx.x >> 5;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128, c0 = static_cast<int64_t>(blockIdx.x) * 64;
   Eight<T> v[4];
@@ -159,6 +163,8 @@ __global__ void __launch_bounds__(512)
     quantize128_tiles_kernel(const T *__restrict__ X, int64_t R, int64_t C, uint8_t *__restrict__ codes,
                              float *__restrict__ scales) {
   __shared__ float part[16];
+  griddep_launch_dependents();
+  griddep_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128 + ty, c = static_cast<int64_t>(blockIdx.x) * 128 + 8 * tx;
   Eight<T> v[4];
