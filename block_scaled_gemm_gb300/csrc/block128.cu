@@ -67,8 +67,27 @@ int encode(const mxg::HandleView &v, CUtensorMap *tm, CUtensorMapDataType dt, co
              : MXGEMM_ERR_CUDA;
 }
 
+// Parts of K for each of `rem` tiles on `pairs` pairs, in K blocks' time: a part
+// costs its own blocks; splitting, about eight more (sums written and awaited)
+// and four for each part that the first one adds (with half of that, 512 x
+// 4096 x 2048 took 13.8 us instead of 12.0).  Whole against split: 256 x 4096
+// x 8192 29.5 and 22.1 us, 5000 x 4112 x 8192 133 and 127 us, 4096 x 4096 x
+// 5008 74.8 and 74.3 us.
+int tail_split(int64_t rem, int64_t pairs, int64_t kb) {
+  int best = 1;
+  int64_t cost = kb;
+  for (int64_t s = 2; s * rem <= pairs && s <= kb; ++s) {
+    const int64_t c = cdiv(kb, s) + 4 + 4 * s;
+    if (c < cost) {
+      cost = c;
+      best = static_cast<int>(s);
+    }
+  }
+  return best;
+}
+
 // M > 128: CTA pairs on 256 x 256 tiles, one pair per two SMs.
-int run_pair(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, bool bf16,
+int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, bool bf16,
              int variant, cudaStream_t stream) {
   CUtensorMap tA, tB, tC;
   std::memset(&tC, 0, sizeof(tC));
@@ -77,8 +96,22 @@ int run_pair(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const 
   p.m_tiles = static_cast<int>(cdiv(p.M, 256));
   p.n_tiles = static_cast<int>(cdiv(p.N, 256));
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  if (tiles >= kLim) return MXGEMM_ERR_INVALID_VALUE;
-  p.tiles = static_cast<int>(tiles);
+  if (tiles >= kLim - 65536) return MXGEMM_ERR_INVALID_VALUE;
+  const int64_t pairs = v.sm_count / 2, rem = tiles % pairs;
+  p.dp_tiles = static_cast<int>(tiles - rem);
+  p.split = rem ? tail_split(rem, pairs, p.kb) : 1;
+  p.tail_items = static_cast<int>(rem) * p.split;
+  if (p.split > 1) {
+    using P = mxg::PairCfg<0>;
+    uint8_t *ws = nullptr;
+    if (int st = mxg::handle_workspace(h, static_cast<size_t>(p.tail_items) * 2 * P::EPI_WARPS * 32 * 128 * sizeof(float),
+                                       stream, &ws))
+      return st;
+    p.partials = reinterpret_cast<float *>(ws);
+    p.flags = v.flags;
+    static_assert(mxg::kFlags >= 1024 * 2 * P::EPI_WARPS, "a flag for each tail item's warps");
+    if (p.tail_items > 1024) return MXGEMM_ERR_UNSUPPORTED_DEVICE;  // (above 2048 SMs)
+  }
   p.tma_store = !p.use_acc && static_cast<int64_t>(p.N) * eb % 16 == 0;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (encode(v, &tA, u8, A, p.K, p.M, p.K, 128, 128) ||
@@ -86,7 +119,7 @@ int run_pair(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const 
       (p.tma_store && encode(v, &tC, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                              p.C, p.N, p.M, static_cast<int64_t>(p.N) * eb, bf16 ? 64 : 32, 32)))
     return MXGEMM_ERR_CUDA;
-  const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, v.sm_count / 2));
+  const int grid = 2 * static_cast<int>(p.dp_tiles > 0 ? pairs : p.tail_items);
   switch (variant) {
 #define MXG_PAIR(V)                                                                                     \
   case V:                                                                                               \
@@ -238,7 +271,7 @@ extern "C" int mxgemm_run_block128(mxgemm_handle_t h, int64_t M, int64_t N, int6
     return MXGEMM_ERR_CUDA;
   }
   const int st = M <= 128 ? run_skinny(v, p, A, B, nk, variant, stream)
-                          : run_pair(v, p, A, B, nk, bf16, variant, stream);
+                          : run_pair(h, v, p, A, B, nk, bf16, variant, stream);
   if (st != MXGEMM_OK) return st;
   ++*v.launches;
   if (v.prof_after && cudaEventRecord(v.prof_after, stream) != cudaSuccess) {

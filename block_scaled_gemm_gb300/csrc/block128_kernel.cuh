@@ -45,7 +45,12 @@ struct B128Params {
   unsigned long long timeout_ns;
   int stall_producer;
   // pairs
-  int m_tiles, n_tiles, tiles;
+  int m_tiles, n_tiles;
+  // whole tiles [0, dp_tiles), a multiple of the grid's pairs, then the last
+  // tail_items / split tiles with their K cut into `split` parts, one pair each
+  int dp_tiles, split, tail_items;
+  float *partials;  // tail item x CTA of the pair x epilogue warp: 32 x 128 sums
+  unsigned *flags;  // the same, one word each: the sums are there (0 between launches)
   int tma_store;  // C's rows are multiples of 16 bytes and nothing is added
   // skinny
   int nm;      // M rounded up to 16
@@ -135,6 +140,28 @@ struct PairCfg {
   static_assert(OFF_SC % 16 == 0 && SLOT_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
+// Work i of pair `unit`: a tile and its K blocks [kb, ke).  The tiles that do not
+// fill the last wave (all of them where there are fewer than pairs) are cut
+// along K, and the first part's pair adds the others' sums in order.
+struct PairWork {
+  int tile, kb, ke, part, item;
+};
+__device__ __forceinline__ bool pair_work(const B128Params &p, int unit, int units, int i, PairWork &w) {
+  const int t = unit + i * units;
+  w.part = 0;
+  w.kb = 0;
+  w.ke = p.kb;
+  w.tile = t;
+  w.item = t - p.dp_tiles;
+  if (w.item < 0) return true;
+  if (w.item >= p.tail_items) return false;
+  w.tile = p.dp_tiles + w.item / p.split;
+  w.part = w.item % p.split;
+  w.kb = static_cast<int>(static_cast<long long>(w.part) * p.kb / p.split);
+  w.ke = static_cast<int>(static_cast<long long>(w.part + 1) * p.kb / p.split);
+  return true;
+}
+
 // Warp roles (per CTA, 384 threads): warp 0 loads, warp 1 of the pair's first
 // CTA issues the MMAs (and allocates TMEM in both), warp 2 brings the scales
 // (with a scale for each column, those by warp 3), warps 4-11 are the
@@ -211,11 +238,12 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     uint32_t ph = 0;
     long long issued = 0;
     bool ok = !p.stall_producer;
-    for (int t = unit; ok && t < p.tiles; t += units) {
+    PairWork w;
+    for (int i = 0; ok && pair_work(p, unit, units, i, w); ++i) {
       int mt, nt;
-      tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
+      tile_coords(w.tile, p.m_tiles, p.n_tiles, mt, nt);
       const int row = mt * 256 + 128 * static_cast<int>(rank), col = nt * 256 + 128 * static_cast<int>(rank);
-      for (int ks = 0; ks < kb; ++ks) {
+      for (int ks = w.kb; ks < w.ke; ++ks) {
         if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * st, ph ^ 1u, wc, 0x01 | (st << 8)))) {
           ok = false;
           break;
@@ -265,8 +293,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         const uint64_t dA = smem_desc(base + C::OFF_A, 0, 1024, 2);
         const uint64_t dB = smem_desc(base + C::OFF_B, kKM ? 0 : 16384, 1024, 2);
         constexpr uint32_t kBStep = (kKM ? 32 : 4096) >> 4;
-        for (int t = unit; ok && t < p.tiles; t += units) {
-          for (int ks = 0; ks < kb; ++ks, ++it) {
+        PairWork w;
+        for (int i = 0; ok && pair_work(p, unit, units, i, w); ++i) {
+          for (int ks = w.kb; ks < w.ke; ++ks, ++it) {
             const uint32_t buf = it & 1u;
             ok = wait_phase<false>(bar_full + 8 * st, ph, wc, 0x03 | (st << 8));
             if (!ok) break;
@@ -297,11 +326,12 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     const bool cols = warp == 3;  // the columns' scales, else the rows'
     uint32_t n = 0;               // groups of eight K blocks so far
     bool ok = true;
-    for (int t = unit; ok && t < p.tiles; t += units) {
+    PairWork w;
+    for (int i = 0; ok && pair_work(p, unit, units, i, w); ++i) {
       int mt, nt;
-      tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
+      tile_coords(w.tile, p.m_tiles, p.n_tiles, mt, nt);
       const int row0 = mt * 256 + 128 * static_cast<int>(rank);
-      for (int k0 = 0; k0 < kb; k0 += C::KB, ++n) {
+      for (int k0 = w.kb; k0 < w.ke; k0 += C::KB, ++n) {
         const uint32_t slot = n & 1u;
         ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_empty + 8 * slot, ((n >> 1) & 1u) ^ 1u, wc, 0x09));
         if (!ok) break;
@@ -347,9 +377,10 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     uint32_t empty_at = mapa_shared(bar_acc_empty, 0);  // of the pair's first CTA
     uint32_t n = 0;  // groups of eight K blocks so far
     bool ok = true;
-    for (int t = unit; ok && t < p.tiles; t += units) {
+    PairWork pw;
+    for (int i = 0; ok && pair_work(p, unit, units, i, pw); ++i) {
       int mt, nt;
-      tile_coords(t, p.m_tiles, p.n_tiles, mt, nt);
+      tile_coords(pw.tile, p.m_tiles, p.n_tiles, mt, nt);
       const int row0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const int col0 = nt * 256 + 128 * half;
       float acc[128];
@@ -374,8 +405,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));
       if (!ok) break;
       scale_at(0);
+      const int steps = pw.ke - pw.kb;
 #pragma unroll 1
-      for (int ks = 0; ks < kb; ++ks) {
+      for (int ks = 0; ks < steps; ++ks) {
         ok = warp_wait(full_at, full_ph, wc, 0x05);
         if (!ok) break;
         tc_fence_after();
@@ -427,17 +459,47 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         full_ph ^= (full_at >> 3) & 1u;
         full_at ^= 8u;
         empty_at ^= 8u;
-        if (ks + 1 == kb || ((ks + 1) & (C::KB - 1)) == 0) {  // the group's scales have been read
+        if (ks + 1 == steps || ((ks + 1) & (C::KB - 1)) == 0) {  // the group's scales have been read
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_sc_empty + 8 * (n & 1u));
           ++n;
-          if (ks + 1 == kb) break;
+          if (ks + 1 == steps) break;
           ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));
           if (!ok) break;
         }
         scale_at(ks + 1);
       }
       if (!ok) break;
+      if (p.split > 1 && pw.item >= 0) {
+        // 16-byte pieces of a thread's sums, 32 lanes side by side
+        auto slot = [&](int item) { return (item * 2 + static_cast<int>(rank)) * C::EPI_WARPS + w; };
+        if (pw.part > 0) {
+          float4 *to = reinterpret_cast<float4 *>(p.partials) + static_cast<int64_t>(slot(pw.item)) * 1024 + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) to[32 * j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p.flags + slot(pw.item)), "r"(1u) : "memory");
+          continue;
+        }
+        for (int r = 1; ok && r < p.split; ++r) {
+          unsigned *flag = p.flags + slot(pw.item + r);
+          ok = wait_flags(flag, 1, 1u, wc, 0x06);
+          if (!ok) break;
+          const float4 *from = reinterpret_cast<const float4 *>(p.partials) + static_cast<int64_t>(slot(pw.item + r)) * 1024 + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float4 x = __ldcg(from + 32 * j);
+            acc[4 * j] += x.x;
+            acc[4 * j + 1] += x.y;
+            acc[4 * j + 2] += x.z;
+            acc[4 * j + 3] += x.w;
+          }
+          __syncwarp();
+          if (lane == 0) *flag = 0;  // for the next launch
+        }
+        if (!ok) break;
+      }
       // C: rows row0 .. +31, columns col0 .. +127, in pieces of 128 bytes a
       // row through this warp's 4 KB (16-byte units swizzled by the row)
       if (row0 >= p.M || col0 >= p.N) continue;

@@ -86,6 +86,18 @@ def test_product(handles, m, n, k, nk, b_block):
         check(run(handles[nk], nk, a, sa, b, sb, b_block, out), ref, mag, out)
 
 
+@pytest.mark.parametrize("b_block", [128, 1])
+def test_whole_and_split_tiles_together(handles, b_block):
+    """99 tiles: a full wave of whole ones, and 23 whose K is split over the idle
+    pairs, added in a fixed order."""
+    m, n, k = 2600, 2300, 4096
+    a, sa, b, sb = operands(m, n, k, b_block, 12)
+    ref, mag = plain64.product(plain64.value(a), sa, plain64.value(b), sb, b_block)
+    C = run(handles[True], True, a, sa, b, sb, b_block)
+    check(C, ref, mag, "f32")
+    assert torch.equal(C, run(handles[True], True, a, sa, b, sb, b_block))
+
+
 @pytest.mark.parametrize("m,n,k", [(5, 300, 272), (300, 300, 272), (300, 257, 4096)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_accumulates(handles, m, n, k, out):
