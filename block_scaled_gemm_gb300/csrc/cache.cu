@@ -113,13 +113,32 @@ int encode_cache(const mxg::HandleView &v, const mxg::CacheView &c, int d, int b
   return MXGEMM_OK;
 }
 
-// Many query rows: one CTA for each 256 of a sequence and key/value head.
+// Many query rows: one CTA for each 256 of a sequence and key/value head, or, of
+// few such row tiles, up to 16 for each (44 row tiles of 61102 keys: 816 ->
+// 296 us).  The grid has room for every split of the rows into sequences;
+// the count of row tiles that decides is that of equal ones.
+int64_t equal_row_tiles(const mxg::AttnParams &p) {
+  constexpr int64_t kRows = mxg::PromptCfg<128>::ROWS;
+  return (p.b.tokens * p.group / p.b.batch + kRows - 1) / kRows * p.b.batch * p.c.kv_heads;
+}
+
 template <int D>
-int run_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t ctas, cudaStream_t stream) {
+int run_prompt(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::PromptCfg<D>;
+  const int64_t rows = p.b.tokens * p.group;
+  const int64_t items = (rows / S::ROWS + p.b.batch) * p.c.kv_heads;
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, v.sm_count / equal_row_tiles(p))));
+  if (items > mxg::kCounters) p.parts = 1;
+  if (items * p.parts >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+  if (p.parts > 1) {
+    uint8_t *ws = nullptr;
+    if (int st = mxg::handle_workspace(h, static_cast<size_t>(items) * p.parts * S::PARTIAL * sizeof(float), stream, &ws))
+      return st;
+    p.partials = reinterpret_cast<float *>(ws);
+  }
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
-  return mxg::launch(mxg::cache_prompt_kernel<D>, dim3(static_cast<unsigned>(ctas)), S::THREADS, S::SMEM_BYTES, 1, stream,
+  return mxg::launch(mxg::cache_prompt_kernel<D>, dim3(static_cast<unsigned>(items * p.parts)), S::THREADS, S::SMEM_BYTES, 1, stream,
                      tK, tV, p);
 }
 
@@ -209,12 +228,15 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   p.counters = v.counters;
   p.timeout_ns = v.timeout_ns;
   // Rows (query tokens x heads of a group) of an ordinary sequence decide: many
-  // go to the tensor cores by 256, where they make CTAs enough; few to the
-  // kernel whose items are 8 or 16 rows.
-  const int64_t ctas = (tokens * p.group / mxg::PromptCfg<128>::ROWS + batch) * p.c.kv_heads;
+  // go to the tensor cores by 256, few to the kernel whose items are 8 or 16.
+  // At 64 rows both take the same time on 32 row tiles of 8192 keys (70 us); on
+  // 128 the first takes 106 us and the second 219, and with more than 16 rows
+  // the second reads the keys again; but it cuts them for all SMs where the
+  // first's row tiles times 16 do not fill half of them.
   int st;
-  if (tokens * p.group >= 64 * batch && ctas >= 16 && ctas < kLim) {
-    st = cache->head_dim == 128 ? run_prompt<128>(v, p, ctas, stream) : run_prompt<64>(v, p, ctas, stream);
+  const int64_t rows = tokens * p.group;
+  if (rows >= 64 * batch || (rows > 16 * batch && equal_row_tiles(p) * 32 >= v.sm_count)) {
+    st = cache->head_dim == 128 ? run_prompt<128>(h, v, p, stream) : run_prompt<64>(h, v, p, stream);
   } else {
     const bool two = tokens * p.group > 8 * batch;
     st = cache->head_dim == 128 ? (two ? run_decode<128, 2>(h, v, p, stream) : run_decode<128, 1>(h, v, p, stream))

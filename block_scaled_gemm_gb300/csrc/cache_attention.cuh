@@ -42,8 +42,9 @@ struct AttnParams {
   int64_t window, sinks;
   __nv_bfloat16 *O;
   float *lse;
-  float *partials;     // two slots per CTA
-  unsigned *counters;  // one per CTA, zero between launches
+  float *partials;     // of split items: two slots per CTA (prompts: one for each part)
+  unsigned *counters;  // arrivals at split items, zero between launches
+  int parts;           // prompts: CTAs that a row tile's keys may be cut for
   unsigned long long timeout_ns;
 };
 

@@ -17,6 +17,10 @@
 // (D = 128); while they work on one Q tile, the other one's softmax runs.  The
 // running maximum is moved, and O in TMEM rescaled, only when it grows by 2^8.
 //
+// Where the row tiles are fewer than the SMs, each one's keys are cut into parts
+// for as many CTAs; they leave FP32 partials in the workspace, and the one that
+// arrives last adds them in order.
+//
 // Warps (512 threads): 0 TMA loads of the pages' codes, and the scales;
 // 1 MMAs; 4-7 convert codes to FP16 in the MMA's layout (128-byte swizzle);
 // 8-11 and 12-15 the softmax of the two Q tiles.
@@ -43,6 +47,7 @@ struct PromptCfg {
   static constexpr int NUM_BARS = 4 + 2 * 4 + 2 + 4 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int PARTIAL = ROWS * (D + 2);  // floats of a partial: O by 4 d and row, m, l
   static constexpr int THREADS = 512;
   // registers a thread: 128 at launch, then of the four groups of four warps
   // (56 + 88 + 2 x 184 = 4 x 128: the block's own)
@@ -106,8 +111,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   // ------------------------------------------------------------ this CTA's rows
   // Sequence b's row tiles are numbered from f(b) = floor(q_start group / 256) + b
   // (room for all of them); the last tiles, which see most keys, come first.
-  const int h = static_cast<int>(blockIdx.x % p.c.kv_heads);
-  const int64_t id = static_cast<int64_t>(gridDim.x) / p.c.kv_heads - 1 - blockIdx.x / p.c.kv_heads;
+  const int item = static_cast<int>(blockIdx.x / p.parts);
+  const int h = static_cast<int>(item % p.c.kv_heads);
+  const int64_t id = static_cast<int64_t>(gridDim.x) / p.parts / p.c.kv_heads - 1 - item / p.c.kv_heads;
   auto f = [&](int b) -> int64_t {
     const int64_t q = p.b.q_start ? p.b.q_start[b] : b;
     return q * p.group / S::ROWS + b;
@@ -127,8 +133,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const int win_lo = p.window > 0 ? static_cast<int>(min(max(static_cast<int64_t>(0), pos_first - p.window + 1), static_cast<int64_t>(end))) : 0;
   const int lo = win_lo >> 7;
   const int ns = static_cast<int>(min((min(p.sinks, static_cast<int64_t>(win_lo)) + 127) >> 7, static_cast<int64_t>(lo)));
-  const int tiles = max(1, ns + ((end + 127) >> 7) - lo);
-  auto tile_key = [&](int j) { return (j < ns ? j : lo + j - ns) * 128; };
+  const int all_tiles = max(1, ns + ((end + 127) >> 7) - lo);
+  // this CTA's part of them: four at least
+  const int parts = min(p.parts, max(1, all_tiles >> 2)), part = static_cast<int>(blockIdx.x % p.parts);
+  if (part >= parts) return;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(part) * all_tiles / parts);
+  const int tiles = static_cast<int>(static_cast<int64_t>(part + 1) * all_tiles / parts) - tile0;
+  auto tile_key = [&](int j) { return (j + tile0 < ns ? j + tile0 : lo + j + tile0 - ns) * 128; };
 
   const uint32_t bars = base + S::OFF_BAR;
   const uint32_t k8_full = bars, v8_full = bars + 8, k8_empty = bars + 16, v8_empty = bars + 24;
@@ -482,12 +493,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         tc_fence_after();
         const float k = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;
+        float *slot = p.partials + (static_cast<int64_t>(item) * p.parts + part) * S::PARTIAL;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(to + 32 * c, o);
           tmem_ld_done(o);
-          if (live) {
+          if (parts > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4 *>(slot)[(8 * c + e) * S::ROWS + r] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (live) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t x[4];
@@ -501,9 +517,67 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             }
           }
         }
-        if (live && p.lse)
+        if (parts > 1) {
+          slot[S::ROWS * D + r] = m;
+          slot[S::ROWS * D + S::ROWS + r] = l;
+        } else if (live && p.lse) {
           p.lse[static_cast<int64_t>(s.first + tok) * p.heads + head] =
               l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994530942f;
+        }
+      }
+    }
+    if (parts > 1) {
+      // (every softmax warp comes here: all their waits are bounded)
+      __threadfence();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (threadIdx.x == 256) *tmem_slot = atomicAdd(p.counters + item, 1u) == static_cast<unsigned>(parts - 1) ? 1u : 0u;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (*reinterpret_cast<volatile uint32_t *>(tmem_slot)) {
+        if (threadIdx.x == 256) p.counters[item] = 0;  // for the next launch
+        __threadfence();
+        const float *first = p.partials + static_cast<int64_t>(item) * p.parts * S::PARTIAL;
+        if (r < rows) {
+          const int tok = (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
+          float top = -INFINITY, sum = 0.f;
+          for (int c = 0; c < parts; ++c) top = fmaxf(top, __ldcg(first + c * S::PARTIAL + S::ROWS * D + r));
+          for (int c = 0; c < parts; ++c) {
+            const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
+            if (mc != -INFINITY) sum = fmaf(__ldcg(first + c * S::PARTIAL + S::ROWS * D + S::ROWS + r), ex2(mc - top), sum);
+          }
+          const float k = sum == 0.f ? 0.f : 1.f / sum;
+          __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float4 a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int c = 0; c < parts; ++c) {
+              const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
+              const float f = mc == -INFINITY ? 0.f : ex2(mc - top) * k;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(first + c * S::PARTIAL) + (d / 4 + e) * S::ROWS + r);
+                a[e].x = fmaf(x.x, f, a[e].x);
+                a[e].y = fmaf(x.y, f, a[e].y);
+                a[e].z = fmaf(x.z, f, a[e].z);
+                a[e].w = fmaf(x.w, f, a[e].w);
+              }
+            }
+            uint32_t x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(a[e].x, a[e].y), z = __floats2bfloat162_rn(a[e].z, a[e].w);
+              x[2 * e] = *reinterpret_cast<const uint32_t *>(&y);
+              x[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&z);
+            }
+            *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4 *>(dst + d + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+          if (p.lse)
+            p.lse[static_cast<int64_t>(s.first + tok) * p.heads + head] =
+                sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.69314718055994530942f;
+        }
       }
     }
   }

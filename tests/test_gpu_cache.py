@@ -142,6 +142,8 @@ PROMPTS = [  # as PROMPT, with rows enough for whole tiles of the tensor cores
     ([300, 129], [130, 129], 8, 8, 128, 64), ([1100], [1100], 4, 4, 128, 64), ([257, 700, 500], [129, 300, 333], 6, 2, 64, 16),
     ([900, 64, 2], [300, 64, 2], 8, 7, 128, 32), ([513, 512, 511], [513, 200, 511], 8, 1, 128, 128), ([400], [257], 16, 3, 64, 128),
     ([0, 1500, 40], [9, 700, 31], 8, 4, 128, 16),
+    # few row tiles: their keys are cut into parts
+    ([5000], [70], 1, 1, 128, 64), ([3001, 0, 129], [40, 2, 100], 1, 8, 64, 32), ([2500, 2600], [64, 1], 2, 4, 128, 128),
 ]
 
 
