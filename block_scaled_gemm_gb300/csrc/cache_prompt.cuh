@@ -17,6 +17,13 @@
 // (D = 128); while they work on one Q tile, the other one's softmax runs.  The
 // running maximum is moved, and O in TMEM rescaled, only when it grows by 2^8.
 //
+// Measured: 2 x 2048 tokens (the second 1741) over 8190 (5733) keys, 32/8 heads of
+// 128: 334 us, 1.14 PFLOP/s, 0.59 of the measured FP16 rate; a key tile takes about
+// 3250 cycles where the four products alone take 2048 and shared memory's traffic
+// 2560.  A Q tile's chain (softmax, P V, the next Q K^T into the same columns)
+// is what is left.  Half steps of 64 keys with two S a Q tile shorten the chain but
+// read Q twice (409 us); two threads a row with 16 softmax warps took 410 us.
+//
 // Where the row tiles are fewer than the SMs, each one's keys are cut into parts
 // for as many CTAs; they leave FP32 partials in the workspace, and the one that
 // arrives last adds them in order.

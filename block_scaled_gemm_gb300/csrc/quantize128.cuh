@@ -5,6 +5,10 @@
 //   top = max(max |x|, 2^-100), scale = top / 448,
 //   code = E4M3(clamp(x * (448 / top), +-448)), round to nearest even
 //
+// Measured: 8192 x 8192 BF16 by rows 31.1 us (6.5 TB/s, 0.96 of the measured copy
+// rate; with a warp for each block, two loads of 8 bytes a lane, 79 us), 5000 x 4096
+// FP32 by columns 17.3 us (6.0 TB/s; reading X twice, one column a thread, 190 us).
+//
 // All in FP32 with IEEE division: 448 / top is finite for top >= 2^-100, and
 // the saturating hardware conversion is the clamp.  HBM-bound: every kernel
 // reads X once, keeps its block in registers until the maximum is known, and
