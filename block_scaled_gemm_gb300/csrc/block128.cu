@@ -86,7 +86,7 @@ int tail_split(int64_t rem, int64_t pairs, int64_t kb) {
   return best;
 }
 
-// M > 128: CTA pairs on 256 x 256 tiles, one pair per two SMs.
+// M > 64: CTA pairs on 256 x 256 tiles, one pair per two SMs.
 int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, bool bf16,
              int variant, cudaStream_t stream) {
   CUtensorMap tA, tB, tC;
@@ -178,13 +178,14 @@ int run_skinny_nt(const mxg::HandleView &v, mxg::B128Params &p, const void *A, c
   }
 }
 
-// M <= 128: transposed, the kernel for M rounded up to 16, 32, 64 or 128.
+// M <= 64: transposed, the kernel for M rounded up to 16, 32 or 64.  (N = K =
+// 8192: 16 rows 16 us, 64 rows 21 us; 128 rows took 33 us so, and 25 us on the
+// pairs, whose time is the same for 65 to 256 rows.)
 int run_skinny(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, int variant,
                cudaStream_t stream) {
   if (p.M <= 16) return run_skinny_nt<16>(v, p, A, B, nk, variant, stream);
   if (p.M <= 32) return run_skinny_nt<32>(v, p, A, B, nk, variant, stream);
-  if (p.M <= 64) return run_skinny_nt<64>(v, p, A, B, nk, variant, stream);
-  return run_skinny_nt<128>(v, p, A, B, nk, variant, stream);
+  return run_skinny_nt<64>(v, p, A, B, nk, variant, stream);
 }
 
 }  // namespace
@@ -270,7 +271,7 @@ extern "C" int mxgemm_run_block128(mxgemm_handle_t h, int64_t M, int64_t N, int6
     cudaGetLastError();
     return MXGEMM_ERR_CUDA;
   }
-  const int st = M <= 128 ? run_skinny(v, p, A, B, nk, variant, stream)
+  const int st = M <= 64 ? run_skinny(v, p, A, B, nk, variant, stream)
                           : run_pair(h, v, p, A, B, nk, bf16, variant, stream);
   if (st != MXGEMM_OK) return st;
   ++*v.launches;

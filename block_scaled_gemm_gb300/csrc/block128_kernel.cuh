@@ -14,7 +14,7 @@
 // one block runs while the other is being added.
 //
 // Two kernels:
-//   b128_pair_kernel    M > 128: CTA pairs (cta_group::2), 256 x 256 tiles,
+//   b128_pair_kernel    M > 64: CTA pairs (cta_group::2), 256 x 256 tiles,
 //                       each CTA with 128 rows of A and 128 columns of B a
 //                       K block: 32 KB of operands per 512 cycles and SM.
 //                       Bound by the epilogue beside the MMAs: the MMA
@@ -23,7 +23,7 @@
 //                       8192 x 28672 x 8192 BF16: 1240 us (3.1 PFLOP/s, 0.81 of
 //                       the measured 8-bit rate) in short runs at 2.07 GHz,
 //                       1360-1450 us under the power limit (1.7 GHz).
-//   b128_skinny_kernel  M <= 128: transposed, 128 columns of B on the MMA's
+//   b128_skinny_kernel  M <= 64: transposed, 128 columns of B on the MMA's
 //                       128-row side and the rows of A as its N, K split over
 //                       a cluster; bound by reading B once: 16 x 8192 x 8192
 //                       15.9 us (4.3 TB/s), 16 x 16384 x 16384 5.4 TB/s.
@@ -610,12 +610,12 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// M <= 128: C^T[n, m] for 128 columns n of B and the rows m of A.
+// M <= 64: C^T[n, m] for 128 columns n of B and the rows m of A.
 template <int NT>
 struct SkinnyCfg {
   static constexpr int BT_BYTES = 128 * 128;  // 128 columns of B
   static constexpr int AT_BYTES = NT * 128;   // up to NT rows of A
-  static constexpr int STAGES = NT <= 16 ? 11 : NT <= 32 ? 10 : NT <= 64 ? 8 : 6;
+  static constexpr int STAGES = NT <= 16 ? 11 : NT <= 32 ? 10 : 8;
   static constexpr int BUFS = 4;  // accumulators
   static constexpr int OFF_BT = 0;
   static constexpr int OFF_AT = OFF_BT + STAGES * BT_BYTES;

@@ -32,7 +32,8 @@ int cache_args(const mxg::HandleView &v, const mxgemm_cache_t *c, int64_t batch,
   if (c->head_dim != 64 && c->head_dim != 128) return MXGEMM_ERR_INVALID_VALUE;
   if (c->kv_heads < 1 || c->kv_heads > 65535 || c->num_pages < 0 || c->num_pages >= kLim)
     return MXGEMM_ERR_INVALID_VALUE;
-  if (table_pitch >= kLim || table_pitch * c->page_size >= kLim ||
+  // (positions of whole tiles, and rows of query tokens x heads, stay below 2^31)
+  if (table_pitch >= kLim || table_pitch * c->page_size > kLim / 2 ||
       c->num_pages * c->kv_heads >= kLim / c->page_size)
     return MXGEMM_ERR_INVALID_VALUE;
   if (!q_start && tokens != batch) return MXGEMM_ERR_INVALID_VALUE;
@@ -204,7 +205,8 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   mxg::AttnParams p;
   if (int st = cache_args(v, cache, batch, page_table, table_pitch, kv_len, q_start, tokens, &p.c, &p.b))
     return st;
-  if (heads < 1 || heads >= (1 << 16) || heads % cache->kv_heads != 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (heads < 1 || heads >= (1 << 16) || heads % cache->kv_heads != 0 || tokens * heads >= kLim)
+    return MXGEMM_ERR_INVALID_VALUE;
   if (q_pitch < heads * cache->head_dim || !std::isfinite(scale)) return MXGEMM_ERR_INVALID_VALUE;
   if ((causal != 0 && causal != 1) || window < 0 || sinks < 0) return MXGEMM_ERR_INVALID_VALUE;
   if (batch == 0 || tokens == 0) return MXGEMM_OK;

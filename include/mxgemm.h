@@ -442,10 +442,11 @@ int mxgemm_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t C, i
  *   K, V             : num_pages x kv_heads x page_size x head_dim codes,
  *                      16-byte aligned
  *   K_scale, V_scale : num_pages x kv_heads float, positive and finite
- *   page_size        : 16, 32, 64 or 128;  head_dim : 64 or 128.
+ *   page_size        : 16, 32, 64 or 128;  head_dim : 64 or 128;
+ *   num_pages * kv_heads * page_size < 2^31.
  * Which pages a sequence has, in order, is row b of a page table: batch rows
- * of int32, table_pitch entries apart; entries past a sequence's last page
- * are not read.  A page number outside [0, num_pages) or a length that is
+ * of int32, table_pitch entries apart (table_pitch * page_size <= 2^30);
+ * entries past a sequence's last page are not read.  A page number outside [0, num_pages) or a length that is
  * negative or does not fit the table is not followed: what it names counts as
  * absent, and MXGEMM_ERR_INVALID_VALUE is recorded in the handle's device
  * status word. */
@@ -502,13 +503,15 @@ int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t 
  *   O : tokens x heads x head_dim bfloat16, dense;  lse : tokens x heads
  *   float, or NULL.
  *   page_table, kv_len, q_start : as for mxgemm_cache_append.
- *   scale : finite.  window, sinks >= 0.
+ *   scale : finite.  window, sinks >= 0.  tokens * heads < 2^31.
  * Sums and softmax statistics are FP32; the codes enter the products exactly,
  * the weights p rounded to FP16.  Places past a sequence's end and absent
  * pages may hold anything, NaN codes included.  The split of the work, and so
  * the order of the sums, depends on the lengths and sizes alone: equal calls
  * give equal bits.  Q and O 16-byte aligned, q_pitch % 8 == 0
- * (MXGEMM_ERR_MISALIGNED).  The handle's workspace holds partial results. */
+ * (MXGEMM_ERR_MISALIGNED).  The handle's workspace holds partial results; it
+ * grows with the first call of a size, which therefore comes before a stream
+ * capture (as for mxgemm_run_block128 with few or ragged tiles). */
 int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
                            int64_t heads, const int32_t *page_table, int64_t table_pitch,
                            const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
