@@ -128,18 +128,27 @@ int run_prompt(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   using S = mxg::PromptCfg<D>;
   const int64_t rows = p.b.tokens * p.group;
   const int64_t items = (rows / S::ROWS + p.b.batch) * p.c.kv_heads;
-  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, v.sm_count / equal_row_tiles(p))));
-  if (items > mxg::kCounters) p.parts = 1;
-  if (items * p.parts >= kLim) return MXGEMM_ERR_INVALID_VALUE;
+  if (items >= kLim - 16 * mxg::kCounters) return MXGEMM_ERR_INVALID_VALUE;
+  const int64_t tiles = equal_row_tiles(p), over = tiles % v.sm_count;
+  p.items = p.whole = static_cast<int>(items);
+  p.parts = over > 0 ? static_cast<int>(std::min<int64_t>(16, v.sm_count / over)) : 1;
   if (p.parts > 1) {
-    uint8_t *ws = nullptr;
-    if (int st = mxg::handle_workspace(h, static_cast<size_t>(items) * p.parts * S::PARTIAL * sizeof(float), stream, &ws))
-      return st;
-    p.partials = reinterpret_cast<float *>(ws);
+    if (tiles >= v.sm_count) p.whole -= static_cast<int>(std::min(items, over));
+    else p.whole = 0;
+    const int cut = p.items - p.whole;
+    if (cut > mxg::kCounters) {
+      p.whole = p.items;
+    } else {
+      uint8_t *ws = nullptr;
+      if (int st = mxg::handle_workspace(h, static_cast<size_t>(cut) * p.parts * S::PARTIAL * sizeof(float), stream, &ws))
+        return st;
+      p.partials = reinterpret_cast<float *>(ws);
+    }
   }
+  const int grid = p.whole + (p.items - p.whole) * p.parts;
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
-  return mxg::launch(mxg::cache_prompt_kernel<D>, dim3(static_cast<unsigned>(items * p.parts)), S::THREADS, S::SMEM_BYTES, 1, stream,
+  return mxg::launch(mxg::cache_prompt_kernel<D>, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, 1, stream,
                      tK, tV, p);
 }
 

@@ -50,7 +50,8 @@ struct AttnParams {
   float *lse;
   float *partials;     // of split items: two slots per CTA (prompts: one for each part)
   unsigned *counters;  // arrivals at split items, zero between launches
-  int parts;           // prompts: CTAs that a row tile's keys may be cut for
+  int items, whole;    // prompts: row tiles (all heads'), and how many of them, the first, have one CTA each
+  int parts;           // CTAs that each other one's keys may be cut for
   unsigned long long timeout_ns;
 };
 

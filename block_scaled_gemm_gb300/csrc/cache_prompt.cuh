@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   // ------------------------------------------------------------ this CTA's rows
   // Sequence b's row tiles are numbered from f(b) = floor(q_start group / 256) + b
   // (room for all of them); the last tiles, which see most keys, come first.
-  const int item = static_cast<int>(blockIdx.x / p.parts);
+  const int beyond = static_cast<int>(blockIdx.x) - p.whole;  // among the CTAs of row tiles whose keys are cut
+  const int item = beyond < 0 ? static_cast<int>(blockIdx.x) : p.whole + beyond / p.parts;
   const int h = static_cast<int>(item % p.c.kv_heads);
-  const int64_t id = static_cast<int64_t>(gridDim.x) / p.parts / p.c.kv_heads - 1 - item / p.c.kv_heads;
+  const int64_t id = p.items / p.c.kv_heads - 1 - item / p.c.kv_heads;
   auto f = [&](int b) -> int64_t {
     const int64_t q = p.b.q_start ? p.b.q_start[b] : b;
     return q * p.group / S::ROWS + b;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const int ns = static_cast<int>(min((min(p.sinks, static_cast<int64_t>(win_lo)) + 127) >> 7, static_cast<int64_t>(lo)));
   const int all_tiles = max(1, ns + ((end + 127) >> 7) - lo);
   // this CTA's part of them: four at least
-  const int parts = min(p.parts, max(1, all_tiles >> 2)), part = static_cast<int>(blockIdx.x % p.parts);
+  const int parts = beyond < 0 ? 1 : min(p.parts, max(1, all_tiles >> 2)), part = beyond < 0 ? 0 : beyond % p.parts;
   if (part >= parts) return;
   const int tile0 = static_cast<int>(static_cast<int64_t>(part) * all_tiles / parts);
   const int tiles = static_cast<int>(static_cast<int64_t>(part + 1) * all_tiles / parts) - tile0;
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         tc_fence_after();
         const float k = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;
-        float *slot = p.partials + (static_cast<int64_t>(item) * p.parts + part) * S::PARTIAL;
+        float *slot = p.partials + (static_cast<int64_t>(item - p.whole) * p.parts + part) * S::PARTIAL;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -537,12 +538,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       // (every softmax warp comes here: all their waits are bounded)
       __threadfence();
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (threadIdx.x == 256) *tmem_slot = atomicAdd(p.counters + item, 1u) == static_cast<unsigned>(parts - 1) ? 1u : 0u;
+      if (threadIdx.x == 256) *tmem_slot = atomicAdd(p.counters + item - p.whole, 1u) == static_cast<unsigned>(parts - 1) ? 1u : 0u;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (*reinterpret_cast<volatile uint32_t *>(tmem_slot)) {
-        if (threadIdx.x == 256) p.counters[item] = 0;  // for the next launch
+        if (threadIdx.x == 256) p.counters[item - p.whole] = 0;  // for the next launch
         __threadfence();
-        const float *first = p.partials + static_cast<int64_t>(item) * p.parts * S::PARTIAL;
+        const float *first = p.partials + static_cast<int64_t>(item - p.whole) * p.parts * S::PARTIAL;
         if (r < rows) {
           const int tok = (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
           float top = -INFINITY, sum = 0.f;

@@ -159,6 +159,20 @@ def test_prompts(h, lens, news, kv, group, d, page, causal, window, sinks):
     assert mx.mxgemm_get_device_status(h) == (0, 0)
 
 
+@pytest.mark.parametrize("lens,news,kv,d", [([2500], [64], 160, 64), ([1900, 700, 64], [70, 64, 66], 60, 128),
+                                             ([40, 2000], [40, 300], 80, 64)])
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (False, 700, 130)])
+def test_prompts_of_more_row_tiles_than_sms(h, lens, news, kv, d, causal, window, sinks):
+    """The row tiles past a multiple of the SMs have their keys cut for several CTAs."""
+    m = Made(lens, kv, d, 16, seed=kv)
+    q = queries(m, sum(news), kv)
+    O, L = attend(h, m, q, news, causal=causal, window=window, sinks=sinks)
+    check(m, q, news, O, L, causal=causal, window=window, sinks=sinks)
+    again, L2 = attend(h, m, q, news, causal=causal, window=window, sinks=sinks)
+    assert torch.equal(O, again) and torch.equal(L, L2)
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
+
+
 @pytest.mark.parametrize("f,scale", [(2.0 ** 20, 0.08), (2.0 ** -40, 0.08), (1.0, -0.1)])
 def test_prompts_with_wide_scales(h, f, scale):
     """Page scales over 2^30, queries past FP16's range, a negative scale."""
