@@ -369,40 +369,55 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       // Q over a power of two of its row, |q| < 2, in FP16; rows past the last are zero
       float cq;
       {
-        uint32_t u[D / 2];
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + static_cast<int64_t>(s.first + tok) * p.q_pitch +
-                                                           static_cast<int64_t>(head) * D);
+        // whole rows side by side, kUnits lanes (16 bytes each) a row
+        constexpr int kUnits = D / 8, kRows = 32 / kUnits;
+        const int64_t mine = static_cast<int64_t>(s.first + tok) * p.q_pitch + static_cast<int64_t>(head) * D;
+        const int unit = lane % kUnits, sub = lane / kUnits;
+        uint4 x[32 / kRows];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
-          u[4 * c] = w.x; u[4 * c + 1] = w.y; u[4 * c + 2] = w.z; u[4 * c + 3] = w.w;
+        for (int n = 0; n < 32 / kRows; ++n) {
+          const int from = kRows * n + sub;
+          const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, from);
+          x[n] = 128 * i + 32 * qd + from < rows ? *reinterpret_cast<const uint4 *>(p.Q + at + 8 * unit) : make_uint4(0, 0, 0, 0);
         }
-        float top = 0.f;
+        float top = 0.f;  // of this thread's row
+        const uint32_t dst = base + S::OFF_Q + i * S::TILE16 + (unit >> 3) * 16384;
+        auto exponent = [](float t) { return t > 0.f ? min(max((__float_as_int(t) >> 23) - 127, -126), 126) : 0; };
 #pragma unroll
-        for (int c = 0; c < D / 2; ++c)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[c] << 16)), fabsf(__uint_as_float(u[c] & 0xFFFF0000u))));
-        const int e = top > 0.f ? min(max((__float_as_int(top) >> 23) - 127, -126), 126) : 0;
-        // (a negative scale's sign goes to Q: the exponents' factors are positive)
-        const float inv = copysignf(__int_as_float((127 - e) << 23), p.scale);
-        cq = fabsf(p.scale) * 1.44269504088896340736f * __int_as_float((127 + e) << 23);
-        const int rr = 32 * qd + lane;
-        const uint32_t dst = base + S::OFF_Q + i * S::TILE16 + rr * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t x[4];
+        for (int n = 0; n < 32 / kRows; ++n) {
+          const int rr = 32 * qd + kRows * n + sub;
+          const uint32_t u[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+          float t = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            x[k] = half2_of(__uint_as_float(u[4 * c + k] << 16) * inv, __uint_as_float(u[4 * c + k] & 0xFFFF0000u) * inv);
-          st_shared_v4(dst + (c >> 3) * 16384 + (((c & 7) ^ (rr & 7)) << 4), x[0], x[1], x[2], x[3]);
+            t = fmaxf(t, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+#pragma unroll
+          for (int o = kUnits / 2; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+          const float own = __shfl_sync(0xFFFFFFFFu, t, (lane % kRows) * kUnits);
+          if (lane / kRows == n) top = own;
+          // (a negative scale's sign goes to Q: the exponents' factors are positive)
+          const float inv = copysignf(__int_as_float((127 - exponent(t)) << 23), p.scale);
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = half2_of(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xFFFF0000u) * inv);
+          st_shared_v4(dst + rr * 128 + (((unit & 7) ^ (rr & 7)) << 4), y[0], y[1], y[2], y[3]);
         }
+        cq = fabsf(p.scale) * 1.44269504088896340736f * __int_as_float((127 + exponent(top)) << 23);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full + 8 * i);
       }
       const int pos = pos0 + tok;
-      // positions of this warp's rows
-      const int pos_min = pos0 + (row0 + min(128 * i + 32 * qd, rows - 1)) / p.group;
-      const int pos_max = pos0 + (row0 + min(128 * i + 32 * qd + 31, rows - 1)) / p.group;
+      // this thread's row sees keys [row_from, row_to) and the first tokens; all
+      // rows of the warp see [all_from, all_to)
+      auto window_from = [&](int pos) {
+        return p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(0), pos - p.window + 1));
+      };
+      const int w0 = 128 * i + 32 * qd;
+      const int row_to = p.causal ? min(end, pos + 1) : end, row_from = window_from(pos);
+      const int all_to = p.causal ? min(end, pos0 + (row0 + min(w0, rows - 1)) / p.group + 1) : end;
+      const int all_from = window_from(pos0 + (row0 + min(w0 + 31, rows - 1)) / p.group);
       const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
       const uint32_t ts = tmem + S::TM_S + 128 * i + lanes, to = tmem + S::TM_O + 128 * i + lanes;
       float m = -INFINITY, l = 0.f;
@@ -420,13 +435,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int c = 0; c < 4; ++c) tmem_ld_done(v[c]);
         const uint32_t there = groups[j & 3];
         const int jlast = key0 + 127;
-        const bool whole = there == 0xFFu && jlast < end && (!p.causal || jlast <= pos_min) &&
-                           (p.window == 0 || pos_max - key0 < p.window || jlast < p.sinks);
+        const bool whole = there == 0xFFu && jlast < all_to && (key0 >= all_from || jlast < p.sinks);
         if (!whole) {
           // columns [from, upto) and [0, sink) of the tile are seen
-          const int upto = min(p.causal ? min(end, pos + 1) : end, s.len) - key0;
-          const int from = p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(128), pos - p.window + 1 - key0)));
-          const int sink = p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(0), min(p.sinks - key0, static_cast<int64_t>(128))));
+          const int upto = row_to - key0, from = row_from - key0;
+          const int sink = static_cast<int>(min(p.sinks, static_cast<int64_t>(end))) - key0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t seen = low_bits(upto - 32 * c) & (~low_bits(from - 32 * c) | low_bits(sink - 32 * c)) &
@@ -499,19 +512,30 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       if (ok) ok = wait(o_done + 8 * i, (tiles - 1) & 1, 0x4F);
       if (ok) {
         tc_fence_after();
-        const float k = l == 0.f ? 0.f : 1.f / l;
-        __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;
-        float *slot = p.partials + (static_cast<int64_t>(item - p.whole) * p.parts + part) * S::PARTIAL;
+        const int at = (s.first + tok) * p.heads + head;
+        if (parts > 1) {
+          float *slot = p.partials + (static_cast<int64_t>(item - p.whole) * p.parts + part) * S::PARTIAL;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(to + 32 * c, o);
-          tmem_ld_done(o);
-          if (parts > 1) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * c, o);
+            tmem_ld_done(o);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               reinterpret_cast<uint4 *>(slot)[(8 * c + e) * S::ROWS + r] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else if (live) {
+          }
+          slot[S::ROWS * D + r] = m;
+          slot[S::ROWS * D + S::ROWS + r] = l;
+        } else {
+          // through the rows of Q, whose products are done: a store of whole
+          // lines, where a thread's own row would touch 32
+          const float k = l == 0.f ? 0.f : 1.f / l;
+          const uint32_t rr = 32 * qd + lane, q_row = base + S::OFF_Q + i * S::TILE16 + rr * 128;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * c, o);
+            tmem_ld_done(o);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t x[4];
@@ -521,16 +545,22 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                                                                __uint_as_float(o[8 * e + 2 * w + 1]) * k);
                 x[w] = *reinterpret_cast<const uint32_t *>(&y);
               }
-              *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * e) = make_uint4(x[0], x[1], x[2], x[3]);
+              st_shared_v4(q_row + (c >> 1) * 16384 + (((4 * (c & 1) + e) ^ (rr & 7)) << 4), x[0], x[1], x[2], x[3]);
             }
           }
-        }
-        if (parts > 1) {
-          slot[S::ROWS * D + r] = m;
-          slot[S::ROWS * D + S::ROWS + r] = l;
-        } else if (live && p.lse) {
-          p.lse[static_cast<int64_t>(s.first + tok) * p.heads + head] =
-              l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994530942f;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int from = 4 * j + (lane >> 3), q = lane & 7;
+            const int64_t to_row = __shfl_sync(0xFFFFFFFFu, at, from);
+            if (128 * i + 32 * qd + from < rows) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<uint4 *>(p.O + to_row * D + 64 * c + 8 * q) =
+                    ld_shared_v4(q_row + (from - lane) * 128 + c * 16384 + ((q ^ (from & 7)) << 4));
+            }
+          }
+          if (live && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994530942f;
         }
       }
     }
