@@ -19,15 +19,16 @@
 // memory; no other warp waits for it.  Running maximum, sum and O stay in
 // the warp until the end of its run.
 //
-// Measured: 64 sequences of 2048-8192 tokens, 64/8 heads of 128: 120 us (5.6
+// Measured: 64 sequences of 2048-8192 tokens, 64/8 heads of 128: 121 us (5.6
 // TB/s, 0.82 of the measured copy rate); two of 91752 and 131071 tokens, 32/4 heads:
-// 59 us (3.8 TB/s: 57 CTAs' partials join for each item, about 8 us, and the
+// 54 us (4.2 TB/s: some 50 CTAs' partials join for each item, about 8 us, and the
 // first codes arrive 3 us after the start).  The warps' chains of dependent
 // instructions bound it: issue slots are used to 46 %.
 //
 // Work: an item is one sequence, key/value head and ROWS query rows; all
-// items' tiles, laid end to end, are cut into equal ranges, one per CTA.  An
-// item that spans CTAs leaves FP32 partials in the workspace and the CTA that
+// items' tiles, laid end to end, are cut into equal ranges, one per CTA, or,
+// where items are few, each one's into parts for CTAs of its own.  An item
+// that spans CTAs leaves FP32 partials in the workspace and the CTA that
 // arrives last adds them, in order: the result does not depend on timing.
 #pragma once
 #include <cuda_bf16.h>
@@ -178,11 +179,13 @@ struct Cursor {
   }
 };
 
-// Tiles of sequence b (none past the batch).
-__device__ __forceinline__ int64_t sequence_tiles(const AttnParams &p, int rows, int b) {
+// Items of sequence b (none past the batch), and tiles of each.
+__device__ __forceinline__ int64_t sequence_items(const AttnParams &p, int rows, int b, int &tiles) {
+  tiles = 1;
   if (b >= p.b.batch) return 0;
   const Sequence s = load_sequence(p.b, p.c, b);
-  return item_count(p, s, rows) * key_tiles(p, s).tiles;
+  tiles = key_tiles(p, s).tiles;
+  return item_count(p, s, rows);
 }
 __device__ __forceinline__ int64_t warp_prefix(int64_t v) {  // inclusive
   const int lane = threadIdx.x & 31;
@@ -235,6 +238,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   float *merge = reinterpret_cast<float *>(sm + S::OFF_MERGE);
   float *ml = reinterpret_cast<float *>(sm + S::OFF_ML);
   int *last_at = reinterpret_cast<int *>(sm + S::OFF_MISC);
+  // how tiles are cut: all of them and the CTAs that share them, or 0 and the
+  // first and the last CTA of this one's item; then the range's first tile
+  // (kept here: registers are short)
+  int64_t *cut = reinterpret_cast<int64_t *>(sm + S::OFF_MISC + 8);
 
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 33);  // the bytes' arrive, and the lanes' copies
@@ -246,31 +253,81 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   griddep_wait();
   // All tiles (each warp counts for itself, 32 sequences at a time), and this
   // CTA's range of them: ranges of four tiles at least.
-  const int64_t mine = sequence_tiles(p, ROWS, lane), upto = warp_prefix(mine);  // the first 32 sequences
+  int mt;
+  int64_t mi = sequence_items(p, ROWS, lane, mt);
+  int64_t mine = mi * mt, upto = warp_prefix(mine);  // the first 32 sequences
   int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  for (int b = 32; b < p.b.batch; b += 32)
-    total += __shfl_sync(0xFFFFFFFFu, warp_prefix(sequence_tiles(p, ROWS, b + lane)), 31);
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 3) / 4);
-  if (blockIdx.x >= ctas) return;
-  auto first_tile = [&](int64_t u) { return quotient(u * total, ctas); };
-  auto cta_of = [&](int64_t x) { return quotient((x + 1) * ctas - 1, total); };  // the CTA whose range holds tile x
-  const int64_t x0 = first_tile(blockIdx.x), x1 = first_tile(blockIdx.x + 1);
-  // the sequence of tile x0, and where its tiles begin
+  unsigned all_items = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mi));
+  for (int b = 32; b < p.b.batch; b += 32) {
+    int tiles;
+    const int64_t items = sequence_items(p, ROWS, b + lane, tiles);
+    total += __shfl_sync(0xFFFFFFFFu, warp_prefix(items * tiles), 31);
+    all_items += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(items));
+  }
+  // the sequence of the range's first tile, and where its tiles begin
   int b0 = 0;
-  int64_t base_b = 0;
-  {
-    int64_t m = mine, u = upto;
+  int64_t base_b = 0, x0, x1;
+  auto next_sequences = [&]() {  // the next 32
+    base_b += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    b0 += 32;
+    mi = sequence_items(p, ROWS, b0 + lane, mt);
+    mine = mi * mt;
+    upto = warp_prefix(mine);
+  };
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 3) / 4);
+  // Few items: each one's tiles are cut for CTAs of its own, into parts of q tiles
+  // at most, since a CTA that ends two items' parts ends late (17 tiles for
+  // each of 8 heads: 16.5 -> 10.8 us).  And no more parts than pay: one costs
+  // the join 0.12 us, four tiles more a CTA 2 us, which is least at parts of
+  // sqrt(0.24 tiles) (one head of 20000 keys: 27.2 -> 18 us).
+  const bool own = 4 * static_cast<int64_t>(all_items) <= gridDim.x;
+  if (own) {
+    const int64_t room = gridDim.x - all_items, q = max(static_cast<int64_t>(4), quotient(total + room - 1, room));
+    auto parts_of = [&](int tiles) {
+      const int64_t n = max(q, static_cast<int64_t>(sqrtf(0.24f * tiles)));
+      return quotient(tiles + n - 1, n);
+    };
+    int64_t base_u = 0, units, u;
     uint32_t past;
-    while (!(past = __ballot_sync(0xFFFFFFFFu, base_b + u > x0))) {
-      base_b += __shfl_sync(0xFFFFFFFFu, u, 31);
-      b0 += 32;
-      m = sequence_tiles(p, ROWS, b0 + lane);
-      u = warp_prefix(m);
+    for (;;) {
+      units = mi * parts_of(mt);
+      u = warp_prefix(units);
+      past = __ballot_sync(0xFFFFFFFFu, base_u + u > blockIdx.x);
+      if (past) break;
+      if (b0 + 32 >= p.b.batch) return;
+      base_u += __shfl_sync(0xFFFFFFFFu, u, 31);
+      next_sequences();
     }
     const int i = __ffs(past) - 1;
-    base_b += __shfl_sync(0xFFFFFFFFu, u - m, i);
+    base_u += __shfl_sync(0xFFFFFFFFu, u - units, i);
+    base_b += __shfl_sync(0xFFFFFFFFu, upto - mine, i);
     b0 += i;
+    const int tiles = __shfl_sync(0xFFFFFFFFu, mt, i);
+    const int64_t parts = parts_of(tiles), rel = blockIdx.x - base_u, item = quotient(rel, parts), part = rel - item * parts;
+    x0 = base_b + item * tiles + quotient(part * tiles, parts);
+    x1 = base_b + item * tiles + quotient((part + 1) * tiles, parts);
+    if (threadIdx.x == 0) {
+      cut[0] = 0;
+      cut[1] = blockIdx.x - part;
+      cut[2] = blockIdx.x - part + parts - 1;
+    }
+  } else {
+    if (blockIdx.x >= ctas) return;
+    auto first_tile = [&](int64_t u) { return quotient(u * total, ctas); };
+    x0 = first_tile(blockIdx.x);
+    x1 = first_tile(blockIdx.x + 1);
+    uint32_t past;
+    while (!(past = __ballot_sync(0xFFFFFFFFu, base_b + upto > x0))) next_sequences();
+    const int i = __ffs(past) - 1;
+    base_b += __shfl_sync(0xFFFFFFFFu, upto - mine, i);
+    b0 += i;
+    if (threadIdx.x == 0) {
+      cut[0] = total;
+      cut[1] = ctas;
+    }
   }
+
+  if (threadIdx.x == 0) cut[3] = x0;
 
   const int lg = p.c.page_log2, per = lg == 4 ? 2 : 1;  // pages of a tile
   const uint32_t box_bytes = (lg == 4 ? 16 : 32) * D;
@@ -571,8 +628,14 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         }
       }
     __syncthreads();
-    const bool split = item_beg < x0 || item_end > x1;
-    const int64_t u0 = split ? cta_of(item_beg) : 0, u1 = split ? cta_of(item_end - 1) : 0;
+    const bool split = item_beg < cut[3] || item_end > x1;
+    // the CTAs that share the item
+    int64_t u0 = 0, u1 = 0;
+    if (split) {
+      const int64_t all = cut[0], n = cut[1];
+      u0 = all ? quotient((item_beg + 1) * n - 1, all) : n;
+      u1 = all ? quotient(item_end * n - 1, all) : cut[2];
+    }
     float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (blockIdx.x == u0)) * S::PARTIAL;
     const int hr = threadIdx.x >> 4, hd = threadIdx.x & 15;  // output: row of 8, four of 64 d
 #pragma unroll

@@ -194,6 +194,20 @@ def test_long_sequence_is_split(h):
     assert torch.equal(O, again) and torch.equal(L, L2)
 
 
+@pytest.mark.parametrize("n,kv,group,d,page", [(40, 4, 4, 128, 32), (50, 2, 8, 64, 16), (33, 3, 2, 64, 128), (130, 1, 16, 128, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
+def test_many_sequences(h, n, kv, group, d, page, window, sinks):
+    """More sequences than a warp counts at a time, and more heads of theirs than
+    CTAs are handed out for one by one; every seventh or so is empty."""
+    lens = [37 * i * i % 701 * (i % 7 != 3) for i in range(n)]
+    m = Made(lens, kv, d, page, seed=n)
+    q = queries(m, n, kv * group)
+    O, L = attend(h, m, q, None, window=window, sinks=sinks)
+    check(m, q, [1] * n, O, L, window=window, sinks=sinks)
+    again, L2 = attend(h, m, q, None, window=window, sinks=sinks)
+    assert torch.equal(O, again) and torch.equal(L, L2)
+
+
 def test_queries_before_the_first_key(h):
     """More queries than the sequence has tokens: the first ones see nothing."""
     m = Made([3, 0, 200], 1, 64, 16)
