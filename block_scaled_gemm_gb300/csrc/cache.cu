@@ -114,10 +114,11 @@ int encode_cache(const mxg::HandleView &v, const mxg::CacheView &c, int d, int b
   return MXGEMM_OK;
 }
 
-// Many query rows: one CTA for each 256 of a sequence and key/value head, or, of
-// few such row tiles, up to 16 for each (44 row tiles of 61102 keys: 816 ->
-// 296 us).  The grid has room for every split of the rows into sequences;
-// the count of row tiles that decides is that of equal ones.
+// Many query rows: one CTA for each 256 of a sequence and key/value head.  The
+// row tiles that do not fill a round of the SMs, all of them where they are
+// few, get up to 16 CTAs each (44 row tiles of 61102 keys: 816 -> 296 us; the
+// last 24 of 480: 334 -> 328 us).  The grid has room for every split of the rows
+// into sequences; the count of row tiles that decides is that of equal ones.
 int64_t equal_row_tiles(const mxg::AttnParams &p) {
   constexpr int64_t kRows = mxg::PromptCfg<128>::ROWS;
   return (p.b.tokens * p.group / p.b.batch + kRows - 1) / kRows * p.b.batch * p.c.kv_heads;

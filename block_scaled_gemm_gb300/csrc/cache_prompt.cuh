@@ -18,15 +18,18 @@
 // running maximum is moved, and O in TMEM rescaled, only when it grows by 2^8.
 //
 // Measured: 2 x 2048 tokens (the second 1741) over 8190 (5733) keys, 32/8 heads of
-// 128: 334 us, 1.14 PFLOP/s, 0.59 of the measured FP16 rate; a key tile takes about
-// 3250 cycles where the four products alone take 2048 and shared memory's traffic
+// 128: 313 us, 1.21 PFLOP/s, 0.64 of the measured FP16 rate (one of 1200 tokens over
+// 16000 keys, a row tile an SM, 216 us, 0.73); a key tile takes 1.65 us, some 3200
+// cycles, where the four products alone take 2048 and shared memory's traffic
 // 2560.  A Q tile's chain (softmax, P V, the next Q K^T into the same columns)
-// is what is left.  Half steps of 64 keys with two S a Q tile shorten the chain but
-// read Q twice (409 us); two threads a row with 16 softmax warps took 410 us.
+// is what is left, and about 8 us before a row tile's first and after its last
+// product.  Half steps of 64 keys with two S a Q tile shorten the chain but
+// read Q twice (409 us); two threads a row with 16 softmax warps took 410 us;
+// CTAs that stay for the next row tile took 338 us.
 //
-// Where the row tiles are fewer than the SMs, each one's keys are cut into parts
-// for as many CTAs; they leave FP32 partials in the workspace, and the one that
-// arrives last adds them in order.
+// Where the row tiles are fewer than the SMs, and for those past a multiple of
+// them, each one's keys are cut into parts for several CTAs; they leave FP32
+// partials in the workspace, and the one that arrives last adds them in order.
 //
 // Warps (512 threads): 0 TMA loads of the pages' codes, and the scales;
 // 1 MMAs; 4-7 convert codes to FP16 in the MMA's layout (128-byte swizzle);
