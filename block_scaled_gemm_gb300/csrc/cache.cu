@@ -239,6 +239,7 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.counters = v.counters;
   p.timeout_ns = v.timeout_ns;
+  p.stall_producer = v.stall_producer;
   // Rows (query tokens x heads of a group) of an ordinary sequence decide: many
   // go to the tensor cores by 256, few to the kernel whose items are 8 or 16.
   // At 64 rows both take the same time on 32 row tiles of 8192 keys (70 us); on

@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 
 #include "cache_common.cuh"
+#include "ring.h"
 
 namespace mxg {
 
@@ -54,6 +55,7 @@ struct AttnParams {
   int items, whole;    // prompts: row tiles (all heads'), and how many of them, the first, have one CTA each
   int parts;           // CTAs that each other one's keys may be cut for
   unsigned long long timeout_ns;
+  int stall_producer;  // tests: nothing is loaded
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   };
   int64_t px = x0 + warp;  // next tile to load
   int pst = 0;
-  for (int i = 0; i < STAGES && px < x1; ++i, px += 4) {
+  for (int i = 0; i < STAGES && px < x1 && !p.stall_producer; ++i, px += 4) {
     issue(px, pst);
     pst = pst + 1 == STAGES ? 0 : pst + 1;
   }
@@ -606,8 +608,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       // this stage's reads come before the next load into it
       fence_proxy_async_smem();
       __syncwarp();
-      if (alive && px < x1) issue(px, st);
-      px += 4;
+      if (alive && px < x1) {
+        issue(px, st);
+        px += 4;
+      }
       if (++st == STAGES) {
         st = 0;
         ph ^= 1u;
@@ -760,12 +764,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     __syncthreads();  // ml and merge are free for the next item
   }
   // after a wait that gave up: loads still on their way land first
-  for (int i = 0; !alive && i < STAGES; ++i) {
-    wait_stage(st, ph);
-    if (++st == STAGES) {
-      st = 0;
-      ph ^= 1u;
-    }
+  if (!alive) {
+    const int64_t issued = (px - (cut[3] + warp)) / 4;
+    for (int64_t i = ring_pending(issued, STAGES); i < issued; ++i)
+      wait_stage(static_cast<int>(i % STAGES), ring_parity(i, STAGES));
   }
 }
 

@@ -1,0 +1,49 @@
+"""Calls whose waits give up: they end with a status, and the handle works as
+before afterwards.  The test hook keeps loads from being issued, so that nothing
+is on its way when a kernel ends; test_ring.py plays the rest on the CPU."""
+import pytest
+import torch
+
+import test_gpu_cache as tc
+
+pytestmark = pytest.mark.gpu
+
+mx = pytest.importorskip("block_scaled_gemm_gb300")
+
+
+@pytest.fixture
+def h():
+    h = mx.mxgemm_create(0)
+    yield h
+    mx.mxgemm_destroy(h)
+
+
+class Stalled:
+    """Short waits, and loads held back as `how` says."""
+
+    def __init__(self, h, how=1):
+        self.h, self.how = h, how
+
+    def __enter__(self):
+        mx.mxgemm_set_option(self.h, mx.OPT_WAIT_TIMEOUT_NS, 20_000_000)
+        mx.mxgemm_set_option(self.h, mx.OPT_TEST_STALL_PRODUCER, self.how)
+
+    def __exit__(self, *_):
+        mx.mxgemm_set_option(self.h, mx.OPT_TEST_STALL_PRODUCER, 0)
+        mx.mxgemm_set_option(self.h, mx.OPT_WAIT_TIMEOUT_NS, 2_000_000_000)
+
+
+# whole items, items of several CTAs, both counts of rows an item
+@pytest.mark.parametrize("lens,kv,group,d,page", [([100, 40], 1, 4, 128, 16), ([20011, 64], 1, 8, 128, 64), ([3000, 700], 2, 16, 64, 32)])
+def test_single_tokens(h, lens, kv, group, d, page):
+    m = tc.Made(lens, kv, d, page)
+    q = tc.queries(m, len(lens), kv * group)
+    want, lse = tc.attend(h, m, q, None)
+    tc.check(m, q, [1] * len(lens), want, lse)
+    with Stalled(h):
+        tc.attend(h, m, q, None)
+    for _ in range(2):  # before and after the status is read
+        O, L = tc.attend(h, m, q, None)
+        assert torch.equal(O, want) and torch.equal(L, lse)
+        status, detail = mx.mxgemm_get_device_status(h)
+        assert (status, detail) == ((mx.ERR_TIMEOUT, 0x31) if _ == 0 else (0, 0))
