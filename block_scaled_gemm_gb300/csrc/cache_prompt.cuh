@@ -204,9 +204,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- loads
       const int lg = p.c.page_log2, npg = 128 >> lg;  // pages of a tile
-      bool ok = true;
+      bool ok = !p.stall_producer;
       int k_loads = 0, v_loads = 0;
-      for (int j = 0; j < tiles; ++j) {
+      for (int j = 0; ok && j < tiles; ++j) {
         const int key0 = tile_key(j);
         // lane g < 8: the 16 keys of group g
         int pg = -1;
@@ -246,11 +246,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         if (load) tma_load_2d(base + S::OFF_V8 + (lane << lg) * D, &tmV, 0, row, v8_full);
         ++v_loads;
       }
-      // after a wait that gave up: loads on their way land before the CTA ends
-      if (!ok) {
-        if (k_loads > 0) wait_phase<false>(k8_full, (k_loads - 1) & 1, wn, 0x43);
-        if (v_loads > 0) wait_phase<false>(v8_full, (v_loads - 1) & 1, wn, 0x43);
-      }
+      // The last loads land before the CTA ends, whoever gave up: the
+      // converters may have left without waiting for them.
+      if (k_loads > 0) wait_phase<false>(k8_full, ring_parity(k_loads - 1, 1), wn, 0x43);
+      if (v_loads > 0) wait_phase<false>(v8_full, ring_parity(v_loads - 1, 1), wn, 0x43);
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMAs
       if (elect_one()) {

@@ -47,3 +47,20 @@ def test_single_tokens(h, lens, kv, group, d, page):
         assert torch.equal(O, want) and torch.equal(L, lse)
         status, detail = mx.mxgemm_get_device_status(h)
         assert (status, detail) == ((mx.ERR_TIMEOUT, 0x31) if _ == 0 else (0, 0))
+
+
+# row tiles with a CTA each, and row tiles whose keys are cut into parts
+@pytest.mark.parametrize("lens,news,kv,group,d,page", [([1100], [1100], 4, 4, 128, 64), ([400], [257], 160, 3, 64, 128),
+                                                       ([5000], [70], 1, 1, 128, 64), ([3001, 0, 129], [40, 2, 100], 1, 8, 64, 32)])
+def test_prompts(h, lens, news, kv, group, d, page):
+    m = tc.Made(lens, kv, d, page)
+    q = tc.queries(m, sum(news), kv * group)
+    want, lse = tc.attend(h, m, q, news)
+    tc.check(m, q, news, want, lse)
+    with Stalled(h):
+        tc.attend(h, m, q, news)
+    for read in (0, 1):
+        O, L = tc.attend(h, m, q, news)
+        assert torch.equal(O, want) and torch.equal(L, lse)
+        status, detail = mx.mxgemm_get_device_status(h)
+        assert (status == mx.ERR_TIMEOUT and 0x41 <= detail <= 0x4F) if read == 0 else (status, detail) == (0, 0)
