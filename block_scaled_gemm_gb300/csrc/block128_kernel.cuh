@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
   griddep_launch_dependents();  // the next kernel's set-up may begin
   griddep_wait();               // no global memory before the kernel before has ended
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
-  const WaitCtl wn{p.status, never, p.timeout_ns};
+  const WaitCtl wn{p.status, never, landing_limit(p.timeout_ns)};
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
   const int kb = p.kb;
 
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(SkinnyCfg<NT>::THREADS, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 4);
   volatile int *never = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 8);  // never raised
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
-  const WaitCtl wn{p.status, never, p.timeout_ns};
+  const WaitCtl wn{p.status, never, landing_limit(p.timeout_ns)};
 
   auto load_step = [&](int st, int ks) {
     const uint32_t fb = bar_full + 8 * st;

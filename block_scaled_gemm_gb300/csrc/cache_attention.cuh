@@ -380,12 +380,12 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   };
   load_q();
   // bounded wait (whole warp): the loads of this stage have landed
-  auto wait_stage = [&](int st, uint32_t ph) -> bool {
+  auto wait_stage = [&](int st, uint32_t ph, unsigned long long limit) -> bool {
     bool ok = mbar_try_wait(bars + 8 * st, ph);
     if (!ok) {
       const uint64_t t0 = globaltimer_ns();
       for (uint32_t i = 1; !(ok = mbar_try_wait(bars + 8 * st, ph)); ++i)
-        if ((i & 31u) == 0 && globaltimer_ns() - t0 > p.timeout_ns) {
+        if ((i & 31u) == 0 && globaltimer_ns() - t0 > limit) {
           if (atomicCAS(p.b.status, 0, 6) == 0) atomicExch(p.b.status + 1, 0x31);
           break;
         }
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
 
     for (; x < seg_end; x += 4) {
       const int key0 = at.key(x);
-      if (alive) alive = wait_stage(st, ph);
+      if (alive) alive = wait_stage(st, ph, p.timeout_ns);
       const uint32_t kb = ring + st * S::STAGE, vb = kb + 32 * D;
       // S^T: keys 16 mt + g (+ 8) x rows; two sums for the halves of D, so that
       // chains of dependent MMAs are half as long
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   if (!alive) {
     const int64_t issued = (px - (cut[3] + warp)) / 4;
     for (int64_t i = ring_pending(issued, STAGES); i < issued; ++i)
-      wait_stage(static_cast<int>(i % STAGES), ring_parity(i, STAGES));
+      wait_stage(static_cast<int>(i % STAGES), ring_parity(i, STAGES), landing_limit(p.timeout_ns));
   }
 }
 

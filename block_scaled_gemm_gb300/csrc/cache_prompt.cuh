@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl wc{p.b.status, abort_flag, p.timeout_ns};
-  const WaitCtl wn{p.b.status, never, p.timeout_ns};
+  const WaitCtl wn{p.b.status, never, landing_limit(p.timeout_ns)};
   auto wait = [&](uint32_t bar, uint32_t parity, int detail) {
     return __all_sync(0xFFFFFFFFu, wait_phase<false>(bar, parity, wc, detail));
   };

@@ -22,4 +22,11 @@ MXG_HOST_DEVICE constexpr int64_t ring_pending(int64_t issued, int stages) {
   return issued > stages ? issued - stages : 0;
 }
 
+// Limit (ns) of the waits at a kernel's end for what is on its way: loads and
+// MMAs that were issued end by themselves, in microseconds, and they must have
+// before the CTA does, however short the caller's limit for the other waits is.
+MXG_HOST_DEVICE constexpr unsigned long long landing_limit(unsigned long long timeout_ns) {
+  return timeout_ns > 2000000000ull ? timeout_ns : 2000000000ull;
+}
+
 }  // namespace mxg

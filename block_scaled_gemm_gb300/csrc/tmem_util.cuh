@@ -5,6 +5,7 @@
 
 #include "mxgemm_kernel.cuh"
 #include "ptx.cuh"
+#include "ring.h"
 
 namespace mxg {
 

@@ -54,6 +54,9 @@ int main() {
           }
           for (int i = 0; i < tiles; ++i) bad += pending[i];  // landed after the end
         }
+  for (unsigned long long ns : {1ull, 1000ull, 1999999999ull})  // a short limit is not one for what is on its way
+    bad += mxg::landing_limit(ns) != 2000000000ull;
+  bad += mxg::landing_limit(5000000000ull) != 5000000000ull;
   printf("%ld %ld\n", checked, bad);
   return 0;
 }
