@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);
   volatile int *never = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 8);  // never raised
+  volatile int *peer_fills = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 12);  // first CTA: the second's fills + 1
 
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmA);
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     mbar_init(bar_final, 1);
     *abort_flag = 0;
     *never = 0;
+    *peer_fills = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -244,14 +246,18 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     int st = 0;
     uint32_t ph = 0;
     long long issued = 0;
-    bool ok = !p.stall_producer;
+    bool ok = true;
+    // (tests: no loads, or, of one CTA of each pair, two)
+    const long long stop = p.stall_producer == 1 ? 0 : p.stall_producer == 2 + static_cast<int>(rank) ? 2 : -1;
     PairWork w;
     for (int i = 0; ok && pair_work(p, unit, units, i, w); ++i) {
       int mt, nt;
       tile_coords(w.tile, p.m_tiles, p.n_tiles, mt, nt);
       const int row = mt * 256 + 128 * static_cast<int>(rank), col = nt * 256 + 128 * static_cast<int>(rank);
       for (int ks = w.kb; ks < w.ke; ++ks) {
-        if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * st, ph ^ 1u, wc, 0x01 | (st << 8)))) {
+        // (a producer that is stopped waits for a fill that it does not issue)
+        if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(issued == stop ? bar_full + 8 * st : bar_empty + 8 * st,
+                                                       issued == stop ? ph : ph ^ 1u, wc, 0x01 | (st << 8)))) {
           ok = false;
           break;
         }
@@ -270,18 +276,36 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         }
       }
     }
-    // Before the CTA may finish: every fill's MMA has released its stage; and
-    // where a wait gave up, the fills that are still on their way land (the
-    // full barriers are the first CTA's).
-    bool clean = true;
-    const int n = static_cast<int>(issued < C::STAGES ? issued : C::STAGES);
-    for (int i = 0; i < n; ++i) {
-      const int s = (st + C::STAGES - n + i) % C::STAGES;
-      const uint32_t par = (s < st ? ph : ph ^ 1u);  // parity of that stage's last fill
-      if (clean)
-        clean = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * s, par, wc, 0x11 | (s << 8)));
-      if (!clean && rank == 0) wait_phase<false>(bar_full + 8 * s, par, wn, 0x11 | (s << 8));
+    // Before the CTA may finish: every fill's MMA has released its stage.  Where
+    // a wait gave up, the fills that are still on their way land: both CTAs'
+    // loads count on the first one's full barriers, so it waits for all of them,
+    // and the second one says how many it has issued.  A fill that only one of
+    // them issued lacks the other's share: the barrier is told so.
+    if (rank == 1 && leader)
+      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(base + C::OFF_MISC + 12, 0)),
+                   "r"(static_cast<int>(issued < 0x7FFFFFFF ? issued + 1 : 0x7FFFFFFF))
+                   : "memory");
+    bool clean = ok;
+    for (long long i = ring_pending(issued, C::STAGES); clean && i < issued; ++i) {
+      const int s = static_cast<int>(i % C::STAGES);
+      clean = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * s, ring_parity(i, C::STAGES), wc, 0x11 | (s << 8)));
     }
+    if (!clean && rank == 0 && leader) {
+      // (the other producer's waits are bounded: it says so in time)
+      const uint64_t t0 = globaltimer_ns();
+      while (*peer_fills == 0 && globaltimer_ns() - t0 < 2 * wn.timeout_ns) {
+      }
+      const long long theirs = *peer_fills ? *peer_fills - 1 : issued, most = issued > theirs ? issued : theirs;
+      for (long long i = ring_pending(most, C::STAGES); i < most; ++i) {
+        const int s = static_cast<int>(i % C::STAGES);
+        const uint32_t fb = bar_full + 8 * s;
+        if (i >= issued) mbar_arrive_expect_tx(fb, C::STAGE_TX / 2);
+        if (i >= theirs)
+          asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(fb), "r"(C::STAGE_TX / 2) : "memory");
+        wait_phase<false>(fb, ring_parity(i, C::STAGES), wn, 0x11 | (s << 8));
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // One thread runs the whole loop.  What comes between the epilogue's
@@ -323,11 +347,12 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             }
           }
         }
-        tc_commit_pair(bar_final, 0x1);
+        tc_commit_pair(bar_final, 0x3);
       }
       __syncwarp();
-      wait_phase<false>(bar_final, 0, wn, 0x04);
     }
+    // the last of what the commits signal in either CTA
+    wait_phase<false>(bar_final, 0, wn, 0x04);
   } else if (warp == 2 || kCols) {
     // ------------------------------------------------------------ scales
     const bool cols = warp == 3;  // the columns' scales, else the rows'

@@ -638,7 +638,7 @@ int mxgemm_set_option(mxgemm_handle_t h, int option, int64_t value) {
       h->timeout_ns = value;
       return MXGEMM_OK;
     case MXGEMM_OPT_TEST_STALL_PRODUCER:
-      if (value < 0 || value > 1) return MXGEMM_ERR_INVALID_VALUE;
+      if (value < 0 || value > 3) return MXGEMM_ERR_INVALID_VALUE;
       h->stall_producer = static_cast<int>(value);
       return MXGEMM_OK;
     case MXGEMM_OPT_SCHEDULER:

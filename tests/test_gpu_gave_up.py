@@ -1,9 +1,11 @@
 """Calls whose waits give up: they end with a status, and the handle works as
-before afterwards.  The test hook keeps loads from being issued, so that nothing
-is on its way when a kernel ends; test_ring.py plays the rest on the CPU."""
+before afterwards.  The test hook keeps loads from being issued; where one CTA of a
+pair stops alone, what the other has loaded lands long before the waits run out."""
 import pytest
 import torch
 
+import plain64
+import test_gpu_block128 as tb
 import test_gpu_cache as tc
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +66,23 @@ def test_prompts(h, lens, news, kv, group, d, page):
         assert torch.equal(O, want) and torch.equal(L, lse)
         status, detail = mx.mxgemm_get_device_status(h)
         assert (status == mx.ERR_TIMEOUT and 0x41 <= detail <= 0x4F) if read == 0 else (status, detail) == (0, 0)
+
+
+# the CTAs of a pair stop at different loads: what one of them has issued alone lands before the pair ends
+@pytest.mark.parametrize("how", [1, 2, 3])
+@pytest.mark.parametrize("nk", [True, False])
+@pytest.mark.parametrize("m,n,k,b_block", [(300, 304, 400, 128), (300, 304, 1200, 1), (2100, 2304, 1680, 128)])
+def test_products(h, m, n, k, b_block, nk, how):
+    mx.mxgemm_set_option(h, mx.OPT_B_MAJOR, mx.B_N_BY_K if nk else mx.B_K_BY_N)
+    a, sa, b, sb = tb.operands(m, n, k, b_block, 1)
+    ref, mag = plain64.product(plain64.value(a), sa, plain64.value(b), sb, b_block)
+    if not nk:
+        b, sb = b.t().contiguous(), sb.t().contiguous()
+    dev = [t.to(tb.DEV) for t in (a, sa, b, sb)]
+    C = torch.zeros(m, n, device=tb.DEV)
+    with Stalled(h, how):
+        mx.mxgemm_run_block128(h, m, n, k, *dev, C, b_block=b_block)
+        assert mx.mxgemm_get_device_status(h)[0] == mx.ERR_TIMEOUT
+    mx.mxgemm_run_block128(h, m, n, k, *dev, C, b_block=b_block)
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
+    tb.check(C.cpu(), ref, mag, "f32")
