@@ -99,18 +99,16 @@ int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, co
   if (tiles >= kLim - 65536) return MXGEMM_ERR_INVALID_VALUE;
   const int64_t pairs = v.sm_count / 2, rem = tiles % pairs;
   p.dp_tiles = static_cast<int>(tiles - rem);
-  p.split = rem ? tail_split(rem, pairs, p.kb) : 1;
+  using P = mxg::PairCfg<0>;
+  p.split = rem && rem * 2 * P::EPI_WARPS <= mxg::kCounters ? tail_split(rem, pairs, p.kb) : 1;
   p.tail_items = static_cast<int>(rem) * p.split;
   if (p.split > 1) {
-    using P = mxg::PairCfg<0>;
     uint8_t *ws = nullptr;
     if (int st = mxg::handle_workspace(h, static_cast<size_t>(p.tail_items) * 2 * P::EPI_WARPS * 32 * 128 * sizeof(float),
                                        stream, &ws))
       return st;
     p.partials = reinterpret_cast<float *>(ws);
-    p.flags = v.flags;
-    static_assert(mxg::kFlags >= 1024 * 2 * P::EPI_WARPS, "a flag for each tail item's warps");
-    if (p.tail_items > 1024) return MXGEMM_ERR_UNSUPPORTED_DEVICE;  // (above 2048 SMs)
+    p.counters = v.counters;
   }
   p.tma_store = !p.use_acc && static_cast<int64_t>(p.N) * eb % 16 == 0;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

@@ -56,8 +56,8 @@ struct B128Params {
   // whole tiles [0, dp_tiles), a multiple of the grid's pairs, then the last
   // tail_items / split tiles with their K cut into `split` parts, one pair each
   int dp_tiles, split, tail_items;
-  float *partials;  // tail item x CTA of the pair x epilogue warp: 32 x 128 sums
-  unsigned *flags;  // the same, one word each: the sums are there (0 between launches)
+  float *partials;     // tail item x CTA of the pair x epilogue warp: 32 x 128 sums
+  unsigned *counters;  // tail tile x CTA of the pair x epilogue warp: parts that are there (0 between launches)
   int tma_store;  // C's rows are multiples of 16 bytes and nothing is added
   // skinny
   int nm;      // M rounded up to 16
@@ -149,7 +149,8 @@ struct PairCfg {
 
 // Work i of pair `unit`: a tile and its K blocks [kb, ke).  The tiles that do not
 // fill the last wave (all of them where there are fewer than pairs) are cut
-// along K, and the first part's pair adds the others' sums in order.
+// along K, and the pair whose part is done last adds the parts' sums in order.
+// A pair has one part at most: part `unit`.
 struct PairWork {
   int tile, kb, ke, part, item;
 };
@@ -247,8 +248,10 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     uint32_t ph = 0;
     long long issued = 0;
     bool ok = true;
-    // (tests: no loads, or, of one CTA of each pair, two)
-    const long long stop = p.stall_producer == 1 ? 0 : p.stall_producer == 2 + static_cast<int>(rank) ? 2 : -1;
+    // (tests: no loads, or, of one CTA of each pair, two, or none of the first pair)
+    const long long stop = p.stall_producer == 1 || (p.stall_producer == 4 && unit == 0) ? 0
+                           : p.stall_producer == 2 + static_cast<int>(rank)              ? 2
+                                                                                         : -1;
     PairWork w;
     for (int i = 0; ok && pair_work(p, unit, units, i, w); ++i) {
       int mt, nt;
@@ -408,7 +411,23 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     uint32_t full_at = bar_acc_full, full_ph = 0;
     uint32_t empty_at = mapa_shared(bar_acc_empty, 0);  // of the pair's first CTA
     uint32_t n = 0;  // groups of eight K blocks so far
-    bool ok = true;
+    // This warp's part of a tile whose K is cut is there: whether it is the last
+    // one.  Nobody waits: the warp that arrives last adds, and leaves the counter
+    // at zero for the next launch.
+    auto arrive = [&](int item) -> bool {
+      __threadfence();
+      __syncwarp();
+      unsigned before = 0;
+      if (lane == 0) {
+        unsigned *at = p.counters + (item / p.split * 2 + static_cast<int>(rank)) * C::EPI_WARPS + w;
+        before = atomicAdd(at, 1u);
+        if (before == static_cast<unsigned>(p.split) - 1u) *at = 0;
+      }
+      before = __shfl_sync(0xFFFFFFFFu, before, 0);
+      __threadfence();
+      return before == static_cast<unsigned>(p.split) - 1u;
+    };
+    bool ok = true, arrived = false;
     PairWork pw;
     for (int i = 0; ok && pair_work(p, unit, units, i, pw); ++i) {
       int mt, nt;
@@ -504,21 +523,25 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       if (!ok) break;
       if (p.split > 1 && pw.item >= 0) {
         // 16-byte pieces of a thread's sums, 32 lanes side by side
-        auto slot = [&](int item) { return (item * 2 + static_cast<int>(rank)) * C::EPI_WARPS + w; };
-        if (pw.part > 0) {
-          float4 *to = reinterpret_cast<float4 *>(p.partials) + static_cast<int64_t>(slot(pw.item)) * 1024 + lane;
+        auto slot = [&](int part) {
+          return reinterpret_cast<float4 *>(p.partials) +
+                 static_cast<int64_t>(((pw.item - pw.part + part) * 2 + static_cast<int>(rank)) * C::EPI_WARPS + w) * 1024 + lane;
+        };
+        float4 *to = slot(pw.part);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) to[32 * j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p.flags + slot(pw.item)), "r"(1u) : "memory");
-          continue;
+        for (int j = 0; j < 32; ++j) to[32 * j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+        arrived = true;
+        if (!arrive(pw.item)) continue;
+        // The last of the tile's parts: all of their sums, in order.  Its own are
+        // still here, but for the first two (a + b is b + a) they are read back.
+        if (pw.part > 1) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) acc[j] = 0.f;
         }
-        for (int r = 1; ok && r < p.split; ++r) {
-          unsigned *flag = p.flags + slot(pw.item + r);
-          ok = wait_flags(flag, 1, 1u, wc, 0x06);
-          if (!ok) break;
-          const float4 *from = reinterpret_cast<const float4 *>(p.partials) + static_cast<int64_t>(slot(pw.item + r)) * 1024 + lane;
+#pragma unroll 1
+        for (int r = 0; r < p.split; ++r) {
+          if (r == pw.part && r <= 1) continue;
+          const float4 *from = slot(r);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float4 x = __ldcg(from + 32 * j);
@@ -527,10 +550,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             acc[4 * j + 2] += x.z;
             acc[4 * j + 3] += x.w;
           }
-          __syncwarp();
-          if (lane == 0) *flag = 0;  // for the next launch
         }
-        if (!ok) break;
       }
       // C: rows row0 .. +31, columns col0 .. +127, in pieces of 128 bytes a
       // row through this warp's 4 KB (16-byte units swizzled by the row)
@@ -622,6 +642,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         }
       }
     }
+    // (after a wait that gave up too: the counters belong to the next launch)
+    if (p.split > 1 && !arrived && unit < p.tail_items) arrive(unit);
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }

@@ -23,15 +23,12 @@ struct HandleView {
   cudaEvent_t prof_before, prof_after;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   unsigned *counters;  // kCounters words, zero between launches
-  unsigned *flags;     // kFlags words, zero between launches
 };
 
 // Counters of a handle: the arrivals of work split over CTAs, each taken by
-// at most one piece of work of a launch and left at zero by it.
+// at most one piece of work of a launch and left at zero by it, also where a
+// wait of the launch gave up.
 constexpr int kCounters = 4096;
-// Flags of a handle: one for each warp's part of a sum that is there, set by
-// its writer and cleared by its reader.
-constexpr int kFlags = 16384;
 
 HandleView handle_view(mxgemm_handle_t h);
 

@@ -105,7 +105,7 @@ struct mxgemm_ctx {
   // creation; each launch writes and waits for its own epoch (never 0)
   unsigned *flags = nullptr;
   unsigned epoch = 0;
-  unsigned *counters = nullptr;  // mxg::kCounters and mxg::kFlags words, zero between launches
+  unsigned *counters = nullptr;  // mxg::kCounters words, zero between launches
   Workspace ws;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   long long timeout_ns = 2000000000LL;
@@ -605,9 +605,9 @@ int mxgemm_create(mxgemm_handle_t *out, int device) {
     return MXGEMM_ERR_CUDA;
   }
   // a flag slot per epilogue warp of every CTA a grid can have
-  // (and, behind them, the counters of split attention work)
+  // (and, behind them, the counters of work split over CTAs)
   const size_t flag_bytes = static_cast<size_t>(h->sm_count) * mxg::Cfg<1>::EPI_WARPS * sizeof(unsigned);
-  const size_t counter_bytes = (mxg::kCounters + mxg::kFlags) * sizeof(unsigned);
+  const size_t counter_bytes = mxg::kCounters * sizeof(unsigned);
   if (cudaMalloc(&h->flags, flag_bytes + counter_bytes) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->d_status);
@@ -638,7 +638,7 @@ int mxgemm_set_option(mxgemm_handle_t h, int option, int64_t value) {
       h->timeout_ns = value;
       return MXGEMM_OK;
     case MXGEMM_OPT_TEST_STALL_PRODUCER:
-      if (value < 0 || value > 3) return MXGEMM_ERR_INVALID_VALUE;
+      if (value < 0 || value > 4) return MXGEMM_ERR_INVALID_VALUE;
       h->stall_producer = static_cast<int>(value);
       return MXGEMM_OK;
     case MXGEMM_OPT_SCHEDULER:
@@ -837,10 +837,6 @@ int mxgemm_get_device_status(mxgemm_handle_t h, mxgemm_stream_t stream_, int *st
   if (cudaMemcpy(hostv, h->d_status, sizeof(hostv), cudaMemcpyDeviceToHost) != cudaSuccess)
     return MXGEMM_ERR_CUDA;
   if (cudaMemset(h->d_status, 0, sizeof(hostv)) != cudaSuccess) return MXGEMM_ERR_CUDA;
-  // (a launch that gave up may have left some of these set)
-  if (hostv[0] == MXGEMM_ERR_TIMEOUT &&
-      cudaMemset(h->counters, 0, (mxg::kCounters + mxg::kFlags) * sizeof(unsigned)) != cudaSuccess)
-    return MXGEMM_ERR_CUDA;
   *status_out = hostv[0];
   if (detail_out) *detail_out = hostv[1];
   return MXGEMM_OK;
@@ -888,7 +884,7 @@ HandleView handle_view(mxgemm_handle_t h) {
   return HandleView{h->device,   h->sm_count,    h->d_status, static_cast<unsigned long long>(h->timeout_ns),
                     h->stall_producer, h->a_fmt, h->b_fmt,    h->b_major,
                     &h->launches, h->prof_before, h->prof_after, h->encode,
-                    h->counters, h->counters + mxg::kCounters};
+                    h->counters};
 }
 
 int handle_workspace(mxgemm_handle_t h, size_t bytes, cudaStream_t stream, uint8_t **ptr) {

@@ -95,9 +95,10 @@ typedef enum {
   MXGEMM_OPT_WAIT_TIMEOUT_NS = 2,
   /* Test hook for the failure-detection path: when 1, the load-issuing warp
    * of the next launches issues no loads, so the consumer waits run out and
-   * the kernel reports MXGEMM_ERR_TIMEOUT.  2 and 3: in mxgemm_run_block128
+   * the kernel reports MXGEMM_ERR_TIMEOUT.  2 to 4: in mxgemm_run_block128
    * with M > 64, the first (2) or the second (3) CTA of each pair stops after
-   * its second load; as 1 elsewhere.  Default 0. */
+   * its second load, or the first pair alone loads nothing (4); as 1
+   * elsewhere.  Default 0. */
   MXGEMM_OPT_TEST_STALL_PRODUCER = 3,
   /* Tile scheduler: 0 = static striding over a persistent grid of one CTA
    * (pair) per SM; 1 = cluster launch control ("TLX API Quick Reference",

@@ -86,3 +86,38 @@ def test_products(h, m, n, k, b_block, nk, how):
     mx.mxgemm_run_block128(h, m, n, k, *dev, C, b_block=b_block)
     assert mx.mxgemm_get_device_status(h) == (0, 0)
     tb.check(C.cpu(), ref, mag, "f32")
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 300, 4096), (300, 304, 6416), (2600, 2304, 4096)])
+@pytest.mark.parametrize("hidden", [False, True])
+def test_tiles_cut_along_k(h, m, n, k, hidden):
+    """One part of a tile whose K is cut gives up, the others are done: later calls
+    do not take what is left of it for theirs, be its status read, hidden behind an
+    earlier one, or not read yet."""
+    mx.mxgemm_set_option(h, mx.OPT_B_MAJOR, mx.B_N_BY_K)
+    a, sa, b, sb = tb.operands(m, n, k, 128, 1)
+    ref, mag = plain64.product(plain64.value(a), sa, plain64.value(b), sb, 128)
+    dev = [t.to(tb.DEV) for t in (a, sa, b, sb)]
+    C = torch.zeros(m, n, device=tb.DEV)
+    call = lambda: mx.mxgemm_run_block128(h, m, n, k, *dev, C)
+    call()
+    want = C.cpu()
+    tb.check(want, ref, mag, "f32")
+    for read in (True, False):
+        if hidden:  # a page number that names no page
+            pages = tc.Made([40], 1, 64, 16)
+            pages.table[0][1] = -1
+            tc.attend(h, pages, tc.queries(pages, 1, 1), None)
+        with Stalled(h, 4):
+            call()
+        if read:
+            assert mx.mxgemm_get_device_status(h)[0] == (mx.ERR_INVALID_VALUE if hidden else mx.ERR_TIMEOUT)
+        other = [t.flip(0).contiguous() for t in dev]  # other sums than the ones that were left
+        mx.mxgemm_run_block128(h, m, n, k, *other, C)
+        for _ in range(2):
+            C.zero_()
+            call()
+            assert torch.equal(C.cpu(), want)
+        if not read:
+            mx.mxgemm_get_device_status(h)
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
