@@ -189,6 +189,18 @@ int launch_gemm(mxgemm_ctx *h, const CUtensorMap &tA, const CUtensorMap &tB,
   return mxg::launch_tiled_epi<CG, 0>(L, m, kp, units, stream);
 }
 
+// A status word's two ints into `out`, after all work on `stream`, and zero
+// into the word before any that follows on it: all in the order of `stream`,
+// since other streams need not wait for the default one.
+int read_and_clear(int *word, int (&out)[2], cudaStream_t stream) {
+  if (cudaMemcpyAsync(out, word, sizeof(out), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaMemsetAsync(word, 0, sizeof(out), stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  return MXGEMM_OK;
+}
+
 int launch_blocks(int64_t work, int per_block) {
   int64_t b = cdiv(work, per_block);
   if (b < 1) b = 1;
@@ -615,7 +627,9 @@ int mxgemm_create(mxgemm_handle_t *out, int device) {
     return MXGEMM_ERR_OUT_OF_MEMORY;
   }
   h->counters = h->flags + flag_bytes / sizeof(unsigned);
-  if (cudaMemset(h->flags, 0, flag_bytes + counter_bytes) != cudaSuccess) {
+  // (done before the first launch, on whichever stream)
+  if (cudaMemset(h->flags, 0, flag_bytes + counter_bytes) != cudaSuccess ||
+      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->flags);
     cudaFree(h->d_status);
@@ -833,10 +847,7 @@ int mxgemm_get_device_status(mxgemm_handle_t h, mxgemm_stream_t stream_, int *st
   DeviceGuard g(h->device);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   int hostv[2] = {0, 0};
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return MXGEMM_ERR_CUDA;
-  if (cudaMemcpy(hostv, h->d_status, sizeof(hostv), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return MXGEMM_ERR_CUDA;
-  if (cudaMemset(h->d_status, 0, sizeof(hostv)) != cudaSuccess) return MXGEMM_ERR_CUDA;
+  if (read_and_clear(h->d_status, hostv, stream) != MXGEMM_OK) return MXGEMM_ERR_CUDA;
   *status_out = hostv[0];
   if (detail_out) *detail_out = hostv[1];
   return MXGEMM_OK;
@@ -1435,15 +1446,9 @@ extern "C" int mxgemm_noalloc_get_status(mxgemm_stream_t stream_, int *status_ou
   int st = noalloc_setup(dev, &nd);
   if (st != MXGEMM_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  // a plain synchronous copy into the caller's host ints: no pinned staging
-  // buffer is allocated
+  // a copy into the caller's host ints: no pinned staging buffer is allocated
   int hostv[2] = {0, 0};
-  if (cudaStreamSynchronize(stream) != cudaSuccess ||
-      cudaMemcpy(hostv, nd->status, sizeof(hostv), cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(nd->status, 0, sizeof(hostv)) != cudaSuccess) {
-    cudaGetLastError();
-    return MXGEMM_ERR_CUDA;
-  }
+  if (read_and_clear(nd->status, hostv, stream) != MXGEMM_OK) return MXGEMM_ERR_CUDA;
   *status_out = hostv[0];
   if (detail_out) *detail_out = hostv[1];
   return MXGEMM_OK;
