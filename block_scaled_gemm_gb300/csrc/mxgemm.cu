@@ -34,6 +34,13 @@ using mxg::KParams;
 struct Workspace {
   uint8_t *ptr = nullptr;
   size_t bytes = 0;
+  bool in_graph = false;  // a captured graph may hold its address
+};
+
+// Outgrown workspaces whose addresses graphs may hold.
+struct Outgrown {
+  uint8_t *ptr;
+  Outgrown *next;
 };
 
 // Everything a run needs besides its launches, keyed by the run's arguments.
@@ -107,6 +114,7 @@ struct mxgemm_ctx {
   unsigned epoch = 0;
   unsigned *counters = nullptr;  // mxg::kCounters words, zero between launches
   Workspace ws;
+  Outgrown *outgrown = nullptr;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   long long timeout_ns = 2000000000LL;
   int mode = 0;
@@ -158,23 +166,59 @@ int encode_2d(mxgemm_ctx *h, CUtensorMap *tm, CUtensorMapDataType dt, const void
   return r == CUDA_SUCCESS ? MXGEMM_OK : MXGEMM_ERR_CUDA;
 }
 
+bool capturing(cudaStream_t stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return st == cudaStreamCaptureStatusActive;
+}
+
+// A call on `stream` is about to use the workspace: a graph that is being
+// captured holds its address from now on.
+void use_workspace(mxgemm_ctx *h, cudaStream_t stream) {
+  if (h->ws.ptr && !h->ws.in_graph) h->ws.in_graph = capturing(stream);
+}
+
+// A workspace of at least `bytes`, for a call on `stream`.  An outgrown block
+// whose address a graph may hold is kept until the handle is destroyed; others
+// are freed in stream order.
 int ensure_workspace(mxgemm_ctx *h, size_t bytes, cudaStream_t stream) {
-  if (h->ws.bytes >= bytes) return MXGEMM_OK;
-  if (h->ws.ptr) {
+  if (h->ws.bytes >= bytes) {
+    use_workspace(h, stream);
+    return MXGEMM_OK;
+  }
+  const bool graph = capturing(stream);
+  if (h->ws.ptr && (h->ws.in_graph || graph)) {
+    Outgrown *kept = new (std::nothrow) Outgrown{h->ws.ptr, h->outgrown};
+    if (!kept) return MXGEMM_ERR_OUT_OF_MEMORY;
+    h->outgrown = kept;
+  } else if (h->ws.ptr) {
     // stream-ordered: earlier work on this stream still using it finishes first
     cudaFreeAsync(h->ws.ptr, stream);
-    h->ws.ptr = nullptr;
-    h->ws.bytes = 0;
   }
+  h->ws = Workspace{};
+  for (Plan &pl : h->plans) pl.valid = false;
   void *p = nullptr;
   size_t want = round_up(bytes, size_t(2) << 20);
-  if (cudaMallocAsync(&p, want, stream) != cudaSuccess) {
+  cudaError_t err;
+  if (graph) {
+    // outside the capture: what a graph allocates is its own
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    err = cudaMalloc(&p, want);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+  } else {
+    err = cudaMallocAsync(&p, want, stream);
+  }
+  if (err != cudaSuccess) {
     cudaGetLastError();
     return MXGEMM_ERR_OUT_OF_MEMORY;
   }
   h->ws.ptr = static_cast<uint8_t *>(p);
   h->ws.bytes = want;
-  for (Plan &pl : h->plans) pl.valid = false;
+  h->ws.in_graph = graph;
   return MXGEMM_OK;
 }
 
@@ -535,6 +579,7 @@ int run_swapab(mxgemm_ctx *h, int64_t M, int64_t N, int64_t K, const void *A, co
     pl.ws = h->ws.ptr;
     pl.valid = true;
   }
+  use_workspace(h, stream);
   if (plan->pad_b) {
     mxg::pad_rows_kernel<<<launch_blocks(K * (plan->npad / 16), 256), 256, 0, stream>>>(
         static_cast<const uint8_t *>(B), K, N, plan->npad, h->ws.ptr, 8);
@@ -805,6 +850,7 @@ int mxgemm_run(mxgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *A
   }
 
   // ---- launches: [B re-pitch], scale repack, GEMM
+  use_workspace(h, stream);
   if (plan->pad_b) {
     mxg::pad_rows_kernel<<<launch_blocks(K * (plan->npad / 16), 256), 256, 0, stream>>>(
         static_cast<const uint8_t *>(B), K, N, plan->npad, h->ws.ptr + off_b, plan->b_bits);
@@ -872,6 +918,11 @@ int mxgemm_destroy(mxgemm_handle_t h) {
     DeviceGuard g(h->device);
     cudaDeviceSynchronize();
     if (h->ws.ptr) cudaFree(h->ws.ptr);
+    while (Outgrown *o = h->outgrown) {
+      h->outgrown = o->next;
+      cudaFree(o->ptr);
+      delete o;
+    }
     if (h->d_status) cudaFree(h->d_status);
     if (h->flags) cudaFree(h->flags);
     HostPipe &hp = h->hp;

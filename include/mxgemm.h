@@ -37,6 +37,11 @@
  * and its internal workspace is reused in stream order, so concurrent calls
  * on different streams need different handles.
  *
+ * Graphs: calls may be captured, with or without an earlier call of their
+ * sizes.  A captured call holds the handle's workspace of that time, which
+ * later, larger calls do not free: it lives until mxgemm_destroy, so the handle
+ * has to outlive its graphs, and a replay counts as a call on its stream.
+ *
  * Entry points: mxgemm_run (device operands), mxgemm_run_host (host
  * operands, copies pipelined with the GEMM), mxgemm_run_noalloc (no device
  * allocation, fixed scratch; with mxgemm_noalloc_get_status and
@@ -512,9 +517,8 @@ int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t 
  * pages may hold anything, NaN codes included.  The split of the work, and so
  * the order of the sums, depends on the lengths and sizes alone: equal calls
  * give equal bits.  Q and O 16-byte aligned, q_pitch % 8 == 0
- * (MXGEMM_ERR_MISALIGNED).  The handle's workspace holds partial results; it
- * grows with the first call of a size, which therefore comes before a stream
- * capture (as for mxgemm_run_block128 with few or ragged tiles). */
+ * (MXGEMM_ERR_MISALIGNED).  The handle's workspace holds partial results (as for
+ * mxgemm_run_block128 with few or ragged tiles). */
 int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
                            int64_t heads, const int32_t *page_table, int64_t table_pitch,
                            const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
