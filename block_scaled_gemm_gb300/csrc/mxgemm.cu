@@ -109,7 +109,8 @@ struct mxgemm_ctx {
   int sm_count = 0;
   int *d_status = nullptr;  // [0] status code, [1] detail
   // partial-sum flags: one slot per (CTA, epilogue warp), zeroed once at
-  // creation; each launch writes and waits for its own epoch (never 0)
+  // creation; each launch writes and waits for its own epoch (never 0), and a
+  // captured one has them zeroed before it
   unsigned *flags = nullptr;
   unsigned epoch = 0;
   unsigned *counters = nullptr;  // mxg::kCounters words, zero between launches
@@ -165,6 +166,8 @@ int encode_2d(mxgemm_ctx *h, CUtensorMap *tm, CUtensorMapDataType dt, const void
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MXGEMM_OK : MXGEMM_ERR_CUDA;
 }
+
+size_t flag_words(const mxgemm_ctx *h) { return static_cast<size_t>(h->sm_count) * mxg::Cfg<1>::EPI_WARPS; }
 
 bool capturing(cudaStream_t stream) {
   cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
@@ -663,7 +666,7 @@ int mxgemm_create(mxgemm_handle_t *out, int device) {
   }
   // a flag slot per epilogue warp of every CTA a grid can have
   // (and, behind them, the counters of work split over CTAs)
-  const size_t flag_bytes = static_cast<size_t>(h->sm_count) * mxg::Cfg<1>::EPI_WARPS * sizeof(unsigned);
+  const size_t flag_bytes = flag_words(h) * sizeof(unsigned);
   const size_t counter_bytes = mxg::kCounters * sizeof(unsigned);
   if (cudaMalloc(&h->flags, flag_bytes + counter_bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -851,6 +854,13 @@ int mxgemm_run(mxgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *A
 
   // ---- launches: [B re-pitch], scale repack, GEMM
   use_workspace(h, stream);
+  // A captured launch has the same epoch in every replay: its flags, which
+  // would be the last replay's, are cleared with it.
+  if (plan->kp.sk_ctas > 0 && capturing(stream) &&
+      cudaMemsetAsync(h->flags, 0, flag_words(h) * sizeof(unsigned), stream) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
   if (plan->pad_b) {
     mxg::pad_rows_kernel<<<launch_blocks(K * (plan->npad / 16), 256), 256, 0, stream>>>(
         static_cast<const uint8_t *>(B), K, N, plan->npad, h->ws.ptr + off_b, plan->b_bits);

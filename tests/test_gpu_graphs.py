@@ -1,5 +1,7 @@
 """Captured calls and a workspace that grows afterwards: a graph keeps the block
 that it was captured with, and a call that is captured first needs none before."""
+import ctypes
+
 import pytest
 import torch
 
@@ -118,3 +120,58 @@ def test_mx_product_captured_before_growth(h):
         assert torch.equal(C, want)
         grow(h)
     del graph
+
+
+def node_types(call):
+    """cudaGraphNodeType of each node that `call` adds to a capture (kernel 0, memset 2)."""
+    rt = ctypes.CDLL("libcudart.so.13")
+    s = torch.cuda.Stream()
+    graph, n = ctypes.c_void_p(), ctypes.c_size_t(0)
+    with torch.cuda.stream(s):
+        assert rt.cudaStreamBeginCapture(ctypes.c_void_p(s.cuda_stream), 1) == 0
+        call()
+        assert rt.cudaStreamEndCapture(ctypes.c_void_p(s.cuda_stream), ctypes.byref(graph)) == 0
+    assert rt.cudaGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes, kind = (ctypes.c_void_p * n.value)(), ctypes.c_int()
+    assert rt.cudaGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    kinds = []
+    for node in nodes:
+        assert rt.cudaGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        kinds.append(kind.value)
+    assert rt.cudaGraphDestroy(graph) == 0
+    return kinds
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_mx_product_with_shared_tiles_is_replayed(h, packed):
+    """Tiles that several CTAs share: a replay waits for its own partial sums, not for
+    the last replay's, which came of other inputs."""
+    g = torch.Generator().manual_seed(4)
+    M, N, K = 2560, 2560, 8192  # 100 tiles of 256 x 256, 64 K steps
+    mx.mxgemm_set_option(h, mx.OPT_SCALE_LAYOUT, mx.SCALES_PACKED if packed else mx.SCALES_ROW_MAJOR)
+    sources = [tb.random_codes((M, K), g).to(DEV) for _ in range(3)]
+    A, B = sources[0].clone(), tb.random_codes((N, K), g).to(DEV)
+    n = M * K // 32 if not packed else mx.mxgemm_scale_bytes(M, K, False, mx.SCALES_PACKED)
+    As, Bs = (torch.randint(124, 130, (n,), generator=g, dtype=torch.uint8).to(DEV) for _ in range(2))
+    C = torch.empty(M, N, device=DEV)
+    call = lambda: mx.mxgemm_run(h, M, N, K, A, As, B, Bs, C, stream=torch.cuda.current_stream())
+    want = []
+    for a in sources:
+        A.copy_(a)
+        call()
+        torch.cuda.synchronize()
+        want.append(C.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    assert 2 in node_types(call)  # the flags of the shared tiles are cleared by every replay
+    for i in (0, 1, 2, 1, 0, 2, 0):
+        A.copy_(sources[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C, want[i])
+        if i == 2:
+            call()
+            torch.cuda.synchronize()
+            assert torch.equal(C, want[i])
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
