@@ -205,6 +205,15 @@ IN_F32 = 0
 IN_BF16 = 1
 
 
+def _in_dtype(X) -> int:
+    """IN_F32 or IN_BF16 as X's dtype says; a bare address counts as float32."""
+    import torch
+    dtype = getattr(X, "dtype", torch.float32)
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise ValueError(f"X: float32 or bfloat16 (or x_dtype given), not {dtype}")
+    return IN_BF16 if dtype is torch.bfloat16 else IN_F32
+
+
 def mxgemm_quantize(X, R, C, codes, scales, along_cols=False, x_dtype=None, stream=None,
                     check: bool = True, rand_bits=None, scale_layout=SCALES_ROW_MAJOR) -> int:
     """MX-quantize the R x C device matrix X (float32 or bfloat16) into E4M3
@@ -216,8 +225,7 @@ def mxgemm_quantize(X, R, C, codes, scales, along_cols=False, x_dtype=None, stre
     order a run with OPT_SCALE_LAYOUT = SCALES_PACKED reads
     (mxgemm_scale_bytes bytes)."""
     if x_dtype is None:
-        import torch
-        x_dtype = IN_BF16 if getattr(X, "dtype", None) == torch.bfloat16 else IN_F32
+        x_dtype = _in_dtype(X)
     lib = library()
     if rand_bits is None and scale_layout == SCALES_ROW_MAJOR:
         st = lib.mxgemm_quantize(_ptr(X), int(x_dtype), int(R), int(C), int(bool(along_cols)),
@@ -309,8 +317,7 @@ def mxgemm_quantize_block128(X, R, C, codes, scales, block=BLOCK_ROWS, x_dtype=N
     C x round_up(R, 16), scales C x ceil(R/128)), BLOCK_TILES 128 x 128 (codes
     R x C, scales ceil(R/128) x ceil(C/128))."""
     if x_dtype is None:
-        import torch
-        x_dtype = IN_BF16 if getattr(X, "dtype", None) == torch.bfloat16 else IN_F32
+        x_dtype = _in_dtype(X)
     st = library().mxgemm_quantize_block128(_ptr(X), int(x_dtype), int(R), int(C), int(block),
                                             _ptr(codes), _ptr(scales), _stream(stream))
     if check:
