@@ -326,16 +326,19 @@ def mxgemm_quantize_block128(X, R, C, codes, scales, block=BLOCK_ROWS, x_dtype=N
 
 
 class Cache:
-    """An 8-bit key/value cache: uint8 tensors K and V (pages x kv heads x page
-    size x head dim) and float32 tensors of their scales (pages x kv heads)."""
+    """An 8-bit key/value cache: tensors K and V of E4M3 codes (uint8 or float8_e4m3fn,
+    pages x kv heads x page size x head dim) and float32 tensors of their scales
+    (pages x kv heads)."""
 
     def __init__(self, K, V, K_scale, V_scale):
         shape, dims = K.shape, K_scale.shape
         if len(shape) != 4 or V.shape != shape or dims != shape[:2] or V_scale.shape != dims:
             raise ValueError("K and V: pages x kv heads x page size x head dim, scales: pages x kv heads")
-        if not (K.element_size() == V.element_size() == 1 and K_scale.element_size() == V_scale.element_size() == 4
+        import torch
+        if not (all(t.element_size() == 1 and (t.dtype is torch.float8_e4m3fn or not t.is_floating_point()) for t in (K, V))
+                and K_scale.dtype is V_scale.dtype is torch.float32
                 and K.is_contiguous() and V.is_contiguous() and K_scale.is_contiguous() and V_scale.is_contiguous()):
-            raise ValueError("a cache is dense, with 8-bit codes and float32 scales")
+            raise ValueError("a cache is dense, with E4M3 codes and float32 scales")
         self.K, self.V, self.K_scale, self.V_scale = K, V, K_scale, V_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
         self._c = _CACHE_STRUCT.pack(K.data_ptr(), V.data_ptr(), K_scale.data_ptr(), V_scale.data_ptr(),

@@ -19,3 +19,18 @@ def test_quantizers_take_their_types_and_addresses(quantize):
     """Refused by the library for other reasons (no device pointers)."""
     for x in (torch.zeros(64, 64), torch.zeros(64, 64).bfloat16(), None):
         assert getattr(mx, quantize)(x, 64, 64, None, None, check=False) == mx.ERR_INVALID_VALUE
+
+
+def test_cache_refuses_other_scales_and_codes():
+    codes, scales = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.ones(3, 2)
+    mx.Cache(codes, codes.clone(), scales, scales.clone())
+    f8 = codes.view(torch.float8_e4m3fn)
+    mx.Cache(f8, f8.clone(), scales, scales.clone())
+    for wrong in (scales.int(), scales.view(torch.int32), scales.double(), scales.half()):
+        for pair in ((wrong, scales), (scales, wrong), (wrong, wrong)):
+            with pytest.raises(ValueError):
+                mx.Cache(codes, codes, *pair)
+    e5, z = codes.view(torch.float8_e5m2), codes.view(torch.float8_e4m3fnuz)
+    for pair in ((e5, codes), (codes, e5), (z, z), (codes.half(), codes.half())):
+        with pytest.raises(ValueError):
+            mx.Cache(*pair, scales, scales)
