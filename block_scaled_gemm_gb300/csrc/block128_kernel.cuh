@@ -451,6 +451,10 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         for (int i = 0; i < kRows; ++i)
           s[i] = sc[(ks & (C::KB - 1)) * C::AS_PITCH + 32 * q + (kCols ? (lane >> 2) + 8 * i : lane)];
         sc += C::KB * C::AS_PITCH + (ks & (C::KB - 1)) * C::BS_PITCH;
+        // (The product of the scales has to stay in FP32's normal range, which the
+        // interface asks for: a test of it here, for each K block, with a loop in
+        // two steps for the others, 110 -> 122 us at 2048 x 9728 x 8192; by the
+        // warps that bring the scales, 139 us.)
         if constexpr (!kCols) s[0] *= sc[half];
       };
       ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));

@@ -414,6 +414,12 @@ int mxgemm_noalloc_set_option(int option, int64_t value);
  *             MXGEMM_B_N_BY_K, ceil(K/128) x ceil(N/b_block) for
  *             MXGEMM_B_K_BY_N.
  *   C       : M x N, out_dtype; use_acc as for mxgemm_run.
+ * Range of the scales: the two scales of a block are multiplied in FP32 before
+ * they meet its sum, so A_scale * B_scale is to be 0 or in FP32's normal range
+ * (2^-126 <= |product| < 2^128); below it the scaled sum loses bits or becomes
+ * 0 although it may be normal itself.  With b_block = 1 and M > 64 the sum meets
+ * B's scale first, which is to be 0 or between 2^-94 and 2^89 in magnitude, and
+ * then A's.
  * A, B and C 16-byte aligned, the scales 4-byte (MXGEMM_ERR_MISALIGNED).
  * MXGEMM_OPT_A_FORMAT and MXGEMM_OPT_B_FORMAT may be E4M3 or E5M2 (others:
  * MXGEMM_ERR_INVALID_VALUE); the wait limit, the stall hook, the profile
