@@ -9,8 +9,10 @@
 //   o = (sum_j w_j V_j) / (sum_j w_j / vs_j):
 // the weights that meet the codes in the tensor cores are at most 2^8 and the
 // largest is near 1 whatever the pages' scales are, so FP16 (11 bits) holds
-// them, and V's codes, E4M3, are exact in FP16.  So are K's, and Q's BF16 after
-// its row is divided by a power of two; sums are FP32.
+// them, and V's codes, E4M3, are exact in FP16.  So are K's.  A row of Q is
+// multiplied by a power of two that brings its largest value to 2^15 .. 2^16: its
+// BF16 values are then exact in FP16 down to 2^-32 of that, and below they are
+// off by 2^-40 of it at most.  Sums are FP32.
 //
 // Transposed: S^T = K Q^T and O^T = V^T P^T with mma.m16n8k16, so that 8
 // query rows (the heads of a group) fill the MMA's narrow side and K and V,
@@ -99,6 +101,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ void cp_async4_cache(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+
+// Exponent of the power of two for a row of Q whose largest magnitude is `top`
+// (0 for a row of zeros; 2^126 is the largest, whose reciprocal is normal).
+__device__ __forceinline__ int q_exponent(float top) {
+  return top > 0.f ? min(142 - (__float_as_int(top) >> 23), 126) : 0;
+}
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
 
 constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100, for 1 / vs
 
@@ -425,17 +434,16 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      // the row over 2^e, |q| < 2 (2^e of its largest; 1 for a row of zeros)
-      const int e = top > 0.f ? min(max((__float_as_int(top) >> 23) - 127, -126), 126) : 0;
-      const float inv = __int_as_float((127 - e) << 23);
+      const int e = q_exponent(top);
+      const float up = pow2(e);
 #pragma unroll
       for (int i = 0; i < KW; ++i)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t b = u[2 * i + c];
-          q[n][i][c] = half2_of(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv);
+          q[n][i][c] = half2_of(__uint_as_float(b << 16) * up, __uint_as_float(b & 0xFFFF0000u) * up);
         }
-      const float c = p.scale * 1.44269504088896340736f * __int_as_float((127 + e) << 23);
+      const float c = p.scale * 1.44269504088896340736f * pow2(-e);
       cq[n][0] = __shfl_sync(0xFFFFFFFFu, c, 8 * t);
       cq[n][1] = __shfl_sync(0xFFFFFFFFu, c, 8 * t + 4);
     }

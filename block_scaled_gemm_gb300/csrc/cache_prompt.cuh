@@ -7,9 +7,9 @@
 // One CTA takes 256 query rows of a sequence and key/value head (row = token *
 // group + head of the group, so that a group's heads share what is read) as
 // two tiles of 128, and walks the keys in tiles of 128:
-//   S_i = Q_i K^T    tcgen05.mma.kind::f16, Q (BF16 over a power of two of its
-//                    row, exact in FP16) and K (E4M3 converted to FP16,
-//                    exact) in shared memory, S in TMEM
+//   S_i = Q_i K^T    tcgen05.mma.kind::f16, Q (BF16 times its row's power of two,
+//                    in FP16) and K (E4M3 converted to FP16, exact) in shared
+//                    memory, S in TMEM
 //   P_i              softmax warps, one thread a row: S from TMEM, P (FP16)
 //                    back into S's columns
 //   O_i += P_i V     P from TMEM, V (FP16) in shared memory, O in TMEM
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     if (i < nq) {
       const bool live = r < rows;
       const int tok = (row0 + (live ? r : 0)) / p.group, head = h * p.group + (row0 + (live ? r : 0)) % p.group;
-      // Q over a power of two of its row, |q| < 2, in FP16; rows past the last are zero
+      // Q times its row's power of two in FP16; rows past the last are zero
       float cq;
       {
         // whole rows side by side, kUnits lanes (16 bytes each) a row
@@ -384,7 +384,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         }
         float top = 0.f;  // of this thread's row
         const uint32_t dst = base + S::OFF_Q + i * S::TILE16 + (unit >> 3) * 16384;
-        auto exponent = [](float t) { return t > 0.f ? min(max((__float_as_int(t) >> 23) - 127, -126), 126) : 0; };
 #pragma unroll
         for (int n = 0; n < 32 / kRows; ++n) {
           const int rr = 32 * qd + kRows * n + sub;
@@ -398,14 +397,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           const float own = __shfl_sync(0xFFFFFFFFu, t, (lane % kRows) * kUnits);
           if (lane / kRows == n) top = own;
           // (a negative scale's sign goes to Q: the exponents' factors are positive)
-          const float inv = copysignf(__int_as_float((127 - exponent(t)) << 23), p.scale);
+          const float up = copysignf(pow2(q_exponent(t)), p.scale);
           uint32_t y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            y[k] = half2_of(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xFFFF0000u) * inv);
+            y[k] = half2_of(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
           st_shared_v4(dst + rr * 128 + (((unit & 7) ^ (rr & 7)) << 4), y[0], y[1], y[2], y[3]);
         }
-        cq = fabsf(p.scale) * 1.44269504088896340736f * __int_as_float((127 + exponent(top)) << 23);
+        cq = fabsf(p.scale) * 1.44269504088896340736f * pow2(-q_exponent(top));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full + 8 * i);

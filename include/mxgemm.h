@@ -519,7 +519,8 @@ int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t 
  *   page_table, kv_len, q_start : as for mxgemm_cache_append.
  *   scale : finite.  window, sinks >= 0.  tokens * heads < 2^31.
  * Sums and softmax statistics are FP32; the codes enter the products exactly,
- * the weights p rounded to FP16.  Places past a sequence's end and absent
+ * and so does Q down to 2^-32 of the largest value of its row (a token's head),
+ * below to 2^-40 of that; the weights p are rounded to FP16.  Places past a sequence's end and absent
  * pages may hold anything, NaN codes included.  The split of the work, and so
  * the order of the sums, depends on the lengths and sizes alone: equal calls
  * give equal bits.  Q and O 16-byte aligned, q_pitch % 8 == 0
