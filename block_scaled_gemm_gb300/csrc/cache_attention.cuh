@@ -4,15 +4,17 @@
 //   x_j = scale * q . k_j,  k_j = ks * K_j,  v_j = vs * V_j   (ks, vs per page)
 //   o = sum_j e^(x_j) v_j / sum_j e^(x_j)
 //
-// A page's vs goes into the exponent: with w_j = 2^(x_j log2 e + log2 vs - m),
+// A page's vs goes into the exponent: with w_j = 2^(x_j log2 e + log2 vs - m + 7),
 // m the running maximum of that exponent,
-//   o = (sum_j w_j V_j) / (sum_j w_j / vs_j):
-// the weights that meet the codes in the tensor cores are at most 2^8 and the
-// largest is near 1 whatever the pages' scales are, so FP16 (11 bits) holds
-// them, and V's codes, E4M3, are exact in FP16.  So are K's.  A row of Q is
-// multiplied by a power of two that brings its largest value to 2^15 .. 2^16: its
-// BF16 values are then exact in FP16 down to 2^-32 of that, and below they are
-// off by 2^-40 of it at most.  Sums are FP32.
+//   o = (sum_j w_j V_j) / (2^7 sum_j 2^-7 w_j / vs_j):
+// the weights that meet the codes in the tensor cores are at most 2^15 and the
+// largest is near 2^7 whatever the pages' scales are, so FP16 holds them: with
+// 11 bits down to 2^-21 of the largest, and to 2^-32 of it below, so that the many
+// small weights of a long sequence count beside a large one.  FP16 also holds
+// V's and K's codes, E4M3, exactly.  A row of Q is multiplied by a power of two
+// that brings its largest value to 2^15 .. 2^16: its BF16 values are then exact in
+// FP16 down to 2^-32 of that, and below they are off by 2^-40 of it at most.  Sums
+// are FP32.
 //
 // Transposed: S^T = K Q^T and O^T = V^T P^T with mma.m16n8k16, so that 8
 // query rows (the heads of a group) fill the MMA's narrow side and K and V,
@@ -108,6 +110,8 @@ __device__ __forceinline__ int q_exponent(float top) {
   return top > 0.f ? min(142 - (__float_as_int(top) >> 23), 126) : 0;
 }
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
+
+constexpr float kWeightUp = 7.f, kWeightDown = 0.0078125f;  // weights carry 2^7, and sums give it back
 
 constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100, for 1 / vs
 
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[mt][n][j] += s1[mt][n][j];
-      // exponents; ivs = 1 / vs
+      // exponents; ivs = 2^-7 / vs
       const bool ok0 = pg_ok[2 * st] != 0, ok1 = per == 2 ? pg_ok[2 * st + 1] != 0 : ok0;
       float ivs[2];
       const int jlast = key0 + 31;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       for (int mt = 0; mt < 2; ++mt) {
         const float ks = sc[4 * st + (per == 2 ? mt : 0)], vs = sc[4 * st + 2 + (per == 2 ? mt : 0)];
         const float v1 = fmaxf(vs, kScaleFloor), lv = lg2(v1);
-        ivs[mt] = __frcp_rn(v1);
+        ivs[mt] = __frcp_rn(v1) * kWeightDown;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+        const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kWeightUp, m1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kWeightUp;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const float w0 = ex2(s[mt][n][0] - m0), w1 = ex2(s[mt][n][1] - m1);
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         if (split) {
           *reinterpret_cast<float4 *>(part + r * D + d) = a;
         } else if (r < rows) {
-          const float k = sum == 0.f ? 0.f : 1.f / sum;
+          const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
           const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * k, a.y * k), hi = __floats2bfloat162_rn(a.z * k, a.w * k);
           *reinterpret_cast<uint2 *>(p.O + (static_cast<int64_t>(tok) * p.heads + head) * D + d) =
@@ -750,7 +754,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
 #pragma unroll
           for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
           if (rr >= rows) continue;
-          const float k = sum == 0.f ? 0.f : 1.f / sum;
+          const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           const int tok = at.s.first + (row0 + rr) / p.group, head = h * p.group + (row0 + rr) % p.group;
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) {

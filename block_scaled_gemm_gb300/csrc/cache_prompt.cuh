@@ -2,7 +2,7 @@
 // rows (chunks of prompts), on the tensor cores.
 //
 // The mathematics is that of cache_attention.cuh: w_j = 2^(x_j log2 e +
-// log2 vs - m) meets the codes, o = (sum w_j V_j) / (sum w_j / vs_j).
+// log2 vs - m + 7) meets the codes, o = (sum w_j V_j) / (2^7 sum 2^-7 w_j / vs_j).
 //
 // One CTA takes 256 query rows of a sequence and key/value head (row = token *
 // group + head of the group, so that a group's heads share what is read) as
@@ -51,7 +51,7 @@ struct PromptCfg {
   static constexpr int OFF_V = OFF_K + 2 * TILE16;  // two buffers
   static constexpr int OFF_K8 = OFF_V + 2 * TILE16;
   static constexpr int OFF_V8 = OFF_K8 + TILE8;
-  static constexpr int OFF_SC = OFF_V8 + TILE8;  // [4 tiles][ks, log2 vs, 1/vs][8 groups of 16 keys]
+  static constexpr int OFF_SC = OFF_V8 + TILE8;  // [4 tiles][ks, log2 vs, 2^-7/vs][8 groups of 16 keys]
   static constexpr int OFF_PG = OFF_SC + 4 * 3 * 8 * 4;  // [4 tiles] bit mask of the groups that are there
   static constexpr int OFF_BAR = OFF_PG + 16;
   static constexpr int NUM_BARS = 4 + 2 * 4 + 2 + 4 + 2 + 2 + 1;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           float *sc = scales + (j & 3) * 24 + lane;
           sc[0] = ks;
           sc[8] = lg2(vs);
-          sc[16] = __frcp_rn(vs);
+          sc[16] = __frcp_rn(vs) * kWeightDown;
         }
         if (lane == 0) groups[j & 3] = there;
         __syncwarp();
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             tmem_st_wait();
           }
         }
-        const float ms = m == -INFINITY ? 0.f : m;
+        const float ms = m == -INFINITY ? 0.f : m - kWeightUp;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         } else {
           // through the rows of Q, whose products are done: a store of whole
           // lines, where a thread's own row would touch 32
-          const float k = l == 0.f ? 0.f : 1.f / l;
+          const float k = l == 0.f ? 0.f : kWeightDown / l;
           const uint32_t rr = 32 * qd + lane, q_row = base + S::OFF_Q + i * S::TILE16 + rr * 128;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
             if (mc != -INFINITY) sum = fmaf(__ldcg(first + c * S::PARTIAL + S::ROWS * D + S::ROWS + r), ex2(mc - top), sum);
           }
-          const float k = sum == 0.f ? 0.f : 1.f / sum;
+          const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;
 #pragma unroll 1
           for (int d = 0; d < D; d += 16) {

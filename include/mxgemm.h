@@ -520,7 +520,8 @@ int mxgemm_cache_append(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t 
  *   scale : finite.  window, sinks >= 0.  tokens * heads < 2^31.
  * Sums and softmax statistics are FP32; the codes enter the products exactly,
  * and so does Q down to 2^-32 of the largest value of its row (a token's head),
- * below to 2^-40 of that; the weights p are rounded to FP16.  Places past a sequence's end and absent
+ * below to 2^-40 of that; the weights p are rounded to FP16's 11 bits down to
+ * 2^-21 of a row's largest, and to 2^-32 of it below.  Places past a sequence's end and absent
  * pages may hold anything, NaN codes included.  The split of the work, and so
  * the order of the sums, depends on the lengths and sizes alone: equal calls
  * give equal bits.  Q and O 16-byte aligned, q_pitch % 8 == 0
