@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     in.to(p, ROWS, x);
     const int h = in.h, key0 = in.key(x);
     int pg = -1;
-    if (lane < per && key0 + 16 * lane < in.k.end) pg = load_page(p.b, p.c, in.b, (key0 + 16 * lane) >> lg);
+    // (a page of which no query sees a key is left alone: a window may have passed it)
+    const int k0 = key0 + 16 * lane;
+    if (lane < per && k0 < in.k.end && (k0 + 32 / per > in.k.win_lo || k0 < p.sinks)) pg = load_page(p.b, p.c, in.b, k0 >> lg);
     const uint32_t bar = bars + 8 * st;
     const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
     if (lane < per) {

@@ -208,9 +208,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       int k_loads = 0, v_loads = 0;
       for (int j = 0; ok && j < tiles; ++j) {
         const int key0 = tile_key(j);
-        // lane g < 8: the 16 keys of group g
+        // lane g < 8: the 16 keys of group g, unless none of the rows sees a key of
+        // their page (a window may have passed it)
         int pg = -1;
-        if (lane < 8 && key0 + 16 * lane < end) pg = load_page(p.b, p.c, b, (key0 + 16 * lane) >> lg);
+        const int k0 = key0 + 16 * lane, page0 = k0 >> lg << lg;
+        if (lane < 8 && k0 < end && (page0 + (1 << lg) > win_lo || page0 < p.sinks)) pg = load_page(p.b, p.c, b, k0 >> lg);
         float ks = 1.f, vs = 1.f;
         if (pg >= 0) {
           const int64_t cell = static_cast<int64_t>(pg) * p.c.kv_heads + h;

@@ -460,7 +460,9 @@ int mxgemm_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t C, i
  *   num_pages * kv_heads * page_size < 2^31.
  * Which pages a sequence has, in order, is row b of a page table: batch rows
  * of int32, table_pitch entries apart (table_pitch * page_size <= 2^30);
- * entries past a sequence's last page are not read.  A page number outside [0, num_pages) or a length that is
+ * entries past a sequence's last page are not read, nor are those of pages of
+ * which no query of an attention call sees a key (a sliding window may have
+ * passed them, and their pages may be others' by then).  A page number outside [0, num_pages) or a length that is
  * negative or does not fit the table is not followed: what it names counts as
  * absent, and MXGEMM_ERR_INVALID_VALUE is recorded in the handle's device
  * status word. */
