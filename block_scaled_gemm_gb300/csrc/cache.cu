@@ -232,8 +232,10 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   p.group = static_cast<int>(heads / cache->kv_heads);
   p.scale = scale;
   p.causal = causal;
-  p.window = window;
-  p.sinks = sinks;
+  // (positions stay below 2^31: a longer window sees as much, and the kernels'
+  // sums with these stay far from 64 bits' end)
+  p.window = std::min(window, kLim);
+  p.sinks = std::min(sinks, kLim);
   p.O = static_cast<__nv_bfloat16 *>(O);
   p.lse = lse;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);

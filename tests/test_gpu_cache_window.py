@@ -41,3 +41,16 @@ def test_passed_pages(h, lens, news, kv, group, d, page, window, sinks):
     O, L = tc.attend(h, m, q, news, window=window, sinks=sinks)
     assert mx.mxgemm_get_device_status(h) == (0, 0)
     tc.check(m, q, n, O, L, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("longest", [2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1])
+@pytest.mark.parametrize("lens,news", [([3, 0, 200], [7, 2, 5]), ([60, 200], [200, 130])])
+def test_the_longest_windows_see_everything(h, lens, news, longest):
+    """Also where a sequence has more queries than keys: the first ones stand before position 0."""
+    m = tc.Made(lens, 2, 64, 16)
+    q = tc.queries(m, sum(news), 4)
+    want, lse = tc.attend(h, m, q, news)
+    tc.check(m, q, news, want, lse)
+    for window, sinks in ((longest, 0), (longest, longest), (1, longest)):
+        O, L = tc.attend(h, m, q, news, window=window, sinks=sinks)
+        assert torch.equal(O, want) and torch.equal(L, lse)
