@@ -671,8 +671,8 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
 #pragma unroll
       for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w * ROWS + r]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (ml[w * ROWS + r] != -INFINITY) sum += ml[(4 + w) * ROWS + r] * ex2(ml[w * ROWS + r] - top);
+      for (int w = 0; w < 4; ++w)  // (a sum of NaN stays one, also where no weight gave a maximum)
+        sum = fmaf(ml[(4 + w) * ROWS + r], ml[w * ROWS + r] == -INFINITY ? 0.f : ex2(ml[w * ROWS + r] - top), sum);
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) {
         __syncthreads();

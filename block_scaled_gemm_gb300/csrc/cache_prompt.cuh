@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           for (int c = 0; c < parts; ++c) top = fmaxf(top, __ldcg(first + c * S::PARTIAL + S::ROWS * D + r));
           for (int c = 0; c < parts; ++c) {
             const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
-            if (mc != -INFINITY) sum = fmaf(__ldcg(first + c * S::PARTIAL + S::ROWS * D + S::ROWS + r), ex2(mc - top), sum);
+            sum = fmaf(__ldcg(first + c * S::PARTIAL + S::ROWS * D + S::ROWS + r), mc == -INFINITY ? 0.f : ex2(mc - top), sum);
           }
           const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;

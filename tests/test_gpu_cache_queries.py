@@ -49,3 +49,22 @@ def test_queries_at_the_ends_of_their_type(h, news):
         q[0, 1] = 0
         O, L = tc.attend(h, m, q, news, scale=scale)
         tc.check(m, q, n, O, L, scale=scale)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,news,kv,group,d,page", [
+    ([300, 77], None, 2, 4, 128, 32), ([9000, 64], None, 1, 16, 64, 64), ([20011], None, 1, 8, 128, 64),  # whole, split
+    ([300, 250], [200, 100], 8, 4, 128, 64), ([5000], [70], 1, 1, 128, 64)])  # prompts, the second with its keys cut
+def test_nan_stays_in_its_row(h, lens, news, kv, group, d, page, value):
+    """A query that is not finite gives a NaN output and log-sum-exp, and no other row one."""
+    m = tc.Made(lens, kv, d, page, seed=sum(lens))
+    n = news or [1] * len(lens)
+    q = tc.queries(m, sum(n), kv * group)
+    want, lse = tc.attend(h, m, q, news)
+    bad = torch.zeros(sum(n), kv * group, dtype=torch.bool)
+    bad[0, 0] = bad[-1, -1] = True
+    q[0, 0] = value if value != value else q[0, 0]
+    q[0, 0, 1] = q[-1, -1, 1] = value
+    O, L = tc.attend(h, m, q, news)
+    assert torch.isnan(O[bad]).all() and torch.isnan(L[bad]).all()
+    assert torch.equal(O[~bad], want[~bad]) and torch.equal(L[~bad], lse[~bad])
