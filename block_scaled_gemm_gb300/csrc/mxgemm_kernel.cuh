@@ -43,6 +43,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "ring.h"
 
 namespace mxg {
 
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(Cfg<CG>::THREADS, 1)
   const bool fused = C::HAS_SCALE_WARP && p.fused_scales != 0;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);
+  volatile int *never = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 8);  // never raised before 2 s
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -502,6 +504,7 @@ __global__ void __launch_bounds__(Cfg<CG>::THREADS, 1)
     mbar_init(bar_stg_go, 1);
     for (int i = 0; i < C::EPI_WARPS; ++i) mbar_init(bar_cin + 8 * i, 1);
     *abort_flag = 0;
+    *never = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -783,9 +786,11 @@ __global__ void __launch_bounds__(Cfg<CG>::THREADS, 1)
         }
       }
       // Drain: every stage's last fill has been consumed (its MMA commit has
-      // arrived) before this CTA may finish.
+      // arrived) before this CTA may finish; where a wait gave up, it stays for as
+      // long as a load takes at most, whatever the other waits' limit is.
+      const WaitCtl wd{p.status, never, landing_limit(p.timeout_ns)};
       for (int i = 0; i < C::STAGES; ++i) {
-        if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * nst, nph ^ 1u, wc, 0x11 | (nst << 8))))
+        if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * nst, nph ^ 1u, wd, 0x11 | (nst << 8))))
           break;
         if (++nst == C::STAGES) {
           nst = 0;
@@ -1015,11 +1020,7 @@ __global__ void __launch_bounds__(Cfg<CG>::THREADS, 1)
         else tc_commit_pair(bar_final, 0x1);
       }
       __syncwarp();
-      WaitCtl wf = wc;
-      wf.abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 8);  // never raised
-      if (lane == 0) *wf.abort_flag = 0;
-      __syncwarp();
-      wait_phase<false>(bar_final, 0, wf, 0x04);
+      wait_phase<false>(bar_final, 0, WaitCtl{p.status, never, landing_limit(p.timeout_ns)}, 0x04);
     }
   } else if (C::HAS_SCALE_WARP && warp == C::SCALE_WARP) {
     // ------------------------------------------------------------ scale loader
@@ -1156,11 +1157,8 @@ __global__ void __launch_bounds__(Cfg<CG>::THREADS, 1)
       // after a failed wait: a staging load still in flight lands before
       // the CTA may finish
       if (staged) {
-        WaitCtl wf = wc;
-        wf.abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 12);  // never raised
-        if (lane == 0) *wf.abort_flag = 0;
-        __syncwarp();
-        __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_stg, sph, wf, 0x0B));
+        const WaitCtl wd{p.status, never, landing_limit(p.timeout_ns)};
+        __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_stg, sph, wd, 0x0B));
       }
     }
   } else {
@@ -1351,7 +1349,9 @@ __global__ void __launch_bounds__(Cfg<CG>::THREADS, 1)
                   tma_load_2d(region + (2 * cc + rh) * 2048, &tmC, colb + cc * CCOLS, row0w + 16 * rh, cbar);
           }
           __syncwarp();
-          if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(cbar, 0, wc, 0x0E | ((t & 0xFFFF) << 16)))) break;
+          // (this warp's own loads: they land whoever gives up)
+          const WaitCtl wd{p.status, never, landing_limit(p.timeout_ns)};
+          if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(cbar, 0, wd, 0x0E | ((t & 0xFFFF) << 16)))) break;
           const int r16 = lane & 15;
           const uint32_t swz = r16 & 7;
 #pragma unroll

@@ -61,6 +61,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "ring.h"
 
 namespace mxg {
 
@@ -293,10 +294,11 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS, 1)
       }
     }
     // drain: every fill of this launch has been consumed before the CTA
-    // may finish (a stage never filled passes at once)
+    // may finish (a stage never filled passes at once); where a wait gave up, it
+    // stays for as long as a load takes at most, whatever the other waits' limit is
     for (int i = 0; i < S::STAGES; ++i) {
-      if (!__all_sync(0xFFFFFFFFu, swap_wait<false>(bar_empty + 8 * st, ph ^ 1u, p.status, abort_flag,
-                                                    p.timeout_ns, 0x11 | (st << 8))))
+      if (!__all_sync(0xFFFFFFFFu, swap_wait<false>(bar_empty + 8 * st, ph ^ 1u, p.status, never,
+                                                    landing_limit(p.timeout_ns), 0x11 | (st << 8))))
         break;
       if (++st == S::STAGES) {
         st = 0;
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS, 1)
     // before the ring may be reused for the cluster reduction
     if (leader) tc_commit(bar_final);
     __syncwarp();
-    swap_wait<false>(bar_final, 0, p.status, never, p.timeout_ns, 0x04);
+    swap_wait<false>(bar_final, 0, p.status, never, landing_limit(p.timeout_ns), 0x04);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale builder
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS, 1)
       for (int slot = 0; slot < S::SD; ++slot)
         if ((pending >> slot) & 1u)
           __all_sync(0xFFFFFFFFu, swap_wait<false>(bar_stg + 8 * slot, (sph >> slot) & 1u, p.status, never,
-                                                   p.timeout_ns, 0x0B | (slot << 8)));
+                                                   landing_limit(p.timeout_ns), 0x0B | (slot << 8)));
     }
   } else {
     // ------------------------------------------------------------ epilogue (load)
