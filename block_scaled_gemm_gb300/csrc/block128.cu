@@ -68,11 +68,12 @@ int encode(const mxg::HandleView &v, CUtensorMap *tm, CUtensorMapDataType dt, co
 }
 
 // Parts of K for each of `rem` tiles on `pairs` pairs, in K blocks' time: a part
-// costs its own blocks; splitting, about eight more (sums written and awaited)
-// and four for each part that the first one adds (with half of that, 512 x
-// 4096 x 2048 took 13.8 us instead of 12.0).  Whole against split: 256 x 4096
-// x 8192 29.5 and 22.1 us, 5000 x 4112 x 8192 133 and 127 us, 4096 x 4096 x
-// 5008 74.8 and 74.3 us.
+// costs its own blocks; splitting, about eight more (sums written, counted and
+// read) and four for each part whose sums the last one adds (with half of that,
+// 512 x 4096 x 2048 takes 13.8 us instead of 11.2).  Whole against split, in a
+// graph: 256 x 4096 x 8192 28.9 and 21.6 us, 128 x 8192 x 8192 29.5 and 24.5,
+// 5000 x 4112 x 8192 (B K x N) 146 and 139.5, 4096 x 4096 x 5008 75.7 and 74.9,
+// with a scale for each column 108.6 and 102.6.
 int tail_split(int64_t rem, int64_t pairs, int64_t kb) {
   int best = 1;
   int64_t cost = kb;
@@ -177,8 +178,8 @@ int run_skinny_nt(const mxg::HandleView &v, mxg::B128Params &p, const void *A, c
 }
 
 // M <= 64: transposed, the kernel for M rounded up to 16, 32 or 64.  (N = K =
-// 8192: 16 rows 16 us, 64 rows 21 us; 128 rows took 33 us so, and 25 us on the
-// pairs, whose time is the same for 65 to 256 rows.)
+// 8192, B in L2: 16 rows 16 us, 64 rows 21-22 us; 128 rows took 33 us so, and
+// 24 us on the pairs, whose time is the same for 65 to 256 rows.)
 int run_skinny(const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, int variant,
                cudaStream_t stream) {
   if (p.M <= 16) return run_skinny_nt<16>(v, p, A, B, nk, variant, stream);

@@ -22,14 +22,18 @@
 //                       a block's MMAs wait until its accumulator is read.
 //                       8192 x 28672 x 8192 BF16: 1240 us (3.1 PFLOP/s, 0.81 of
 //                       the measured 8-bit rate) in short runs at 2.07 GHz,
-//                       1360-1450 us under the power limit (1.7 GHz).
+//                       1360-1450 us under the power limit (1.7 GHz).  K of the
+//                       last tiles is cut for several pairs; the one that is done
+//                       last adds their sums, in order, and nobody waits.
 //   b128_skinny_kernel  M <= 64: transposed, 128 columns of B on the MMA's
 //                       128-row side and the rows of A as its N, K split over
 //                       a cluster; bound by reading B once: 16 x 8192 x 8192
-//                       15.9 us (4.3 TB/s), 16 x 16384 x 16384 5.4 TB/s.
+//                       15.9 us (4.3 TB/s) with B in L2 and 23 us without, 16 x
+//                       16384 x 16384 5.4 TB/s from DRAM.
 //
 // Waits are bounded as in the other kernels: one that runs out records
-// MXGEMM_ERR_TIMEOUT, the roles drain and return.
+// MXGEMM_ERR_TIMEOUT, the roles drain and return, and loads that are on their way
+// land first.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

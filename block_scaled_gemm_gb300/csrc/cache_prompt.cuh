@@ -18,7 +18,7 @@
 // running maximum is moved, and O in TMEM rescaled, only when it grows by 2^8.
 //
 // Measured: 2 x 2048 tokens (the second 1741) over 8190 (5733) keys, 32/8 heads of
-// 128: 313 us, 1.21 PFLOP/s, 0.64 of the measured FP16 rate (one of 1200 tokens over
+// 128: 315 us, 1.21 PFLOP/s, 0.63 of the measured FP16 rate (one of 1200 tokens over
 // 16000 keys, a row tile an SM, 216 us, 0.73); a key tile takes 1.65 us, some 3200
 // cycles, where the four products alone take 2048 and shared memory's traffic
 // 2560.  A Q tile's chain (softmax, P V, the next Q K^T into the same columns)

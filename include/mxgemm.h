@@ -309,15 +309,26 @@ int mxgemm_scale_bytes(int64_t R, int64_t C, int along_cols, int scale_layout,
 int mxgemm_set_option(mxgemm_handle_t h, int option, int64_t value);
 
 /* Synchronize `stream`, then read and clear the handle's device status word.
- * *status_out receives MXGEMM_OK or MXGEMM_ERR_TIMEOUT; *detail_out (may be
- * NULL) receives where the first failing wait was (role | stage << 8 |
- * tile << 16), 0 when none.  Roles: 0x01 producer (free stage), 0x02 MMA
- * issuer (free accumulator), 0x03 MMA issuer (full stage), 0x04 MMA issuer
- * (final commit), 0x05 epilogue (full accumulator), 0x06 epilogue (stream-K
+ * *status_out receives MXGEMM_OK, MXGEMM_ERR_TIMEOUT (a wait ran out, and the
+ * call's result is incomplete) or, of the cache's calls, MXGEMM_ERR_INVALID_VALUE
+ * (a length, a row start or a page number on the device was not followed).  The
+ * word keeps the first of them until it is read; nothing else of the handle has to
+ * be put right after one.  *detail_out (may be NULL) receives where it was, 0 when
+ * none: of a wait, role | stage << 8 | tile << 16.  Roles: 0x01 producer (free
+ * stage), 0x02 MMA issuer (free accumulator), 0x03 MMA issuer (full stage), 0x04 MMA
+ * issuer (final commit), 0x05 epilogue (full accumulator), 0x06 epilogue (stream-K
  * partials), 0x07 / 0x08 cluster-launch-control response / free slot,
- * 0x09 scale loader (free stage), 0x0A scale loader (staged scale rows),
- * 0x0B scale loader (staging load at exit), 0x0C producer (scale loader's
- * first staging load), 0x11 producer (drain at exit). */
+ * 0x09 scale loader (free stage), 0x0A scale loader (staged scale rows), in
+ * mxgemm_run_block128 epilogue (scales), 0x0B scale loader (staging load at exit),
+ * 0x0C producer (scale loader's first staging load), 0x0E epilogue (C's old
+ * values), 0x11 producer (drain at exit); attention of few query rows: 0x31 (codes);
+ * of many: 0x41 / 0x42 loader (free place for K / V), 0x43 loader (drain at exit),
+ * 0x44 to 0x48 MMA issuer (Q, K, V, weights, final commit), 0x49 / 0x4B converters
+ * (codes of K / V), 0x4A / 0x4C converters (free place for K / V), 0x4D softmax
+ * (scores), 0x4E / 0x4F softmax (output).  Of a value on the device: 0x21 a length
+ * that is negative or does not fit the page table, 0x22 row starts that do not ascend
+ * within the tokens, 0x23 a page number that names no page, 0x24 a length shorter than
+ * the sequence's new tokens (append). */
 int mxgemm_get_device_status(mxgemm_handle_t h, mxgemm_stream_t stream,
                              int *status_out, int *detail_out);
 
