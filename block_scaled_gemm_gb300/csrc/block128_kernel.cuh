@@ -357,9 +357,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         tc_commit_pair(bar_final, 0x3);
       }
       __syncwarp();
+      wait_phase<false>(bar_final, 0, wn, 0x04);
     }
-    // the last of what the commits signal in either CTA
-    wait_phase<false>(bar_final, 0, wn, 0x04);
   } else if (warp == 2 || kCols) {
     // ------------------------------------------------------------ scales
     const bool cols = warp == 3;  // the columns' scales, else the rows'
@@ -404,6 +403,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // the last of what the commits signal in the second CTA (not before its own
+    // work is nearly done: the wait's limit is not one for a whole call)
+    if (rank == 1 && warp == 2) wait_phase<false>(bar_final, 0, wn, 0x04);
   }
   } else {
     // ------------------------------------------------------------ epilogue
