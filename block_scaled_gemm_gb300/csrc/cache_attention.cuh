@@ -111,6 +111,17 @@ __device__ __forceinline__ int q_exponent(float top) {
 }
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
 
+// 1 / vs from log2 vs as it went into the exponents, whose error (2^-22 of the
+// logarithm) then drops out of the sums of weights.
+__device__ __forceinline__ float inverse_of_log2(float lv) { return ex2(-lv); }
+// The natural logarithm of a row's sum of weights, 2^m times `sum`; -inf where it saw
+// no key.  The sum's power of two is taken apart: lg2's error is 2^-22 near 1, and 2^-22
+// of the result elsewhere.
+__device__ __forceinline__ float log_sum(float m, float sum) {
+  const int k = min((__float_as_int(sum) >> 23) - 127, 126);
+  return sum == 0.f ? -INFINITY : (m + static_cast<float>(k) + lg2(sum * pow2(-k))) * 0.69314718055994530942f;
+}
+
 constexpr float kWeightUp = 7.f, kWeightDown = 0.0078125f;  // weights carry 2^7, and sums give it back
 
 constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100, for 1 / vs
@@ -522,7 +533,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       for (int mt = 0; mt < 2; ++mt) {
         const float ks = sc[4 * st + (per == 2 ? mt : 0)], vs = sc[4 * st + 2 + (per == 2 ? mt : 0)];
         const float v1 = fmaxf(vs, kScaleFloor), lv = lg2(v1);
-        ivs[mt] = __frcp_rn(v1) * kWeightDown;
+        ivs[mt] = inverse_of_log2(lv) * kWeightDown;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -709,8 +720,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
           part[ROWS * D + ROWS + r] = sum;
         } else if (r < rows && p.lse) {
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
-          p.lse[static_cast<int64_t>(tok) * p.heads + head] =
-              sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.69314718055994530942f;
+          p.lse[static_cast<int64_t>(tok) * p.heads + head] = log_sum(top, sum);
         }
       }
     }
@@ -765,8 +775,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
                 make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
           }
           if (hd == 0 && p.lse)
-            p.lse[static_cast<int64_t>(tok) * p.heads + head] =
-                sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.69314718055994530942f;
+            p.lse[static_cast<int64_t>(tok) * p.heads + head] = log_sum(top, sum);
         }
       }
     }

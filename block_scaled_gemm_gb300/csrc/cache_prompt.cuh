@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         if (lane < 8) {
           float *sc = scales + (j & 3) * 24 + lane;
           sc[0] = ks;
-          sc[8] = lg2(vs);
-          sc[16] = __frcp_rn(vs) * kWeightDown;
+          const float lv = lg2(vs);
+          sc[8] = lv;
+          sc[16] = inverse_of_log2(lv) * kWeightDown;
         }
         if (lane == 0) groups[j & 3] = there;
         __syncwarp();
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                     ld_shared_v4(q_row + (from - lane) * 128 + c * 16384 + ((q ^ (from & 7)) << 4));
             }
           }
-          if (live && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994530942f;
+          if (live && p.lse) p.lse[at] = log_sum(m, l);
         }
       }
     }
@@ -616,8 +617,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             *reinterpret_cast<uint4 *>(dst + d + 8) = make_uint4(x[4], x[5], x[6], x[7]);
           }
           if (p.lse)
-            p.lse[static_cast<int64_t>(s.first + tok) * p.heads + head] =
-                sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.69314718055994530942f;
+            p.lse[static_cast<int64_t>(s.first + tok) * p.heads + head] = log_sum(top, sum);
         }
       }
     }

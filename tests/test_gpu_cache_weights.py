@@ -50,3 +50,23 @@ def test_small_weights_count(h, length, new, group, d, page, bits, allowed):
     tol = 2.0 ** -8 * o.abs() + allowed * mag
     assert (err <= tol).all(), f"worst {float((err / tol.clamp(min=1e-300)).max())} of the tolerance"
     assert ((L.double() - lse).abs() <= 2.0 ** -19 * (1 + size)).all()
+
+
+@pytest.mark.parametrize("lens,news,kv,group,d,page", [([7] * 40, None, 8, 4, 64, 16), ([20] * 30, [8] * 30, 8, 8, 64, 32), ([90] * 20, [64] * 20, 4, 2, 128, 128)])
+@pytest.mark.parametrize("vscale", [2.0 ** -16, 2.0 ** -60, 2.0 ** 14])
+def test_log_sum_whatever_the_page_scales(h, lens, news, kv, group, d, page, vscale):
+    """Sequences of one page, whose V has scales that are no powers of two and far from 1.
+    They go into the exponents and out of the sums again: beyond the logits' error, lse
+    has the roundings of values up to 2^5, 2^-19 in all (2^-17 where their exponents are
+    up to 2^7)."""
+    for seed in range(4):
+        m = tc.Made(lens, kv, d, page, seed=seed, scales=(-12, -7))
+        m.sV = vscale * (1 + torch.rand(m.sV.shape, generator=m.g))
+        n = news or [1] * len(lens)
+        q = tc.queries(m, sum(n), kv * group, seed=seed)
+        O, L = tc.attend(h, m, q, news, scale=0.02)
+        o, lse, mag, size = plain64.attention(plain64.value(m.K), m.sK, plain64.value(m.V), m.sV, m.table, m.kv_len, tc.starts_of(n), q, 0.02)
+        assert ((O.double() - o).abs() <= 2.0 ** -8 * o.abs() + 2.0 ** -10 * mag).all()
+        err = (L.double() - lse).abs()
+        allowed = (2.0 ** -17 if vscale == 2.0 ** -60 else 2.0 ** -19) * (1 + size)
+        assert (err <= allowed).all(), f"lse: worst {float((err / allowed).max())} of the tolerance"
