@@ -25,7 +25,7 @@
 //
 // Measured: 64 sequences of 2048-8192 tokens, 64/8 heads of 128: 120 us (5.6
 // TB/s, 0.83 of the measured copy rate); two of 91752 and 131071 tokens, 32/4 heads:
-// 53 us (4.3 TB/s: some 50 CTAs' partials join for each item, about 8 us, and the
+// 54 us (4.2 TB/s: some 50 CTAs' partials join for each item, about 8 us, and the
 // first codes arrive 3 us after the start).  The warps' chains of dependent
 // instructions bound it: issue slots are used to 46 %.
 //
