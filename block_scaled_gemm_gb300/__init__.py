@@ -31,11 +31,14 @@ __all__ = [
     "mxgemm_quantize", "IN_F32", "IN_BF16", "EXPORTED_SYMBOLS", "Gemm", "OPT_SCALE_LAYOUT", "OPT_ELEMENT_LAYOUT", "OPT_B_MAJOR", "B_K_BY_N", "B_N_BY_K", "ELEMS_BYTE", "ELEMS_PACKED",
     "SCALES_ROW_MAJOR", "SCALES_PACKED", "mxgemm_scale_bytes", "mxgemm_noalloc_get_status",
     "mxgemm_noalloc_set_option", "mxgemm_run_block128", "mxgemm_quantize_block128", "BLOCK_ROWS", "BLOCK_COLS",
-    "BLOCK_TILES", "Cache", "mxgemm_cache_append", "mxgemm_cache_attention",
+    "BLOCK_TILES", "Cache", "mxgemm_cache_append", "mxgemm_cache_attention", "OUT_E4M3", "ACT_SILU", "ACT_GELU_TANH",
+    "mxgemm_run_gated_block128", "mxgemm_gated_backward", "mxgemm_norm_rope", "mxgemm_norm_rope_backward",
+    "mxgemm_rope_frequencies", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS", "mxgemm_cache_attention_shared",
 ]
 
 OUT_F32 = 0
 OUT_BF16 = 1
+OUT_E4M3 = 2
 
 OPT_MODE = 1
 OPT_WAIT_TIMEOUT_NS = 2
@@ -61,6 +64,16 @@ BLOCK_ROWS = 0
 BLOCK_COLS = 1
 BLOCK_TILES = 2
 
+# activations of a gated block (mxgemm_act_t)
+ACT_SILU = 0
+ACT_GELU_TANH = 1
+
+# frequencies of the rotation (mxgemm_rope_scaling_t)
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_BY_PARTS = 3
+
 # element formats (mxgemm_format_t); one element per byte, sub-byte codes in
 # the low bits
 FMT_E4M3 = 0
@@ -84,7 +97,8 @@ EXPORTED_SYMBOLS = (
     "mxgemm_get_launch_count", "mxgemm_run_noalloc", "mxgemm_run_host", "mxgemm_quantize",
     "mxgemm_quantize_sr", "mxgemm_quantize_ex", "mxgemm_scale_bytes", "mxgemm_noalloc_get_status",
     "mxgemm_noalloc_set_option", "mxgemm_run_block128", "mxgemm_quantize_block128",
-    "mxgemm_cache_append", "mxgemm_cache_attention",
+    "mxgemm_cache_append", "mxgemm_cache_attention", "mxgemm_run_gated_block128", "mxgemm_gated_backward",
+    "mxgemm_norm_rope", "mxgemm_norm_rope_backward", "mxgemm_rope_frequencies", "mxgemm_cache_attention_shared",
 )
 
 _lib = None
@@ -92,6 +106,10 @@ _lib = None
 
 # mxgemm_cache_t
 _CACHE_STRUCT = struct.Struct("PPPPqiii4x")
+# mxgemm_gated_grads_t, mxgemm_heads_t, mxgemm_rope_t
+_GRADS_STRUCT = struct.Struct("12P")
+_HEADS_STRUCT = struct.Struct("PqPqPqPPq")
+_ROPE_STRUCT = struct.Struct("PPiif4x")
 
 
 class MxgemmError(RuntimeError):
@@ -154,6 +172,20 @@ def library():
         lib.mxgemm_cache_attention.argtypes = [vp, ctypes.c_char_p, i64, i64, vp, i64, vp, vp, i64, vp, i64,
                                                ctypes.c_float, i32, i64, i64, vp, vp, vp]
         lib.mxgemm_cache_attention.restype = i32
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.mxgemm_run_gated_block128.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp]
+        lib.mxgemm_run_gated_block128.restype = i32
+        lib.mxgemm_gated_backward.argtypes = [vp, vp, vp, i32, i64, i64, i32, ctypes.c_char_p, vp]
+        lib.mxgemm_gated_backward.restype = i32
+        lib.mxgemm_norm_rope.argtypes = [ctypes.c_char_p, ctypes.c_char_p, i64, i64, i32, i32, f32, ctypes.c_char_p, vp]
+        lib.mxgemm_norm_rope.restype = i32
+        lib.mxgemm_norm_rope_backward.argtypes = [vp, *lib.mxgemm_norm_rope.argtypes]
+        lib.mxgemm_norm_rope_backward.restype = i32
+        lib.mxgemm_rope_frequencies.argtypes = [i64, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64)]
+        lib.mxgemm_rope_frequencies.restype = i32
+        lib.mxgemm_cache_attention_shared.argtypes = [vp, ctypes.c_char_p, i64, i64, vp, i64, vp, vp, i64, i64, vp, i64,
+                                                      f32, i32, vp, vp, vp]
+        lib.mxgemm_cache_attention_shared.restype = i32
         lib.mxgemm_status_string.argtypes = [i32]
         lib.mxgemm_status_string.restype = ctypes.c_char_p
         _lib = lib
@@ -389,13 +421,8 @@ def mxgemm_cache_append(h, cache: Cache, page_table, kv_len, new_K, new_V, q_sta
     return st
 
 
-def mxgemm_cache_attention(h, cache: Cache, page_table, kv_len, Q, O, q_start=None, scale=None,
-                           causal=True, window=0, sinks=0, lse=None, stream=None,
-                           check: bool = True) -> int:
-    """Attention of Q (tokens x heads x head dim bfloat16) over a cache into O
-    (the same shape, dense) and, where given, lse (tokens x heads float32).
-    page_table, kv_len and q_start as for mxgemm_cache_append; scale defaults
-    to 1 / sqrt(head dim); window = 0 is no window."""
+def _queries(cache, Q, O, lse):
+    """Shape and pitch of an attention's queries, with its outputs checked against them."""
     import torch
     shape = Q.shape
     pitch = _token_pitch(shape, Q.stride(), "Q")
@@ -405,6 +432,17 @@ def mxgemm_cache_attention(h, cache: Cache, page_table, kv_len, Q, O, q_start=No
         raise ValueError("Q: tokens x heads x head dim")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse: a dense float32 tensor, tokens x heads")
+    return shape, pitch
+
+
+def mxgemm_cache_attention(h, cache: Cache, page_table, kv_len, Q, O, q_start=None, scale=None,
+                           causal=True, window=0, sinks=0, lse=None, stream=None,
+                           check: bool = True) -> int:
+    """Attention of Q (tokens x heads x head dim bfloat16) over a cache into O
+    (the same shape, dense) and, where given, lse (tokens x heads float32).
+    page_table, kv_len and q_start as for mxgemm_cache_append; scale defaults
+    to 1 / sqrt(head dim); window = 0 is no window."""
+    shape, pitch = _queries(cache, Q, O, lse)
     batch, width, table, lens, starts = _batch(page_table, kv_len, q_start)
     st = library().mxgemm_cache_attention(
         h, cache._c, batch, shape[1], table, width, lens, starts, shape[0], Q.data_ptr(), pitch,
@@ -413,6 +451,141 @@ def mxgemm_cache_attention(h, cache: Cache, page_table, kv_len, Q, O, q_start=No
     if check:
         _check(st, "mxgemm_cache_attention")
     return st
+
+
+def mxgemm_cache_attention_shared(h, cache: Cache, page_table, kv_len, shared, Q, O, q_start=None, scale=None,
+                                  causal=True, lse=None, stream=None, check: bool = True) -> int:
+    """mxgemm_cache_attention for sequences whose first `shared` tokens are in the same
+    pages (as far as each sequence reaches): those are read once for the whole batch.
+    Other arguments as there, without a window."""
+    shape, pitch = _queries(cache, Q, O, lse)
+    batch, width, table, lens, starts = _batch(page_table, kv_len, q_start)
+    st = library().mxgemm_cache_attention_shared(
+        h, cache._c, batch, shape[1], table, width, lens, starts, shape[0], shared, Q.data_ptr(), pitch,
+        shape[2] ** -0.5 if scale is None else scale, 1 if causal else 0, O.data_ptr(),
+        None if lse is None else lse.data_ptr(), _stream(stream))
+    if check:
+        _check(st, "mxgemm_cache_attention_shared")
+    return st
+
+
+def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H, H_scale=None, act=ACT_SILU,
+                              out_dtype=OUT_BF16, gate=None, up=None, stream=None, check: bool = True) -> int:
+    """H = act(A.G) * (A.U) with the operands of mxgemm_run_block128 (both weights as the
+    handle's OPT_B_MAJOR says): float32, bfloat16, or OUT_E4M3 codes with H_scale
+    (M x ceil(N/128)), the operand of the next product.  gate and up (M x N bfloat16)
+    receive A.G and A.U for mxgemm_gated_backward."""
+    st = library().mxgemm_run_gated_block128(h, int(M), int(N), int(K), _ptr(A), _ptr(A_scale), _ptr(G), _ptr(G_scale),
+                                             _ptr(U), _ptr(U_scale), int(act), _ptr(H), _ptr(H_scale), int(out_dtype),
+                                             _ptr(gate), _ptr(up), _stream(stream))
+    if check:
+        _check(st, "mxgemm_run_gated_block128")
+    return st
+
+
+def mxgemm_gated_backward(gate, up, dH, R, C, dgate=None, dup=None, dgate_rows=None, dup_rows=None, dgate_cols=None,
+                          dup_cols=None, hidden_cols=None, act=ACT_SILU, x_dtype=None, stream=None,
+                          check: bool = True) -> int:
+    """The gradient of act(gate) * up (R x C bfloat16) for dH (float32 or bfloat16).
+    dgate, dup: R x C bfloat16; the others pairs (codes, scales) as
+    mxgemm_quantize_block128 makes them, by rows or by columns.  What is None is
+    left out."""
+    if x_dtype is None:
+        x_dtype = _in_dtype(dH)
+    pairs = [p if p is not None else (None, None) for p in (dgate_rows, dup_rows, dgate_cols, dup_cols, hidden_cols)]
+    out = _GRADS_STRUCT.pack(*(_ptr(x) or 0 for x in (dgate, dup, *(y for p in pairs for y in p))))
+    st = library().mxgemm_gated_backward(_ptr(gate), _ptr(up), _ptr(dH), int(x_dtype), int(R), int(C), int(act), out,
+                                         _stream(stream))
+    if check:
+        _check(st, "mxgemm_gated_backward")
+    return st
+
+
+def _heads(x, y, weight, name, dy=None, dweight=None):
+    """mxgemm_heads_t of (tokens, heads, head dim) tensors, and what they have to agree on."""
+    import torch
+    like = y if dy is None else dy
+    if y.shape != like.shape or y.dtype != like.dtype or (x is not None and (x.shape != y.shape or x.dtype != y.dtype)):
+        raise ValueError(f"{name}: tensors of one shape and type")
+    if y.dtype is not torch.float32 and y.dtype is not torch.bfloat16:
+        raise ValueError(f"{name}: float32 or bfloat16")
+    at = [0, 0] * 3
+    for i, t in enumerate((x, dy, y)):
+        if t is not None:
+            at[2 * i:2 * i + 2] = t.data_ptr(), _token_pitch(t.shape, t.stride(), name)
+    if weight is not None:
+        if x is None:
+            raise ValueError(f"{name}: a norm needs the values")
+        if weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != y.shape[2:] or not weight.is_contiguous():
+            raise ValueError(f"{name}'s weight: head dim float32 or bfloat16 values")
+    if dweight is not None and (weight is None or dweight.dtype is not torch.float32 or dweight.shape != y.shape[2:]
+                                or not dweight.is_contiguous()):
+        raise ValueError(f"{name}'s weight's gradient: head dim float32 values, of a weight")
+    return _HEADS_STRUCT.pack(*at, _ptr(weight) or 0, _ptr(dweight) or 0, y.shape[1])
+
+
+def _rope(positions, freqs, interleaved, factor, tokens):
+    import torch
+    if freqs is None:
+        return None
+    if positions is None or positions.dtype is not torch.int32 or positions.numel() != tokens or not positions.is_contiguous():
+        raise ValueError("positions: a dense int32 tensor, one for each token")
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs: a dense float64 tensor, one for each pair")
+    return _ROPE_STRUCT.pack(positions.data_ptr(), freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, factor)
+
+
+def _rope_call(name, handle, q, k, weights, positions, freqs, interleaved, factor, eps, stream, check):
+    """q and k: (values, result, weight, dy, dweight) each, k's result None for none."""
+    import torch
+    y = q[1]
+    shape = y.shape
+    heads = [None if t[1] is None else _heads(t[0], t[1], t[2], n, t[3], t[4]) for t, n in ((q, "q"), (k, "k"))]
+    if heads[1] is not None and (k[1].shape[0] != shape[0] or k[1].shape[2] != shape[2] or k[1].dtype != y.dtype):
+        raise ValueError("q and k: tokens x heads x head dim of one type")
+    kinds = {w.dtype for w in weights if w is not None}
+    if len(kinds) > 1:
+        raise ValueError("q's and k's weights: one type")
+    w_dtype = IN_BF16 if torch.bfloat16 in kinds else IN_F32
+    st = getattr(library(), name)(*handle, heads[0], heads[1], shape[0], shape[2], IN_BF16 if y.dtype is torch.bfloat16 else IN_F32,
+                                  w_dtype, eps, _rope(positions, freqs, interleaved, factor, shape[0]), _stream(stream))
+    if check:
+        _check(st, name)
+    return st
+
+
+def mxgemm_norm_rope(q, k, q_out, k_out, positions=None, freqs=None, interleaved=False, factor=1.0, q_weight=None,
+                     k_weight=None, eps=1e-6, stream=None, check: bool = True) -> int:
+    """Norms of queries and keys for each head (with a weight; without one no norm) and
+    the rotation of each head's first 2 * len(freqs) values by positions[t] * freqs[j],
+    in one pass.  q, k and the results: tokens x heads x head dim, float32 or bfloat16,
+    slices of a projection's output will do; k and k_out may be None, and a result may be
+    its input.  positions: int32; freqs: float64 (mxgemm_rope_frequencies), None for no
+    rotation."""
+    return _rope_call("mxgemm_norm_rope", (), (q, q_out, q_weight, None, None), (k, k_out, k_weight, None, None),
+                      (q_weight, k_weight), positions, freqs, interleaved, factor, eps, stream, check)
+
+
+def mxgemm_norm_rope_backward(h, dq_out, dk_out, dq, dk, q=None, k=None, positions=None, freqs=None, interleaved=False,
+                              factor=1.0, q_weight=None, k_weight=None, dq_weight=None, dk_weight=None, eps=1e-6,
+                              stream=None, check: bool = True) -> int:
+    """The gradient of mxgemm_norm_rope: from dq_out and dk_out (of its results) to dq and
+    dk (of its inputs q and k, which a norm needs) and, where given, the weights'
+    dq_weight and dk_weight (float32, set)."""
+    return _rope_call("mxgemm_norm_rope_backward", (h,), (q, dq, q_weight, dq_out, dq_weight),
+                      (k, dk, k_weight, dk_out, dk_weight), (q_weight, k_weight), positions, freqs, interleaved, factor, eps,
+                      stream, check)
+
+
+def mxgemm_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, scale=1.0, trained=0.0, slow=1.0, fast=4.0):
+    """Frequencies for mxgemm_norm_rope, a float64 CPU tensor of rot / 2: base^(-2j/rot),
+    stretched for long contexts as `scaling` says (ROPE_LINEAR, ROPE_BASE,
+    ROPE_BY_PARTS)."""
+    import torch
+    out = (ctypes.c_double * max(1, int(rot) // 2))()
+    _check(library().mxgemm_rope_frequencies(int(rot), float(base), int(scaling), float(scale), float(trained), float(slow),
+                                             float(fast), out), "mxgemm_rope_frequencies")
+    return torch.tensor(out[:int(rot) // 2], dtype=torch.float64)
 
 
 def mxgemm_set_option(h, option: int, value: int) -> None:

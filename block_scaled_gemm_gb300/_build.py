@@ -19,9 +19,10 @@ ROOT = PKG.parent
 SRC_DIR = PKG / "csrc"
 # translation units: the C interface with the tiled kernel (B given K x N),
 # the tiled kernel's variants for B given N x K, the skinny-problem kernel, the
-# product with block-128 scales, and the 8-bit key/value cache
+# product with block-128 scales, the 8-bit key/value cache, the gated pair of
+# products with its gradient, and head norms with the position rotation
 UNITS = [SRC_DIR / "mxgemm.cu", SRC_DIR / "tiled_kmajor.cu", SRC_DIR / "swapab.cu",
-         SRC_DIR / "block128.cu", SRC_DIR / "cache.cu"]
+         SRC_DIR / "block128.cu", SRC_DIR / "cache.cu", SRC_DIR / "gated.cu", SRC_DIR / "rope.cu"]
 OBJ_DIR = PKG / "_build"
 HEADER = ROOT / "include" / "mxgemm.h"
 LIB = PKG / "libmxgemm.so"

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "block128_host.h"
 #include "block128_kernel.cuh"
 #include "context.h"
 #include "launch.h"
@@ -16,10 +17,10 @@
 
 namespace {
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-constexpr int64_t kLim = int64_t(1) << 31;
+using mxg::aligned;
+using mxg::cdiv;
+using mxg::encode;
+using mxg::kLim;
 
 // Row (tile) blocks past a grid's y limit go to further launches.
 constexpr int64_t kGridY = 65535;
@@ -52,21 +53,6 @@ int launch_quantize128(const T *x, int64_t R, int64_t C, int block, uint8_t *cd,
   return MXGEMM_OK;
 }
 
-// 2-D tensor map of bytes (or of C's elements), 128-byte swizzle: dims
-// {inner, outer}, row pitch in bytes, box.
-int encode(const mxg::HandleView &v, CUtensorMap *tm, CUtensorMapDataType dt, const void *base, int64_t inner,
-           int64_t outer, int64_t pitch, uint32_t box_inner, uint32_t box_outer) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  return v.encode(tm, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? MXGEMM_OK
-             : MXGEMM_ERR_CUDA;
-}
-
 // Parts of K for each of `rem` tiles on `pairs` pairs, in K blocks' time: a part
 // costs its own blocks; splitting, about eight more (sums written, counted and
 // read) and four for each part whose sums the last one adds (with half of that,
@@ -87,43 +73,56 @@ int tail_split(int64_t rem, int64_t pairs, int64_t kb) {
   return best;
 }
 
-// M > 64: CTA pairs on 256 x 256 tiles, one pair per two SMs.
-int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, bool bf16,
-             int variant, cudaStream_t stream) {
-  CUtensorMap tA, tB, tC;
-  std::memset(&tC, 0, sizeof(tC));
-  const int eb = bf16 ? 2 : 4;
-  p.idesc_fmt = mxg::fmt_bits(v.a_fmt, v.b_fmt);
+}  // namespace
+
+namespace mxg {
+
+int pair_plan(mxgemm_handle_t h, const HandleView &v, B128Params &p, int tile_n, cudaStream_t stream) {
   p.m_tiles = static_cast<int>(cdiv(p.M, 256));
-  p.n_tiles = static_cast<int>(cdiv(p.N, 256));
+  p.n_tiles = static_cast<int>(cdiv(p.N, tile_n));
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   if (tiles >= kLim - 65536) return MXGEMM_ERR_INVALID_VALUE;
   const int64_t pairs = v.sm_count / 2, rem = tiles % pairs;
   p.dp_tiles = static_cast<int>(tiles - rem);
-  using P = mxg::PairCfg<0>;
-  p.split = rem && rem * 2 * P::EPI_WARPS <= mxg::kCounters ? tail_split(rem, pairs, p.kb) : 1;
+  using P = PairCfg<0>;
+  p.split = rem && rem * 2 * P::EPI_WARPS <= kCounters ? tail_split(rem, pairs, p.kb) : 1;
   p.tail_items = static_cast<int>(rem) * p.split;
   if (p.split > 1) {
     uint8_t *ws = nullptr;
-    if (int st = mxg::handle_workspace(h, static_cast<size_t>(p.tail_items) * 2 * P::EPI_WARPS * 32 * 128 * sizeof(float),
-                                       stream, &ws))
+    if (int st = handle_workspace(h, static_cast<size_t>(p.tail_items) * 2 * P::EPI_WARPS * 32 * 128 * sizeof(float),
+                                  stream, &ws))
       return st;
     p.partials = reinterpret_cast<float *>(ws);
     p.counters = v.counters;
   }
+  return MXGEMM_OK;
+}
+
+}  // namespace mxg
+
+namespace {
+
+// M > 64: CTA pairs on 256 x 256 tiles, one pair per two SMs.
+int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, const void *A, const void *B, bool nk, bool bf16,
+             int variant, cudaStream_t stream) {
+  mxg::PairMaps<false> tm;
+  std::memset(&tm, 0, sizeof(tm));
+  const int eb = bf16 ? 2 : 4;
+  p.idesc_fmt = mxg::fmt_bits(v.a_fmt, v.b_fmt);
+  if (int st = mxg::pair_plan(h, v, p, 256, stream)) return st;
   p.tma_store = !p.use_acc && static_cast<int64_t>(p.N) * eb % 16 == 0;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (encode(v, &tA, u8, A, p.K, p.M, p.K, 128, 128) ||
-      (nk ? encode(v, &tB, u8, B, p.K, p.N, p.K, 128, 128) : encode(v, &tB, u8, B, p.N, p.K, p.N, 128, 128)) ||
-      (p.tma_store && encode(v, &tC, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+  if (encode(v, &tm.A, u8, A, p.K, p.M, p.K, 128, 128) ||
+      (nk ? encode(v, &tm.B, u8, B, p.K, p.N, p.K, 128, 128) : encode(v, &tm.B, u8, B, p.N, p.K, p.N, 128, 128)) ||
+      (p.tma_store && encode(v, &tm.C, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                              p.C, p.N, p.M, static_cast<int64_t>(p.N) * eb, bf16 ? 64 : 32, 32)))
     return MXGEMM_ERR_CUDA;
-  const int grid = 2 * static_cast<int>(p.dp_tiles > 0 ? pairs : p.tail_items);
+  const int grid = mxg::pair_grid(v, p);
   switch (variant) {
 #define MXG_PAIR(V)                                                                                     \
   case V:                                                                                               \
     return mxg::launch(mxg::b128_pair_kernel<V>, dim3(grid), mxg::PairCfg<V>::THREADS,                  \
-                       mxg::PairCfg<V>::SMEM_BYTES, 2, stream, tA, tB, tC, p);
+                       mxg::PairCfg<V>::SMEM_BYTES, 2, stream, tm, p);
     MXG_PAIR(0)
     MXG_PAIR(1)
     MXG_PAIR(2)

@@ -38,6 +38,8 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "gated_math.cuh"
+#include "quantize128.cuh"
 #include "tmem_util.cuh"
 
 namespace mxg {
@@ -66,6 +68,12 @@ struct B128Params {
   // skinny
   int nm;      // M rounded up to 16
   int splits;  // CTAs of a cluster that share a column block's K
+  // gated pairs of products: B and b_scale are the gate's, C is H
+  const float *u_scale;
+  float *h_scale;             // of H as codes
+  __nv_bfloat16 *gate, *up;   // what the gradient needs, or null
+  int act;                    // mxgemm_act_t
+  int tma_keep;               // gate's and up's rows are multiples of 16 bytes
 };
 
 // Instruction descriptor of kind::f8f6f4: FP32 accumulator, M x N; the
@@ -119,10 +127,23 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 constexpr int kB128Bf16 = 1;    // BF16 output (else FP32)
 constexpr int kB128KMajor = 2;  // B given N x K (else K x N)
 constexpr int kB128Cols = 4;    // a scale of B for each column (else for 128)
+constexpr int kB128Gated = 8;   // two products and their gate (M > 64): H = act(A G^T) * (A U^T)
+constexpr int kB128Codes = 16;  // H as E4M3 codes with a scale for each 1 x 128
+
+// The tensor maps of a pair kernel.
+template <bool GATED>
+struct PairMaps {
+  CUtensorMap A, B, C;
+};
+template <>
+struct PairMaps<true> {
+  CUtensorMap A, B, C, U, gate, up;  // U: the other weight; gate, up: BF16, M x N
+};
 
 template <int V>
 struct PairCfg {
-  static constexpr bool COLS = (V & kB128Cols) != 0;
+  static constexpr bool COLS = (V & kB128Cols) != 0, GATED = (V & kB128Gated) != 0, CODES = (V & kB128Codes) != 0;
+  static_assert(!GATED || !COLS, "a gated pair has a scale for each 128 x 128");
   static constexpr int STAGES = 5;
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // per CTA
   static constexpr uint32_t STAGE_TX = 2 * (A_BYTES + B_BYTES);   // both CTAs
@@ -137,9 +158,11 @@ struct PairCfg {
   static constexpr int AS_PITCH = 132, BS_PITCH = COLS ? 260 : 4;
   static constexpr int SLOT_BYTES = KB * (AS_PITCH + BS_PITCH) * 4;
   static constexpr int OFF_SC = OFF_STG + EPI_WARPS * 4096;
-  static constexpr int OFF_BAR = OFF_SC + 2 * SLOT_BYTES;  // (accumulators' pairs 16-byte aligned)
-  // full, empty, acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], final
-  static constexpr int NUM_BARS = 2 * STAGES + 8 + 1;
+  // codes: a row's largest value of each half of the columns, [2][8 warps][32], and what the halves agree on
+  static constexpr int OFF_TOP = OFF_SC + 2 * SLOT_BYTES, TOP_BYTES = CODES ? 2 * EPI_WARPS * 32 * 4 + 4 * 4 : 0;
+  static constexpr int OFF_BAR = OFF_TOP + TOP_BYTES;  // (accumulators' pairs 16-byte aligned)
+  // full, empty, acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], final, codes: the halves' [4]
+  static constexpr int NUM_BARS = 2 * STAGES + 8 + 1 + (CODES ? 4 : 0);
   static_assert((OFF_BAR + 16 * STAGES) % 16 == 0, "barrier pairs");
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -186,9 +209,10 @@ __device__ __forceinline__ bool pair_work(const B128Params &p, int unit, int uni
 // one line for all rows, for comparison, 1533 us).
 template <int V>
 __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
-    b128_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmC, const B128Params p) {
+    b128_pair_kernel(const __grid_constant__ PairMaps<(V & kB128Gated) != 0> tm, const B128Params p) {
   using C = PairCfg<V>;
+  constexpr bool kGated = C::GATED, kCodes = C::CODES;
+  constexpr int kTileN = kGated ? 128 : 256;  // columns of C (of H) of a tile
   constexpr bool kBF16 = (V & kB128Bf16) != 0, kKM = (V & kB128KMajor) != 0, kCols = (V & kB128Cols) != 0;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -196,6 +220,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
   uint8_t *sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  // a gated pair's first CTA brings the gate's columns, the second the other weight's
+  const CUtensorMap *tmB = &tm.B;
+  if constexpr (kGated) tmB = rank ? &tm.U : &tm.B;
 
   const uint32_t bar_full = base + C::OFF_BAR;
   const uint32_t bar_empty = bar_full + 8 * C::STAGES;
@@ -204,18 +231,21 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
   const uint32_t bar_sc_full = bar_acc_empty + 16;
   const uint32_t bar_sc_empty = bar_sc_full + 16;
   const uint32_t bar_final = bar_sc_empty + 16;
+  const uint32_t bar_halves = bar_final + 8;  // codes: one for each quarter of the rows
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);
   volatile int *never = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 8);  // never raised
   volatile int *peer_fills = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 12);  // first CTA: the second's fills + 1
 
   if (threadIdx.x == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tm.A);
+    tma_prefetch_desc(tmB);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
+    if constexpr (kCodes)
+      for (int s = 0; s < 4; ++s) mbar_init(bar_halves + 8 * s, 2);
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_acc_full + 8 * b, 1);
       mbar_init(bar_acc_empty + 8 * b, 2 * C::EPI_WARPS);
@@ -260,7 +290,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     for (int i = 0; ok && pair_work(p, unit, units, i, w); ++i) {
       int mt, nt;
       tile_coords(w.tile, p.m_tiles, p.n_tiles, mt, nt);
-      const int row = mt * 256 + 128 * static_cast<int>(rank), col = nt * 256 + 128 * static_cast<int>(rank);
+      const int row = mt * 256 + 128 * static_cast<int>(rank), col = nt * kTileN + (kGated ? 0 : 128 * static_cast<int>(rank));
       for (int ks = w.kb; ks < w.ke; ++ks) {
         // (a producer that is stopped waits for a fill that it does not issue)
         if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(issued == stop ? bar_full + 8 * st : bar_empty + 8 * st,
@@ -271,9 +301,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, C::STAGE_TX);
           const uint32_t fb = mapa_shared(bar_full + 8 * st, 0);
-          tma_load_2d_pair(base + C::OFF_A + st * C::A_BYTES, &tmA, ks * 128, row, fb);
-          if constexpr (kKM) tma_load_2d_pair(base + C::OFF_B + st * C::B_BYTES, &tmB, ks * 128, col, fb);
-          else tma_load_2d_pair(base + C::OFF_B + st * C::B_BYTES, &tmB, col, ks * 128, fb);
+          tma_load_2d_pair(base + C::OFF_A + st * C::A_BYTES, &tm.A, ks * 128, row, fb);
+          if constexpr (kKM) tma_load_2d_pair(base + C::OFF_B + st * C::B_BYTES, tmB, ks * 128, col, fb);
+          else tma_load_2d_pair(base + C::OFF_B + st * C::B_BYTES, tmB, col, ks * 128, fb);
         }
         __syncwarp();
         ++issued;
@@ -382,9 +412,15 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             const int r = 4 * i + (lane >> 3);
             cp_async4(as + (j * C::AS_PITCH + r) * 4, p.a_scale + static_cast<int64_t>(min(row0 + r, p.M - 1)) * kb + k);
           }
-          if (!kCols && lane < 16)
-            cp_async4(bs + (j * C::BS_PITCH + (lane >> 3)) * 4,
-                      p.b_scale + min(static_cast<int64_t>(2 * nt + (lane >> 3)), p.bs_cols - 1) * p.bs_n + k * p.bs_k);
+          if (!kCols && lane < 16) {
+            const float *from = p.b_scale;
+            int64_t block = min(static_cast<int64_t>(2 * nt + (lane >> 3)), p.bs_cols - 1);
+            if constexpr (kGated) {
+              from = lane >> 3 ? p.u_scale : p.b_scale;
+              block = nt;
+            }
+            cp_async4(bs + (j * C::BS_PITCH + (lane >> 3)) * 4, from + block * p.bs_n + k * p.bs_k);
+          }
         } else if constexpr (kKM) {
           const int j = lane & 7, k = min(k0 + j, kb - 1);
 #pragma unroll 8
@@ -413,7 +449,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
     const int w = warp - 4, q = warp & 3, half = w >> 2;
     const uint32_t stg = base + C::OFF_STG + w * 4096;
     // accumulator and barrier of the block to come: the two of each alternate
-    uint32_t acc_at = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
+    // (a gated pair: 64 columns of the gate, and the same of the other product, 128 further on)
+    uint32_t acc_at = tmem + (static_cast<uint32_t>(32 * q) << 16) + (kGated ? 64 : 128) * half;
     uint32_t full_at = bar_acc_full, full_ph = 0;
     uint32_t empty_at = mapa_shared(bar_acc_empty, 0);  // of the pair's first CTA
     uint32_t n = 0;  // groups of eight K blocks so far
@@ -433,13 +470,22 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       __threadfence();
       return before == static_cast<unsigned>(p.split) - 1u;
     };
+    // Codes: the two warps of a row's halves meet (a wait like the others, bounded).
+    uint32_t meetings = 0;
+    volatile float *tops = reinterpret_cast<volatile float *>(sm + C::OFF_TOP);
+    volatile int *agreed = reinterpret_cast<volatile int *>(sm + C::OFF_TOP + 2 * C::EPI_WARPS * 32 * 4);
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_halves + 8 * q);
+      return __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_halves + 8 * q, meetings++ & 1u, wc, 0x0B));
+    };
     bool ok = true, arrived = false;
     PairWork pw;
     for (int i = 0; ok && pair_work(p, unit, units, i, pw); ++i) {
       int mt, nt;
       tile_coords(pw.tile, p.m_tiles, p.n_tiles, mt, nt);
       const int row0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
-      const int col0 = nt * 256 + 128 * half;
+      const int col0 = nt * kTileN + kTileN / 2 * half;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -448,8 +494,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       // With a scale for each column a thread has a fragment, four rows (lane / 4
       // + 8 i, scales s) and 32 columns, so that it reads 32 columns' scales for
       // each block and not 128.
+      // (gated: s its scale times the gate's, s[1] times the other weight's)
       constexpr int kRows = kCols ? 4 : 1;
-      float s[kRows];
+      float s[kGated ? 2 : kRows];
       const float *sc;
       auto scale_at = [&](int ks) {
         sc = reinterpret_cast<const float *>(sm + C::OFF_SC + (n & 1u) * C::SLOT_BYTES);
@@ -461,7 +508,12 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         // interface asks for: a test of it here, for each K block, with a loop in
         // two steps for the others, 110 -> 122 us at 2048 x 9728 x 8192; by the
         // warps that bring the scales, 139 us.)
-        if constexpr (!kCols) s[0] *= sc[half];
+        if constexpr (kGated) {
+          s[1] = s[0] * sc[1];
+          s[0] *= sc[0];
+        } else if constexpr (!kCols) {
+          s[0] *= sc[half];
+        }
       };
       ok = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_sc_full + 8 * (n & 1u), (n >> 1) & 1u, wc, 0x0A));
       if (!ok) break;
@@ -478,7 +530,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             tmem_ld_16x256b_x4(acc_at + 32 * c, r);
             tmem_ld_16x256b_x4(acc_at + 32 * c + (16u << 16), r + 16);
           } else {
-            tmem_ld_32x32b_x32(acc_at + 32 * c, r);
+            tmem_ld_32x32b_x32(acc_at + 32 * c + (kGated && c >= 2 ? 64 : 0), r);
           }
         };
         load(0, v[0]);
@@ -502,8 +554,8 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
                 a = r.x;
                 b = r.y;
               } else {
-                a = fmaf(x, s[0], a);
-                b = fmaf(y, s[0], b);
+                a = fmaf(x, s[kGated ? c >> 1 : 0], a);
+                b = fmaf(y, s[kGated ? c >> 1 : 0], b);
               }
             }
           }
@@ -540,8 +592,25 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         float4 *to = slot(pw.part);
 #pragma unroll
         for (int j = 0; j < 32; ++j) to[32 * j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-        arrived = true;
-        if (!arrive(pw.item)) continue;
+        if constexpr (kCodes) {
+          // a row's scale needs both halves, so both are finished by one CTA: the
+          // first half's warp counts for the two, once the other's part is there
+          __threadfence();
+          ok = meet();
+          if (!ok) break;
+          arrived = true;
+          if (half == 0) {
+            const bool mine = arrive(pw.item);
+            if (lane == 0) agreed[q] = mine;
+          }
+          ok = meet();
+          if (!ok) break;
+          __threadfence();
+          if (!agreed[q]) continue;
+        } else {
+          arrived = true;
+          if (!arrive(pw.item)) continue;
+        }
         // The last of the tile's parts: all of their sums, in order.  Its own are
         // still here, but for the first two (a + b is b + a) they are read back.
         if (pw.part > 1) {
@@ -564,7 +633,9 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       }
       // C: rows row0 .. +31, columns col0 .. +127, in pieces of 128 bytes a
       // row through this warp's 4 KB (16-byte units swizzled by the row)
-      if (row0 >= p.M || col0 >= p.N) continue;
+      if constexpr (!kCodes) {
+        if (row0 >= p.M || col0 >= p.N) continue;
+      }
       // piece c: columns 32 c .. +31 in FP32, or 64 c .. +63 in BF16
       auto stage_f32 = [&](int c) {
 #pragma unroll
@@ -611,10 +682,77 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
           }
         }
       };
-      if (p.tma_store) {
+      if constexpr (kGated) {
+        // acc: 64 values of the gate, then 64 of the other product
+        if (p.gate && row0 < p.M && col0 < p.N) {
+          if (p.tma_keep) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+              stage_bf16(c);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(c ? &tm.up : &tm.gate, stg, col0, row0);
+                bulk_commit_group();
+              }
+            }
+          } else {
+            if (lane == 0) bulk_wait_read_all();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              __syncwarp();
+              stage_f32(c);
+              __syncwarp();
+              const int col = col0 + (c & 1) * 32 + lane, rows = min(32, p.M - row0);
+              const float *from = reinterpret_cast<const float *>(sm + (stg - base));
+              __nv_bfloat16 *to = c < 2 ? p.gate : p.up;
+              if (col < p.N)
+                for (int r = 0; r < rows; ++r)
+                  to[static_cast<int64_t>(row0 + r) * p.N + col] =
+                      __float2bfloat16_rn(from[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]);
+            }
+            __syncwarp();
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 64; ++j) acc[j] = gated(acc[j], acc[64 + j], p.act);
+      }
+      if constexpr (kCodes) {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) top = fmaxf(top, fabsf(acc[j]));
+        volatile float *slot = tops + (meetings & 1u) * C::EPI_WARPS * 32 + lane;
+        slot[32 * w] = top;
+        ok = meet();
+        if (!ok) break;
+        top = fmaxf(fmaxf(top, slot[32 * (w ^ 4)]), kQ128Least);
+        if (half == 0 && row0 + lane < p.M) p.h_scale[static_cast<int64_t>(row0 + lane) * p.bs_cols + nt] = __fdiv_rn(top, 448.0f);
+        if (row0 >= p.M || col0 >= p.N) continue;
+        const float inv = __fdiv_rn(448.0f, top);
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float *a = acc + 16 * j + 4 * e;
+            x[e] = mx_e4m3x2(a[0] * inv, a[1] * inv) | (mx_e4m3x2(a[2] * inv, a[3] * inv) << 16);
+          }
+          st_shared_v4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), x[0], x[1], x[2], x[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tm.C, stg, col0, row0);
+          bulk_commit_group();
+        }
+      } else if (p.tma_store) {
         constexpr int kCol = kBF16 ? 64 : 32;
 #pragma unroll
-        for (int c = 0; c < 128 / kCol; ++c) {
+        for (int c = 0; c < kTileN / 2 / kCol; ++c) {
           if (lane == 0) bulk_wait_read_all();
           __syncwarp();
           if constexpr (kBF16) stage_bf16(c);
@@ -622,13 +760,14 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && col0 + c * kCol < p.N) {
-            tma_store_2d(&tmC, stg, col0 + c * kCol, row0);
+            tma_store_2d(&tm.C, stg, col0 + c * kCol, row0);
             bulk_commit_group();
           }
         }
       } else {
+        if (kGated && lane == 0) bulk_wait_read_all();  // (gate and up may have gone by TMA)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kTileN / 2 / 32; ++c) {
           __syncwarp();
           stage_f32(c);
           __syncwarp();
@@ -653,7 +792,7 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
       }
     }
     // (after a wait that gave up too: the counters belong to the next launch)
-    if (p.split > 1 && !arrived && unit < p.tail_items) arrive(unit);
+    if (p.split > 1 && !arrived && unit < p.tail_items && !(kCodes && half)) arrive(unit);
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }

@@ -119,52 +119,157 @@ int encode_cache(const mxg::HandleView &v, const mxg::CacheView &c, int d, int b
 // few, get up to 16 CTAs each (44 row tiles of 61102 keys: 816 -> 296 us; the
 // last 24 of 480: 334 -> 328 us).  The grid has room for every split of the rows
 // into sequences; the count of row tiles that decides is that of equal ones.
-int64_t equal_row_tiles(const mxg::AttnParams &p) {
+// (Shared keys: all sequences' rows are one.)
+int64_t equal_row_tiles(const mxg::AttnParams &p, int64_t sequences) {
   constexpr int64_t kRows = mxg::PromptCfg<128>::ROWS;
-  return (p.b.tokens * p.group / p.b.batch + kRows - 1) / kRows * p.b.batch * p.c.kv_heads;
+  return (p.b.tokens * p.group / sequences + kRows - 1) / kRows * sequences * p.c.kv_heads;
 }
 
+// Bytes of the handle's workspace before the partials: what the launch over the
+// shared keys leaves for the next.
+int64_t left_bytes(const mxg::AttnParams &p, int d) {
+  return p.shared ? (p.b.tokens * p.heads * (d + 2) * static_cast<int64_t>(sizeof(float)) + 255) / 256 * 256 : 0;
+}
+void left_views(mxg::AttnParams &p, int d, uint8_t *ws) {
+  if (!p.shared) return;
+  p.pre = reinterpret_cast<float *>(ws);
+  p.pre_ml = reinterpret_cast<float2 *>(p.pre + p.b.tokens * p.heads * d);
+}
+
+// How row tiles and their keys are cut: fills in p, and gives the bytes of the
+// partials, or -1 where there are too many.
 template <int D>
-int run_prompt(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+int64_t plan_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t sequences) {
   using S = mxg::PromptCfg<D>;
   const int64_t rows = p.b.tokens * p.group;
-  const int64_t items = (rows / S::ROWS + p.b.batch) * p.c.kv_heads;
-  if (items >= kLim - 16 * mxg::kCounters) return MXGEMM_ERR_INVALID_VALUE;
-  const int64_t tiles = equal_row_tiles(p), over = tiles % v.sm_count;
+  const int64_t items = (rows / S::ROWS + sequences) * p.c.kv_heads;
+  if (items >= kLim - 16 * mxg::kCounters) return -1;
+  const int64_t tiles = equal_row_tiles(p, sequences), over = tiles % v.sm_count;
   p.items = p.whole = static_cast<int>(items);
   p.parts = over > 0 ? static_cast<int>(std::min<int64_t>(16, v.sm_count / over)) : 1;
   if (p.parts > 1) {
     if (tiles >= v.sm_count) p.whole -= static_cast<int>(std::min(items, over));
     else p.whole = 0;
     const int cut = p.items - p.whole;
-    if (cut > mxg::kCounters) {
-      p.whole = p.items;
-    } else {
-      uint8_t *ws = nullptr;
-      if (int st = mxg::handle_workspace(h, static_cast<size_t>(cut) * p.parts * S::PARTIAL * sizeof(float), stream, &ws))
-        return st;
-      p.partials = reinterpret_cast<float *>(ws);
-    }
+    if (cut > mxg::kCounters) p.whole = p.items;
+    else return static_cast<int64_t>(cut) * p.parts * S::PARTIAL * static_cast<int64_t>(sizeof(float));
+  }
+  return 0;
+}
+
+template <int D, int MODE>
+int run_prompt(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+  using S = mxg::PromptCfg<D>;
+  const int64_t bytes = plan_prompt<D>(v, p, MODE == mxg::kSharedKeys ? 1 : p.b.batch), left = left_bytes(p, D);
+  if (bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (left + bytes > 0) {
+    uint8_t *ws = nullptr;
+    if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + bytes), stream, &ws)) return st;
+    left_views(p, D, ws);
+    p.partials = reinterpret_cast<float *>(ws + left);
   }
   const int grid = p.whole + (p.items - p.whole) * p.parts;
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
-  return mxg::launch(mxg::cache_prompt_kernel<D>, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, 1, stream,
+  return mxg::launch(mxg::cache_prompt_kernel<D, MODE>, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, 1, stream,
                      tK, tV, p);
 }
 
 template <int D, int NT>
+int decode_grid(const mxg::HandleView &v) {
+  return std::min(mxg::DecodeCfg<D, NT>::CTAS * v.sm_count, mxg::kCounters);
+}
+template <int D, int NT>
+int64_t decode_bytes(const mxg::HandleView &v) {
+  return static_cast<int64_t>(decode_grid<D, NT>(v)) * 2 * mxg::DecodeCfg<D, NT>::PARTIAL * sizeof(float);
+}
+
+template <int D, int NT, int MODE>
 int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::DecodeCfg<D, NT>;
-  const int grid = std::min(S::CTAS * v.sm_count, mxg::kCounters);
+  const int grid = decode_grid<D, NT>(v);
+  const int64_t left = left_bytes(p, D);
   uint8_t *ws = nullptr;
-  if (int st = mxg::handle_workspace(h, static_cast<size_t>(grid) * 2 * S::PARTIAL * sizeof(float), stream, &ws))
-    return st;
-  p.partials = reinterpret_cast<float *>(ws);
+  if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + decode_bytes<D, NT>(v)), stream, &ws)) return st;
+  left_views(p, D, ws);
+  p.partials = reinterpret_cast<float *>(ws + left);
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, std::min(p.c.page_size, 32), true, &tK, &tV)) return st;
-  return mxg::launch(mxg::cache_decode_kernel<D, NT>, dim3(static_cast<unsigned>(grid)), 128, S::SMEM_BYTES, 1, stream, tK,
+  return mxg::launch(mxg::cache_decode_kernel<D, NT, MODE>, dim3(static_cast<unsigned>(grid)), 128, S::SMEM_BYTES, 1, stream, tK,
                      tV, p);
+}
+
+// Rows (query tokens x heads of a group) of an ordinary sequence decide: many
+// go to the tensor cores by 256, few to the kernel whose items are 8 or 16.
+// At 64 rows both take the same time on 32 row tiles of 8192 keys (70 us); on
+// 128 the first takes 106 us and the second 219, and with more than 16 rows
+// the second reads the keys again; but it cuts them for all SMs where the
+// first's row tiles times 16 do not fill half of them.
+bool takes_prompt(const mxg::HandleView &v, const mxg::AttnParams &p) {
+  const int64_t rows = p.b.tokens * p.group;
+  return rows >= 64 * p.b.batch || (rows > 16 * p.b.batch && equal_row_tiles(p, p.b.batch) * 32 >= v.sm_count);
+}
+// (of the kernel for few rows: items of 16)
+bool takes_two(const mxg::AttnParams &p) { return p.b.tokens * p.group > 8 * p.b.batch; }
+
+template <int D, int MODE>
+int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+  if (takes_prompt(v, p)) return run_prompt<D, MODE>(h, v, p, stream);
+  return takes_two(p) ? run_decode<D, 2, MODE>(h, v, p, stream) : run_decode<D, 1, MODE>(h, v, p, stream);
+}
+
+// The shared keys for all tokens, then each sequence's own, which finishes.
+template <int D>
+int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+  mxg::AttnParams first = p;
+  // (the block that the first launch leaves its results in is not to grow under the second)
+  const int64_t one = plan_prompt<D>(v, first, 1);
+  int64_t two = takes_two(p) ? decode_bytes<D, 2>(v) : decode_bytes<D, 1>(v);
+  if (takes_prompt(v, p)) {
+    mxg::AttnParams second = p;
+    two = plan_prompt<D>(v, second, p.b.batch);
+  }
+  if (one < 0 || two < 0) return MXGEMM_ERR_INVALID_VALUE;
+  uint8_t *ws = nullptr;
+  if (int st = mxg::handle_workspace(h, static_cast<size_t>(left_bytes(p, D) + std::max(one, two)), stream, &ws)) return st;
+  if (int st = run_prompt<D, mxg::kSharedKeys>(h, v, first, stream)) return st;
+  ++*v.launches;
+  return run_attention<D, mxg::kOwnKeys>(h, v, p, stream);
+}
+
+// The checks of an attention's arguments beyond the cache's; fills the kernels' view.
+int attention_args(const mxg::HandleView &v, const mxgemm_cache_t *cache, int64_t batch, int64_t heads, int64_t tokens, const void *Q,
+                   int64_t q_pitch, float scale, int causal, int64_t window, int64_t sinks, void *O, float *lse, mxg::AttnParams *p) {
+  if (heads < 1 || heads >= (1 << 16) || heads % cache->kv_heads != 0 || tokens * heads >= kLim)
+    return MXGEMM_ERR_INVALID_VALUE;
+  if (q_pitch < heads * cache->head_dim || !std::isfinite(scale)) return MXGEMM_ERR_INVALID_VALUE;
+  if ((causal != 0 && causal != 1) || window < 0 || sinks < 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (batch == 0 || tokens == 0) return MXGEMM_OK;
+  if (!Q || !O) return MXGEMM_ERR_INVALID_VALUE;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(lse, 4) || q_pitch % 8 != 0)
+    return MXGEMM_ERR_MISALIGNED;
+  if (!mxg::pointer_on_device(Q, v.device) || !mxg::pointer_on_device(O, v.device) ||
+      (lse && !mxg::pointer_on_device(lse, v.device)))
+    return MXGEMM_ERR_INVALID_VALUE;
+  p->Q = static_cast<const __nv_bfloat16 *>(Q);
+  p->q_pitch = q_pitch;
+  p->heads = static_cast<int>(heads);
+  p->group = static_cast<int>(heads / cache->kv_heads);
+  p->scale = scale;
+  p->causal = causal;
+  // (positions stay below 2^31: a longer window sees as much, and the kernels'
+  // sums with these stay far from 64 bits' end)
+  p->window = std::min(window, kLim);
+  p->sinks = std::min(sinks, kLim);
+  p->O = static_cast<__nv_bfloat16 *>(O);
+  p->lse = lse;
+  p->counters = v.counters;
+  p->timeout_ns = v.timeout_ns;
+  p->stall_producer = v.stall_producer;
+  p->shared = 0;
+  p->pre = nullptr;
+  p->pre_ml = nullptr;
+  return MXGEMM_OK;
 }
 
 }  // namespace
@@ -215,48 +320,38 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   mxg::AttnParams p;
   if (int st = cache_args(v, cache, batch, page_table, table_pitch, kv_len, q_start, tokens, &p.c, &p.b))
     return st;
-  if (heads < 1 || heads >= (1 << 16) || heads % cache->kv_heads != 0 || tokens * heads >= kLim)
-    return MXGEMM_ERR_INVALID_VALUE;
-  if (q_pitch < heads * cache->head_dim || !std::isfinite(scale)) return MXGEMM_ERR_INVALID_VALUE;
-  if ((causal != 0 && causal != 1) || window < 0 || sinks < 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (int st = attention_args(v, cache, batch, heads, tokens, Q, q_pitch, scale, causal, window, sinks, O, lse, &p)) return st;
   if (batch == 0 || tokens == 0) return MXGEMM_OK;
-  if (!Q || !O) return MXGEMM_ERR_INVALID_VALUE;
-  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(lse, 4) || q_pitch % 8 != 0)
-    return MXGEMM_ERR_MISALIGNED;
-  if (!mxg::pointer_on_device(Q, v.device) || !mxg::pointer_on_device(O, v.device) ||
-      (lse && !mxg::pointer_on_device(lse, v.device)))
-    return MXGEMM_ERR_INVALID_VALUE;
-  p.Q = static_cast<const __nv_bfloat16 *>(Q);
-  p.q_pitch = q_pitch;
-  p.heads = static_cast<int>(heads);
-  p.group = static_cast<int>(heads / cache->kv_heads);
-  p.scale = scale;
-  p.causal = causal;
-  // (positions stay below 2^31: a longer window sees as much, and the kernels'
-  // sums with these stay far from 64 bits' end)
-  p.window = std::min(window, kLim);
-  p.sinks = std::min(sinks, kLim);
-  p.O = static_cast<__nv_bfloat16 *>(O);
-  p.lse = lse;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  p.counters = v.counters;
-  p.timeout_ns = v.timeout_ns;
-  p.stall_producer = v.stall_producer;
-  // Rows (query tokens x heads of a group) of an ordinary sequence decide: many
-  // go to the tensor cores by 256, few to the kernel whose items are 8 or 16.
-  // At 64 rows both take the same time on 32 row tiles of 8192 keys (70 us); on
-  // 128 the first takes 106 us and the second 219, and with more than 16 rows
-  // the second reads the keys again; but it cuts them for all SMs where the
-  // first's row tiles times 16 do not fill half of them.
-  int st;
-  const int64_t rows = tokens * p.group;
-  if (rows >= 64 * batch || (rows > 16 * batch && equal_row_tiles(p) * 32 >= v.sm_count)) {
-    st = cache->head_dim == 128 ? run_prompt<128>(h, v, p, stream) : run_prompt<64>(h, v, p, stream);
-  } else {
-    const bool two = tokens * p.group > 8 * batch;
-    st = cache->head_dim == 128 ? (two ? run_decode<128, 2>(h, v, p, stream) : run_decode<128, 1>(h, v, p, stream))
-                                : (two ? run_decode<64, 2>(h, v, p, stream) : run_decode<64, 1>(h, v, p, stream));
-  }
+  const int st = cache->head_dim == 128 ? run_attention<128, mxg::kAllKeys>(h, v, p, stream)
+                                        : run_attention<64, mxg::kAllKeys>(h, v, p, stream);
+  if (st != MXGEMM_OK) return st;
+  ++*v.launches;
+  return MXGEMM_OK;
+}
+
+extern "C" int mxgemm_cache_attention_shared(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch, int64_t heads,
+                                             const int32_t *page_table, int64_t table_pitch, const int32_t *kv_len,
+                                             const int32_t *q_start, int64_t tokens, int64_t shared, const void *Q,
+                                             int64_t q_pitch, float scale, int causal, void *O, float *lse,
+                                             mxgemm_stream_t stream_) {
+  if (!h) return MXGEMM_ERR_INVALID_VALUE;
+  const mxg::HandleView v = mxg::handle_view(h);
+  mxg::CurrentDevice g(v.device);
+  mxg::AttnParams p;
+  if (int st = cache_args(v, cache, batch, page_table, table_pitch, kv_len, q_start, tokens, &p.c, &p.b))
+    return st;
+  if (shared < 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (int st = attention_args(v, cache, batch, heads, tokens, Q, q_pitch, scale, causal, 0, 0, O, lse, &p)) return st;
+  if (batch == 0 || tokens == 0) return MXGEMM_OK;
+  // whole pages and whole tiles of the kernel for few rows; what is over is read as
+  // each sequence's own.  (No sequence is longer than its table.)
+  const int64_t unit = std::max(cache->page_size, 32);
+  p.shared = static_cast<int>(std::min(shared, table_pitch * cache->page_size) / unit * unit);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const bool d128 = cache->head_dim == 128;
+  const int st = p.shared == 0 ? (d128 ? run_attention<128, mxg::kAllKeys>(h, v, p, stream) : run_attention<64, mxg::kAllKeys>(h, v, p, stream))
+                               : (d128 ? run_shared<128>(h, v, p, stream) : run_shared<64>(h, v, p, stream));
   if (st != MXGEMM_OK) return st;
   ++*v.launches;
   return MXGEMM_OK;

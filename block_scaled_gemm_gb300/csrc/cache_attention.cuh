@@ -60,7 +60,16 @@ struct AttnParams {
   int parts;           // CTAs that each other one's keys may be cut for
   unsigned long long timeout_ns;
   int stall_producer;  // tests: nothing is loaded
+  // attention behind shared tokens: keys [0, shared), a multiple of 32 and of the
+  // pages, are one launch's, the others the next's, which adds what the first left of
+  // each token and head: sums over `pre`'s D values, and in `pre_ml` maximum and sum
+  int shared;
+  float *pre;
+  float2 *pre_ml;
 };
+
+// What a launch computes: all keys; the shared ones for all tokens; the others.
+constexpr int kAllKeys = 0, kSharedKeys = 1, kOwnKeys = 2;
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -126,6 +135,16 @@ constexpr float kWeightUp = 7.f, kWeightDown = 0.0078125f;  // weights carry 2^7
 
 constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100, for 1 / vs
 
+// The sums (m, l) of some keys of a row and (pm, pl) of the others: the factors of
+// both, over the common maximum that m becomes, and l their sum.
+__device__ __forceinline__ float2 join_sums(float &m, float &l, float pm, float pl) {
+  const float top = fmaxf(m, pm);
+  const float2 f = make_float2(m == -INFINITY ? 0.f : ex2(m - top), pm == -INFINITY ? 0.f : ex2(pm - top));
+  l = l * f.x + pl * f.y;
+  m = top;
+  return f;
+}
+
 // Which keys of a sequence any of its queries sees, as tiles of 32: `ns` tiles
 // of first tokens from key 0, then the tiles from tile `lo` on, `tiles` in all
 // (one at least, so that a sequence without keys still has its zeros written).
@@ -135,8 +154,17 @@ struct KeyTiles {
   int win_lo;    // keys < win_lo are seen only as first tokens
 };
 
+template <int MODE>
 __device__ __forceinline__ KeyTiles key_tiles(const AttnParams &p, const Sequence &s) {
   KeyTiles k;
+  if constexpr (MODE == kOwnKeys) {
+    k.end = s.n > 0 && s.len > p.shared ? s.len : 0;  // (a sequence that is within the shared tokens has none)
+    k.win_lo = k.end ? p.shared : 0;
+    k.lo = k.win_lo >> 5;
+    k.ns = 0;
+    k.tiles = max(1, ((k.end + 31) >> 5) - k.lo);
+    return k;
+  }
   const int64_t first = static_cast<int64_t>(s.len) - s.n;  // position of the first query
   k.end = s.n > 0 ? s.len : 0;  // (the last query stands at len - 1)
   int64_t lo = 0;
@@ -160,6 +188,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 // Position in the flat order of tiles: a sequence, and in it an item.
+template <int MODE>
 struct Cursor {
   int b;
   Sequence s;
@@ -195,7 +224,7 @@ struct Cursor {
   }
   __device__ void enter(const AttnParams &p, int rows) {
     s = load_sequence(p.b, p.c, b);
-    k = key_tiles(p, s);
+    k = key_tiles<MODE>(p, s);
     items = item_count(p, s, rows);
   }
   // first key of tile x of the item
@@ -206,11 +235,12 @@ struct Cursor {
 };
 
 // Items of sequence b (none past the batch), and tiles of each.
+template <int MODE>
 __device__ __forceinline__ int64_t sequence_items(const AttnParams &p, int rows, int b, int &tiles) {
   tiles = 1;
   if (b >= p.b.batch) return 0;
   const Sequence s = load_sequence(p.b, p.c, b);
-  tiles = key_tiles(p, s).tiles;
+  tiles = key_tiles<MODE>(p, s).tiles;
   return item_count(p, s, rows);
 }
 __device__ __forceinline__ int64_t warp_prefix(int64_t v) {  // inclusive
@@ -245,7 +275,7 @@ struct DecodeCfg {
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
 };
 
-template <int D, int NT>
+template <int D, int NT, int MODE>
 __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const AttnParams p) {
@@ -280,13 +310,13 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   // All tiles (each warp counts for itself, 32 sequences at a time), and this
   // CTA's range of them: ranges of four tiles at least.
   int mt;
-  int64_t mi = sequence_items(p, ROWS, lane, mt);
+  int64_t mi = sequence_items<MODE>(p, ROWS, lane, mt);
   int64_t mine = mi * mt, upto = warp_prefix(mine);  // the first 32 sequences
   int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
   unsigned all_items = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mi));
   for (int b = 32; b < p.b.batch; b += 32) {
     int tiles;
-    const int64_t items = sequence_items(p, ROWS, b + lane, tiles);
+    const int64_t items = sequence_items<MODE>(p, ROWS, b + lane, tiles);
     total += __shfl_sync(0xFFFFFFFFu, warp_prefix(items * tiles), 31);
     all_items += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(items));
   }
@@ -296,7 +326,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   auto next_sequences = [&]() {  // the next 32
     base_b += __shfl_sync(0xFFFFFFFFu, upto, 31);
     b0 += 32;
-    mi = sequence_items(p, ROWS, b0 + lane, mt);
+    mi = sequence_items<MODE>(p, ROWS, b0 + lane, mt);
     mine = mi * mt;
     upto = warp_prefix(mine);
   };
@@ -358,7 +388,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   const int lg = p.c.page_log2, per = lg == 4 ? 2 : 1;  // pages of a tile
   const uint32_t box_bytes = (lg == 4 ? 16 : 32) * D;
   // ------------------------------------------------------------ loads
-  Cursor at, in;  // of the item being computed, and of the next tile to load
+  Cursor<MODE> at, in;  // of the item being computed, and of the next tile to load
   at.start(p, ROWS, b0, base_b, x0);
   in = at;
   auto issue = [&](int64_t x, int st) {
@@ -684,6 +714,14 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
 #pragma unroll
       for (int w = 0; w < 4; ++w)  // (a sum of NaN stays one, also where no weight gave a maximum)
         sum = fmaf(ml[(4 + w) * ROWS + r], ml[w * ROWS + r] == -INFINITY ? 0.f : ex2(ml[w * ROWS + r] - top), sum);
+      // the row's place in O, and what is left of the shared keys
+      int64_t row_at = 0;
+      float2 fj = make_float2(1.f, 0.f);
+      if (MODE == kOwnKeys && !split && r < rows) {
+        row_at = static_cast<int64_t>(at.s.first + (row0 + r) / p.group) * p.heads + h * p.group + (row0 + r) % p.group;
+        const float2 pre = p.pre_ml[row_at];
+        fj = join_sums(top, sum, pre.x, pre.y);
+      }
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) {
         __syncthreads();
@@ -709,6 +747,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         } else if (r < rows) {
           const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
+          if constexpr (MODE == kOwnKeys) {
+            const float4 b = *reinterpret_cast<const float4 *>(p.pre + row_at * D + d);
+            a = make_float4(a.x * fj.x + b.x * fj.y, a.y * fj.x + b.y * fj.y, a.z * fj.x + b.z * fj.y, a.w * fj.x + b.w * fj.y);
+          }
           const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * k, a.y * k), hi = __floats2bfloat162_rn(a.z * k, a.w * k);
           *reinterpret_cast<uint2 *>(p.O + (static_cast<int64_t>(tok) * p.heads + head) * D + d) =
               make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
@@ -766,8 +808,17 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
 #pragma unroll
           for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
           if (rr >= rows) continue;
-          const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           const int tok = at.s.first + (row0 + rr) / p.group, head = h * p.group + (row0 + rr) % p.group;
+          if constexpr (MODE == kOwnKeys) {
+            const int64_t row_at = static_cast<int64_t>(tok) * p.heads + head;
+            const float2 pre = p.pre_ml[row_at], f = join_sums(top, sum, pre.x, pre.y);
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+              const float4 b = *reinterpret_cast<const float4 *>(p.pre + row_at * D + 64 * e + 4 * hd);
+              a[e] = make_float4(a[e].x * f.x + b.x * f.y, a[e].y * f.x + b.y * f.y, a[e].z * f.x + b.z * f.y, a[e].w * f.x + b.w * f.y);
+            }
+          }
+          const float k = sum == 0.f ? 0.f : kWeightDown / sum;
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) {
             const __nv_bfloat162 lo = __floats2bfloat162_rn(a[e].x * k, a[e].y * k), hi = __floats2bfloat162_rn(a[e].z * k, a[e].w * k);

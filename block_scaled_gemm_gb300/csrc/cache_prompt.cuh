@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 // where scale * ks underflows or is 0.
 constexpr float kTinyFactor = 1.1754943508222875080e-38f;  // 2^-126
 
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     cache_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const AttnParams p) {
@@ -129,9 +129,28 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     const int64_t q = p.b.q_start ? p.b.q_start[b] : b;
     return q * p.group / S::ROWS + b;
   };
-  const int b = warp_find(p.b.batch, f, id);
-  const Sequence s = load_sequence(p.b, p.c, b);
-  const int64_t row_first = (id - f(b)) * S::ROWS;
+  int b;
+  Sequence s;
+  if constexpr (MODE == kSharedKeys) {
+    // all tokens' rows together, over the pages of the longest sequence: no entry of
+    // the table past a sequence's end is read, and no key that none has
+    int most = 0;
+    b = 0;
+    for (int i = lane; i < p.b.batch; i += 32) {
+      const int len = load_sequence(p.b, p.c, i).len;
+      if (len > most) {
+        most = len;
+        b = i;
+      }
+    }
+    const int longest = __reduce_max_sync(0xFFFFFFFFu, most);
+    b = __reduce_min_sync(0xFFFFFFFFu, most == longest ? b : p.b.batch - 1);
+    s = Sequence{min(p.shared, longest), 0, static_cast<int>(p.b.tokens)};
+  } else {
+    b = warp_find(p.b.batch, f, id);
+    s = load_sequence(p.b, p.c, b);
+  }
+  const int64_t row_first = (MODE == kSharedKeys ? id : id - f(b)) * S::ROWS;
   const int64_t row_count = static_cast<int64_t>(s.n) * p.group;
   if (row_first < 0 || row_first >= row_count) return;
   const int row0 = static_cast<int>(row_first);
@@ -140,8 +159,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const int pos0 = s.len - s.n;
   // keys that any of the rows sees: tiles of first tokens, then from tile `lo`
   const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
-  const int end = p.causal ? max(0, min(s.len, pos_last + 1)) : s.len;
-  const int win_lo = p.window > 0 ? static_cast<int>(min(max(static_cast<int64_t>(0), pos_first - p.window + 1), static_cast<int64_t>(end))) : 0;
+  int end = p.causal && MODE != kSharedKeys ? max(0, min(s.len, pos_last + 1)) : s.len;
+  if (MODE == kOwnKeys && end <= p.shared) end = 0;  // (within the shared tokens: no key of its own)
+  const int win_lo = MODE == kOwnKeys ? min(p.shared, end) : p.window > 0 ? static_cast<int>(min(max(static_cast<int64_t>(0), pos_first - p.window + 1), static_cast<int64_t>(end))) : 0;
   const int lo = win_lo >> 7;
   const int ns = static_cast<int>(min((min(p.sinks, static_cast<int64_t>(win_lo)) + 127) >> 7, static_cast<int64_t>(lo)));
   const int all_tiles = max(1, ns + ((end + 127) >> 7) - lo);
@@ -416,11 +436,29 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       // this thread's row sees keys [row_from, row_to) and the first tokens; all
       // rows of the warp see [all_from, all_to)
       auto window_from = [&](int pos) {
+        if (MODE == kOwnKeys) return p.shared;
         return p.window == 0 ? 0 : static_cast<int>(max(static_cast<int64_t>(0), pos - p.window + 1));
       };
       const int w0 = 128 * i + 32 * qd;
-      const int row_to = p.causal ? min(end, pos + 1) : end, row_from = window_from(pos);
-      const int all_to = p.causal ? min(end, pos0 + (row0 + min(w0, rows - 1)) / p.group + 1) : end;
+      int row_to = p.causal ? min(end, pos + 1) : end, row_from = window_from(pos);
+      int all_to = p.causal ? min(end, pos0 + (row0 + min(w0, rows - 1)) / p.group + 1) : end;
+      if constexpr (MODE == kSharedKeys) {
+        // the token's own sequence, which may be shorter than the shared tokens
+        int lo = 0, hi = p.b.batch;
+        if (p.b.q_start) {
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.b.q_start[mid] <= tok) lo = mid;
+            else hi = mid;
+          }
+        } else {
+          lo = tok;
+        }
+        const Sequence own = load_sequence(p.b, p.c, lo);
+        const int at = tok - own.first;
+        row_to = at < 0 || at >= own.n ? 0 : max(0, min(end, p.causal ? own.len - own.n + at + 1 : own.len));
+        all_to = __reduce_min_sync(0xFFFFFFFFu, live ? row_to : end);
+      }
       const int all_from = window_from(pos0 + (row0 + min(w0 + 31, rows - 1)) / p.group);
       const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
       const uint32_t ts = tmem + S::TM_S + 128 * i + lanes, to = tmem + S::TM_O + 128 * i + lanes;
@@ -533,6 +571,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         } else {
           // through the rows of Q, whose products are done: a store of whole
           // lines, where a thread's own row would touch 32
+          float2 fj = make_float2(1.f, 0.f);
+          if constexpr (MODE == kOwnKeys) {
+            const float2 pre = live ? p.pre_ml[at] : make_float2(-INFINITY, 0.f);
+            fj = join_sums(m, l, pre.x, pre.y);
+          }
+          if constexpr (MODE == kSharedKeys) {
+            if (live) p.pre_ml[at] = make_float2(m, l);
+          }
           const float k = l == 0.f ? 0.f : kWeightDown / l;
           const uint32_t rr = 32 * qd + lane, q_row = base + S::OFF_Q + i * S::TILE16 + rr * 128;
 #pragma unroll
@@ -540,8 +586,28 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             uint32_t o[32];
             tmem_ld_32x32b_x32(to + 32 * c, o);
             tmem_ld_done(o);
+            if constexpr (MODE == kSharedKeys) {
+              if (live) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.pre + static_cast<int64_t>(at) * D + 32 * c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              }
+            }
+            if constexpr (MODE == kOwnKeys) {
+              if (live) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.pre + static_cast<int64_t>(at) * D + 32 * c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 y = src[e];
+                  o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * fj.x + y.x * fj.y);
+                  o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * fj.x + y.y * fj.y);
+                  o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * fj.x + y.z * fj.y);
+                  o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * fj.x + y.w * fj.y);
+                }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < (MODE == kSharedKeys ? 0 : 4); ++e) {
               uint32_t x[4];
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
@@ -554,7 +620,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           }
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < (MODE == kSharedKeys ? 0 : 8); ++j) {
             const int from = 4 * j + (lane >> 3), q = lane & 7;
             const int64_t to_row = __shfl_sync(0xFFFFFFFFu, at, from);
             if (128 * i + 32 * qd + from < rows) {
@@ -564,7 +630,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                     ld_shared_v4(q_row + (from - lane) * 128 + c * 16384 + ((q ^ (from & 7)) << 4));
             }
           }
-          if (live && p.lse) p.lse[at] = log_sum(m, l);
+          if (MODE != kSharedKeys && live && p.lse) p.lse[at] = log_sum(m, l);
         }
       }
     }
@@ -586,17 +652,31 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
             sum = fmaf(__ldcg(first + c * S::PARTIAL + S::ROWS * D + S::ROWS + r), mc == -INFINITY ? 0.f : ex2(mc - top), sum);
           }
-          const float k = sum == 0.f ? 0.f : kWeightDown / sum;
-          __nv_bfloat16 *dst = p.O + (static_cast<int64_t>(s.first + tok) * p.heads + head) * D;
+          const int64_t row_at = static_cast<int64_t>(s.first + tok) * p.heads + head;
+          // the parts' factors: over their maximum, times fj.x, plus the shared keys' sums times fj.y
+          const float part_top = top;
+          float2 fj = make_float2(1.f, 0.f);
+          if constexpr (MODE == kOwnKeys) {
+            const float2 pre = p.pre_ml[row_at];
+            fj = join_sums(top, sum, pre.x, pre.y);
+          }
+          const float k = MODE == kSharedKeys ? 1.f : sum == 0.f ? 0.f : kWeightDown / sum;
+          __nv_bfloat16 *dst = p.O + row_at * D;
 #pragma unroll 1
           for (int d = 0; d < D; d += 16) {
             float4 a[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e = 0; e < 4; ++e) {
+              a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if constexpr (MODE == kOwnKeys) {
+                const float4 y = *reinterpret_cast<const float4 *>(p.pre + row_at * D + d + 4 * e);
+                a[e] = make_float4(y.x * fj.y * k, y.y * fj.y * k, y.z * fj.y * k, y.w * fj.y * k);
+              }
+            }
 #pragma unroll 2
             for (int c = 0; c < parts; ++c) {
               const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
-              const float f = mc == -INFINITY ? 0.f : ex2(mc - top) * k;
+              const float f = mc == -INFINITY ? 0.f : ex2(mc - part_top) * (fj.x * k);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float4 x = __ldcg(reinterpret_cast<const float4 *>(first + c * S::PARTIAL) + (d / 4 + e) * S::ROWS + r);
@@ -606,18 +686,23 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                 a[e].w = fmaf(x.w, f, a[e].w);
               }
             }
-            uint32_t x[8];
+            if constexpr (MODE == kSharedKeys) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(a[e].x, a[e].y), z = __floats2bfloat162_rn(a[e].z, a[e].w);
-              x[2 * e] = *reinterpret_cast<const uint32_t *>(&y);
-              x[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&z);
+              for (int e = 0; e < 4; ++e) *reinterpret_cast<float4 *>(p.pre + row_at * D + d + 4 * e) = a[e];
+            } else {
+              uint32_t x[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(a[e].x, a[e].y), z = __floats2bfloat162_rn(a[e].z, a[e].w);
+                x[2 * e] = *reinterpret_cast<const uint32_t *>(&y);
+                x[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&z);
+              }
+              *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4 *>(dst + d + 8) = make_uint4(x[4], x[5], x[6], x[7]);
             }
-            *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4 *>(dst + d + 8) = make_uint4(x[4], x[5], x[6], x[7]);
           }
-          if (p.lse)
-            p.lse[static_cast<int64_t>(s.first + tok) * p.heads + head] = log_sum(top, sum);
+          if constexpr (MODE == kSharedKeys) p.pre_ml[row_at] = make_float2(top, sum);
+          else if (p.lse) p.lse[row_at] = log_sum(top, sum);
         }
       }
     }

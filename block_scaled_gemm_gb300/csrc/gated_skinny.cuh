@@ -1,0 +1,360 @@
+// gated_skinny.cuh -- the gated pair of products for M <= 64 rows:
+//
+//   H[m,n] = act(sum_k A[m,k] G[n,k]) * (sum_k A[m,k] U[n,k]),  blocks of 128 scaled
+//
+// Bound by reading both weights once.  Transposed, as the single product's kernel
+// for few rows: 128 columns of a weight on the MMA's 128-row side and the rows of A
+// as its N.  A step of the ring is one K block of one column block: 16 KB of each
+// weight and A's rows.  All steps of all column blocks, laid end to end, are cut
+// into equal ranges, one for each CTA, so that no SM waits for a last wave and the
+// loads go on across column blocks.  A column block that spans CTAs leaves FP32
+// partials in the workspace, and the CTA that arrives last adds them, in order, and
+// finishes it: nobody waits for another CTA.
+//
+// Waits are bounded as in the other kernels.  The epilogue's warps go on to the end
+// after a wait that gave up, without waiting again: their barrier and the arrivals
+// at shared column blocks stay whole, and the counters are left at zero.
+#pragma once
+#include "block128_kernel.cuh"
+
+namespace mxg {
+
+struct GatedSkinnyParams {
+  B128Params b;
+  int n_tiles;
+  int64_t total;       // steps: column blocks x K blocks
+  float *partials;     // two slots a CTA: [2 NT / 4][128 columns] of four
+  unsigned *counters;  // of the CTA with a shared column block's first step
+  int h_type;          // mxgemm_out_dtype_t
+};
+
+template <int NT>
+struct GatedSkinnyCfg {
+  static constexpr int BT_BYTES = 128 * 128, AT_BYTES = NT * 128;
+  static constexpr int STAGE = 2 * BT_BYTES + AT_BYTES;
+  static constexpr int STAGES = NT <= 32 ? 6 : 5;
+  static constexpr int BUFS = 4;  // accumulators, each of both products
+  // scales of A, for each epilogue warp [2 groups][4 steps][NT]
+  static constexpr int OFF_CS = STAGES * STAGE;
+  // codes: rows' largest values, [2][4 warps][NT]
+  static constexpr int OFF_TOP = OFF_CS + 4 * 2 * 4 * NT * 4;
+  static constexpr int OFF_BAR = OFF_TOP + 2 * 4 * NT * 4;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr uint32_t TM_COLS = 2 * NT * BUFS;
+  static constexpr int THREADS = 6 * 32;
+  static constexpr int PARTIAL = 2 * NT * 128;  // floats
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(STAGE % 1024 == 0 && OFF_BAR % 8 == 0 && TM_COLS <= 512, "layout");
+};
+
+template <int NT, bool kKM>
+__global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
+    gated_skinny_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
+                        const __grid_constant__ CUtensorMap tmA, const GatedSkinnyParams gp) {
+  using S = GatedSkinnyCfg<NT>;
+  const B128Params &p = gp.b;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kb = p.kb;
+  const int64_t total = gp.total, ctas = gridDim.x;
+  const int64_t u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
+  const int steps = static_cast<int>(u1 - u0);
+  const int tile0 = static_cast<int>(u0 / kb), k0 = static_cast<int>(u0 - static_cast<int64_t>(tile0) * kb);
+
+  const uint32_t bar_full = base + S::OFF_BAR;
+  const uint32_t bar_empty = bar_full + 8 * S::STAGES;
+  const uint32_t bar_acc_full = bar_empty + 8 * S::STAGES;
+  const uint32_t bar_acc_empty = bar_acc_full + 8 * S::BUFS;
+  const uint32_t bar_final = bar_acc_empty + 8 * S::BUFS;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 4);
+  volatile int *never = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 8);  // never raised
+  volatile int *last = reinterpret_cast<volatile int *>(sm + S::OFF_MISC + 12);
+  const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+  const WaitCtl wn{p.status, never, landing_limit(p.timeout_ns)};
+
+  auto load_step = [&](int st, int i) {  // step i of this CTA's
+    const int64_t u = u0 + i;
+    const int tile = static_cast<int>(u / kb), ks = static_cast<int>(u - static_cast<int64_t>(tile) * kb);
+    const uint32_t fb = bar_full + 8 * st, to = base + st * S::STAGE;
+    mbar_arrive_expect_tx(fb, 2 * S::BT_BYTES + p.nm * 128);
+    if constexpr (kKM) {
+      tma_load_2d(to, &tmG, ks * 128, tile * 128, fb);
+      tma_load_2d(to + S::BT_BYTES, &tmU, ks * 128, tile * 128, fb);
+    } else {
+      tma_load_2d(to, &tmG, tile * 128, ks * 128, fb);
+      tma_load_2d(to + S::BT_BYTES, &tmU, tile * 128, ks * 128, fb);
+    }
+    tma_load_2d(to + 2 * S::BT_BYTES, &tmA, ks * 128, 0, fb);
+  };
+  // the first ring round goes out before the rest of the set-up
+  const int n_early = p.stall_producer ? 0 : min(S::STAGES, steps);
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmG);
+      tma_prefetch_desc(&tmU);
+      tma_prefetch_desc(&tmA);
+      for (int s = 0; s < S::STAGES; ++s) {
+        mbar_init(bar_full + 8 * s, 1);
+        mbar_init(bar_empty + 8 * s, 1);
+      }
+      for (int b = 0; b < S::BUFS; ++b) {
+        mbar_init(bar_acc_full + 8 * b, 1);
+        mbar_init(bar_acc_empty + 8 * b, 4);
+      }
+      mbar_init(bar_final, 1);
+      *abort_flag = 0;
+      *never = 0;
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    griddep_launch_dependents();  // the next kernel's set-up may begin
+    griddep_wait();               // no global memory before the kernel before has ended
+    if (lane < n_early) load_step(lane, lane);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_u32(tmem_slot), S::TM_COLS);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one() != 0;
+    int issued = n_early;
+    for (; issued < steps && !p.stall_producer; ++issued) {
+      const int st = issued % S::STAGES;
+      if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * st, ring_parity(issued, S::STAGES) ^ 1u, wc, 0x01 | (st << 8))))
+        break;
+      if (leader) load_step(st, issued);
+      __syncwarp();
+    }
+    // every fill has been consumed (or, after a wait that gave up, has landed)
+    // before the CTA may finish
+    bool clean = true;
+    for (int64_t i = ring_pending(issued, S::STAGES); i < issued; ++i) {
+      const int s = static_cast<int>(i % S::STAGES);
+      const uint32_t par = ring_parity(i, S::STAGES);
+      if (clean) clean = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_empty + 8 * s, par, wc, 0x11 | (s << 8)));
+      if (!clean) wait_phase<false>(bar_full + 8 * s, par, wn, 0x11 | (s << 8));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one() != 0;
+    const uint32_t idesc = idesc_f8(128, p.nm, !kKM, false) | p.idesc_fmt;
+    for (int i = 0; i < steps; ++i) {
+      const int st = i % S::STAGES, buf = i % S::BUFS;
+      if (!__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_empty + 8 * buf, ((i / S::BUFS) & 1) ^ 1u, wc, 0x02)) ||
+          !__all_sync(0xFFFFFFFFu, wait_phase<false>(bar_full + 8 * st, ring_parity(i, S::STAGES), wc, 0x03 | (st << 8))))
+        break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t at = base + st * S::STAGE, sA = at + 2 * S::BT_BYTES;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t sB = at + w * S::BT_BYTES;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f8<1>(tmem + 2 * NT * buf + NT * w,
+                      kKM ? smem_desc(sB + 32 * k, 0, 1024, 2) : smem_desc(sB + 4096 * k, 16384, 1024, 2),
+                      smem_desc(sA + 32 * k, 0, 1024, 2), idesc, k != 0);
+        }
+        tc_commit(bar_empty + 8 * st);
+        tc_commit(bar_acc_full + 8 * buf);
+      }
+      __syncwarp();
+    }
+    if (leader) tc_commit(bar_final);
+    __syncwarp();
+    wait_phase<false>(bar_final, 0, wn, 0x04);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, n = 32 * q + lane;  // this lane's column of the block
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float *cs = reinterpret_cast<float *>(sm + S::OFF_CS) + q * 8 * NT;
+    float *tops = reinterpret_cast<float *>(sm + S::OFF_TOP);
+    float acc[2][NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) acc[0][m] = acc[1][m] = 0.f;
+    // Scales, a group of four steps ahead: of the weights lane 2 j + w has step j's
+    // of weight w, and A's 4 x NT, NT / 8 of them by each lane, go through the
+    // warp's shared memory.  (gt, gk): the group's first column block and K block.
+    constexpr int kPer = NT / 8;
+    float nb = 0.f, sb = 0.f, na[kPer];
+    int gt = tile0, gk = k0;
+    auto step_at = [&](int j, int &t, int &k) {
+      t = gt;
+      k = gk + j;
+      while (k >= kb) {
+        k -= kb;
+        ++t;
+      }
+      t = min(t, gp.n_tiles - 1);  // (past the last step: anything)
+    };
+    auto fetch = [&]() {
+      int t, k;
+      if (lane < 8) {
+        step_at(lane >> 1, t, k);
+        nb = __ldg((lane & 1 ? p.u_scale : p.b_scale) + t * p.bs_n + k * p.bs_k);
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = lane + 32 * j, m = i % NT;
+        step_at(i / NT, t, k);
+        na[j] = m < p.M ? __ldg(p.a_scale + static_cast<int64_t>(m) * kb + k) : 0.f;
+      }
+      step_at(4, gt, gk);
+    };
+    fetch();
+    bool have = true;
+    int tile = tile0, k = k0, begin = k0, ends = 0;
+    for (int i = 0; i < steps; ++i) {
+      if ((i & 3) == 0) {
+        sb = nb;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) cs[((i >> 2) & 1) * 4 * NT + lane + 32 * j] = na[j];
+        __syncwarp();
+        fetch();
+      }
+      const int buf = i % S::BUFS;
+      if (have) have = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_full + 8 * buf, (i / S::BUFS) & 1, wc, 0x05));
+      tc_fence_after();
+      const float4 *c4 = reinterpret_cast<const float4 *>(cs + ((i >> 2) & 1) * 4 * NT + (i & 3) * NT);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const float sw = __shfl_sync(0xFFFFFFFFu, sb, 2 * (i & 3) + w);
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(lane_addr + 2 * NT * buf + NT * w + 16 * c, v);
+          tmem_ld_done(v);
+          if (w == 1 && c == NT / 16 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_acc_empty + 8 * buf);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 f = c4[4 * c + e];
+            float *a = acc[w] + 16 * c + 4 * e;
+            a[0] = fmaf(__uint_as_float(v[4 * e + 0]), f.x * sw, a[0]);
+            a[1] = fmaf(__uint_as_float(v[4 * e + 1]), f.y * sw, a[1]);
+            a[2] = fmaf(__uint_as_float(v[4 * e + 2]), f.z * sw, a[2]);
+            a[3] = fmaf(__uint_as_float(v[4 * e + 3]), f.w * sw, a[3]);
+          }
+        }
+      }
+      if (++k < kb && i + 1 < steps) continue;
+      // -------------------------------------------------------- the end of this
+      // CTA's part [begin, k) of the column block
+      bool finish = true;
+      if (begin > 0 || k < kb) {
+        const int64_t first = static_cast<int64_t>(tile) * kb, end = first + kb;
+        const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = (end * ctas - 1) / total;  // the CTAs that share it
+        auto slot = [&](int64_t c) {
+          return reinterpret_cast<float4 *>(gp.partials + (2 * c + (c == c0)) * S::PARTIAL) + n;
+        };
+        float4 *to = slot(blockIdx.x);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int j = 0; j < NT / 4; ++j)
+            to[(w * (NT / 4) + j) * 128] = make_float4(acc[w][4 * j], acc[w][4 * j + 1], acc[w][4 * j + 2], acc[w][4 * j + 3]);
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (threadIdx.x == 64) {
+          const bool mine = atomicAdd(gp.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+          if (mine) gp.counters[c0] = 0;  // for the next launch
+          *last = mine;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        finish = *last != 0;
+        if (finish) {
+          __threadfence();
+#pragma unroll
+          for (int m = 0; m < NT; ++m) acc[0][m] = acc[1][m] = 0.f;
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float4 *from = slot(c);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int j = 0; j < NT / 4; ++j) {
+                const float4 o = __ldcg(from + (w * (NT / 4) + j) * 128);
+                acc[w][4 * j] += o.x;
+                acc[w][4 * j + 1] += o.y;
+                acc[w][4 * j + 2] += o.z;
+                acc[w][4 * j + 3] += o.w;
+              }
+          }
+        }
+      }
+      if (finish) {
+        const int col = tile * 128 + n;
+        const bool live = col < p.N && have;
+        if (p.gate && live) {
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            if (m < p.M) {
+              p.gate[static_cast<int64_t>(m) * p.N + col] = __float2bfloat16_rn(acc[0][m]);
+              p.up[static_cast<int64_t>(m) * p.N + col] = __float2bfloat16_rn(acc[1][m]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < NT; ++m) acc[0][m] = gated(acc[0][m], acc[1][m], p.act);
+        if (gp.h_type == 2) {
+          float *mine = tops + (ends & 1) * 4 * NT;
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(acc[0][m])));
+            if (lane == m % 32) mine[q * NT + m] = __uint_as_float(t);
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (n < p.M && have) {
+            const float t = fmaxf(fmaxf(mine[n], mine[NT + n]), fmaxf(mine[2 * NT + n], mine[3 * NT + n]));
+            p.h_scale[static_cast<int64_t>(n) * p.bs_cols + tile] = __fdiv_rn(fmaxf(t, kQ128Least), 448.0f);
+          }
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            if (m < p.M && live) {
+              const float t = fmaxf(fmaxf(mine[m], mine[NT + m]), fmaxf(mine[2 * NT + m], mine[3 * NT + m]));
+              static_cast<uint8_t *>(p.C)[static_cast<int64_t>(m) * p.N + col] =
+                  static_cast<uint8_t>(mx_e4m3(acc[0][m] * __fdiv_rn(448.0f, fmaxf(t, kQ128Least))));
+            }
+          ++ends;
+        } else if (live) {
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            if (m < p.M) {
+              const int64_t at = static_cast<int64_t>(m) * p.N + col;
+              if (gp.h_type == 1) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(acc[0][m]);
+              else static_cast<float *>(p.C)[at] = acc[0][m];
+            }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m) acc[0][m] = acc[1][m] = 0.f;
+      ++tile;
+      k = begin = 0;
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<1>(tmem, S::TM_COLS);
+}
+
+}  // namespace mxg

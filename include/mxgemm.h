@@ -51,6 +51,11 @@
  * For 8-bit layers with coarser scales: mxgemm_run_block128 (the product with
  * one FP32 scale per block of 128), mxgemm_quantize_block128 (its operands),
  * and the 8-bit key/value cache: mxgemm_cache_append, mxgemm_cache_attention.
+ * What a transformer layer needs around them: mxgemm_run_gated_block128 and
+ * mxgemm_gated_backward (a gated feed-forward block), mxgemm_norm_rope and
+ * mxgemm_norm_rope_backward (norms of queries and keys with the rotation by
+ * positions; frequencies by mxgemm_rope_frequencies), and
+ * mxgemm_cache_attention_shared (sequences that share their first tokens).
  */
 #ifndef MXGEMM_H_
 #define MXGEMM_H_
@@ -68,7 +73,8 @@ typedef void *mxgemm_stream_t;
 
 typedef enum {
   MXGEMM_OUT_F32 = 0,
-  MXGEMM_OUT_BF16 = 1
+  MXGEMM_OUT_BF16 = 1,
+  MXGEMM_OUT_E4M3 = 2 /* mxgemm_run_gated_block128 alone: codes, with scales of their own */
 } mxgemm_out_dtype_t;
 
 typedef enum {
@@ -461,6 +467,148 @@ typedef enum {
 int mxgemm_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t C, int block,
                              void *codes, float *scales, mxgemm_stream_t stream);
 
+/* Activations of a gated feed-forward block. */
+typedef enum {
+  MXGEMM_ACT_SILU = 0,     /* g / (1 + e^-g) */
+  MXGEMM_ACT_GELU_TANH = 1 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} mxgemm_act_t;
+
+/* Both projections of a gated feed-forward block, their activation and product
+ * in one kernel, on `stream`:
+ *
+ *   H[m,n] = act(g[m,n]) * u[m,n],   g = A . G^T,  u = A . U^T
+ *
+ * with the products of mxgemm_run_block128 (b_block = 128), whose arguments these
+ * are: A M x K with A_scale; G and U the two weights with their scales, both N x K
+ * or both K x N as MXGEMM_OPT_B_MAJOR says.  g, u and H stay in FP32 until H is
+ * rounded once.
+ *   M, N : each in [0, 2^31 - 512];  K in [16, 2^31 - 512], K % 16 == 0;  N % 16 == 0
+ *          with K x N weights or MXGEMM_OUT_E4M3.  M == 0 or N == 0 is a no-op.
+ *   H    : M x N: MXGEMM_OUT_F32, MXGEMM_OUT_BF16 (H_scale NULL), or
+ *          MXGEMM_OUT_E4M3: codes with H_scale M x ceil(N/128) float, as
+ *          mxgemm_quantize_block128 makes them by MXGEMM_BLOCK_ROWS (the operand
+ *          of the down-projection).
+ *   gate, up : M x N bfloat16 that receive g and u for mxgemm_gated_backward, or
+ *          both NULL.
+ * Alignment, ranges of the scales, formats and options as for
+ * mxgemm_run_block128 (gate and up 16-byte aligned); outputs must not overlap
+ * operands or each other.  With the split of the work, the order of the sums depends on
+ * the sizes alone: equal calls give equal bits. */
+int mxgemm_run_gated_block128(mxgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *A,
+                              const float *A_scale, const void *G, const float *G_scale,
+                              const void *U, const float *U_scale, int act, void *H,
+                              float *H_scale, int h_dtype, void *gate, void *up,
+                              mxgemm_stream_t stream);
+
+/* A quantized matrix: codes and scales of mxgemm_quantize_block128; both NULL where
+ * it is not wanted. */
+typedef struct {
+  void *codes;
+  float *scales;
+} mxgemm_block128_t;
+
+/* What mxgemm_gated_backward writes; what is NULL is left out. */
+typedef struct {
+  void *dgate, *dup;                 /* R x C bfloat16 */
+  mxgemm_block128_t dgate_rows, dup_rows; /* by MXGEMM_BLOCK_ROWS: for the gradient of A */
+  mxgemm_block128_t dgate_cols, dup_cols; /* by MXGEMM_BLOCK_COLS: for the gradients of G and U */
+  mxgemm_block128_t hidden_cols;     /* act(gate) * up, by MXGEMM_BLOCK_COLS: for the gradient
+                                        of the down-projection's weight */
+} mxgemm_gated_grads_t;
+
+/* The gradient of H = act(gate) * up, on `stream`:
+ *
+ *   dgate = dH * up * act'(gate),   dup = dH * act(gate)
+ *
+ * of R x C matrices: gate and up bfloat16 (as mxgemm_run_gated_block128 keeps
+ * them), dH float (MXGEMM_IN_F32) or bfloat16 (MXGEMM_IN_BF16).  Formed in FP32 and
+ * rounded once to each output; the quantized ones are what
+ * mxgemm_quantize_block128 makes of the FP32 values.  Values must be finite.
+ * R, C in [0, 2^31 - 128); C % 16 == 0 where an output is quantized.  At least one
+ * output.  All matrices and codes 16-byte aligned, scales 4-byte; outputs overlap
+ * neither inputs nor each other.  Runs on the current device, needs no handle and
+ * allocates nothing; errors as for mxgemm_quantize. */
+int mxgemm_gated_backward(const void *gate, const void *up, const void *dH, int dh_dtype,
+                          int64_t R, int64_t C, int act, const mxgemm_gated_grads_t *out,
+                          mxgemm_stream_t stream);
+
+/* The heads of a projection's output (queries, or keys) for mxgemm_norm_rope and
+ * its gradient: `tokens` rows of heads x head_dim values, each row's start a pitch
+ * (in elements) from the one before. */
+typedef struct {
+  const void *x;        /* as the projection gave them (gradient: NULL if weight is) */
+  int64_t x_pitch;
+  const void *dy;       /* gradient: of the result */
+  int64_t dy_pitch;
+  void *out;            /* the result; gradient: dx */
+  int64_t out_pitch;
+  const void *weight;   /* head_dim values of the norm, or NULL: no norm */
+  float *dweight;       /* gradient: head_dim, or NULL */
+  int64_t heads;        /* 0: none */
+} mxgemm_heads_t;
+
+/* The rotation by positions; NULL, or rot = 0: none. */
+typedef struct {
+  const int32_t *positions; /* one for each token */
+  const double *freqs;      /* rot / 2: radians a position */
+  int32_t rot;              /* values of a head that are rotated, the first; a multiple of 16, at
+                               most head_dim; the others pass */
+  int32_t interleaved;      /* pairs (2 j, 2 j + 1); 0: pairs (j, j + rot / 2) */
+  float factor;             /* the rotated values are multiplied by it */
+} mxgemm_rope_t;
+
+/* Norms of queries and keys for each head and the rotation by positions, in one
+ * pass, on `stream`:
+ *
+ *   n = x / sqrt(mean x^2 + eps) * weight     (mean over the head's values)
+ *   y = n with pair j of the first `rot` values turned by positions[t] * freqs[j]:
+ *       (a, b) -> factor (a cos - b sin, b cos + a sin)
+ *
+ * q and k (k may be NULL) are told by mxgemm_heads_t; out may be x itself with the
+ * same pitch, else outputs overlap nothing.  x, dy and out float or bfloat16
+ * (x_dtype), weights float or bfloat16 (w_dtype).  head_dim 64 or 128; tokens * heads <
+ * 2^31, heads < 65536.  FP32 throughout, rounded once; the angles are exact to
+ * 2^-24 of half a turn at any position (the frequencies' products with positions are
+ * reduced in 64 bits).  mean x^2 is to be in FP32's range.  x, dy and out 16-byte
+ * aligned with pitches that are multiples of 8, weights aligned to 8 of their
+ * elements (MXGEMM_ERR_MISALIGNED).  Runs on the current device, needs no handle and
+ * allocates nothing; errors as for mxgemm_quantize. */
+int mxgemm_norm_rope(const mxgemm_heads_t *q, const mxgemm_heads_t *k, int64_t tokens,
+                     int64_t head_dim, int x_dtype, int w_dtype, float eps,
+                     const mxgemm_rope_t *rope, mxgemm_stream_t stream);
+
+/* Its gradient, on `stream`: with dn = dy turned back (times factor) and r =
+ * 1 / sqrt(mean x^2 + eps),
+ *
+ *   dweight = sum over tokens and heads of dn r x
+ *   dx = r (dn weight - r x mean(dn weight r x)),   or dn without a norm
+ *
+ * Arguments as for mxgemm_norm_rope, with x the projection's values again; out (dx)
+ * may be dy itself with the same pitch.  dweight is FP32, set (not added to), and
+ * summed in an order that depends on the sizes alone: equal calls give equal bits.
+ * The handle's workspace holds its partial sums. */
+int mxgemm_norm_rope_backward(mxgemm_handle_t h, const mxgemm_heads_t *q,
+                              const mxgemm_heads_t *k, int64_t tokens, int64_t head_dim,
+                              int x_dtype, int w_dtype, float eps, const mxgemm_rope_t *rope,
+                              mxgemm_stream_t stream);
+
+/* How frequencies are stretched for contexts longer than the trained one. */
+typedef enum {
+  MXGEMM_ROPE_PLAIN = 0,   /* f_j = base^(-2j/rot) */
+  MXGEMM_ROPE_LINEAR = 1,  /* f_j / scale */
+  MXGEMM_ROPE_BASE = 2,    /* the base times scale^(rot/(rot-2)): the slowest pair is stretched
+                              by scale, the fastest stays */
+  MXGEMM_ROPE_BY_PARTS = 3 /* pairs that turn `fast` times or more over `trained` positions stay,
+                              those of `slow` turns or fewer are divided by scale, between
+                              them linear in the turns */
+} mxgemm_rope_scaling_t;
+
+/* Frequencies for mxgemm_rope_t, in HOST memory: rot / 2 doubles (copy them to the
+ * device once).  rot even and >= 0; base > 0; scale >= 1; for
+ * MXGEMM_ROPE_BY_PARTS trained > 0 and 0 < slow < fast.  Touches no GPU. */
+int mxgemm_rope_frequencies(int64_t rot, double base, int scaling, double scale,
+                            double trained, double slow, double fast, double *freqs);
+
 /* A key/value cache held in pages of E4M3 codes, with one FP32 scale for each
  * page and key/value head (value = code * scale).  The caller owns the device
  * memory; the struct is read during the call only.
@@ -546,6 +694,20 @@ int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64
                            const void *Q, int64_t q_pitch, float scale, int causal,
                            int64_t window, int64_t sinks, void *O, float *lse,
                            mxgemm_stream_t stream);
+
+/* mxgemm_cache_attention for a batch whose sequences share their first `shared`
+ * tokens: the same result, with the shared keys and values read once for the whole
+ * batch instead of once for each sequence.  The caller promises that the rows of
+ * the page table agree on the first floor(shared / page_size) pages, each as far as its
+ * sequence reaches (the longest sequence's row is read); everything else is as
+ * without sharing, and any shared >= 0 that keeps the promise is allowed: a part of a
+ * page, more than some sequence has, 0.  Arguments otherwise as for mxgemm_cache_attention, without a window.  Two
+ * launches; partial results of the shared part are FP32 in the handle's workspace. */
+int mxgemm_cache_attention_shared(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
+                                  int64_t heads, const int32_t *page_table, int64_t table_pitch,
+                                  const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
+                                  int64_t shared, const void *Q, int64_t q_pitch, float scale,
+                                  int causal, void *O, float *lse, mxgemm_stream_t stream);
 
 /* Static description of a status code. */
 const char *mxgemm_status_string(int status);
