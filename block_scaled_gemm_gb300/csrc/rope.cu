@@ -84,27 +84,30 @@ int rope_args(int device, const mxgemm_heads_t *q, const mxgemm_heads_t *k, int6
   return MXGEMM_OK;
 }
 
-template <typename T, int D, int TT>
-int launch_forward(mxg::RopeParams &p, cudaStream_t stream) {
-  // heads of a block: all of a tensor's where a token has a warp, else one pass
-  constexpr int kStep = 8 / TT * mxg::RopeCfg<D>::HEADS;
-  for (mxg::RopeTensor &t : p.t) t.chunks = t.heads == 0 ? 0 : TT == 8 ? 1 : static_cast<int>(cdiv(t.heads, kStep));
-  const dim3 grid(static_cast<unsigned>(cdiv(p.tokens, TT)), static_cast<unsigned>(p.t[0].chunks + p.t[1].chunks));
-  return mxg::launch(mxg::norm_rope_kernel<T, D, TT>, grid, 256, 0, 1, stream, p);
+// Steps of a token: a warp's heads at a time.
+template <typename C>
+int64_t count_steps(mxg::RopeParams &p) {
+  int64_t steps = 0;
+  for (mxg::RopeTensor &t : p.t) steps += t.steps = static_cast<int>(cdiv(t.heads, C::HEADS));
+  return steps;
 }
 
 template <typename T, int D>
 int run_forward(mxg::RopeParams &p, cudaStream_t stream) {
-  return p.tokens >= 2432 ? launch_forward<T, D, 8>(p, stream) : launch_forward<T, D, 1>(p, stream);
+  // three blocks an SM, no more warps than steps
+  using C = mxg::RopeCfg<T, D, false>;
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), 8), 3 * 152);
+  return mxg::launch(mxg::norm_rope_kernel<T, D>, dim3(static_cast<unsigned>(grid)), 256, C::SMEM_BYTES, 1, stream, p);
 }
 
 template <typename T, int D>
 int run_backward(mxgemm_handle_t h, const mxg::HandleView &v, mxg::RopeParams &p, cudaStream_t stream) {
-  // blocks that stay: two an SM, shared out by the tensors' heads
-  const int64_t groups = cdiv(p.tokens, 8), all = p.t[0].heads + p.t[1].heads;
+  // two blocks an SM, shared out by the tensors' steps
+  using C = mxg::RopeCfg<T, D, true>;
+  const int64_t all = count_steps<C>(p);
   int blocks = 0, rows = 0;
   for (mxg::RopeTensor &t : p.t) {
-    t.blocks = t.heads ? static_cast<int>(std::min(groups, std::max<int64_t>(1, 2 * v.sm_count * t.heads / all))) : 0;
+    t.blocks = t.heads ? static_cast<int>(std::min(cdiv(p.tokens * t.steps, 8), std::max<int64_t>(1, 2 * v.sm_count * t.steps / all))) : 0;
     const int g = mxg::rope_group(t.blocks);
     blocks += t.blocks;
     rows += t.blocks + (t.blocks + g - 1) / g;
@@ -115,7 +118,7 @@ int run_backward(mxgemm_handle_t h, const mxg::HandleView &v, mxg::RopeParams &p
     p.partials = reinterpret_cast<float *>(ws);
     p.counters = v.counters;
   }
-  return mxg::launch(mxg::norm_rope_backward_kernel<T, D>, dim3(blocks), 256, 0, 1, stream, p);
+  return mxg::launch(mxg::norm_rope_backward_kernel<T, D>, dim3(blocks), 256, C::SMEM_BYTES, 1, stream, p);
 }
 
 }  // namespace

@@ -16,13 +16,17 @@
 // happens in registers.  A head is D / 16 lanes, each with two runs of eight
 // values that hold whole pairs in either layout (run s of the first half of the
 // rotated values and run s of the second), so that a rotation needs no exchange
-// between lanes.  Cosines and sines are computed once for a block's tokens and
-// shared through shared memory by all heads.
+// between lanes.  All tokens' heads, four or eight at a time, are cut into equal
+// ranges for the warps, each of which works by itself: its lanes copy what they will
+// read themselves into a ring in shared memory, three steps ahead (cp.async: what is
+// on its way takes no registers), and it computes a token's cosines and sines once
+// for all of that token's heads in its range.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "tmem_util.cuh"
 
 namespace mxg {
 
@@ -33,8 +37,8 @@ struct RopeTensor {
   const void *w;  // or null: no norm
   float *dw;
   int heads;
-  int chunks;     // blocks along a token's heads (forward)
-  int blocks;     // blocks of this tensor (backward)
+  int steps;   // of a token: the heads that a warp takes at a time
+  int blocks;  // of this tensor (backward)
 };
 
 struct RopeParams {
@@ -46,43 +50,40 @@ struct RopeParams {
   const double *freqs;
   int rot, interleaved;
   float *partials;     // backward: a row of D for each block, then one for each group of blocks
-  unsigned *counters;  // backward: groups of queries, groups of keys, then one for each tensor
+  unsigned *counters;  // backward: one for each tensor, then groups of queries, groups of keys
 };
 
-// Eight consecutive values (16-byte aligned) in FP32.
+// Eight consecutive values in FP32, in pairs.
 struct F8 {
-  float v[8];
+  float2 v[4];
 };
-__device__ __forceinline__ F8 load8(const float *p) {
-  const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+__device__ __forceinline__ F8 floats_of(const uint4 (&w)[2], float) {
+  return F8{{make_float2(__uint_as_float(w[0].x), __uint_as_float(w[0].y)), make_float2(__uint_as_float(w[0].z), __uint_as_float(w[0].w)),
+             make_float2(__uint_as_float(w[1].x), __uint_as_float(w[1].y)), make_float2(__uint_as_float(w[1].z), __uint_as_float(w[1].w))}};
 }
-__device__ __forceinline__ F8 load8(const __nv_bfloat16 *p) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ F8 floats_of(const uint4 (&w)[1], __nv_bfloat16) {
+  const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
   F8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(u[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) r.v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
   return r;
 }
 __device__ __forceinline__ void store8(float *p, const F8 &a) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+  reinterpret_cast<float4 *>(p)[0] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const F8 &a) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a.v[2 * i], a.v[2 * i + 1]);
+    const __nv_bfloat162 h = __float22bfloat162_rn(a.v[i]);
     u[i] = *reinterpret_cast<const uint32_t *>(&h);
   }
   *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ F8 load_weight8(const void *w, int at, int bf16) {
-  return bf16 ? load8(static_cast<const __nv_bfloat16 *>(w) + at) : load8(static_cast<const float *>(w) + at);
+__device__ __forceinline__ F8 shared_run(const float *w) {
+  const float4 a = *reinterpret_cast<const float4 *>(w), b = *reinterpret_cast<const float4 *>(w + 4);
+  return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
 // A frequency (radians a position) as a fraction of a turn, times 2^64.
@@ -98,9 +99,19 @@ __device__ __forceinline__ float2 angle_at(uint64_t turn, int pos, float factor)
   return make_float2(c * factor, s * factor);
 }
 
-template <int D>
+template <typename T, int D, bool BACK>
 struct RopeCfg {
   static constexpr int LANES = D / 16, HEADS = 32 / LANES;  // lanes of a head, heads of a warp
+  static constexpr int WORDS = sizeof(T) / 2;               // 16-byte words of a run
+  static constexpr int PIECES = (BACK ? 4 : 2) * WORDS;     // words of a lane: dy and x, or x
+  static constexpr int STAGES = 4;
+  static constexpr int OFF_TURN = 0;                        // [D / 2] turns a position
+  static constexpr int OFF_W = OFF_TURN + D / 2 * 8;        // [2][D] weights
+  static constexpr int OFF_CS = OFF_W + 2 * D * 4;          // [8 warps][cosines, sines][D / 2]
+  static constexpr int OFF_POS = OFF_CS + 8 * D / 2 * 8;    // [8 warps][STAGES] positions
+  static constexpr int OFF_RING = OFF_POS + 8 * STAGES * 4;  // [8 warps][STAGES][PIECES][32 lanes]
+  static constexpr int SMEM_BYTES = OFF_RING + 8 * STAGES * PIECES * 512;
+  static_assert(OFF_RING % 16 == 0, "alignment");
 };
 
 // The two runs of a head's lane, and whether they are rotated.
@@ -115,32 +126,31 @@ __device__ __forceinline__ Runs runs_of(int sub, int rot) {
   return Runs{at, at + 8, false};
 }
 
-// The lane's eight angles of a token: cs holds its rot / 2.
-__device__ __forceinline__ void lane_angles(const float2 *cs, int sub, int rot, int interleaved, bool turned, float2 (&k)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int j = !interleaved ? 8 * sub + e : e < 4 ? 4 * sub + e : (rot >> 2) + 4 * sub + e - 4;
-    k[e] = turned ? cs[j] : make_float2(1.f, 0.f);
-  }
-}
-
-// Pairs turned forward (BACK = false) or back.
+// A lane's pairs turned forward, or back; c and s are a token's rot / 2 cosines and
+// sines, and sub the lane of the head.
 template <bool BACK>
-__device__ __forceinline__ void turn(F8 &a, F8 &b, const float2 (&k)[8], int interleaved) {
-  auto one = [](float &x, float &y, float2 cs) {
-    const float s = BACK ? -cs.y : cs.y, u = x, v = y;
-    x = u * cs.x - v * s;
-    y = v * cs.x + u * s;
-  };
-  if (interleaved) {
+__device__ __forceinline__ void turn(F8 &a, F8 &b, const float *c, const float *s, int sub, int rot, int interleaved) {
+  if (interleaved) {  // (x, y) -> (x, y) c + (y, x) (-s, s)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      one(a.v[2 * e], a.v[2 * e + 1], k[e]);
-      one(b.v[2 * e], b.v[2 * e + 1], k[4 + e]);
+    for (int k = 0; k < 2; ++k) {
+      F8 &x = k ? b : a;
+      const int j = (k ? rot >> 2 : 0) + 4 * sub;
+      const float4 cc = *reinterpret_cast<const float4 *>(c + j), ss = *reinterpret_cast<const float4 *>(s + j);
+      const float ca[4] = {cc.x, cc.y, cc.z, cc.w}, sa[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float t = BACK ? -sa[e] : sa[e];
+        x.v[e] = fma2(make_float2(x.v[e].y, x.v[e].x), make_float2(-t, t), mul2(x.v[e], make_float2(ca[e], ca[e])));
+      }
     }
   } else {
+    const F8 cc = shared_run(c + 8 * sub), ss = shared_run(s + 8 * sub);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) one(a.v[e], b.v[e], k[e]);
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = BACK ? make_float2(-ss.v[e].x, -ss.v[e].y) : ss.v[e], u = a.v[e], v = b.v[e];
+      a.v[e] = fma2(v, make_float2(-t.x, -t.y), mul2(u, cc.v[e]));
+      b.v[e] = fma2(u, t, mul2(v, cc.v[e]));
+    }
   }
 }
 
@@ -151,69 +161,162 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
-// Angles of TT tokens from the block's first into cs.
-template <int D, int TT>
-__device__ __forceinline__ void block_angles(const RopeParams &p, int64_t first, float2 (*cs)[D / 2]) {
-  const int half = p.rot >> 1;
-  for (int i = threadIdx.x; i < TT * half; i += 256) {
-    const int t = i / half, j = i - t * half;
-    if (first + t < p.tokens) cs[t][j] = angle_at(turn_of(p.freqs[j]), p.positions[first + t], p.factor);
+__device__ __forceinline__ void rope_copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void rope_copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Where a warp is: a token, and step j of it (the queries' steps, then the keys').
+struct RopeAt {
+  int64_t token;
+  int j, left;  // left: steps of the warp's range
+};
+
+// One warp's walk over its range of the steps of all tokens: the ring of loads that
+// is ahead of it, and the angles of the token that it has reached.
+template <typename T, int D, bool BACK>
+struct RopeWalk {
+  using C = RopeCfg<T, D, BACK>;
+  const RopeParams &p;
+  int first, of_token;  // steps of a token before the keys', and in all (backward: of one tensor)
+  int which_first;      // backward: that tensor
+  int lane, sub, warp;
+  uint8_t *sm;
+  uint32_t ring;
+  Runs r;
+  RopeAt at, ahead;
+  int stage, filled;
+  int64_t angles_of;  // the token whose angles are there
+
+  // warp `w` of `warps`
+  __device__ RopeWalk(const RopeParams &p_, uint8_t *sm_, int64_t w, int64_t warps, int which)
+      : p(p_), which_first(which), lane(threadIdx.x & 31), sub(lane % C::LANES), warp(threadIdx.x >> 5), sm(sm_),
+        ring(smem_u32(sm_ + C::OFF_RING) + (warp * C::STAGES * C::PIECES * 32 + lane) * 16), r(runs_of(sub, p_.rot)), stage(0), filled(0),
+        angles_of(-1) {
+    first = p.t[which].steps;
+    of_token = BACK ? first : first + p.t[1].steps;
+    const int64_t all = p.tokens * of_token, u0 = w * all / warps;
+    at.token = u0 / of_token;
+    at.j = static_cast<int>(u0 - at.token * of_token);
+    at.left = static_cast<int>((w + 1) * all / warps - u0);
+    ahead = at;
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) load();
+  }
+  __device__ void next(RopeAt &a) const {
+    --a.left;
+    if (++a.j == of_token) {
+      a.j = 0;
+      ++a.token;
+    }
+  }
+  __device__ bool more() const { return at.left > 0; }
+  __device__ int which(const RopeAt &a) const { return BACK ? which_first : a.j >= first; }
+  __device__ int head(const RopeAt &a) const { return (a.j - (!BACK && a.j >= first ? first : 0)) * C::HEADS + lane / C::LANES; }
+  // The loads of the place that is ahead, into the next stage (an empty group past the end).
+  __device__ void load() {
+    if (ahead.left > 0) {
+      const RopeTensor &t = p.t[which(ahead)];
+      const int h = head(ahead);
+      if (h < t.heads) {
+        const uint32_t to = ring + filled * C::PIECES * 512;
+#pragma unroll
+        for (int k = 0; k < (BACK ? 2 : 1); ++k) {  // dy, then x
+          const bool dy = BACK && k == 0;
+          if (!dy && BACK && !t.w) continue;
+          const T *from = static_cast<const T *>(dy ? t.dy : t.x) + ahead.token * (dy ? t.dy_pitch : t.x_pitch) + h * D;
+#pragma unroll
+          for (int i = 0; i < C::WORDS; ++i) {
+            rope_copy16(to + (k * 2 * C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from + r.a) + i);
+            rope_copy16(to + (k * 2 * C::WORDS + C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from + r.b) + i);
+          }
+        }
+      }
+      if (lane == 0 && p.rot) rope_copy4(smem_u32(sm + C::OFF_POS) + (warp * C::STAGES + filled) * 4, p.positions + ahead.token);
+      next(ahead);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    filled = filled + 1 == C::STAGES ? 0 : filled + 1;
+  }
+  __device__ float *angles() const { return reinterpret_cast<float *>(sm + C::OFF_CS) + warp * D; }
+  // Waits for the place that has been reached, and its token's angles.
+  __device__ void arrive() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
+    __syncwarp();
+    if (p.rot && at.token != angles_of) {
+      angles_of = at.token;
+      const int pos = *reinterpret_cast<const volatile int *>(sm + C::OFF_POS + (warp * C::STAGES + stage) * 4);
+      const uint64_t *turns = reinterpret_cast<const uint64_t *>(sm + C::OFF_TURN);
+      for (int j = lane; j < p.rot >> 1; j += 32) {
+        const float2 a = angle_at(turns[j], pos, p.factor);
+        angles()[j] = a.x;
+        angles()[D / 2 + j] = a.y;
+      }
+      __syncwarp();
+    }
+  }
+  // Run `i` (0, 1) of tensor k (0: dy where there is one, 1: then x).
+  __device__ F8 run(int k, int i) const {
+    uint4 w[C::WORDS];
+#pragma unroll
+    for (int n = 0; n < C::WORDS; ++n) w[n] = ld_shared_v4(ring + (stage * C::PIECES + (k * 2 + i) * C::WORDS + n) * 512);
+    return floats_of(w, T{});
+  }
+  // Past this place: its stage has been read by this lane (and, positions, by the warp).
+  __device__ void advance() {
+    __syncwarp();
+    load();
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+    next(at);
+  }
+};
+
+// Turns a position and weights of both tensors into shared memory.
+template <typename T, int D, bool BACK>
+__device__ __forceinline__ void rope_tables(const RopeParams &p, uint8_t *sm) {
+  using C = RopeCfg<T, D, BACK>;
+  for (int j = threadIdx.x; j < p.rot >> 1; j += 256) reinterpret_cast<uint64_t *>(sm + C::OFF_TURN)[j] = turn_of(p.freqs[j]);
+  for (int i = threadIdx.x; i < 2 * D; i += 256) {
+    const void *w = p.t[i / D].w;
+    if (w)
+      reinterpret_cast<float *>(sm + C::OFF_W)[i] =
+          p.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i % D]) : static_cast<const float *>(w)[i % D];
   }
 }
-
-// 256 threads: TT tokens, 8 / TT warps each; a warp takes HEADS heads at a time.
-template <typename T, int D, int TT>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const RopeParams p) {
-  using C = RopeCfg<D>;
-  constexpr int WARPS = 8 / TT, STEP = WARPS * C::HEADS;  // warps of a token, heads of a pass
-  __shared__ float2 cs[TT][D / 2];
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 3) norm_rope_kernel(const RopeParams p) {
+  using C = RopeCfg<T, D, false>;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % C::LANES;
-  const int y = blockIdx.y;
-  const RopeTensor &t = p.t[y < p.t[0].chunks ? 0 : 1];
-  const int chunk = y < p.t[0].chunks ? y : y - p.t[0].chunks;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * TT, token = first + warp / WARPS;
-  const int per = (t.heads + t.chunks * STEP - 1) / (t.chunks * STEP) * STEP;  // heads of a chunk
-  const int h_end = min(t.heads, (chunk + 1) * per);
-  const Runs r = runs_of(sub, p.rot);
-  if (p.rot) {
-    block_angles<D, TT>(p, first, cs);
-    __syncthreads();
-  }
-  if (token >= p.tokens) return;
-  float2 k[8];
-  lane_angles(cs[warp / WARPS], sub, p.rot, p.interleaved, r.turned, k);
-  F8 wa, wb;
-  if (t.w) {
-    wa = load_weight8(t.w, r.a, p.w_bf16);
-    wb = load_weight8(t.w, r.b, p.w_bf16);
-  }
-  const T *x = static_cast<const T *>(t.x) + token * t.x_pitch;
-  T *out = static_cast<T *>(t.out) + token * t.out_pitch;
-#pragma unroll 2
-  for (int h0 = chunk * per + (warp % WARPS) * C::HEADS; h0 < h_end; h0 += STEP) {
-    const int h = h0 + lane / C::LANES;
-    F8 a{}, b{};
-    if (h < h_end) {
-      a = load8(x + h * D + r.a);
-      b = load8(x + h * D + r.b);
-    }
+  RopeWalk<T, D, false> walk(p, rope_smem, static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * 8, 0);
+  rope_tables<T, D, false>(p, rope_smem);
+  __syncthreads();
+  const Runs r = walk.r;
+  for (; walk.more(); walk.advance()) {
+    walk.arrive();
+    const int which = walk.which(walk.at), h = walk.head(walk.at);
+    const RopeTensor &t = p.t[which];
+    F8 a = walk.run(0, 0), b = walk.run(0, 1);
     if (t.w) {
-      float sum = 0.f;
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(a.v[e], a.v[e], fmaf(b.v[e], b.v[e], sum));
-      const float inv = 1.f / sqrtf(fmaf(head_sum<C::LANES>(sum), 1.f / D, p.eps));
+      for (int e = 0; e < 4; ++e) sum = fma2(a.v[e], a.v[e], fma2(b.v[e], b.v[e], sum));
+      const float inv = rsqrtf(fmaf(head_sum<C::LANES>(sum.x + sum.y), 1.f / D, p.eps));
+      const float *w = reinterpret_cast<const float *>(rope_smem + C::OFF_W) + which * D;
+      const F8 wa = shared_run(w + r.a), wb = shared_run(w + r.b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a.v[e] *= inv * wa.v[e];
-        b.v[e] *= inv * wb.v[e];
+      for (int e = 0; e < 4; ++e) {
+        a.v[e] = mul2(mul2(a.v[e], make_float2(inv, inv)), wa.v[e]);
+        b.v[e] = mul2(mul2(b.v[e], make_float2(inv, inv)), wb.v[e]);
       }
     }
-    if (r.turned) turn<false>(a, b, k, p.interleaved);
-    if (h < h_end) {
-      store8(out + h * D + r.a, a);
-      store8(out + h * D + r.b, b);
+    if (r.turned) turn<false>(a, b, walk.angles(), walk.angles() + D / 2, walk.sub, p.rot, p.interleaved);
+    if (h < t.heads) {
+      T *out = static_cast<T *>(t.out) + walk.at.token * t.out_pitch + h * D;
+      store8(out + r.a, a);
+      store8(out + r.b, b);
     }
   }
 }
@@ -243,90 +346,77 @@ __host__ __device__ constexpr int rope_group(int blocks) {
   return g;
 }
 
-// The gradient: 256 threads, a token a warp and HEADS heads at a time, blocks that
-// stay for further tokens.  dw is summed in registers over a thread's tokens and
+// The gradient: blocks of eight warps that stay for further tokens.  dw is summed in registers over a thread's tokens and
 // heads, then over the block, and the blocks' sums are added by the block that
 // arrives last, first in groups and then over the groups: no float atomics, so that
 // equal calls give equal bits, and 25 rows to add at most where 608 would take one
 // block longer than the rest of the call.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) norm_rope_backward_kernel(const RopeParams p) {
-  using C = RopeCfg<D>;
-  __shared__ float2 cs[8][D / 2];
+__global__ void __launch_bounds__(256, 2) norm_rope_backward_kernel(const RopeParams p) {
+  using C = RopeCfg<T, D, true>;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
   __shared__ float sums[8][D];
   __shared__ int last;
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % C::LANES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int which = static_cast<int>(blockIdx.x) < p.t[0].blocks ? 0 : 1;
   const RopeTensor &t = p.t[which];
   const int block = blockIdx.x - (which ? p.t[0].blocks : 0);
-  const Runs r = runs_of(sub, p.rot);
-  F8 wa, wb, da{}, db{};
-  if (t.w) {
-    wa = load_weight8(t.w, r.a, p.w_bf16);
-    wb = load_weight8(t.w, r.b, p.w_bf16);
-  }
-  for (int64_t first = static_cast<int64_t>(block) * 8; first < p.tokens; first += static_cast<int64_t>(t.blocks) * 8) {
-    if (p.rot) {
-      __syncthreads();  // the angles before have been read
-      block_angles<D, 8>(p, first, cs);
-      __syncthreads();
+  RopeWalk<T, D, true> walk(p, rope_smem, static_cast<int64_t>(block) * 8 + warp, static_cast<int64_t>(t.blocks) * 8, which);
+  rope_tables<T, D, true>(p, rope_smem);
+  __syncthreads();
+  const Runs r = walk.r;
+  const float *w = reinterpret_cast<const float *>(rope_smem + C::OFF_W) + which * D;
+  F8 da{}, db{};
+  for (; walk.more(); walk.advance()) {
+    walk.arrive();
+    F8 ga = walk.run(0, 0), gb = walk.run(0, 1);
+    if (r.turned) turn<true>(ga, gb, walk.angles(), walk.angles() + D / 2, walk.sub, p.rot, p.interleaved);
+    const int h = walk.head(walk.at);
+    if (t.w) {
+      const F8 xa = walk.run(1, 0), xb = walk.run(1, 1), wa = shared_run(w + r.a), wb = shared_run(w + r.b);
+      float2 ss = make_float2(0.f, 0.f), sd = ss;
+      F8 ya, yb;  // dn w
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ss = fma2(xa.v[e], xa.v[e], fma2(xb.v[e], xb.v[e], ss));
+        ya.v[e] = mul2(ga.v[e], wa.v[e]);
+        yb.v[e] = mul2(gb.v[e], wb.v[e]);
+        sd = fma2(ya.v[e], xa.v[e], fma2(yb.v[e], xb.v[e], sd));
+      }
+      const float inv = rsqrtf(fmaf(head_sum<C::LANES>(ss.x + ss.y), 1.f / D, p.eps));
+      const float m = -head_sum<C::LANES>(sd.x + sd.y) * (1.f / D) * inv * inv * inv;
+      // (a stage that nothing was copied to holds anything)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (h < t.heads) {
+          da.v[e] = fma2(ga.v[e], mul2(xa.v[e], make_float2(inv, inv)), da.v[e]);
+          db.v[e] = fma2(gb.v[e], mul2(xb.v[e], make_float2(inv, inv)), db.v[e]);
+        }
+        ga.v[e] = fma2(xa.v[e], make_float2(m, m), mul2(ya.v[e], make_float2(inv, inv)));
+        gb.v[e] = fma2(xb.v[e], make_float2(m, m), mul2(yb.v[e], make_float2(inv, inv)));
+      }
     }
-    const int64_t token = first + warp;
-    if (token >= p.tokens) continue;
-    float2 k[8];
-    lane_angles(cs[warp], sub, p.rot, p.interleaved, r.turned, k);
-    const T *dy = static_cast<const T *>(t.dy) + token * t.dy_pitch;
-    const T *x = static_cast<const T *>(t.x) + token * t.x_pitch;
-    T *dx = static_cast<T *>(t.out) + token * t.out_pitch;
-    for (int h0 = 0; h0 < t.heads; h0 += C::HEADS) {
-      const int h = h0 + lane / C::LANES;
-      F8 ga{}, gb{}, xa{}, xb{};
-      if (h < t.heads) {
-        ga = load8(dy + h * D + r.a);
-        gb = load8(dy + h * D + r.b);
-        if (t.w) {
-          xa = load8(x + h * D + r.a);
-          xb = load8(x + h * D + r.b);
-        }
-      }
-      if (r.turned) turn<true>(ga, gb, k, p.interleaved);
-      if (t.w) {
-        float ss = 0.f, sd = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(xa.v[e], xa.v[e], fmaf(xb.v[e], xb.v[e], ss));
-          sd = fmaf(ga.v[e] * wa.v[e], xa.v[e], fmaf(gb.v[e] * wb.v[e], xb.v[e], sd));
-        }
-        const float inv = 1.f / sqrtf(fmaf(head_sum<C::LANES>(ss), 1.f / D, p.eps));
-        const float m = head_sum<C::LANES>(sd) * (1.f / D) * inv * inv;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          da.v[e] = fmaf(ga.v[e], xa.v[e] * inv, da.v[e]);
-          db.v[e] = fmaf(gb.v[e], xb.v[e] * inv, db.v[e]);
-          ga.v[e] = inv * (ga.v[e] * wa.v[e] - xa.v[e] * m);
-          gb.v[e] = inv * (gb.v[e] * wb.v[e] - xb.v[e] * m);
-        }
-      }
-      if (h < t.heads) {
-        store8(dx + h * D + r.a, ga);
-        store8(dx + h * D + r.b, gb);
-      }
+    if (h < t.heads) {
+      T *dx = static_cast<T *>(t.out) + walk.at.token * t.out_pitch + h * D;
+      store8(dx + r.a, ga);
+      store8(dx + r.b, gb);
     }
   }
   if (!t.dw) return;
   // this block's row of dw: its warps' heads, then its warps
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    float a = e & 1 ? da.v[e >> 1].y : da.v[e >> 1].x, b = e & 1 ? db.v[e >> 1].y : db.v[e >> 1].x;
 #pragma unroll
     for (int o = C::LANES; o < 32; o <<= 1) {
-      da.v[e] += __shfl_xor_sync(0xFFFFFFFFu, da.v[e], o);
-      db.v[e] += __shfl_xor_sync(0xFFFFFFFFu, db.v[e], o);
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
     }
     if (lane < C::LANES) {
-      sums[warp][r.a + e] = da.v[e];
-      sums[warp][r.b + e] = db.v[e];
+      sums[warp][r.a + e] = a;
+      sums[warp][r.b + e] = b;
     }
   }
   __syncthreads();
