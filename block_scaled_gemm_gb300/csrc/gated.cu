@@ -101,16 +101,22 @@ int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, co
   }
 }
 
-template <typename T>
-int launch_grad(const mxg::GatedGradParams &p, bool tiles, cudaStream_t stream) {
+template <typename T, int ACT>
+int launch_grad(const mxg::GatedGradParams &p, bool tiles, int sms, cudaStream_t stream) {
   if (tiles) {
-    const int64_t grid = p.rb * p.cb;
-    if (grid >= kLim) return MXGEMM_ERR_INVALID_VALUE;
-    return mxg::launch(mxg::gated_grad_tile_kernel<T>, dim3(static_cast<unsigned>(grid)), 512, mxg::GatedGradCfg::SMEM_BYTES, 1, stream, p);
+    const int64_t grid = std::min<int64_t>(p.rb * p.cb, sms);
+    return mxg::launch(mxg::gated_grad_tile_kernel<T, ACT>, dim3(static_cast<unsigned>(grid)), 512, mxg::GatedGradCfg<T>::SMEM_BYTES, 1,
+                       stream, p);
   }
   const int64_t grid = cdiv(p.R * p.C, 2048);
   if (grid >= kLim) return MXGEMM_ERR_INVALID_VALUE;
-  return mxg::launch(mxg::gated_grad_flat_kernel<T>, dim3(static_cast<unsigned>(grid)), 256, 0, 1, stream, p);
+  return mxg::launch(mxg::gated_grad_flat_kernel<T, ACT>, dim3(static_cast<unsigned>(grid)), 256, 0, 1, stream, p);
+}
+
+template <typename T>
+int launch_grad(const mxg::GatedGradParams &p, int act, bool tiles, int sms, cudaStream_t stream) {
+  return act == MXGEMM_ACT_SILU ? launch_grad<T, mxg::kActSilu>(p, tiles, sms, stream)
+                                : launch_grad<T, mxg::kActGeluTanh>(p, tiles, sms, stream);
 }
 
 }  // namespace
@@ -214,11 +220,16 @@ extern "C" int mxgemm_gated_backward(const void *gate, const void *up, const voi
   p.pitch = cdiv(R, 16) * 16;
   p.rb = cdiv(R, 128);
   p.cb = cdiv(C, 128);
-  p.act = act;
   p.dgate = static_cast<__nv_bfloat16 *>(out->dgate);
   p.dup = static_cast<__nv_bfloat16 *>(out->dup);
   for (int i = 0; i < 5; ++i)
     (i < 2 ? p.rows[i] : p.cols[i - 2]) = mxg::Blocks128{static_cast<uint8_t *>(blocks[i]->codes), blocks[i]->scales};
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  return dh_dtype == MXGEMM_IN_F32 ? launch_grad<float>(p, tiles, stream) : launch_grad<__nv_bfloat16>(p, tiles, stream);
+  int sms = 1;
+  if (tiles && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  return dh_dtype == MXGEMM_IN_F32 ? launch_grad<float>(p, act, tiles, sms, stream)
+                                   : launch_grad<__nv_bfloat16>(p, act, tiles, sms, stream);
 }

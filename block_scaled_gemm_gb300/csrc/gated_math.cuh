@@ -7,6 +7,8 @@
 #pragma once
 #include <cstdint>
 
+#include "tmem_util.cuh"
+
 namespace mxg {
 
 constexpr int kActSilu = 0, kActGeluTanh = 1;  // mxgemm_act_t
@@ -25,15 +27,36 @@ __device__ __forceinline__ float act_weight(float g, int act) {
 }
 __device__ __forceinline__ float gated(float g, float u, int act) { return g * act_weight(g, act) * u; }
 
-// dgate, dup and the hidden value of one value's dH.
-struct GatedGrad {
-  float dg, du, h;
+// dgate, dup and the hidden value of two values' dH, in paired FP32 operations.
+struct GatedGrad2 {
+  float2 dg, du, h;
 };
-__device__ __forceinline__ GatedGrad gated_grad(float g, float u, float dh, int act) {
-  const float p = act_weight(g, act), a = g * p;
-  // (past |g| = 100 a (1 - p) is 0, which is not to meet an infinite slope)
-  const float slope = act == kActSilu ? 1.f : kGeluTwo * fmaf(3.f * kGeluCube, fminf(g * g, 1e4f), 1.f);
-  return GatedGrad{dh * u * fmaf(a * (1.f - p), slope, p), dh * a, a * u};
+__device__ __forceinline__ float2 logistic2(float2 e2) {  // 1 / (1 + 2^e2)
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e2.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e2.y));
+  e2 = add2(e2, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e2.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e2.y));
+  return e2;
+}
+template <int ACT>
+__device__ __forceinline__ GatedGrad2 gated_grad(float2 g, float2 u, float2 dh) {
+  auto both = [](float x) { return make_float2(x, x); };
+  constexpr float kLog2 = 1.44269504088896340736f;
+  float2 p, w;  // the logistic function's value, and the activation's derivative
+  if constexpr (ACT == kActSilu) {
+    p = logistic2(mul2(g, both(-kLog2)));
+    const float2 a = mul2(g, p);
+    w = fma2(a, fma2(p, both(-1.f), both(1.f)), p);
+  } else {
+    const float2 gg = mul2(g, g);
+    p = logistic2(mul2(mul2(g, both(-kLog2 * kGeluTwo)), fma2(gg, both(kGeluCube), both(1.f))));
+    // (past |g| = 100 a (1 - p) is 0, which is not to meet an infinite slope)
+    const float2 slope = fma2(make_float2(fminf(gg.x, 1e4f), fminf(gg.y, 1e4f)), both(3.f * kGeluCube * kGeluTwo), both(kGeluTwo));
+    w = fma2(mul2(mul2(g, p), fma2(p, both(-1.f), both(1.f))), slope, p);
+  }
+  const float2 a = mul2(g, p);
+  return GatedGrad2{mul2(mul2(dh, u), w), mul2(dh, a), mul2(a, u)};
 }
 
 }  // namespace mxg
