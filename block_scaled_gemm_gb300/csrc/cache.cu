@@ -10,6 +10,7 @@
 
 #include "cache_append.cuh"
 #include "cache_attention.cuh"
+#include "cache_join.cuh"
 #include "cache_prompt.cuh"
 #include "context.h"
 #include "launch.h"
@@ -119,32 +120,20 @@ int encode_cache(const mxg::HandleView &v, const mxg::CacheView &c, int d, int b
 // few, get up to 16 CTAs each (44 row tiles of 61102 keys: 816 -> 296 us; the
 // last 24 of 480: 334 -> 328 us).  The grid has room for every split of the rows
 // into sequences; the count of row tiles that decides is that of equal ones.
-// (Shared keys: all sequences' rows are one.)
-int64_t equal_row_tiles(const mxg::AttnParams &p, int64_t sequences) {
+int64_t equal_row_tiles(const mxg::AttnParams &p) {
   constexpr int64_t kRows = mxg::PromptCfg<128>::ROWS;
-  return (p.b.tokens * p.group / sequences + kRows - 1) / kRows * sequences * p.c.kv_heads;
-}
-
-// Bytes of the handle's workspace before the partials: what the launch over the
-// shared keys leaves for the next.
-int64_t left_bytes(const mxg::AttnParams &p, int d) {
-  return p.shared ? (p.b.tokens * p.heads * (d + 2) * static_cast<int64_t>(sizeof(float)) + 255) / 256 * 256 : 0;
-}
-void left_views(mxg::AttnParams &p, int d, uint8_t *ws) {
-  if (!p.shared) return;
-  p.pre = reinterpret_cast<float *>(ws);
-  p.pre_ml = reinterpret_cast<float2 *>(p.pre + p.b.tokens * p.heads * d);
+  return (p.b.tokens * p.group / p.b.batch + kRows - 1) / kRows * p.b.batch * p.c.kv_heads;
 }
 
 // How row tiles and their keys are cut: fills in p, and gives the bytes of the
 // partials, or -1 where there are too many.
 template <int D>
-int64_t plan_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t sequences) {
+int64_t plan_prompt(const mxg::HandleView &v, mxg::AttnParams &p) {
   using S = mxg::PromptCfg<D>;
   const int64_t rows = p.b.tokens * p.group;
-  const int64_t items = (rows / S::ROWS + sequences) * p.c.kv_heads;
+  const int64_t items = (rows / S::ROWS + p.b.batch) * p.c.kv_heads;
   if (items >= kLim - 16 * mxg::kCounters) return -1;
-  const int64_t tiles = equal_row_tiles(p, sequences), over = tiles % v.sm_count;
+  const int64_t tiles = equal_row_tiles(p), over = tiles % v.sm_count;
   p.items = p.whole = static_cast<int>(items);
   p.parts = over > 0 ? static_cast<int>(std::min<int64_t>(16, v.sm_count / over)) : 1;
   if (p.parts > 1) {
@@ -158,16 +147,8 @@ int64_t plan_prompt(const mxg::HandleView &v, mxg::AttnParams &p, int64_t sequen
 }
 
 template <int D, int MODE>
-int run_prompt(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+int launch_prompt(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::PromptCfg<D>;
-  const int64_t bytes = plan_prompt<D>(v, p, MODE == mxg::kSharedKeys ? 1 : p.b.batch), left = left_bytes(p, D);
-  if (bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
-  if (left + bytes > 0) {
-    uint8_t *ws = nullptr;
-    if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + bytes), stream, &ws)) return st;
-    left_views(p, D, ws);
-    p.partials = reinterpret_cast<float *>(ws + left);
-  }
   const int grid = p.whole + (p.items - p.whole) * p.parts;
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
@@ -185,18 +166,12 @@ int64_t decode_bytes(const mxg::HandleView &v) {
 }
 
 template <int D, int NT, int MODE>
-int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+int launch_decode(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::DecodeCfg<D, NT>;
-  const int grid = decode_grid<D, NT>(v);
-  const int64_t left = left_bytes(p, D);
-  uint8_t *ws = nullptr;
-  if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + decode_bytes<D, NT>(v)), stream, &ws)) return st;
-  left_views(p, D, ws);
-  p.partials = reinterpret_cast<float *>(ws + left);
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, std::min(p.c.page_size, 32), true, &tK, &tV)) return st;
-  return mxg::launch(mxg::cache_decode_kernel<D, NT, MODE>, dim3(static_cast<unsigned>(grid)), 128, S::SMEM_BYTES, 1, stream, tK,
-                     tV, p);
+  return mxg::launch(mxg::cache_decode_kernel<D, NT, MODE>, dim3(static_cast<unsigned>(decode_grid<D, NT>(v))), 128, S::SMEM_BYTES, 1,
+                     stream, tK, tV, p);
 }
 
 // Rows (query tokens x heads of a group) of an ordinary sequence decide: many
@@ -207,34 +182,82 @@ int run_decode(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
 // first's row tiles times 16 do not fill half of them.
 bool takes_prompt(const mxg::HandleView &v, const mxg::AttnParams &p) {
   const int64_t rows = p.b.tokens * p.group;
-  return rows >= 64 * p.b.batch || (rows > 16 * p.b.batch && equal_row_tiles(p, p.b.batch) * 32 >= v.sm_count);
+  return rows >= 64 * p.b.batch || (rows > 16 * p.b.batch && equal_row_tiles(p) * 32 >= v.sm_count);
 }
 // (of the kernel for few rows: items of 16)
 bool takes_two(const mxg::AttnParams &p) { return p.b.tokens * p.group > 8 * p.b.batch; }
 
+// How an attention runs, and the bytes of its partials (-1: too many row tiles).
+struct AttnPlan {
+  bool prompt, two;
+  int64_t bytes;
+};
+template <int D>
+AttnPlan plan_attention(const mxg::HandleView &v, mxg::AttnParams &p) {
+  AttnPlan a{takes_prompt(v, p), takes_two(p), 0};
+  a.bytes = a.prompt ? plan_prompt<D>(v, p) : a.two ? decode_bytes<D, 2>(v) : decode_bytes<D, 1>(v);
+  return a;
+}
 template <int D, int MODE>
-int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
-  if (takes_prompt(v, p)) return run_prompt<D, MODE>(h, v, p, stream);
-  return takes_two(p) ? run_decode<D, 2, MODE>(h, v, p, stream) : run_decode<D, 1, MODE>(h, v, p, stream);
+int launch_attention(const mxg::HandleView &v, mxg::AttnParams &p, const AttnPlan &a, cudaStream_t stream) {
+  if (a.prompt) return launch_prompt<D, MODE>(v, p, stream);
+  return a.two ? launch_decode<D, 2, MODE>(v, p, stream) : launch_decode<D, 1, MODE>(v, p, stream);
 }
 
-// The shared keys for all tokens, then each sequence's own, which finishes.
+template <int D>
+int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+  const AttnPlan a = plan_attention<D>(v, p);
+  if (a.bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
+  if (a.bytes > 0) {
+    uint8_t *ws = nullptr;
+    if (int st = mxg::handle_workspace(h, static_cast<size_t>(a.bytes), stream, &ws)) return st;
+    p.partials = reinterpret_cast<float *>(ws);
+  }
+  return launch_attention<D, mxg::kAllKeys>(v, p, a, stream);
+}
+
+// Parts of the shared keys for each of `tiles` row tiles, in key tiles' time: a CTA
+// takes its own and about five more, and each part costs the next launch a twentieth.
+int shared_parts(int64_t tiles, int64_t key_tiles, int64_t sms) {
+  int best = 1;
+  double least = 1e300;
+  for (int64_t n = 1; n <= std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4)); ++n) {
+    const double cost = static_cast<double>((tiles * n + sms - 1) / sms) * (static_cast<double>((key_tiles + n - 1) / n) + 5) + 0.05 * n;
+    if (cost < least) {
+      least = cost;
+      best = static_cast<int>(n);
+    }
+  }
+  return best;
+}
+
+// The shared keys for all tokens, then each sequence's own, then both joined.
 template <int D>
 int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+  using S = mxg::PromptCfg<D>;
+  p.left_tiles = static_cast<int>((p.b.tokens * p.group + S::ROWS - 1) / S::ROWS);
+  const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
+  p.left_parts = shared_parts(items, (p.shared + S::KT - 1) / S::KT, v.sm_count);
+  const int64_t left = items * p.left_parts * S::PARTIAL * static_cast<int64_t>(sizeof(float));
+  const int64_t rows = p.b.tokens * p.heads, own = rows * (D + 2) * static_cast<int64_t>(sizeof(float));
+  const int64_t blocks = (p.b.tokens * p.group + mxg::JoinCfg<D>::ROWS - 1) / mxg::JoinCfg<D>::ROWS;
   mxg::AttnParams first = p;
-  // (the block that the first launch leaves its results in is not to grow under the second)
-  const int64_t one = plan_prompt<D>(v, first, 1);
-  int64_t two = takes_two(p) ? decode_bytes<D, 2>(v) : decode_bytes<D, 1>(v);
-  if (takes_prompt(v, p)) {
-    mxg::AttnParams second = p;
-    two = plan_prompt<D>(v, second, p.b.batch);
-  }
-  if (one < 0 || two < 0) return MXGEMM_ERR_INVALID_VALUE;
+  const AttnPlan a = plan_attention<D>(v, p);
+  if (items * p.left_parts >= kLim || a.bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
   uint8_t *ws = nullptr;
-  if (int st = mxg::handle_workspace(h, static_cast<size_t>(left_bytes(p, D) + std::max(one, two)), stream, &ws)) return st;
-  if (int st = run_prompt<D, mxg::kSharedKeys>(h, v, first, stream)) return st;
+  if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + (own + 15) / 16 * 16 + a.bytes), stream, &ws)) return st;
+  p.left = first.left = reinterpret_cast<float *>(ws);
+  p.own = reinterpret_cast<float *>(ws + left);
+  p.own_ml = reinterpret_cast<float2 *>(p.own + rows * D);
+  p.partials = reinterpret_cast<float *>(ws + left + (own + 15) / 16 * 16);
+  first.items = static_cast<int>(items);
+  first.whole = 0;
+  first.parts = first.left_parts;
+  if (int st = launch_prompt<D, mxg::kSharedKeys>(v, first, stream)) return st;
   ++*v.launches;
-  return run_attention<D, mxg::kOwnKeys>(h, v, p, stream);
+  if (int st = launch_attention<D, mxg::kOwnKeys>(v, p, a, stream)) return st;
+  ++*v.launches;
+  return mxg::launch(mxg::cache_join_kernel<D>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.c.kv_heads)), 256, 0, 1, stream, p);
 }
 
 // The checks of an attention's arguments beyond the cache's; fills the kernels' view.
@@ -266,9 +289,9 @@ int attention_args(const mxg::HandleView &v, const mxgemm_cache_t *cache, int64_
   p->counters = v.counters;
   p->timeout_ns = v.timeout_ns;
   p->stall_producer = v.stall_producer;
-  p->shared = 0;
-  p->pre = nullptr;
-  p->pre_ml = nullptr;
+  p->shared = p->left_parts = p->left_tiles = 0;
+  p->left = p->own = nullptr;
+  p->own_ml = nullptr;
   return MXGEMM_OK;
 }
 
@@ -323,8 +346,7 @@ extern "C" int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *c
   if (int st = attention_args(v, cache, batch, heads, tokens, Q, q_pitch, scale, causal, window, sinks, O, lse, &p)) return st;
   if (batch == 0 || tokens == 0) return MXGEMM_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const int st = cache->head_dim == 128 ? run_attention<128, mxg::kAllKeys>(h, v, p, stream)
-                                        : run_attention<64, mxg::kAllKeys>(h, v, p, stream);
+  const int st = cache->head_dim == 128 ? run_attention<128>(h, v, p, stream) : run_attention<64>(h, v, p, stream);
   if (st != MXGEMM_OK) return st;
   ++*v.launches;
   return MXGEMM_OK;
@@ -350,7 +372,7 @@ extern "C" int mxgemm_cache_attention_shared(mxgemm_handle_t h, const mxgemm_cac
   p.shared = static_cast<int>(std::min(shared, table_pitch * cache->page_size) / unit * unit);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const bool d128 = cache->head_dim == 128;
-  const int st = p.shared == 0 ? (d128 ? run_attention<128, mxg::kAllKeys>(h, v, p, stream) : run_attention<64, mxg::kAllKeys>(h, v, p, stream))
+  const int st = p.shared == 0 ? (d128 ? run_attention<128>(h, v, p, stream) : run_attention<64>(h, v, p, stream))
                                : (d128 ? run_shared<128>(h, v, p, stream) : run_shared<64>(h, v, p, stream));
   if (st != MXGEMM_OK) return st;
   ++*v.launches;

@@ -61,12 +61,20 @@ struct AttnParams {
   unsigned long long timeout_ns;
   int stall_producer;  // tests: nothing is loaded
   // attention behind shared tokens: keys [0, shared), a multiple of 32 and of the
-  // pages, are one launch's, the others the next's, which adds what the first left of
-  // each token and head: sums over `pre`'s D values, and in `pre_ml` maximum and sum
+  // pages, are one launch's, which leaves partials in `left`, `left_parts` of each row
+  // tile, numbered as its CTAs; the others are the next's, which leaves its sums of
+  // each row (token x head) in `own` and `own_ml`; a third joins them
   int shared;
-  float *pre;
-  float2 *pre_ml;
+  float *left, *own;
+  float2 *own_ml;
+  int left_parts, left_tiles;  // parts of a row tile, row tiles of a key/value head
 };
+
+// Rows of a row tile of the kernel for prompts, and a partial of it: sums of O by
+// 4 d and row, then maximum and sum of each row.
+constexpr int kTileRows = 256;
+template <int D>
+constexpr int kTilePartial = kTileRows * (D + 2);
 
 // What a launch computes: all keys; the shared ones for all tokens; the others.
 constexpr int kAllKeys = 0, kSharedKeys = 1, kOwnKeys = 2;
@@ -134,16 +142,6 @@ __device__ __forceinline__ float log_sum(float m, float sum) {
 constexpr float kWeightUp = 7.f, kWeightDown = 0.0078125f;  // weights carry 2^7, and sums give it back
 
 constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100, for 1 / vs
-
-// The sums (m, l) of some keys of a row and (pm, pl) of the others: the factors of
-// both, over the common maximum that m becomes, and l their sum.
-__device__ __forceinline__ float2 join_sums(float &m, float &l, float pm, float pl) {
-  const float top = fmaxf(m, pm);
-  const float2 f = make_float2(m == -INFINITY ? 0.f : ex2(m - top), pm == -INFINITY ? 0.f : ex2(pm - top));
-  l = l * f.x + pl * f.y;
-  m = top;
-  return f;
-}
 
 // Which keys of a sequence any of its queries sees, as tiles of 32: `ns` tiles
 // of first tokens from key 0, then the tiles from tile `lo` on, `tiles` in all
@@ -714,14 +712,6 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
 #pragma unroll
       for (int w = 0; w < 4; ++w)  // (a sum of NaN stays one, also where no weight gave a maximum)
         sum = fmaf(ml[(4 + w) * ROWS + r], ml[w * ROWS + r] == -INFINITY ? 0.f : ex2(ml[w * ROWS + r] - top), sum);
-      // the row's place in O, and what is left of the shared keys
-      int64_t row_at = 0;
-      float2 fj = make_float2(1.f, 0.f);
-      if (MODE == kOwnKeys && !split && r < rows) {
-        row_at = static_cast<int64_t>(at.s.first + (row0 + r) / p.group) * p.heads + h * p.group + (row0 + r) % p.group;
-        const float2 pre = p.pre_ml[row_at];
-        fj = join_sums(top, sum, pre.x, pre.y);
-      }
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) {
         __syncthreads();
@@ -744,13 +734,13 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         const int d = 64 * e + 4 * hd;
         if (split) {
           *reinterpret_cast<float4 *>(part + r * D + d) = a;
+        } else if (MODE == kOwnKeys) {
+          if (r < rows)
+            *reinterpret_cast<float4 *>(
+                p.own + (static_cast<int64_t>(at.s.first + (row0 + r) / p.group) * p.heads + h * p.group + (row0 + r) % p.group) * D + d) = a;
         } else if (r < rows) {
           const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
-          if constexpr (MODE == kOwnKeys) {
-            const float4 b = *reinterpret_cast<const float4 *>(p.pre + row_at * D + d);
-            a = make_float4(a.x * fj.x + b.x * fj.y, a.y * fj.x + b.y * fj.y, a.z * fj.x + b.z * fj.y, a.w * fj.x + b.w * fj.y);
-          }
           const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * k, a.y * k), hi = __floats2bfloat162_rn(a.z * k, a.w * k);
           *reinterpret_cast<uint2 *>(p.O + (static_cast<int64_t>(tok) * p.heads + head) * D + d) =
               make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
@@ -760,9 +750,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         if (split) {
           part[ROWS * D + r] = top;
           part[ROWS * D + ROWS + r] = sum;
-        } else if (r < rows && p.lse) {
+        } else if (r < rows && (MODE == kOwnKeys || p.lse)) {
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
-          p.lse[static_cast<int64_t>(tok) * p.heads + head] = log_sum(top, sum);
+          if (MODE == kOwnKeys) p.own_ml[static_cast<int64_t>(tok) * p.heads + head] = make_float2(top, sum);
+          else p.lse[static_cast<int64_t>(tok) * p.heads + head] = log_sum(top, sum);
         }
       }
     }
@@ -810,13 +801,11 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
           if (rr >= rows) continue;
           const int tok = at.s.first + (row0 + rr) / p.group, head = h * p.group + (row0 + rr) % p.group;
           if constexpr (MODE == kOwnKeys) {
-            const int64_t row_at = static_cast<int64_t>(tok) * p.heads + head;
-            const float2 pre = p.pre_ml[row_at], f = join_sums(top, sum, pre.x, pre.y);
+            const int64_t row = static_cast<int64_t>(tok) * p.heads + head;
 #pragma unroll
-            for (int e = 0; e < D / 64; ++e) {
-              const float4 b = *reinterpret_cast<const float4 *>(p.pre + row_at * D + 64 * e + 4 * hd);
-              a[e] = make_float4(a[e].x * f.x + b.x * f.y, a[e].y * f.x + b.y * f.y, a[e].z * f.x + b.z * f.y, a[e].w * f.x + b.w * f.y);
-            }
+            for (int e = 0; e < D / 64; ++e) *reinterpret_cast<float4 *>(p.own + row * D + 64 * e + 4 * hd) = a[e];
+            if (hd == 0) p.own_ml[row] = make_float2(top, sum);
+            continue;
           }
           const float k = sum == 0.f ? 0.f : kWeightDown / sum;
 #pragma unroll

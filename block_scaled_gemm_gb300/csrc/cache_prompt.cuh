@@ -42,7 +42,7 @@ namespace mxg {
 
 template <int D>
 struct PromptCfg {
-  static constexpr int ROWS = 256, KT = 128;
+  static constexpr int ROWS = kTileRows, KT = 128;
   static constexpr int CH = D / 64;            // 128-byte chunks of an FP16 row
   static constexpr int TILE16 = 128 * D * 2;   // 128 rows of FP16: [chunk][128 rows][128 bytes]
   static constexpr int TILE8 = 128 * D;
@@ -57,7 +57,7 @@ struct PromptCfg {
   static constexpr int NUM_BARS = 4 + 2 * 4 + 2 + 4 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-  static constexpr int PARTIAL = ROWS * (D + 2);  // floats of a partial: O by 4 d and row, m, l
+  static constexpr int PARTIAL = kTilePartial<D>;  // floats of a partial: O by 4 d and row, m, l
   static constexpr int THREADS = 512;
   // registers a thread: 128 at launch, then of the four groups of four warps
   // (56 + 88 + 2 x 184 = 4 x 128: the block's own)
@@ -167,6 +167,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const int all_tiles = max(1, ns + ((end + 127) >> 7) - lo);
   // this CTA's part of them: four at least
   const int parts = beyond < 0 ? 1 : min(p.parts, max(1, all_tiles >> 2)), part = beyond < 0 ? 0 : beyond % p.parts;
+  if constexpr (MODE == kSharedKeys) {
+    if (part >= parts) {  // (fewer keys than the host knew of: a partial without any)
+      float *slot = p.left + (static_cast<int64_t>(item) * p.left_parts + part) * S::PARTIAL + S::ROWS * D;
+      slot[threadIdx.x] = threadIdx.x < S::ROWS ? -INFINITY : 0.f;
+    }
+  }
   if (part >= parts) return;
   const int tile0 = static_cast<int>(static_cast<int64_t>(part) * all_tiles / parts);
   const int tiles = static_cast<int>(static_cast<int64_t>(part + 1) * all_tiles / parts) - tile0;
@@ -441,6 +447,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       };
       const int w0 = 128 * i + 32 * qd;
       int row_to = p.causal ? min(end, pos + 1) : end, row_from = window_from(pos);
+      bool no_query = false;  // (shared keys: a row that is no sequence's)
       int all_to = p.causal ? min(end, pos0 + (row0 + min(w0, rows - 1)) / p.group + 1) : end;
       if constexpr (MODE == kSharedKeys) {
         // the token's own sequence, which may be shorter than the shared tokens
@@ -456,7 +463,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         }
         const Sequence own = load_sequence(p.b, p.c, lo);
         const int at = tok - own.first;
-        row_to = at < 0 || at >= own.n ? 0 : max(0, min(end, p.causal ? own.len - own.n + at + 1 : own.len));
+        no_query = at < 0 || at >= own.n;
+        row_to = no_query ? 0 : max(0, min(end, p.causal ? own.len - own.n + at + 1 : own.len));
         all_to = __reduce_min_sync(0xFFFFFFFFu, live ? row_to : end);
       }
       const int all_from = window_from(pos0 + (row0 + min(w0 + 31, rows - 1)) / p.group);
@@ -555,8 +563,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       if (ok) {
         tc_fence_after();
         const int at = (s.first + tok) * p.heads + head;
-        if (parts > 1) {
-          float *slot = p.partials + (static_cast<int64_t>(item - p.whole) * p.parts + part) * S::PARTIAL;
+        if (parts > 1 || MODE == kSharedKeys) {
+          float *slot = MODE == kSharedKeys ? p.left + (static_cast<int64_t>(item) * p.left_parts + part) * S::PARTIAL
+                                            : p.partials + (static_cast<int64_t>(item - p.whole) * p.parts + part) * S::PARTIAL;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -567,18 +576,22 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
               reinterpret_cast<uint4 *>(slot)[(8 * c + e) * S::ROWS + r] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           slot[S::ROWS * D + r] = m;
-          slot[S::ROWS * D + S::ROWS + r] = l;
+          slot[S::ROWS * D + S::ROWS + r] = no_query ? -1.f : l;
+        } else if (MODE == kOwnKeys) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * c, o);
+            tmem_ld_done(o);
+            uint4 *dst = reinterpret_cast<uint4 *>(p.own + static_cast<int64_t>(at) * D + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (live) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          if (live) p.own_ml[at] = make_float2(m, l);
         } else {
           // through the rows of Q, whose products are done: a store of whole
           // lines, where a thread's own row would touch 32
-          float2 fj = make_float2(1.f, 0.f);
-          if constexpr (MODE == kOwnKeys) {
-            const float2 pre = live ? p.pre_ml[at] : make_float2(-INFINITY, 0.f);
-            fj = join_sums(m, l, pre.x, pre.y);
-          }
-          if constexpr (MODE == kSharedKeys) {
-            if (live) p.pre_ml[at] = make_float2(m, l);
-          }
           const float k = l == 0.f ? 0.f : kWeightDown / l;
           const uint32_t rr = 32 * qd + lane, q_row = base + S::OFF_Q + i * S::TILE16 + rr * 128;
 #pragma unroll
@@ -586,28 +599,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             uint32_t o[32];
             tmem_ld_32x32b_x32(to + 32 * c, o);
             tmem_ld_done(o);
-            if constexpr (MODE == kSharedKeys) {
-              if (live) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.pre + static_cast<int64_t>(at) * D + 32 * c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-              }
-            }
-            if constexpr (MODE == kOwnKeys) {
-              if (live) {
-                const float4 *src = reinterpret_cast<const float4 *>(p.pre + static_cast<int64_t>(at) * D + 32 * c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 y = src[e];
-                  o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * fj.x + y.x * fj.y);
-                  o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * fj.x + y.y * fj.y);
-                  o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * fj.x + y.z * fj.y);
-                  o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * fj.x + y.w * fj.y);
-                }
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < (MODE == kSharedKeys ? 0 : 4); ++e) {
+            for (int e = 0; e < 4; ++e) {
               uint32_t x[4];
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
@@ -620,7 +613,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           }
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < (MODE == kSharedKeys ? 0 : 8); ++j) {
+          for (int j = 0; j < 8; ++j) {
             const int from = 4 * j + (lane >> 3), q = lane & 7;
             const int64_t to_row = __shfl_sync(0xFFFFFFFFu, at, from);
             if (128 * i + 32 * qd + from < rows) {
@@ -630,11 +623,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                     ld_shared_v4(q_row + (from - lane) * 128 + c * 16384 + ((q ^ (from & 7)) << 4));
             }
           }
-          if (MODE != kSharedKeys && live && p.lse) p.lse[at] = log_sum(m, l);
+          if (live && p.lse) p.lse[at] = log_sum(m, l);
         }
       }
     }
-    if (parts > 1) {
+    if (parts > 1 && MODE != kSharedKeys) {
       // (every softmax warp comes here: all their waits are bounded)
       __threadfence();
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -653,30 +646,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             sum = fmaf(__ldcg(first + c * S::PARTIAL + S::ROWS * D + S::ROWS + r), mc == -INFINITY ? 0.f : ex2(mc - top), sum);
           }
           const int64_t row_at = static_cast<int64_t>(s.first + tok) * p.heads + head;
-          // the parts' factors: over their maximum, times fj.x, plus the shared keys' sums times fj.y
-          const float part_top = top;
-          float2 fj = make_float2(1.f, 0.f);
-          if constexpr (MODE == kOwnKeys) {
-            const float2 pre = p.pre_ml[row_at];
-            fj = join_sums(top, sum, pre.x, pre.y);
-          }
-          const float k = MODE == kSharedKeys ? 1.f : sum == 0.f ? 0.f : kWeightDown / sum;
+          const float k = MODE == kOwnKeys ? 1.f : sum == 0.f ? 0.f : kWeightDown / sum;
           __nv_bfloat16 *dst = p.O + row_at * D;
 #pragma unroll 1
           for (int d = 0; d < D; d += 16) {
             float4 a[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if constexpr (MODE == kOwnKeys) {
-                const float4 y = *reinterpret_cast<const float4 *>(p.pre + row_at * D + d + 4 * e);
-                a[e] = make_float4(y.x * fj.y * k, y.y * fj.y * k, y.z * fj.y * k, y.w * fj.y * k);
-              }
-            }
+            for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
             for (int c = 0; c < parts; ++c) {
               const float mc = __ldcg(first + c * S::PARTIAL + S::ROWS * D + r);
-              const float f = mc == -INFINITY ? 0.f : ex2(mc - part_top) * (fj.x * k);
+              const float f = mc == -INFINITY ? 0.f : ex2(mc - top) * k;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float4 x = __ldcg(reinterpret_cast<const float4 *>(first + c * S::PARTIAL) + (d / 4 + e) * S::ROWS + r);
@@ -686,22 +666,23 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                 a[e].w = fmaf(x.w, f, a[e].w);
               }
             }
-            if constexpr (MODE == kSharedKeys) {
+            if constexpr (MODE == kOwnKeys) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) *reinterpret_cast<float4 *>(p.pre + row_at * D + d + 4 * e) = a[e];
-            } else {
-              uint32_t x[8];
+              for (int e = 0; e < 4; ++e) *reinterpret_cast<float4 *>(p.own + row_at * D + d + 4 * e) = a[e];
+            }
+            uint32_t x[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(a[e].x, a[e].y), z = __floats2bfloat162_rn(a[e].z, a[e].w);
-                x[2 * e] = *reinterpret_cast<const uint32_t *>(&y);
-                x[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&z);
-              }
+            for (int e = 0; e < (MODE == kOwnKeys ? 0 : 4); ++e) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(a[e].x, a[e].y), z = __floats2bfloat162_rn(a[e].z, a[e].w);
+              x[2 * e] = *reinterpret_cast<const uint32_t *>(&y);
+              x[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&z);
+            }
+            if constexpr (MODE != kOwnKeys) {
               *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
               *reinterpret_cast<uint4 *>(dst + d + 8) = make_uint4(x[4], x[5], x[6], x[7]);
             }
           }
-          if constexpr (MODE == kSharedKeys) p.pre_ml[row_at] = make_float2(top, sum);
+          if (MODE == kOwnKeys) p.own_ml[row_at] = make_float2(top, sum);
           else if (p.lse) p.lse[row_at] = log_sum(top, sum);
         }
       }

@@ -701,8 +701,9 @@ int mxgemm_cache_attention(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64
  * the page table agree on the first floor(shared / page_size) pages, each as far as its
  * sequence reaches (the longest sequence's row is read); everything else is as
  * without sharing, and any shared >= 0 that keeps the promise is allowed: a part of a
- * page, more than some sequence has, 0.  Arguments otherwise as for mxgemm_cache_attention, without a window.  Two
- * launches; partial results of the shared part are FP32 in the handle's workspace. */
+ * page, more than some sequence has, 0.  Arguments otherwise as for
+ * mxgemm_cache_attention, without a window.  Up to three launches; partial results are
+ * FP32 in the handle's workspace. */
 int mxgemm_cache_attention_shared(mxgemm_handle_t h, const mxgemm_cache_t *cache, int64_t batch,
                                   int64_t heads, const int32_t *page_table, int64_t table_pitch,
                                   const int32_t *kv_len, const int32_t *q_start, int64_t tokens,
