@@ -104,6 +104,7 @@ int run_pair(mxgemm_handle_t h, const mxg::HandleView &v, mxg::B128Params &p, co
 template <typename T, int ACT>
 int launch_grad(const mxg::GatedGradParams &p, bool tiles, int sms, cudaStream_t stream) {
   if (tiles) {
+    if (p.rb * p.cb >= kLim - sms) return MXGEMM_ERR_INVALID_VALUE;
     const int64_t grid = std::min<int64_t>(p.rb * p.cb, sms);
     return mxg::launch(mxg::gated_grad_tile_kernel<T, ACT>, dim3(static_cast<unsigned>(grid)), 512, mxg::GatedGradCfg<T>::SMEM_BYTES, 1,
                        stream, p);

@@ -73,8 +73,9 @@ __global__ void __launch_bounds__(256) gated_grad_flat_kernel(const GatedGradPar
 template <typename T>
 struct GatedGradCfg {
   static constexpr int WORDS = 2 + sizeof(T) / 2;  // 16-byte words of eight values of gate, up and dH
-  static constexpr int OFF_TOP = 0;                            // [3][16 warps][128 columns], then [3][128] reciprocals
-  static constexpr int OFF_TILE = OFF_TOP + 3 * 16 * 128 * 4;  // [3][128 columns][32 words]
+  static constexpr int OFF_TOP = 0;                            // [3][32 ty][128 columns] largest values
+  static constexpr int OFF_INV = OFF_TOP + 3 * 32 * 128 * 4;   // [3][128 columns] reciprocals
+  static constexpr int OFF_TILE = OFF_INV + 3 * 128 * 4;       // [3][128 columns][32 words]
   static constexpr int OFF_IN = OFF_TILE + 3 * 128 * 32 * 4;   // the next tile: [4 rows][WORDS][512 threads] words
   static constexpr int SMEM_BYTES = OFF_IN + 4 * WORDS * 512 * 16;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -84,43 +85,54 @@ struct GatedGradCfg {
 __device__ __forceinline__ void grad_copy16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ float abs_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return mx_e4m3x2(a, b) | (mx_e4m3x2(c, d) << 16); }
 
 // One block of 512 threads an SM, which goes from tile to tile and copies the next
 // one's values to shared memory while it stores this one's codes (each thread copies
 // what it will read itself).  Thread (ty, tx) has rows 4 ty .. +3 of columns 8 tx ..
 // +7, so that the four rows' codes of a column are one word of the transposed tile.
+// Issue slots are as short as bandwidth: operations go in pairs, and a row's largest
+// values are exchanged so that each lane ends with one of them and divides once.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGradParams p) {
   using S = GatedGradCfg<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   float *tops = reinterpret_cast<float *>(smem + S::OFF_TOP);
+  float *invs = reinterpret_cast<float *>(smem + S::OFF_INV);
   uint32_t *tile = reinterpret_cast<uint32_t *>(smem + S::OFF_TILE);
   griddep_launch_dependents();
   griddep_wait();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const uint32_t in = smem_u32(smem + S::OFF_IN) + threadIdx.x * 16;
-  const int64_t tiles = p.rb * p.cb;
-  auto load = [&](int64_t t) {
-    const int64_t r0 = t / p.cb * 128 + 4 * ty, c0 = t % p.cb * 128 + 8 * tx;
+  const uint32_t tiles = static_cast<uint32_t>(p.rb * p.cb), cb = static_cast<uint32_t>(p.cb);
+  auto load = [&](uint32_t t) {
+    const uint32_t rblock = t / cb, cblock = t - rblock * cb;
+    const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128 + 8 * tx;
+    const int rows = t < tiles && c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;  // that are there
+    int64_t at = r0 * p.C + c0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool there = t < tiles && c0 < p.C && r0 + i < p.R;
-      const int64_t at = there ? (r0 + i) * p.C + c0 : 0;
+    for (int i = 0; i < 4; ++i, at += p.C) {
+      const int64_t from = i < rows ? at : 0;
       const uint32_t to = in + i * S::WORDS * 8192;
-      grad_copy16(to, p.gate + at, there);
-      grad_copy16(to + 8192, p.up + at, there);
+      grad_copy16(to, p.gate + from, i < rows);
+      grad_copy16(to + 8192, p.up + from, i < rows);
 #pragma unroll
       for (int w = 0; w < S::WORDS - 2; ++w)
-        grad_copy16(to + (2 + w) * 8192, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dH) + at) + w, there);
+        grad_copy16(to + (2 + w) * 8192, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dH) + from) + w, i < rows);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   load(blockIdx.x);
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t rblock = t / p.cb, cblock = t % p.cb;
-    const int64_t r0 = rblock * 128 + 4 * ty, c0 = cblock * 128 + 8 * tx;
-    const bool inside = c0 < p.C;
-    float v[3][4][8];  // dgate, dup, h
+  for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const uint32_t rblock = t / cb, cblock = t - rblock * cb;
+    const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128 + 8 * tx;
+    const int rows = c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;
+    float2 v[3][4][4];  // dgate, dup, h: [row][columns 2 e, + 1]
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -134,72 +146,84 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const GatedGrad2 x = gated_grad<ACT>(two_of(g, e), two_of(u, e), two_of(d, e));
-        v[0][i][2 * e] = x.dg.x;
-        v[0][i][2 * e + 1] = x.dg.y;
-        v[1][i][2 * e] = x.du.x;
-        v[1][i][2 * e + 1] = x.du.y;
-        v[2][i][2 * e] = x.h.x;
-        v[2][i][2 * e + 1] = x.h.y;
+        v[0][i][e] = x.dg;
+        v[1][i][e] = x.du;
+        v[2][i][e] = x.h;
       }
     }
-    // columns' largest: of this thread's rows, of the warp's eight, then of all warps
+    // columns' largest of this thread's rows
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
-      if (!p.cols[m].codes) continue;
+      float c[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float top = fmaxf(fmaxf(fabsf(v[m][0][e]), fabsf(v[m][1][e])), fmaxf(fabsf(v[m][2][e]), fabsf(v[m][3][e])));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        if ((threadIdx.x & 16) == 0) tops[(m * 16 + warp) * 128 + 8 * tx + e] = top;
+      for (int e = 0; e < 4; ++e) {
+        c[2 * e] = abs_max3(fmaxf(fabsf(v[m][0][e].x), fabsf(v[m][1][e].x)), v[m][2][e].x, v[m][3][e].x);
+        c[2 * e + 1] = abs_max3(fmaxf(fabsf(v[m][0][e].y), fabsf(v[m][1][e].y)), v[m][2][e].y, v[m][3][e].y);
       }
+      float4 *to = reinterpret_cast<float4 *>(tops + (m * 32 + ty) * 128 + 8 * tx);
+      to[0] = make_float4(c[0], c[1], c[2], c[3]);
+      to[1] = make_float4(c[4], c[5], c[6], c[7]);
     }
     __syncthreads();
     load(t + gridDim.x);
-    // rows: a row's 128 values are 16 lanes'
+    // the columns' reciprocals and scales
+    if (threadIdx.x < 384) {
+      const int m = threadIdx.x >> 7, c = threadIdx.x & 127;
+      float top = kQ128Least;
+      const float *from = tops + m * 32 * 128 + c;
+#pragma unroll
+      for (int w = 0; w < 32; w += 2) top = abs_max3(top, from[w * 128], from[(w + 1) * 128]);
+      invs[threadIdx.x] = __fdiv_rn(448.0f, top);
+      const int64_t col = static_cast<int64_t>(cblock) * 128 + c;
+      if (p.cols[m].codes && col < p.C) p.cols[m].scales[col * p.rb + rblock] = __fdiv_rn(top, 448.0f);
+    }
+    // rows: a row's 128 values are 16 lanes'.  Of the eight rows of both matrices,
+    // lane tx comes to hold the largest value of row (tx / 2) % 4 of matrix tx / 8.
+    float inv;
+    {
+      float a[8], b[4], c[2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2(&x)[4] = v[k >> 2][k & 3];
+        a[k] = abs_max3(abs_max3(abs_max3(fmaxf(fabsf(x[0].x), fabsf(x[0].y)), x[1].x, x[1].y), x[2].x, x[2].y), x[3].x, x[3].y);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        b[k] = fmaxf(tx & 8 ? a[k + 4] : a[k], __shfl_xor_sync(0xFFFFFFFFu, tx & 8 ? a[k] : a[k + 4], 8));
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        c[k] = fmaxf(tx & 4 ? b[k + 2] : b[k], __shfl_xor_sync(0xFFFFFFFFu, tx & 4 ? b[k] : b[k + 2], 4));
+      float top = fmaxf(tx & 2 ? c[1] : c[0], __shfl_xor_sync(0xFFFFFFFFu, tx & 2 ? c[0] : c[1], 2));
+      top = fmaxf(fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), kQ128Least);
+      inv = __fdiv_rn(448.0f, top);
+      const Blocks128 &to = p.rows[tx >> 3];
+      const int64_t row = r0 + ((tx >> 1) & 3);
+      if ((tx & 1) == 0 && to.codes && row < p.R) to.scales[row * p.cb + cblock] = __fdiv_rn(top, 448.0f);
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
+      int64_t at = r0 * p.C + c0;
       __nv_bfloat16 *plain = m ? p.dup : p.dgate;
+      uint8_t *codes = p.rows[m].codes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool there = inside && r0 + i < p.R;
-        const int64_t at = (r0 + i) * p.C + c0;
-        if (plain && there) {
+      for (int i = 0; i < 4; ++i, at += p.C) {
+        const float2(&x)[4] = v[m][i];
+        if (plain && i < rows) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[m][i][2 * e], v[m][i][2 * e + 1]);
+            const __nv_bfloat162 b = __float22bfloat162_rn(x[e]);
             w[e] = *reinterpret_cast<const uint32_t *>(&b);
           }
           *reinterpret_cast<uint4 *>(plain + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (!p.rows[m].codes) continue;
-        float top = 0.f;
+        if (!codes) continue;
+        const float k = __shfl_sync(0xFFFFFFFFu, inv, (threadIdx.x & 16) | (8 * m + 2 * i));
+        float2 y[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[m][i][e]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        top = fmaxf(top, kQ128Least);
-        const float inv = __fdiv_rn(448.0f, top);
-        if (there) {
-          uint32_t w[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            w[e] = mx_e4m3x2(v[m][i][4 * e] * inv, v[m][i][4 * e + 1] * inv) |
-                   (mx_e4m3x2(v[m][i][4 * e + 2] * inv, v[m][i][4 * e + 3] * inv) << 16);
-          *reinterpret_cast<uint2 *>(p.rows[m].codes + at) = make_uint2(w[0], w[1]);
-          if (tx == 0) p.rows[m].scales[(r0 + i) * p.cb + cblock] = __fdiv_rn(top, 448.0f);
-        }
-      }
-    }
-    // the columns' reciprocals, in the place of the first warp's largest
-    if (threadIdx.x < 384) {
-      const int m = threadIdx.x >> 7, c = threadIdx.x & 127;
-      if (p.cols[m].codes) {
-        float top = kQ128Least;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) top = fmaxf(top, tops[(m * 16 + w) * 128 + c]);
-        tops[m * 16 * 128 + c] = __fdiv_rn(448.0f, top);
-        if (cblock * 128 + c < p.C) p.cols[m].scales[(cblock * 128 + c) * p.rb + rblock] = __fdiv_rn(top, 448.0f);
+        for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], make_float2(k, k));
+        if (i < rows)
+          *reinterpret_cast<uint2 *>(codes + at) = make_uint2(e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
       }
     }
     __syncthreads();
@@ -208,28 +232,35 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
       if (!p.cols[m].codes) continue;
+      const float4 ka = *reinterpret_cast<const float4 *>(invs + m * 128 + 8 * tx), kb = *reinterpret_cast<const float4 *>(invs + m * 128 + 8 * tx + 4);
+      const float2 k[4] = {make_float2(ka.x, ka.y), make_float2(ka.z, ka.w), make_float2(kb.x, kb.y), make_float2(kb.z, kb.w)};
+      uint32_t *to = tile + (m * 128 + 8 * tx) * 32 + (ty ^ (2 * tx));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float inv = tops[m * 16 * 128 + 8 * tx + e];
-        tile[(m * 128 + 8 * tx + e) * 32 + (ty ^ (2 * tx))] =
-            mx_e4m3x2(v[m][0][e] * inv, v[m][1][e] * inv) | (mx_e4m3x2(v[m][2][e] * inv, v[m][3][e] * inv) << 16);
+      for (int e = 0; e < 4; ++e) {
+        float2 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mul2(v[m][i][e], k[e]);
+        to[2 * e * 32] = e4m3x4(y[0].x, y[1].x, y[2].x, y[3].x);
+        to[(2 * e + 1) * 32] = e4m3x4(y[0].y, y[1].y, y[2].y, y[3].y);
       }
     }
     __syncthreads();
+    const int part = threadIdx.x & 7, c = threadIdx.x >> 3;
+    const int64_t col = static_cast<int64_t>(cblock) * 128 + c, row = static_cast<int64_t>(rblock) * 128 + 16 * part;
+    const int64_t to = col * p.pitch + row;
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
       if (!p.cols[m].codes) continue;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int c = (threadIdx.x >> 3) + 64 * i, part = threadIdx.x & 7, x = c >> 3;
-        uint4 w = *reinterpret_cast<const uint4 *>(tile + (m * 128 + c) * 32 + 4 * (part ^ (x >> 1)));
+        const int x = (c >> 3) + 8 * i;
+        uint4 w = *reinterpret_cast<const uint4 *>(tile + (m * 128 + c + 64 * i) * 32 + 4 * (part ^ (x >> 1)));
         if (x & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-        const int64_t col = cblock * 128 + c, row = rblock * 128 + 16 * part;
-        if (col < p.C && row < p.pitch) *reinterpret_cast<uint4 *>(p.cols[m].codes + col * p.pitch + row) = w;
+        if (col + 64 * i < p.C && row < p.pitch) *reinterpret_cast<uint4 *>(p.cols[m].codes + to + 64 * i * p.pitch) = w;
       }
     }
     // (the next tile's largest are written after every thread has passed the second
-    // barrier, and its words after two more)
+    // barrier, its reciprocals after the third, and its words after two more)
   }
 }
 

@@ -94,9 +94,9 @@ int64_t count_steps(mxg::RopeParams &p) {
 
 template <typename T, int D>
 int run_forward(mxg::RopeParams &p, cudaStream_t stream) {
-  // three blocks an SM, no more warps than steps
+  // as many blocks as the SMs hold, no more warps than steps
   using C = mxg::RopeCfg<T, D, false>;
-  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), 8), 3 * 152);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), 8), (sizeof(T) == 4 ? 3 : 4) * 152);
   return mxg::launch(mxg::norm_rope_kernel<T, D>, dim3(static_cast<unsigned>(grid)), 256, C::SMEM_BYTES, 1, stream, p);
 }
 

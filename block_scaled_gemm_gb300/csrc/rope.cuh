@@ -81,8 +81,11 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const F8 &a) {
   }
   *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ F8 shared_run(const float *w) {
-  const float4 a = *reinterpret_cast<const float4 *>(w), b = *reinterpret_cast<const float4 *>(w + 4);
+// A lane's eight values of a table in shared memory whose values 4 k .. + 3 are at
+// [k][lane of the head]: 16-byte loads of a head's lanes lie side by side.
+template <int LANES>
+__device__ __forceinline__ F8 shared_run(const float *w, int sub) {
+  const float4 a = reinterpret_cast<const float4 *>(w)[sub], b = reinterpret_cast<const float4 *>(w)[LANES + sub];
   return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
@@ -106,7 +109,7 @@ struct RopeCfg {
   static constexpr int PIECES = (BACK ? 4 : 2) * WORDS;     // words of a lane: dy and x, or x
   static constexpr int STAGES = 4;
   static constexpr int OFF_TURN = 0;                        // [D / 2] turns a position
-  static constexpr int OFF_W = OFF_TURN + D / 2 * 8;        // [2][D] weights
+  static constexpr int OFF_W = OFF_TURN + D / 2 * 8;        // [2][runs a, b][D / 2] weights
   static constexpr int OFF_CS = OFF_W + 2 * D * 4;          // [8 warps][cosines, sines][D / 2]
   static constexpr int OFF_POS = OFF_CS + 8 * D / 2 * 8;    // [8 warps][STAGES] positions
   static constexpr int OFF_RING = OFF_POS + 8 * STAGES * 4;  // [8 warps][STAGES][PIECES][32 lanes]
@@ -126,30 +129,29 @@ __device__ __forceinline__ Runs runs_of(int sub, int rot) {
   return Runs{at, at + 8, false};
 }
 
-// A lane's pairs turned forward, or back; c and s are a token's rot / 2 cosines and
-// sines, and sub the lane of the head.
+// Where pair j of a token's rot / 2 is in such a table of cosines (or sines).
+template <int LANES>
+__device__ __forceinline__ int pair_place(int j, int rot, int interleaved) {
+  const int k = interleaved ? j >= rot >> 2 : (j >> 2) & 1;
+  const int sub = interleaved ? (j - (k ? rot >> 2 : 0)) >> 2 : j >> 3;
+  return (k * LANES + sub) * 4 + (j & 3);
+}
+// A lane's pairs turned forward, or back, by its cosines and sines.
 template <bool BACK>
-__device__ __forceinline__ void turn(F8 &a, F8 &b, const float *c, const float *s, int sub, int rot, int interleaved) {
+__device__ __forceinline__ void turn(F8 &a, F8 &b, const F8 &c, const F8 &s, int interleaved) {
   if (interleaved) {  // (x, y) -> (x, y) c + (y, x) (-s, s)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      F8 &x = k ? b : a;
-      const int j = (k ? rot >> 2 : 0) + 4 * sub;
-      const float4 cc = *reinterpret_cast<const float4 *>(c + j), ss = *reinterpret_cast<const float4 *>(s + j);
-      const float ca[4] = {cc.x, cc.y, cc.z, cc.w}, sa[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float t = BACK ? -sa[e] : sa[e];
-        x.v[e] = fma2(make_float2(x.v[e].y, x.v[e].x), make_float2(-t, t), mul2(x.v[e], make_float2(ca[e], ca[e])));
-      }
+    for (int e = 0; e < 8; ++e) {
+      float2 &x = e < 4 ? a.v[e] : b.v[e - 4];
+      const float cc = e & 1 ? c.v[e >> 1].y : c.v[e >> 1].x, ss = e & 1 ? s.v[e >> 1].y : s.v[e >> 1].x, t = BACK ? -ss : ss;
+      x = fma2(make_float2(x.y, x.x), make_float2(-t, t), mul2(x, make_float2(cc, cc)));
     }
   } else {
-    const F8 cc = shared_run(c + 8 * sub), ss = shared_run(s + 8 * sub);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 t = BACK ? make_float2(-ss.v[e].x, -ss.v[e].y) : ss.v[e], u = a.v[e], v = b.v[e];
-      a.v[e] = fma2(v, make_float2(-t.x, -t.y), mul2(u, cc.v[e]));
-      b.v[e] = fma2(u, t, mul2(v, cc.v[e]));
+      const float2 t = BACK ? make_float2(-s.v[e].x, -s.v[e].y) : s.v[e], u = a.v[e], v = b.v[e];
+      a.v[e] = fma2(v, make_float2(-t.x, -t.y), mul2(u, c.v[e]));
+      b.v[e] = fma2(u, t, mul2(v, c.v[e]));
     }
   }
 }
@@ -250,11 +252,21 @@ struct RopeWalk {
       const uint64_t *turns = reinterpret_cast<const uint64_t *>(sm + C::OFF_TURN);
       for (int j = lane; j < p.rot >> 1; j += 32) {
         const float2 a = angle_at(turns[j], pos, p.factor);
-        angles()[j] = a.x;
-        angles()[D / 2 + j] = a.y;
+        const int to = pair_place<C::LANES>(j, p.rot, p.interleaved);
+        angles()[to] = a.x;
+        angles()[D / 2 + to] = a.y;
       }
       __syncwarp();
     }
+  }
+  template <bool BACKWARD>
+  __device__ void turned(F8 &a, F8 &b) const {
+    if (r.turned)
+      turn<BACKWARD>(a, b, shared_run<C::LANES>(angles(), sub), shared_run<C::LANES>(angles() + D / 2, sub), p.interleaved);
+  }
+  // This lane's weights of a tensor's run `i`.
+  __device__ F8 weights(int which, int i) const {
+    return shared_run<C::LANES>(reinterpret_cast<const float *>(sm + C::OFF_W) + (2 * which + i) * (D / 2), sub);
   }
   // Run `i` (0, 1) of tensor k (0: dy where there is one, 1: then x).
   __device__ F8 run(int k, int i) const {
@@ -278,14 +290,19 @@ __device__ __forceinline__ void rope_tables(const RopeParams &p, uint8_t *sm) {
   using C = RopeCfg<T, D, BACK>;
   for (int j = threadIdx.x; j < p.rot >> 1; j += 256) reinterpret_cast<uint64_t *>(sm + C::OFF_TURN)[j] = turn_of(p.freqs[j]);
   for (int i = threadIdx.x; i < 2 * D; i += 256) {
+    // value e of run `run` of lane `sub`, of tensor i / D
+    const int run = i / 8 % 2, sub = i % D / 16, e = i % 8;
+    const Runs r = runs_of(sub, p.rot);
+    const int from = (run ? r.b : r.a) + e;
     const void *w = p.t[i / D].w;
     if (w)
-      reinterpret_cast<float *>(sm + C::OFF_W)[i] =
-          p.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i % D]) : static_cast<const float *>(w)[i % D];
+      reinterpret_cast<float *>(sm + C::OFF_W)[(i / D * 2 + run) * (D / 2) + ((e >> 2) * C::LANES + sub) * 4 + (e & 3)] =
+          p.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[from]) : static_cast<const float *>(w)[from];
   }
 }
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 3) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(const RopeParams p) {
   using C = RopeCfg<T, D, false>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   griddep_launch_dependents();
@@ -304,15 +321,14 @@ __global__ void __launch_bounds__(256, 3) norm_rope_kernel(const RopeParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum = fma2(a.v[e], a.v[e], fma2(b.v[e], b.v[e], sum));
       const float inv = rsqrtf(fmaf(head_sum<C::LANES>(sum.x + sum.y), 1.f / D, p.eps));
-      const float *w = reinterpret_cast<const float *>(rope_smem + C::OFF_W) + which * D;
-      const F8 wa = shared_run(w + r.a), wb = shared_run(w + r.b);
+      const F8 wa = walk.weights(which, 0), wb = walk.weights(which, 1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         a.v[e] = mul2(mul2(a.v[e], make_float2(inv, inv)), wa.v[e]);
         b.v[e] = mul2(mul2(b.v[e], make_float2(inv, inv)), wb.v[e]);
       }
     }
-    if (r.turned) turn<false>(a, b, walk.angles(), walk.angles() + D / 2, walk.sub, p.rot, p.interleaved);
+    walk.template turned<false>(a, b);
     if (h < t.heads) {
       T *out = static_cast<T *>(t.out) + walk.at.token * t.out_pitch + h * D;
       store8(out + r.a, a);
@@ -367,15 +383,14 @@ __global__ void __launch_bounds__(256, 2) norm_rope_backward_kernel(const RopePa
   rope_tables<T, D, true>(p, rope_smem);
   __syncthreads();
   const Runs r = walk.r;
-  const float *w = reinterpret_cast<const float *>(rope_smem + C::OFF_W) + which * D;
   F8 da{}, db{};
   for (; walk.more(); walk.advance()) {
     walk.arrive();
     F8 ga = walk.run(0, 0), gb = walk.run(0, 1);
-    if (r.turned) turn<true>(ga, gb, walk.angles(), walk.angles() + D / 2, walk.sub, p.rot, p.interleaved);
+    walk.template turned<true>(ga, gb);
     const int h = walk.head(walk.at);
     if (t.w) {
-      const F8 xa = walk.run(1, 0), xb = walk.run(1, 1), wa = shared_run(w + r.a), wb = shared_run(w + r.b);
+      const F8 xa = walk.run(1, 0), xb = walk.run(1, 1), wa = walk.weights(which, 0), wb = walk.weights(which, 1);
       float2 ss = make_float2(0.f, 0.f), sd = ss;
       F8 ya, yb;  // dn w
 #pragma unroll
