@@ -501,54 +501,82 @@ def mxgemm_gated_backward(gate, up, dH, R, C, dgate=None, dup=None, dgate_rows=N
     return st
 
 
-def _heads(x, y, weight, name, dy=None, dweight=None):
-    """mxgemm_heads_t of (tokens, heads, head dim) tensors, and what they have to agree on."""
-    import torch
-    like = y if dy is None else dy
-    if y.shape != like.shape or y.dtype != like.dtype or (x is not None and (x.shape != y.shape or x.dtype != y.dtype)):
-        raise ValueError(f"{name}: tensors of one shape and type")
-    if y.dtype is not torch.float32 and y.dtype is not torch.bfloat16:
-        raise ValueError(f"{name}: float32 or bfloat16")
-    at = [0, 0] * 3
-    for i, t in enumerate((x, dy, y)):
-        if t is not None:
-            at[2 * i:2 * i + 2] = t.data_ptr(), _token_pitch(t.shape, t.stride(), name)
+_codes = {}  # IN_F32 and IN_BF16 by torch's types, once torch is there
+
+
+def _type_codes():
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: IN_F32, torch.bfloat16: IN_BF16})
+    return _codes
+
+
+def _heads(name, tokens, d, dtype, x, y, weight, dy, dweight):
+    """mxgemm_heads_t of a tensor's values, result and gradient, each (tokens, heads, d) of one type."""
+    at, heads = [], y.shape[1] if y.dim() == 3 else -1
+    for t in (x, dy, y):
+        if t is None:
+            at += (0, 0)
+            continue
+        shape = t.shape
+        if shape != (tokens, heads, d) or t.dtype is not dtype:
+            raise ValueError(f"{name}: tokens x heads x head dim, all tensors of one type")
+        step = t.stride()
+        if step[2] != 1 or (heads > 1 and step[1] != d):
+            raise ValueError(f"{name}: tokens x heads x head dim, each token dense")
+        at += (t.data_ptr(), step[0] if tokens > 1 else heads * d)
+    w = dw = 0
     if weight is not None:
         if x is None:
             raise ValueError(f"{name}: a norm needs the values")
-        if weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != y.shape[2:] or not weight.is_contiguous():
-            raise ValueError(f"{name}'s weight: head dim float32 or bfloat16 values")
-    if dweight is not None and (weight is None or dweight.dtype is not torch.float32 or dweight.shape != y.shape[2:]
-                                or not dweight.is_contiguous()):
-        raise ValueError(f"{name}'s weight's gradient: head dim float32 values, of a weight")
-    return _HEADS_STRUCT.pack(*at, _ptr(weight) or 0, _ptr(dweight) or 0, y.shape[1])
+        if weight.shape != (d,) or not weight.is_contiguous():
+            raise ValueError(f"{name}'s weight: head dim values")
+        w = weight.data_ptr()
+    if dweight is not None:
+        if weight is None or _type_codes().get(dweight.dtype) != IN_F32 or dweight.shape != (d,) or not dweight.is_contiguous():
+            raise ValueError(f"{name}'s weight's gradient: head dim float32 values, of a weight")
+        dw = dweight.data_ptr()
+    return _HEADS_STRUCT.pack(*at, w, dw, heads)
+
+
+_rope_types = {}  # the types of positions and frequencies
 
 
 def _rope(positions, freqs, interleaved, factor, tokens):
-    import torch
     if freqs is None:
         return None
-    if positions is None or positions.dtype is not torch.int32 or positions.numel() != tokens or not positions.is_contiguous():
+    if not _rope_types:
+        import torch
+        _rope_types.update(pos=torch.int32, freqs=torch.float64)
+    if positions is None or positions.dtype is not _rope_types["pos"] or positions.shape != (tokens,) or not positions.is_contiguous():
         raise ValueError("positions: a dense int32 tensor, one for each token")
-    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    n = freqs.numel()
+    if freqs.dtype is not _rope_types["freqs"] or freqs.shape != (n,) or not freqs.is_contiguous():
         raise ValueError("freqs: a dense float64 tensor, one for each pair")
-    return _ROPE_STRUCT.pack(positions.data_ptr(), freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, factor)
+    return _ROPE_STRUCT.pack(positions.data_ptr(), freqs.data_ptr(), 2 * n, 1 if interleaved else 0, factor)
 
 
-def _rope_call(name, handle, q, k, weights, positions, freqs, interleaved, factor, eps, stream, check):
+def _rope_call(name, handle, q, k, positions, freqs, interleaved, factor, eps, stream, check):
     """q and k: (values, result, weight, dy, dweight) each, k's result None for none."""
-    import torch
     y = q[1]
-    shape = y.shape
-    heads = [None if t[1] is None else _heads(t[0], t[1], t[2], n, t[3], t[4]) for t, n in ((q, "q"), (k, "k"))]
-    if heads[1] is not None and (k[1].shape[0] != shape[0] or k[1].shape[2] != shape[2] or k[1].dtype != y.dtype):
-        raise ValueError("q and k: tokens x heads x head dim of one type")
-    kinds = {w.dtype for w in weights if w is not None}
-    if len(kinds) > 1:
-        raise ValueError("q's and k's weights: one type")
-    w_dtype = IN_BF16 if torch.bfloat16 in kinds else IN_F32
-    st = getattr(library(), name)(*handle, heads[0], heads[1], shape[0], shape[2], IN_BF16 if y.dtype is torch.bfloat16 else IN_F32,
-                                  w_dtype, eps, _rope(positions, freqs, interleaved, factor, shape[0]), _stream(stream))
+    if y.dim() != 3:
+        raise ValueError("q: tokens x heads x head dim")
+    tokens, _, d = y.shape
+    dtype = y.dtype
+    types = _type_codes()
+    x_dtype = types.get(dtype)
+    if x_dtype is None:
+        raise ValueError("q: float32 or bfloat16")
+    w_dtype = None
+    for w in (q[2], k[2]):
+        if w is not None:
+            code = types.get(w.dtype)
+            if code is None or (w_dtype is not None and code != w_dtype):
+                raise ValueError("weights: float32 or bfloat16, q's and k's of one type")
+            w_dtype = code
+    st = getattr(library(), name)(*handle, _heads("q", tokens, d, dtype, *q), None if k[1] is None else _heads("k", tokens, d, dtype, *k),
+                                  tokens, d, x_dtype, w_dtype or 0, eps, _rope(positions, freqs, interleaved, factor, tokens),
+                                  _stream(stream))
     if check:
         _check(st, name)
     return st
@@ -563,7 +591,7 @@ def mxgemm_norm_rope(q, k, q_out, k_out, positions=None, freqs=None, interleaved
     its input.  positions: int32; freqs: float64 (mxgemm_rope_frequencies), None for no
     rotation."""
     return _rope_call("mxgemm_norm_rope", (), (q, q_out, q_weight, None, None), (k, k_out, k_weight, None, None),
-                      (q_weight, k_weight), positions, freqs, interleaved, factor, eps, stream, check)
+                      positions, freqs, interleaved, factor, eps, stream, check)
 
 
 def mxgemm_norm_rope_backward(h, dq_out, dk_out, dq, dk, q=None, k=None, positions=None, freqs=None, interleaved=False,
@@ -573,8 +601,7 @@ def mxgemm_norm_rope_backward(h, dq_out, dk_out, dq, dk, q=None, k=None, positio
     dk (of its inputs q and k, which a norm needs) and, where given, the weights'
     dq_weight and dk_weight (float32, set)."""
     return _rope_call("mxgemm_norm_rope_backward", (h,), (q, dq, q_weight, dq_out, dq_weight),
-                      (k, dk, k_weight, dk_out, dk_weight), (q_weight, k_weight), positions, freqs, interleaved, factor, eps,
-                      stream, check)
+                      (k, dk, k_weight, dk_out, dk_weight), positions, freqs, interleaved, factor, eps, stream, check)
 
 
 def mxgemm_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, scale=1.0, trained=0.0, slow=1.0, fast=4.0):

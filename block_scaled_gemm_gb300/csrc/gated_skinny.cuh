@@ -23,7 +23,7 @@ struct GatedSkinnyParams {
   B128Params b;
   int n_tiles;
   int64_t total;       // steps: column blocks x K blocks
-  float *partials;     // two slots a CTA: [2 NT / 4][128 columns] of four
+  float *partials;     // two slots a CTA: [sets][2][ROWS / 4][128 columns] of four
   unsigned *counters;  // of the CTA with a shared column block's first step
   int h_type;          // mxgemm_out_dtype_t
 };
@@ -34,16 +34,22 @@ struct GatedSkinnyCfg {
   static constexpr int STAGE = 2 * BT_BYTES + AT_BYTES;
   static constexpr int STAGES = NT <= 32 ? 6 : 5;
   static constexpr int BUFS = 4;  // accumulators, each of both products
-  // scales of A, for each epilogue warp [2 groups][4 steps][NT]
+  // Epilogue warps: four for the 128 columns, and from 32 rows on two sets of them
+  // with half the rows each (one set: 64 x 8192 x 8192 78 us, most of it in the
+  // sums of parts and the end of column blocks).
+  static constexpr int SETS = NT >= 32 ? 2 : 1, ROWS = NT / SETS, EPI_WARPS = 4 * SETS;
+  static constexpr int PARTS = ROWS >= 32 ? 1 : 4;  // whose loads are on their way at a time when parts are added
+  // scales of A, for each epilogue warp [2 groups][4 steps][ROWS]
   static constexpr int OFF_CS = STAGES * STAGE;
-  // codes: rows' largest values, [2][4 warps][NT]
-  static constexpr int OFF_TOP = OFF_CS + 4 * 2 * 4 * NT * 4;
-  static constexpr int OFF_BAR = OFF_TOP + 2 * 4 * NT * 4;
+  // codes: rows' largest values, [2][4 warps of columns][NT], and their reciprocals [2][NT]
+  static constexpr int OFF_TOP = OFF_CS + EPI_WARPS * 2 * 4 * ROWS * 4;
+  static constexpr int OFF_INV = OFF_TOP + 2 * 4 * NT * 4;
+  static constexpr int OFF_BAR = OFF_INV + 2 * NT * 4;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t TM_COLS = 2 * NT * BUFS;
-  static constexpr int THREADS = 6 * 32;
+  static constexpr int THREADS = (2 + EPI_WARPS) * 32;
   static constexpr int PARTIAL = 2 * NT * 128;  // floats
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(STAGE % 1024 == 0 && OFF_BAR % 8 == 0 && TM_COLS <= 512, "layout");
@@ -105,7 +111,7 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
       }
       for (int b = 0; b < S::BUFS; ++b) {
         mbar_init(bar_acc_full + 8 * b, 1);
-        mbar_init(bar_acc_empty + 8 * b, 4);
+        mbar_init(bar_acc_empty + 8 * b, S::EPI_WARPS);
       }
       mbar_init(bar_final, 1);
       *abort_flag = 0;
@@ -180,17 +186,21 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, n = 32 * q + lane;  // this lane's column of the block
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    float *cs = reinterpret_cast<float *>(sm + S::OFF_CS) + q * 8 * NT;
-    float *tops = reinterpret_cast<float *>(sm + S::OFF_TOP);
-    float acc[2][NT];
+    constexpr int ROWS = S::ROWS;
+    const int q = warp & 3, n = 32 * q + lane;                // this lane's column of the block
+    const int set = (warp - 2) >> 2, row0 = set * ROWS;       // and its rows
+    const int rows = min(ROWS, p.M - row0);                   // that there are (0 or fewer: none)
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + row0;
+    float *cs = reinterpret_cast<float *>(sm + S::OFF_CS) + (warp - 2) * 8 * ROWS;
+    float *tops = reinterpret_cast<float *>(sm + S::OFF_TOP), *invs = reinterpret_cast<float *>(sm + S::OFF_INV);
+    auto all_warps = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * S::EPI_WARPS) : "memory"); };  // of the epilogue
+    float acc[2][ROWS];
 #pragma unroll
-    for (int m = 0; m < NT; ++m) acc[0][m] = acc[1][m] = 0.f;
+    for (int m = 0; m < ROWS; ++m) acc[0][m] = acc[1][m] = 0.f;
     // Scales, a group of four steps ahead: of the weights lane 2 j + w has step j's
-    // of weight w, and A's 4 x NT, NT / 8 of them by each lane, go through the
+    // of weight w, and A's 4 x ROWS, ROWS / 8 of them by each lane, go through the
     // warp's shared memory.  (gt, gk): the group's first column block and K block.
-    constexpr int kPer = NT / 8;
+    constexpr int kPer = ROWS / 8;
     float nb = 0.f, sb = 0.f, na[kPer];
     int gt = tile0, gk = k0;
     auto step_at = [&](int j, int &t, int &k) {
@@ -210,9 +220,9 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
       }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int i = lane + 32 * j, m = i % NT;
-        step_at(i / NT, t, k);
-        na[j] = m < p.M ? __ldg(p.a_scale + static_cast<int64_t>(m) * kb + k) : 0.f;
+        const int i = lane + 32 * j, m = i % ROWS;
+        step_at(i / ROWS, t, k);
+        na[j] = m < rows ? __ldg(p.a_scale + static_cast<int64_t>(row0 + m) * kb + k) : 0.f;
       }
       step_at(4, gt, gk);
     };
@@ -223,37 +233,38 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
       if ((i & 3) == 0) {
         sb = nb;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) cs[((i >> 2) & 1) * 4 * NT + lane + 32 * j] = na[j];
+        for (int j = 0; j < kPer; ++j) cs[((i >> 2) & 1) * 4 * ROWS + lane + 32 * j] = na[j];
         __syncwarp();
         fetch();
       }
       const int buf = i % S::BUFS;
       if (have) have = __all_sync(0xFFFFFFFFu, wait_phase<false>(bar_acc_full + 8 * buf, (i / S::BUFS) & 1, wc, 0x05));
       tc_fence_after();
-      const float4 *c4 = reinterpret_cast<const float4 *>(cs + ((i >> 2) & 1) * 4 * NT + (i & 3) * NT);
+      const float4 *c4 = reinterpret_cast<const float4 *>(cs + ((i >> 2) & 1) * 4 * ROWS + (i & 3) * ROWS);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const float sw = __shfl_sync(0xFFFFFFFFu, sb, 2 * (i & 3) + w);
+        uint32_t v[ROWS / 16][16];
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(lane_addr + 2 * NT * buf + NT * w + 16 * c, v);
-          tmem_ld_done(v);
-          if (w == 1 && c == NT / 16 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_acc_empty + 8 * buf);
-          }
+        for (int c = 0; c < ROWS / 16; ++c) tmem_ld_32x32b_x16(lane_addr + 2 * NT * buf + NT * w + 16 * c, v[c]);
+#pragma unroll
+        for (int c = 0; c < ROWS / 16; ++c) tmem_ld_done(v[c]);
+        if (w == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acc_empty + 8 * buf);
+        }
+#pragma unroll
+        for (int c = 0; c < ROWS / 16; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float4 f = c4[4 * c + e];
             float *a = acc[w] + 16 * c + 4 * e;
-            a[0] = fmaf(__uint_as_float(v[4 * e + 0]), f.x * sw, a[0]);
-            a[1] = fmaf(__uint_as_float(v[4 * e + 1]), f.y * sw, a[1]);
-            a[2] = fmaf(__uint_as_float(v[4 * e + 2]), f.z * sw, a[2]);
-            a[3] = fmaf(__uint_as_float(v[4 * e + 3]), f.w * sw, a[3]);
+            a[0] = fmaf(__uint_as_float(v[c][4 * e + 0]), f.x * sw, a[0]);
+            a[1] = fmaf(__uint_as_float(v[c][4 * e + 1]), f.y * sw, a[1]);
+            a[2] = fmaf(__uint_as_float(v[c][4 * e + 2]), f.z * sw, a[2]);
+            a[3] = fmaf(__uint_as_float(v[c][4 * e + 3]), f.w * sw, a[3]);
           }
-        }
       }
       if (++k < kb && i + 1 < steps) continue;
       // -------------------------------------------------------- the end of this
@@ -263,39 +274,48 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
         const int64_t first = static_cast<int64_t>(tile) * kb, end = first + kb;
         const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = (end * ctas - 1) / total;  // the CTAs that share it
         auto slot = [&](int64_t c) {
-          return reinterpret_cast<float4 *>(gp.partials + (2 * c + (c == c0)) * S::PARTIAL) + n;
+          return reinterpret_cast<float4 *>(gp.partials + (2 * c + (c == c0)) * S::PARTIAL) + set * (ROWS / 2) * 128 + n;
         };
         float4 *to = slot(blockIdx.x);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int j = 0; j < NT / 4; ++j)
-            to[(w * (NT / 4) + j) * 128] = make_float4(acc[w][4 * j], acc[w][4 * j + 1], acc[w][4 * j + 2], acc[w][4 * j + 3]);
+          for (int j = 0; j < ROWS / 4; ++j)
+            if (4 * j < rows) to[(w * (ROWS / 4) + j) * 128] = make_float4(acc[w][4 * j], acc[w][4 * j + 1], acc[w][4 * j + 2], acc[w][4 * j + 3]);
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        all_warps();
         if (threadIdx.x == 64) {
           const bool mine = atomicAdd(gp.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
           if (mine) gp.counters[c0] = 0;  // for the next launch
           *last = mine;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        all_warps();
         finish = *last != 0;
         if (finish) {
           __threadfence();
 #pragma unroll
-          for (int m = 0; m < NT; ++m) acc[0][m] = acc[1][m] = 0.f;
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float4 *from = slot(c);
+          for (int m = 0; m < ROWS; ++m) acc[0][m] = acc[1][m] = 0.f;
+#pragma unroll 1
+          for (int64_t c = c0; c <= c1; c += S::PARTS) {
+            float4 o[S::PARTS][2][ROWS / 4];
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
+            for (int i = 0; i < S::PARTS; ++i)
 #pragma unroll
-              for (int j = 0; j < NT / 4; ++j) {
-                const float4 o = __ldcg(from + (w * (NT / 4) + j) * 128);
-                acc[w][4 * j] += o.x;
-                acc[w][4 * j + 1] += o.y;
-                acc[w][4 * j + 2] += o.z;
-                acc[w][4 * j + 3] += o.w;
-              }
+              for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int j = 0; j < ROWS / 4; ++j)
+                  o[i][w][j] = c + i <= c1 && 4 * j < rows ? __ldcg(slot(c + i) + (w * (ROWS / 4) + j) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < S::PARTS; ++i)
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int j = 0; j < ROWS / 4; ++j) {
+                  acc[w][4 * j] += o[i][w][j].x;
+                  acc[w][4 * j + 1] += o[i][w][j].y;
+                  acc[w][4 * j + 2] += o[i][w][j].z;
+                  acc[w][4 * j + 3] += o[i][w][j].w;
+                }
           }
         }
       }
@@ -304,46 +324,48 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
         const bool live = col < p.N && have;
         if (p.gate && live) {
 #pragma unroll
-          for (int m = 0; m < NT; ++m)
-            if (m < p.M) {
-              p.gate[static_cast<int64_t>(m) * p.N + col] = __float2bfloat16_rn(acc[0][m]);
-              p.up[static_cast<int64_t>(m) * p.N + col] = __float2bfloat16_rn(acc[1][m]);
+          for (int m = 0; m < ROWS; ++m)
+            if (m < rows) {
+              p.gate[static_cast<int64_t>(row0 + m) * p.N + col] = __float2bfloat16_rn(acc[0][m]);
+              p.up[static_cast<int64_t>(row0 + m) * p.N + col] = __float2bfloat16_rn(acc[1][m]);
             }
         }
 #pragma unroll
-        for (int m = 0; m < NT; ++m) acc[0][m] = gated(acc[0][m], acc[1][m], p.act);
-        if (gp.h_type == 2) {
-          float *mine = tops + (ends & 1) * 4 * NT;
+        for (int m = 0; m < ROWS; ++m)
+          if (m < rows) acc[0][m] = gated(acc[0][m], acc[1][m], p.act);
+        if (gp.h_type == 2) {  // MXGEMM_OUT_E4M3
+          float *mine = tops + (ends & 1) * 4 * NT, *inv = invs + (ends & 1) * NT;
 #pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(acc[0][m])));
-            if (lane == m % 32) mine[q * NT + m] = __uint_as_float(t);
-          }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (n < p.M && have) {
-            const float t = fmaxf(fmaxf(mine[n], mine[NT + n]), fmaxf(mine[2 * NT + n], mine[3 * NT + n]));
-            p.h_scale[static_cast<int64_t>(n) * p.bs_cols + tile] = __fdiv_rn(fmaxf(t, kQ128Least), 448.0f);
-          }
-#pragma unroll
-          for (int m = 0; m < NT; ++m)
-            if (m < p.M && live) {
-              const float t = fmaxf(fmaxf(mine[m], mine[NT + m]), fmaxf(mine[2 * NT + m], mine[3 * NT + m]));
-              static_cast<uint8_t *>(p.C)[static_cast<int64_t>(m) * p.N + col] =
-                  static_cast<uint8_t>(mx_e4m3(acc[0][m] * __fdiv_rn(448.0f, fmaxf(t, kQ128Least))));
+          for (int m = 0; m < ROWS; ++m)
+            if (m < rows) {
+              const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(acc[0][m])));
+              if (lane == m) mine[q * NT + row0 + m] = __uint_as_float(t);
             }
+          all_warps();
+          const int row = threadIdx.x - 64;
+          if (row < p.M) {
+            const float t = fmaxf(fmaxf(fmaxf(mine[row], mine[NT + row]), fmaxf(mine[2 * NT + row], mine[3 * NT + row])), kQ128Least);
+            inv[row] = __fdiv_rn(448.0f, t);
+            if (have) p.h_scale[static_cast<int64_t>(row) * p.bs_cols + tile] = __fdiv_rn(t, 448.0f);
+          }
+          all_warps();
+#pragma unroll
+          for (int m = 0; m < ROWS; ++m)
+            if (m < rows && live)
+              static_cast<uint8_t *>(p.C)[static_cast<int64_t>(row0 + m) * p.N + col] = static_cast<uint8_t>(mx_e4m3(acc[0][m] * inv[row0 + m]));
           ++ends;
         } else if (live) {
 #pragma unroll
-          for (int m = 0; m < NT; ++m)
-            if (m < p.M) {
-              const int64_t at = static_cast<int64_t>(m) * p.N + col;
+          for (int m = 0; m < ROWS; ++m)
+            if (m < rows) {
+              const int64_t at = static_cast<int64_t>(row0 + m) * p.N + col;
               if (gp.h_type == 1) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(acc[0][m]);
               else static_cast<float *>(p.C)[at] = acc[0][m];
             }
         }
       }
 #pragma unroll
-      for (int m = 0; m < NT; ++m) acc[0][m] = acc[1][m] = 0.f;
+      for (int m = 0; m < ROWS; ++m) acc[0][m] = acc[1][m] = 0.f;
       ++tile;
       k = begin = 0;
     }

@@ -102,12 +102,12 @@ int run_forward(mxg::RopeParams &p, cudaStream_t stream) {
 
 template <typename T, int D>
 int run_backward(mxgemm_handle_t h, const mxg::HandleView &v, mxg::RopeParams &p, cudaStream_t stream) {
-  // two blocks an SM, shared out by the tensors' steps
+  // as many blocks as the SMs hold, shared out by the tensors' steps
   using C = mxg::RopeCfg<T, D, true>;
   const int64_t all = count_steps<C>(p);
   int blocks = 0, rows = 0;
   for (mxg::RopeTensor &t : p.t) {
-    t.blocks = t.heads ? static_cast<int>(std::min(cdiv(p.tokens * t.steps, 8), std::max<int64_t>(1, 2 * v.sm_count * t.steps / all))) : 0;
+    t.blocks = t.heads ? static_cast<int>(std::min(cdiv(p.tokens * t.steps, 8), std::max<int64_t>(1, (sizeof(T) == 4 ? 1 : 2) * v.sm_count * t.steps / all))) : 0;
     const int g = mxg::rope_group(t.blocks);
     blocks += t.blocks;
     rows += t.blocks + (t.blocks + g - 1) / g;

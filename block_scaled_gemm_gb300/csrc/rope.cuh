@@ -84,9 +84,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const F8 &a) {
 // A lane's eight values of a table in shared memory whose values 4 k .. + 3 are at
 // [k][lane of the head]: 16-byte loads of a head's lanes lie side by side.
 template <int LANES>
-__device__ __forceinline__ F8 shared_run(const float *w, int sub) {
-  const float4 a = reinterpret_cast<const float4 *>(w)[sub], b = reinterpret_cast<const float4 *>(w)[LANES + sub];
-  return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+__device__ __forceinline__ F8 shared_run(uint32_t at, int sub) {
+  at += sub * 16;
+  const uint4 a[2] = {ld_shared_v4(at), ld_shared_v4(at + LANES * 16)};
+  return floats_of(a, 0.f);
 }
 
 // A frequency (radians a position) as a fraction of a turn, times 2^64.
@@ -122,11 +123,13 @@ struct Runs {
   int a, b;
   bool turned;
 };
+// (the lanes' first runs lie side by side, and so do the second)
+template <int D>
 __device__ __forceinline__ Runs runs_of(int sub, int rot) {
   const int n = rot >> 4;
   if (sub < n) return Runs{8 * sub, (rot >> 1) + 8 * sub, true};
-  const int at = rot + 16 * (sub - n);
-  return Runs{at, at + 8, false};
+  const int at = rot + 8 * (sub - n);
+  return Runs{at, at + ((D - rot) >> 1), false};
 }
 
 // Where pair j of a token's rot / 2 is in such a table of cosines (or sines).
@@ -135,6 +138,14 @@ __device__ __forceinline__ int pair_place(int j, int rot, int interleaved) {
   const int k = interleaved ? j >= rot >> 2 : (j >> 2) & 1;
   const int sub = interleaved ? (j - (k ? rot >> 2 : 0)) >> 2 : j >> 3;
   return (k * LANES + sub) * 4 + (j & 3);
+}
+__device__ __forceinline__ uint32_t rope_shared_word(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void rope_store_word(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 // A lane's pairs turned forward, or back, by its cosines and sines.
 template <bool BACK>
@@ -169,118 +180,151 @@ __device__ __forceinline__ void rope_copy16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void rope_copy4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// Where a warp is: a token, and step j of it (the queries' steps, then the keys').
+// Where a warp is: a token, step j of it (the queries' steps, then the keys'), and
+// this lane's head there.  Pointers and the head move on by additions; what depends on
+// the tensor and the token is found anew where those change.
+template <typename T>
 struct RopeAt {
-  int64_t token;
-  int j, left;  // left: steps of the warp's range
+  int token, j, left;  // left: steps of the warp's range
+  int h;
+  T *a, *b;  // the head's first run in one or two matrices
 };
 
 // One warp's walk over its range of the steps of all tokens: the ring of loads that
-// is ahead of it, and the angles of the token that it has reached.
+// is ahead of it, and the angles of the token that it has reached.  Its state is kept
+// small: the registers decide how many blocks an SM holds.
 template <typename T, int D, bool BACK>
 struct RopeWalk {
   using C = RopeCfg<T, D, BACK>;
   const RopeParams &p;
-  int first, of_token;  // steps of a token before the keys', and in all (backward: of one tensor)
-  int which_first;      // backward: that tensor
-  int lane, sub, warp;
-  uint8_t *sm;
-  uint32_t ring;
-  Runs r;
-  RopeAt at, ahead;
+  const int only;  // backward: the one tensor
+  uint32_t sm;     // the block's shared memory
+  int sub, apart;  // lane of the head; from its first run to its second
+  RopeAt<T> at, ahead;  // at: a is the result; ahead: a is dy (backward), and b, or a, x
   int stage, filled;
-  int64_t angles_of;  // the token whose angles are there
+  int angles_of;  // the token whose angles are there
 
   // warp `w` of `warps`
-  __device__ RopeWalk(const RopeParams &p_, uint8_t *sm_, int64_t w, int64_t warps, int which)
-      : p(p_), which_first(which), lane(threadIdx.x & 31), sub(lane % C::LANES), warp(threadIdx.x >> 5), sm(sm_),
-        ring(smem_u32(sm_ + C::OFF_RING) + (warp * C::STAGES * C::PIECES * 32 + lane) * 16), r(runs_of(sub, p_.rot)), stage(0), filled(0),
-        angles_of(-1) {
-    first = p.t[which].steps;
-    of_token = BACK ? first : first + p.t[1].steps;
-    const int64_t all = p.tokens * of_token, u0 = w * all / warps;
-    at.token = u0 / of_token;
-    at.j = static_cast<int>(u0 - at.token * of_token);
+  __device__ RopeWalk(const RopeParams &p_, uint32_t sm_, int64_t w, int64_t warps, int which)
+      : p(p_), only(which), sm(sm_), sub(threadIdx.x % C::LANES), stage(0), filled(0), angles_of(-1) {
+    const Runs r = runs_of<D>(sub, p.rot);
+    apart = r.b - r.a;
+    const int64_t all = p.tokens * of_token(), u0 = w * all / warps;
+    at.token = static_cast<int>(u0 / of_token());
+    at.j = static_cast<int>(u0 - static_cast<int64_t>(at.token) * of_token());
     at.left = static_cast<int>((w + 1) * all / warps - u0);
+    at.h = 0;
+    at.a = at.b = nullptr;
     ahead = at;
+    enter<false>(at);
+    enter<true>(ahead);
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) load();
   }
-  __device__ void next(RopeAt &a) const {
+  __device__ int first() const { return p.t[BACK ? only : 0].steps; }  // steps of a token before the keys'
+  __device__ int of_token() const { return BACK ? first() : first() + p.t[1].steps; }
+  __device__ int which(const RopeAt<T> &a) const { return BACK ? only : a.j >= first(); }
+  __device__ uint32_t ring(int st) const {
+    return sm + C::OFF_RING + (((threadIdx.x >> 5) * C::STAGES + st) * C::PIECES * 32 + (threadIdx.x & 31)) * 16;
+  }
+  __device__ uint32_t position(int st) const { return sm + C::OFF_POS + ((threadIdx.x >> 5) * C::STAGES + st) * 4; }
+  __device__ uint32_t angles() const { return sm + C::OFF_CS + (threadIdx.x >> 5) * (D * 4); }
+  template <bool LOADS>
+  __device__ void enter(RopeAt<T> &a) const {
+    const RopeTensor &t = p.t[which(a)];
+    a.h = (a.j - (!BACK && which(a) ? first() : 0)) * C::HEADS + (threadIdx.x & 31) / C::LANES;
+    const int64_t in_row = static_cast<int64_t>(a.h) * D + runs_of<D>(sub, p.rot).a, token = a.token;
+    if (LOADS) {
+      a.a = static_cast<T *>(const_cast<void *>(BACK ? t.dy : t.x)) + token * (BACK ? t.dy_pitch : t.x_pitch) + in_row;
+      if (BACK) a.b = static_cast<T *>(const_cast<void *>(t.x)) + token * t.x_pitch + in_row;
+    } else {
+      a.a = static_cast<T *>(t.out) + token * t.out_pitch + in_row;
+    }
+  }
+  template <bool LOADS>
+  __device__ void next(RopeAt<T> &a) const {
     --a.left;
-    if (++a.j == of_token) {
-      a.j = 0;
-      ++a.token;
+    ++a.j;
+    if (a.j == first() || (!BACK && a.j == of_token())) {
+      if (BACK || a.j == of_token()) {
+        a.j = 0;
+        ++a.token;
+      }
+      enter<LOADS>(a);
+    } else {
+      a.h += C::HEADS;
+      a.a += C::HEADS * D;
+      if (BACK && LOADS) a.b += C::HEADS * D;
     }
   }
   __device__ bool more() const { return at.left > 0; }
-  __device__ int which(const RopeAt &a) const { return BACK ? which_first : a.j >= first; }
-  __device__ int head(const RopeAt &a) const { return (a.j - (!BACK && a.j >= first ? first : 0)) * C::HEADS + lane / C::LANES; }
+  __device__ bool live() const { return at.h < p.t[which(at)].heads; }
+  __device__ bool norm() const { return p.t[which(at)].w != nullptr; }
   // The loads of the place that is ahead, into the next stage (an empty group past the end).
   __device__ void load() {
     if (ahead.left > 0) {
-      const RopeTensor &t = p.t[which(ahead)];
-      const int h = head(ahead);
-      if (h < t.heads) {
-        const uint32_t to = ring + filled * C::PIECES * 512;
+      if (ahead.h < p.t[which(ahead)].heads) {
+        const uint32_t to = ring(filled);
 #pragma unroll
         for (int k = 0; k < (BACK ? 2 : 1); ++k) {  // dy, then x
-          const bool dy = BACK && k == 0;
-          if (!dy && BACK && !t.w) continue;
-          const T *from = static_cast<const T *>(dy ? t.dy : t.x) + ahead.token * (dy ? t.dy_pitch : t.x_pitch) + h * D;
+          if (k == 1 && !p.t[only].w) continue;
+          const T *from = k ? ahead.b : ahead.a;
 #pragma unroll
           for (int i = 0; i < C::WORDS; ++i) {
-            rope_copy16(to + (k * 2 * C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from + r.a) + i);
-            rope_copy16(to + (k * 2 * C::WORDS + C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from + r.b) + i);
+            rope_copy16(to + (k * 2 * C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from) + i);
+            rope_copy16(to + (k * 2 * C::WORDS + C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from + apart) + i);
           }
         }
       }
-      if (lane == 0 && p.rot) rope_copy4(smem_u32(sm + C::OFF_POS) + (warp * C::STAGES + filled) * 4, p.positions + ahead.token);
-      next(ahead);
+      if ((threadIdx.x & 31) == 0 && p.rot) rope_copy4(position(filled), p.positions + ahead.token);
+      next<true>(ahead);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     filled = filled + 1 == C::STAGES ? 0 : filled + 1;
   }
-  __device__ float *angles() const { return reinterpret_cast<float *>(sm + C::OFF_CS) + warp * D; }
   // Waits for the place that has been reached, and its token's angles.
   __device__ void arrive() {
     asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
     __syncwarp();
     if (p.rot && at.token != angles_of) {
       angles_of = at.token;
-      const int pos = *reinterpret_cast<const volatile int *>(sm + C::OFF_POS + (warp * C::STAGES + stage) * 4);
-      const uint64_t *turns = reinterpret_cast<const uint64_t *>(sm + C::OFF_TURN);
-      for (int j = lane; j < p.rot >> 1; j += 32) {
-        const float2 a = angle_at(turns[j], pos, p.factor);
-        const int to = pair_place<C::LANES>(j, p.rot, p.interleaved);
-        angles()[to] = a.x;
-        angles()[D / 2 + to] = a.y;
+      const int pos = static_cast<int>(rope_shared_word(position(stage)));
+      for (int j = threadIdx.x & 31; j < p.rot >> 1; j += 32) {
+        uint64_t turns;
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(turns) : "r"(sm + C::OFF_TURN + j * 8) : "memory");
+        const float2 a = angle_at(turns, pos, p.factor);
+        const uint32_t to = angles() + pair_place<C::LANES>(j, p.rot, p.interleaved) * 4;
+        rope_store_word(to, __float_as_uint(a.x));
+        rope_store_word(to + D * 2, __float_as_uint(a.y));
       }
       __syncwarp();
     }
   }
   template <bool BACKWARD>
   __device__ void turned(F8 &a, F8 &b) const {
-    if (r.turned)
-      turn<BACKWARD>(a, b, shared_run<C::LANES>(angles(), sub), shared_run<C::LANES>(angles() + D / 2, sub), p.interleaved);
+    if (sub < p.rot >> 4) turn<BACKWARD>(a, b, shared_run<C::LANES>(angles(), sub), shared_run<C::LANES>(angles() + D * 2, sub), p.interleaved);
   }
-  // This lane's weights of a tensor's run `i`.
-  __device__ F8 weights(int which, int i) const {
-    return shared_run<C::LANES>(reinterpret_cast<const float *>(sm + C::OFF_W) + (2 * which + i) * (D / 2), sub);
-  }
+  // This lane's weights of the tensor's run `i`.
+  __device__ F8 weights(int i) const { return shared_run<C::LANES>(sm + C::OFF_W + (2 * which(at) + i) * (D * 2), sub); }
   // Run `i` (0, 1) of tensor k (0: dy where there is one, 1: then x).
   __device__ F8 run(int k, int i) const {
     uint4 w[C::WORDS];
 #pragma unroll
-    for (int n = 0; n < C::WORDS; ++n) w[n] = ld_shared_v4(ring + (stage * C::PIECES + (k * 2 + i) * C::WORDS + n) * 512);
+    for (int n = 0; n < C::WORDS; ++n) w[n] = ld_shared_v4(ring(stage) + ((k * 2 + i) * C::WORDS + n) * 512);
     return floats_of(w, T{});
+  }
+  __device__ void store(const F8 &a, const F8 &b) const {
+    if (live()) {
+      store8(at.a, a);
+      store8(at.a + apart, b);
+    }
   }
   // Past this place: its stage has been read by this lane (and, positions, by the warp).
   __device__ void advance() {
     __syncwarp();
     load();
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    next(at);
+    next<false>(at);
   }
 };
 
@@ -292,7 +336,7 @@ __device__ __forceinline__ void rope_tables(const RopeParams &p, uint8_t *sm) {
   for (int i = threadIdx.x; i < 2 * D; i += 256) {
     // value e of run `run` of lane `sub`, of tensor i / D
     const int run = i / 8 % 2, sub = i % D / 16, e = i % 8;
-    const Runs r = runs_of(sub, p.rot);
+    const Runs r = runs_of<D>(sub, p.rot);
     const int from = (run ? r.b : r.a) + e;
     const void *w = p.t[i / D].w;
     if (w)
@@ -307,21 +351,18 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(
   extern __shared__ __align__(16) uint8_t rope_smem[];
   griddep_launch_dependents();
   griddep_wait();
-  RopeWalk<T, D, false> walk(p, rope_smem, static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * 8, 0);
+  RopeWalk<T, D, false> walk(p, smem_u32(rope_smem), static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * 8, 0);
   rope_tables<T, D, false>(p, rope_smem);
   __syncthreads();
-  const Runs r = walk.r;
   for (; walk.more(); walk.advance()) {
     walk.arrive();
-    const int which = walk.which(walk.at), h = walk.head(walk.at);
-    const RopeTensor &t = p.t[which];
     F8 a = walk.run(0, 0), b = walk.run(0, 1);
-    if (t.w) {
+    if (walk.norm()) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum = fma2(a.v[e], a.v[e], fma2(b.v[e], b.v[e], sum));
       const float inv = rsqrtf(fmaf(head_sum<C::LANES>(sum.x + sum.y), 1.f / D, p.eps));
-      const F8 wa = walk.weights(which, 0), wb = walk.weights(which, 1);
+      const F8 wa = walk.weights(0), wb = walk.weights(1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         a.v[e] = mul2(mul2(a.v[e], make_float2(inv, inv)), wa.v[e]);
@@ -329,11 +370,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(
       }
     }
     walk.template turned<false>(a, b);
-    if (h < t.heads) {
-      T *out = static_cast<T *>(t.out) + walk.at.token * t.out_pitch + h * D;
-      store8(out + r.a, a);
-      store8(out + r.b, b);
-    }
+    walk.store(a, b);
   }
 }
 
@@ -368,7 +405,7 @@ __host__ __device__ constexpr int rope_group(int blocks) {
 // equal calls give equal bits, and 25 rows to add at most where 608 would take one
 // block longer than the rest of the call.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 2) norm_rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) norm_rope_backward_kernel(const RopeParams p) {
   using C = RopeCfg<T, D, true>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   __shared__ float sums[8][D];
@@ -379,48 +416,47 @@ __global__ void __launch_bounds__(256, 2) norm_rope_backward_kernel(const RopePa
   const int which = static_cast<int>(blockIdx.x) < p.t[0].blocks ? 0 : 1;
   const RopeTensor &t = p.t[which];
   const int block = blockIdx.x - (which ? p.t[0].blocks : 0);
-  RopeWalk<T, D, true> walk(p, rope_smem, static_cast<int64_t>(block) * 8 + warp, static_cast<int64_t>(t.blocks) * 8, which);
+  RopeWalk<T, D, true> walk(p, smem_u32(rope_smem), static_cast<int64_t>(block) * 8 + warp, static_cast<int64_t>(t.blocks) * 8, which);
   rope_tables<T, D, true>(p, rope_smem);
   __syncthreads();
-  const Runs r = walk.r;
   F8 da{}, db{};
   for (; walk.more(); walk.advance()) {
     walk.arrive();
     F8 ga = walk.run(0, 0), gb = walk.run(0, 1);
     walk.template turned<true>(ga, gb);
-    const int h = walk.head(walk.at);
     if (t.w) {
-      const F8 xa = walk.run(1, 0), xb = walk.run(1, 1), wa = walk.weights(which, 0), wb = walk.weights(which, 1);
+      // (values and weights are read twice from shared memory, not held)
       float2 ss = make_float2(0.f, 0.f), sd = ss;
-      F8 ya, yb;  // dn w
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ss = fma2(xa.v[e], xa.v[e], fma2(xb.v[e], xb.v[e], ss));
-        ya.v[e] = mul2(ga.v[e], wa.v[e]);
-        yb.v[e] = mul2(gb.v[e], wb.v[e]);
-        sd = fma2(ya.v[e], xa.v[e], fma2(yb.v[e], xb.v[e], sd));
+      for (int i = 0; i < 2; ++i) {
+        const F8 &g = i ? gb : ga, x = walk.run(1, i), w = walk.weights(i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ss = fma2(x.v[e], x.v[e], ss);
+          sd = fma2(mul2(g.v[e], w.v[e]), x.v[e], sd);
+        }
       }
       const float inv = rsqrtf(fmaf(head_sum<C::LANES>(ss.x + ss.y), 1.f / D, p.eps));
       const float m = -head_sum<C::LANES>(sd.x + sd.y) * (1.f / D) * inv * inv * inv;
       // (a stage that nothing was copied to holds anything)
+      const bool live = walk.live();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (h < t.heads) {
-          da.v[e] = fma2(ga.v[e], mul2(xa.v[e], make_float2(inv, inv)), da.v[e]);
-          db.v[e] = fma2(gb.v[e], mul2(xb.v[e], make_float2(inv, inv)), db.v[e]);
+      for (int i = 0; i < 2; ++i) {
+        F8 &g = i ? gb : ga, &d = i ? db : da;
+        const F8 x = walk.run(1, i), w = walk.weights(i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 r = mul2(g.v[e], make_float2(inv, inv));
+          if (live) d.v[e] = fma2(r, x.v[e], d.v[e]);
+          g.v[e] = fma2(r, w.v[e], mul2(x.v[e], make_float2(m, m)));
         }
-        ga.v[e] = fma2(xa.v[e], make_float2(m, m), mul2(ya.v[e], make_float2(inv, inv)));
-        gb.v[e] = fma2(xb.v[e], make_float2(m, m), mul2(yb.v[e], make_float2(inv, inv)));
       }
     }
-    if (h < t.heads) {
-      T *dx = static_cast<T *>(t.out) + walk.at.token * t.out_pitch + h * D;
-      store8(dx + r.a, ga);
-      store8(dx + r.b, gb);
-    }
+    walk.store(ga, gb);
   }
   if (!t.dw) return;
   // this block's row of dw: its warps' heads, then its warps
+  const Runs r = runs_of<D>(lane % C::LANES, p.rot);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float a = e & 1 ? da.v[e >> 1].y : da.v[e >> 1].x, b = e & 1 ? db.v[e >> 1].y : db.v[e >> 1].x;
