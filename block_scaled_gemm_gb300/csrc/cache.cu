@@ -158,11 +158,12 @@ int launch_prompt(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t str
 
 template <int D, int NT>
 int decode_grid(const mxg::HandleView &v) {
-  return std::min(mxg::DecodeCfg<D, NT>::CTAS * v.sm_count, mxg::kCounters);
+  return std::min(mxg::DecodeCfg<D, NT>::CTAS * v.sm_count, mxg::kCounters / 4);
 }
 template <int D, int NT>
-int64_t decode_bytes(const mxg::HandleView &v) {
-  return static_cast<int64_t>(decode_grid<D, NT>(v)) * 2 * mxg::DecodeCfg<D, NT>::PARTIAL * sizeof(float);
+int64_t decode_bytes(const mxg::HandleView &v, const mxg::AttnParams &p) {
+  // two slots a CTA, or, behind shared tokens, a warp
+  return static_cast<int64_t>(decode_grid<D, NT>(v)) * (p.shared ? 8 : 2) * mxg::DecodeCfg<D, NT>::PARTIAL * sizeof(float);
 }
 
 template <int D, int NT, int MODE>
@@ -195,7 +196,7 @@ struct AttnPlan {
 template <int D>
 AttnPlan plan_attention(const mxg::HandleView &v, mxg::AttnParams &p) {
   AttnPlan a{takes_prompt(v, p), takes_two(p), 0};
-  a.bytes = a.prompt ? plan_prompt<D>(v, p) : a.two ? decode_bytes<D, 2>(v) : decode_bytes<D, 1>(v);
+  a.bytes = a.prompt ? plan_prompt<D>(v, p) : a.two ? decode_bytes<D, 2>(v, p) : decode_bytes<D, 1>(v, p);
   return a;
 }
 template <int D, int MODE>
@@ -239,7 +240,7 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
   p.left_parts = shared_parts(items, (p.shared + S::KT - 1) / S::KT, v.sm_count);
   const int64_t left = items * p.left_parts * S::PARTIAL * static_cast<int64_t>(sizeof(float));
-  const int64_t rows = p.b.tokens * p.heads, own = rows * (D + 2) * static_cast<int64_t>(sizeof(float));
+  const int64_t rows = p.b.tokens * p.heads, own = rows * (D + 4) * static_cast<int64_t>(sizeof(float));
   const int64_t blocks = (p.b.tokens * p.group + mxg::JoinCfg<D>::ROWS - 1) / mxg::JoinCfg<D>::ROWS;
   mxg::AttnParams first = p;
   const AttnPlan a = plan_attention<D>(v, p);
@@ -249,6 +250,8 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   p.left = first.left = reinterpret_cast<float *>(ws);
   p.own = reinterpret_cast<float *>(ws + left);
   p.own_ml = reinterpret_cast<float2 *>(p.own + rows * D);
+  p.own_at = a.prompt ? nullptr : reinterpret_cast<int2 *>(p.own_ml + rows);
+  p.own_rows = a.two ? 16 : 8;
   p.partials = reinterpret_cast<float *>(ws + left + (own + 15) / 16 * 16);
   first.items = static_cast<int>(items);
   first.whole = 0;
@@ -292,6 +295,8 @@ int attention_args(const mxg::HandleView &v, const mxgemm_cache_t *cache, int64_
   p->shared = p->left_parts = p->left_tiles = 0;
   p->left = p->own = nullptr;
   p->own_ml = nullptr;
+  p->own_at = nullptr;
+  p->own_rows = 0;
   return MXGEMM_OK;
 }
 

@@ -63,10 +63,14 @@ struct AttnParams {
   // attention behind shared tokens: keys [0, shared), a multiple of 32 and of the
   // pages, are one launch's, which leaves partials in `left`, `left_parts` of each row
   // tile, numbered as its CTAs; the others are the next's, which leaves its sums of
-  // each row (token x head) in `own` and `own_ml`; a third joins them
+  // each row (token x head) in `own` and `own_ml`, or in partials of several warps,
+  // and in `own_at` (null: none is) which: the first one (-1: none), and 16 times how
+  // many more there are plus the row in them; a third joins all
   int shared;
   float *left, *own;
   float2 *own_ml;
+  int2 *own_at;
+  int own_rows;  // of a partial
   int left_parts, left_tiles;  // parts of a row tile, row tiles of a key/value head
 };
 
@@ -268,7 +272,7 @@ struct DecodeCfg {
   static constexpr int OFF_PG = OFF_SC + WARPS * STAGES * 16;    // [warp][stage][2] whether the page is there
   static constexpr int OFF_BAR = OFF_PG + WARPS * STAGES * 8;
   static constexpr int OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+  static constexpr int SMEM_BYTES = OFF_MISC + 192 + 1024;
   static constexpr int PARTIAL = ROWS * (D + 2);  // floats of a partial: O, m, l
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
 };
@@ -292,10 +296,18 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   float *merge = reinterpret_cast<float *>(sm + S::OFF_MERGE);
   float *ml = reinterpret_cast<float *>(sm + S::OFF_ML);
   int *last_at = reinterpret_cast<int *>(sm + S::OFF_MISC);
-  // how tiles are cut: all of them and the CTAs that share them, or 0 and the
-  // first and the last CTA of this one's item; then the range's first tile
+  // Attention behind shared tokens: each warp is a unit of its own, whose sums go to
+  // the workspace without a barrier (items of single tiles, 512 of them: 20 us with
+  // units of a CTA, 4.5 us of them an item's end).  Else a unit is a CTA.
+  constexpr bool kWarps = MODE == kOwnKeys;
+  constexpr int kStep = kWarps ? 1 : 4;  // from a warp's tile to its next
+  const int64_t unit = kWarps ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x : blockIdx.x;
+  const int64_t units_most = kWarps ? 4ll * gridDim.x : gridDim.x;
+  // how tiles are cut: all of them and the units that share them, or 0 and the
+  // first and the last unit of this one's item; then the range's first tile
   // (kept here: registers are short)
-  int64_t *cut = reinterpret_cast<int64_t *>(sm + S::OFF_MISC + 8);
+  int64_t *cut = reinterpret_cast<int64_t *>(sm + S::OFF_MISC + 8) + (kWarps ? 4 * warp : 0);
+  const bool cuts = kWarps ? lane == 0 : threadIdx.x == 0;
 
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 33);  // the bytes' arrive, and the lanes' copies
@@ -328,15 +340,15 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     mine = mi * mt;
     upto = warp_prefix(mine);
   };
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 3) / 4);
+  const int64_t ctas = min(units_most, (total + kStep - 1) / kStep);
   // Few items: each one's tiles are cut for CTAs of its own, into parts of q tiles
   // at most, since a CTA that ends two items' parts ends late (17 tiles for
   // each of 8 heads: 16.5 -> 10.8 us).  And no more parts than pay: one costs
   // the join 0.12 us, four tiles more a CTA 2 us, which is least at parts of
   // sqrt(0.24 tiles) (one head of 20000 keys: 27.2 -> 18 us).
-  const bool own = 4 * static_cast<int64_t>(all_items) <= gridDim.x;
+  const bool own = 4 * static_cast<int64_t>(all_items) <= units_most;
   if (own) {
-    const int64_t room = gridDim.x - all_items, q = max(static_cast<int64_t>(4), quotient(total + room - 1, room));
+    const int64_t room = units_most - all_items, q = max(static_cast<int64_t>(kWarps ? 2 : 4), quotient(total + room - 1, room));
     auto parts_of = [&](int tiles) {
       const int64_t n = max(q, static_cast<int64_t>(sqrtf(0.24f * tiles)));
       return quotient(tiles + n - 1, n);
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     for (;;) {
       units = mi * parts_of(mt);
       u = warp_prefix(units);
-      past = __ballot_sync(0xFFFFFFFFu, base_u + u > blockIdx.x);
+      past = __ballot_sync(0xFFFFFFFFu, base_u + u > unit);
       if (past) break;
       if (b0 + 32 >= p.b.batch) return;
       base_u += __shfl_sync(0xFFFFFFFFu, u, 31);
@@ -357,31 +369,32 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     base_b += __shfl_sync(0xFFFFFFFFu, upto - mine, i);
     b0 += i;
     const int tiles = __shfl_sync(0xFFFFFFFFu, mt, i);
-    const int64_t parts = parts_of(tiles), rel = blockIdx.x - base_u, item = quotient(rel, parts), part = rel - item * parts;
+    const int64_t parts = parts_of(tiles), rel = unit - base_u, item = quotient(rel, parts), part = rel - item * parts;
     x0 = base_b + item * tiles + quotient(part * tiles, parts);
     x1 = base_b + item * tiles + quotient((part + 1) * tiles, parts);
-    if (threadIdx.x == 0) {
+    if (cuts) {
       cut[0] = 0;
-      cut[1] = blockIdx.x - part;
-      cut[2] = blockIdx.x - part + parts - 1;
+      cut[1] = unit - part;
+      cut[2] = unit - part + parts - 1;
     }
   } else {
-    if (blockIdx.x >= ctas) return;
+    if (unit >= ctas) return;
     auto first_tile = [&](int64_t u) { return quotient(u * total, ctas); };
-    x0 = first_tile(blockIdx.x);
-    x1 = first_tile(blockIdx.x + 1);
+    x0 = first_tile(unit);
+    x1 = first_tile(unit + 1);
     uint32_t past;
     while (!(past = __ballot_sync(0xFFFFFFFFu, base_b + upto > x0))) next_sequences();
     const int i = __ffs(past) - 1;
     base_b += __shfl_sync(0xFFFFFFFFu, upto - mine, i);
     b0 += i;
-    if (threadIdx.x == 0) {
+    if (cuts) {
       cut[0] = total;
       cut[1] = ctas;
     }
   }
 
-  if (threadIdx.x == 0) cut[3] = x0;
+  if (cuts) cut[3] = x0;
+  if (kWarps) __syncwarp();
 
   const int lg = p.c.page_log2, per = lg == 4 ? 2 : 1;  // pages of a tile
   const uint32_t box_bytes = (lg == 4 ? 16 : 32) * D;
@@ -446,15 +459,16 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     }
     return __all_sync(0xFFFFFFFFu, ok);
   };
-  int64_t px = x0 + warp;  // next tile to load
+  const int mine_at = kWarps ? 0 : warp;
+  int64_t px = x0 + mine_at;  // next tile to load
   int pst = 0;
-  for (int i = 0; i < STAGES && px < x1 && !p.stall_producer; ++i, px += 4) {
+  for (int i = 0; i < STAGES && px < x1 && !p.stall_producer; ++i, px += kStep) {
     issue(px, pst);
     pst = pst + 1 == STAGES ? 0 : pst + 1;
   }
 
   // ------------------------------------------------------------ items
-  int64_t x = x0 + warp;  // this warp's next tile
+  int64_t x = x0 + mine_at;  // this warp's next tile
   int st = 0;
   uint32_t ph = 0;
   bool alive = true;
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       l[n][0] = l[n][1] = 0.f;
     }
 
-    for (; x < seg_end; x += 4) {
+    for (; x < seg_end; x += kStep) {
       const int key0 = at.key(x);
       if (alive) alive = wait_stage(st, ph, p.timeout_ns);
       const uint32_t kb = ring + st * S::STAGE, vb = kb + 32 * D;
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       __syncwarp();
       if (alive && px < x1) {
         issue(px, st);
-        px += 4;
+        px += kStep;
       }
       if (++st == STAGES) {
         st = 0;
@@ -671,7 +685,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       }
     }
 
-    // ---------------------------------------------------------- the CTA's result
+    // ---------------------------------------------------------- the unit's result
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -679,12 +693,11 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
         l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
         l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
-        if (g == 0) {
+        if (!kWarps && g == 0) {
           ml[warp * ROWS + 8 * n + 2 * t + c] = m[n][c];
           ml[(4 + warp) * ROWS + 8 * n + 2 * t + c] = l[n][c];
         }
       }
-    __syncthreads();
     const bool split = item_beg < cut[3] || item_end > x1;
     // the CTAs that share the item
     int64_t u0 = 0, u1 = 0;
@@ -693,6 +706,33 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       u0 = all ? quotient((item_beg + 1) * n - 1, all) : n;
       u1 = all ? quotient(item_end * n - 1, all) : cut[2];
     }
+    if constexpr (kWarps) {
+      // thread (g, t) has rows 2t, 2t + 1 of each eight and d = (D/8) g .. + D/8 - 1
+      constexpr int kQuads = D / 32;
+      float *part = p.partials + (2 * unit + (unit == u0)) * S::PARTIAL;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = 8 * n + 2 * t + c;
+          if (r >= rows) continue;
+          const int64_t row = static_cast<int64_t>(at.s.first + (row0 + r) / p.group) * p.heads + h * p.group + (row0 + r) % p.group;
+          float *to = (split ? part + r * D : p.own + row * D) + (D / 8) * g;
+#pragma unroll
+          for (int k = 0; k < kQuads; ++k)
+            reinterpret_cast<float4 *>(to)[k] = make_float4(o[n][2 * k][c], o[n][2 * k][c + 2], o[n][2 * k + 1][c], o[n][2 * k + 1][c + 2]);
+          if (g == 0) {
+            if (split) {
+              part[ROWS * D + r] = m[n][c];
+              part[ROWS * D + ROWS + r] = l[n][c];
+            } else {
+              p.own_ml[row] = make_float2(m[n][c], l[n][c]);
+            }
+            if (!split || unit == u0) p.own_at[row] = split ? make_int2(static_cast<int>(u0), static_cast<int>(u1 - u0) * 16 + r) : make_int2(-1, 0);
+          }
+        }
+    } else {
+    __syncthreads();
     float *part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (blockIdx.x == u0)) * S::PARTIAL;
     const int hr = threadIdx.x >> 4, hd = threadIdx.x & 15;  // output: row of 8, four of 64 d
 #pragma unroll
@@ -734,10 +774,6 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         const int d = 64 * e + 4 * hd;
         if (split) {
           *reinterpret_cast<float4 *>(part + r * D + d) = a;
-        } else if (MODE == kOwnKeys) {
-          if (r < rows)
-            *reinterpret_cast<float4 *>(
-                p.own + (static_cast<int64_t>(at.s.first + (row0 + r) / p.group) * p.heads + h * p.group + (row0 + r) % p.group) * D + d) = a;
         } else if (r < rows) {
           const float k = sum == 0.f ? 0.f : kWeightDown / sum;
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
@@ -750,10 +786,9 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         if (split) {
           part[ROWS * D + r] = top;
           part[ROWS * D + ROWS + r] = sum;
-        } else if (r < rows && (MODE == kOwnKeys || p.lse)) {
+        } else if (r < rows && p.lse) {
           const int tok = at.s.first + (row0 + r) / p.group, head = h * p.group + (row0 + r) % p.group;
-          if (MODE == kOwnKeys) p.own_ml[static_cast<int64_t>(tok) * p.heads + head] = make_float2(top, sum);
-          else p.lse[static_cast<int64_t>(tok) * p.heads + head] = log_sum(top, sum);
+          p.lse[static_cast<int64_t>(tok) * p.heads + head] = log_sum(top, sum);
         }
       }
     }
@@ -800,13 +835,6 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
           for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
           if (rr >= rows) continue;
           const int tok = at.s.first + (row0 + rr) / p.group, head = h * p.group + (row0 + rr) % p.group;
-          if constexpr (MODE == kOwnKeys) {
-            const int64_t row = static_cast<int64_t>(tok) * p.heads + head;
-#pragma unroll
-            for (int e = 0; e < D / 64; ++e) *reinterpret_cast<float4 *>(p.own + row * D + 64 * e + 4 * hd) = a[e];
-            if (hd == 0) p.own_ml[row] = make_float2(top, sum);
-            continue;
-          }
           const float k = sum == 0.f ? 0.f : kWeightDown / sum;
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) {
@@ -819,16 +847,17 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
         }
       }
     }
+    }
     seg = seg_end;
     if (seg < x1) {
       at.to(p, ROWS, seg);
       load_q();
     }
-    __syncthreads();  // ml and merge are free for the next item
+    if (!kWarps) __syncthreads();  // ml and merge are free for the next item
   }
   // after a wait that gave up: loads still on their way land first
   if (!alive) {
-    const int64_t issued = (px - (cut[3] + warp)) / 4;
+    const int64_t issued = (px - (cut[3] + mine_at)) / kStep;
     for (int64_t i = ring_pending(issued, STAGES); i < issued; ++i)
       wait_stage(static_cast<int>(i % STAGES), ring_parity(i, STAGES), landing_limit(p.timeout_ns));
   }
