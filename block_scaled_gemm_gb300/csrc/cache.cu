@@ -181,8 +181,10 @@ int launch_decode(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t str
 // 128 the first takes 106 us and the second 219, and with more than 16 rows
 // the second reads the keys again; but it cuts them for all SMs where the
 // first's row tiles times 16 do not fill half of them.
+// (Behind shared tokens, whose own keys are mostly few: from 64 rows on.)
 bool takes_prompt(const mxg::HandleView &v, const mxg::AttnParams &p) {
   const int64_t rows = p.b.tokens * p.group;
+  if (p.shared) return rows >= 64 * p.b.batch;
   return rows >= 64 * p.b.batch || (rows > 16 * p.b.batch && equal_row_tiles(p) * 32 >= v.sm_count);
 }
 // (of the kernel for few rows: items of 16)
@@ -232,7 +234,7 @@ int shared_parts(int64_t tiles, int64_t key_tiles, int64_t sms) {
   return best;
 }
 
-// The shared keys for all tokens, then each sequence's own, then both joined.
+// Each sequence's own keys, then the shared ones for all tokens, then both joined.
 template <int D>
 int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::PromptCfg<D>;
@@ -256,9 +258,9 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   first.items = static_cast<int>(items);
   first.whole = 0;
   first.parts = first.left_parts;
-  if (int st = launch_prompt<D, mxg::kSharedKeys>(v, first, stream)) return st;
-  ++*v.launches;
   if (int st = launch_attention<D, mxg::kOwnKeys>(v, p, a, stream)) return st;
+  ++*v.launches;
+  if (int st = launch_prompt<D, mxg::kSharedKeys>(v, first, stream)) return st;
   ++*v.launches;
   return mxg::launch(mxg::cache_join_kernel<D>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.c.kv_heads)), 256, 0, 1, stream, p);
 }

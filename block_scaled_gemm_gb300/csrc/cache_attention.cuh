@@ -62,7 +62,7 @@ struct AttnParams {
   int stall_producer;  // tests: nothing is loaded
   // attention behind shared tokens: keys [0, shared), a multiple of 32 and of the
   // pages, are one launch's, which leaves partials in `left`, `left_parts` of each row
-  // tile, numbered as its CTAs; the others are the next's, which leaves its sums of
+  // tile, numbered as its CTAs; the others are another's, which leaves its sums of
   // each row (token x head) in `own` and `own_ml`, or in partials of several warps,
   // and in `own_at` (null: none is) which: the first one (-1: none), and 16 times how
   // many more there are plus the row in them; a third joins all
@@ -315,8 +315,11 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     fence_proxy_async_smem();
   }
   __syncwarp();
-  griddep_launch_dependents();
+  // (behind shared tokens the next launch does not need this one's results, and
+  // does not wait for them at its start: it may begin once this one has waited)
+  if (MODE != kOwnKeys) griddep_launch_dependents();
   griddep_wait();
+  if (MODE == kOwnKeys) griddep_launch_dependents();
   // All tiles (each warp counts for itself, 32 sequences at a time), and this
   // CTA's range of them: ranges of four tiles at least.
   int mt;

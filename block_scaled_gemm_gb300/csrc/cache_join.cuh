@@ -31,49 +31,56 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p) {
   const int64_t at = row / p.group * p.heads + h * p.group + row % p.group;  // token x head
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float top = -INFINITY, sum = 0.f;
-  // eight partials' loads at once, then their sums in order, over the maximum so far
-  auto add = [&](int parts, auto top_of, auto sum_of, auto values) {
-    for (int v = 0; v < parts; v += 8) {
-      float m[8], l[8];
-      float4 b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int u = min(v + i, parts - 1);
-        m[i] = v + i < parts ? __ldcg(top_of(u)) : -INFINITY;
-        l[i] = v + i < parts ? __ldcg(sum_of(u)) : 0.f;
-        b[i] = __ldcg(reinterpret_cast<const float4 *>(values(u)));
-      }
-      if (v == 0 && l[0] < 0.f) return false;  // a row that is no sequence's
-      float most = top;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) most = fmaxf(most, m[i]);
-      const float f = top == -INFINITY ? 0.f : ex2(top - most);
-      sum *= f;
-      a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
-      top = most;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float k = m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
-        sum = fmaf(l[i], k, sum);
-        if (k == 0.f) b[i] = make_float4(0.f, 0.f, 0.f, 0.f);  // (a part without keys holds anything)
-        a = make_float4(fmaf(b[i].x, k, a.x), fmaf(b[i].y, k, a.y), fmaf(b[i].z, k, a.z), fmaf(b[i].w, k, a.w));
-      }
-    }
-    return true;
-  };
-  const float *left_ml = left + kTileRows * D + r, *left_o = left + (d4 * kTileRows + r) * 4;
-  if (!add(p.left_parts, [&](int v) { return left_ml + static_cast<int64_t>(v) * kTilePartial<D>; },
-           [&](int v) { return left_ml + kTileRows + static_cast<int64_t>(v) * kTilePartial<D>; },
-           [&](int v) { return left_o + static_cast<int64_t>(v) * kTilePartial<D>; }))
-    return;
+  // the shared keys' parts, then the own keys' sums or parts: eight loads of each
+  // kind at once, then their sums in order, over the maximum so far
   const int2 where = p.own_at ? __ldcg(p.own_at + at) : make_int2(-1, 0);
-  if (where.x < 0) {
-    add(1, [&](int) { return &p.own_ml[at].x; }, [&](int) { return &p.own_ml[at].y; }, [&](int) { return p.own + at * D + 4 * d4; });
-  } else {
-    const int rows = p.own_rows, size = rows * (D + 2), rr = where.y & 15;
-    auto slot = [&](int v) { return p.partials + (2 * static_cast<int64_t>(where.x + v) + (v == 0)) * size; };
-    add((where.y >> 4) + 1, [&](int v) { return slot(v) + rows * D + rr; }, [&](int v) { return slot(v) + rows * (D + 1) + rr; },
-        [&](int v) { return slot(v) + rr * D + 4 * d4; });
+  const int rows = p.own_rows, size = rows * (D + 2), rr = where.y & 15, parts = p.left_parts + (where.x < 0 ? 0 : where.y >> 4) + 1;
+  for (int v = 0; v < parts; v += 8) {
+    float m[8], l[8];
+    float4 b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (v + i >= parts) continue;
+      const float *ml, *o;  // maximum (the sum is `apart` behind it), and the four values
+      int apart;
+      if (v + i < p.left_parts) {
+        const float *part = left + static_cast<int64_t>(v + i) * kTilePartial<D>;
+        ml = part + kTileRows * D + r;
+        o = part + (d4 * kTileRows + r) * 4;
+        apart = kTileRows;
+      } else if (where.x < 0) {
+        ml = &p.own_ml[at].x;
+        o = p.own + at * D + 4 * d4;
+        apart = 1;
+      } else {
+        const int n = v + i - p.left_parts;
+        const float *part = p.partials + (2 * static_cast<int64_t>(where.x + n) + (n == 0)) * size;
+        ml = part + rows * D + rr;
+        o = part + rr * D + 4 * d4;
+        apart = rows;
+      }
+      m[i] = __ldcg(ml);
+      l[i] = __ldcg(ml + apart);
+      b[i] = __ldcg(reinterpret_cast<const float4 *>(o));
+    }
+    if (v == 0 && l[0] < 0.f) return;  // a row that is no sequence's
+    float most = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, m[i]);
+    const float f = top == -INFINITY ? 0.f : ex2(top - most);
+    sum *= f;
+    a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    top = most;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float k = m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
+      sum = fmaf(l[i], k, sum);
+      if (k == 0.f) continue;  // (a part without keys holds anything)
+      a = make_float4(fmaf(b[i].x, k, a.x), fmaf(b[i].y, k, a.y), fmaf(b[i].z, k, a.z), fmaf(b[i].w, k, a.w));
+    }
   }
   const float k = sum == 0.f ? 0.f : kWeightDown / sum;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * k, a.y * k), hi = __floats2bfloat162_rn(a.z * k, a.w * k);

@@ -116,8 +116,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   uint8_t *sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  griddep_launch_dependents();
-  griddep_wait();
+  // (the launch over the own keys comes before the one over the shared, which needs
+  // nothing of it: the first lets the second begin once it has itself waited for what
+  // came before, and the second waits for it at its end, for the launch that joins)
+  if (MODE != kOwnKeys) griddep_launch_dependents();
+  if (MODE != kSharedKeys) griddep_wait();
+  if (MODE == kOwnKeys) griddep_launch_dependents();
   // ------------------------------------------------------------ this CTA's rows
   // Sequence b's row tiles are numbered from f(b) = floor(q_start group / 256) + b
   // (room for all of them); the last tiles, which see most keys, come first.
@@ -152,7 +156,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   }
   const int64_t row_first = (MODE == kSharedKeys ? id : id - f(b)) * S::ROWS;
   const int64_t row_count = static_cast<int64_t>(s.n) * p.group;
-  if (row_first < 0 || row_first >= row_count) return;
+  if (row_first < 0 || row_first >= row_count) {
+    if (MODE == kSharedKeys) griddep_wait();
+    return;
+  }
   const int row0 = static_cast<int>(row_first);
   const int rows = static_cast<int>(min(static_cast<int64_t>(S::ROWS), row_count - row_first));
   const int nq = rows > 128 ? 2 : 1;
@@ -173,7 +180,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       slot[threadIdx.x] = threadIdx.x < S::ROWS ? -INFINITY : 0.f;
     }
   }
-  if (part >= parts) return;
+  if (part >= parts) {
+    if (MODE == kSharedKeys) griddep_wait();
+    return;
+  }
   const int tile0 = static_cast<int>(static_cast<int64_t>(part) * all_tiles / parts);
   const int tiles = static_cast<int>(static_cast<int64_t>(part + 1) * all_tiles / parts) - tile0;
   auto tile_key = [&](int j) { return (j + tile0 < ns ? j + tile0 : lo + j + tile0 - ns) * 128; };
@@ -695,6 +705,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc<1>(tmem, 512);
+  if (MODE == kSharedKeys) griddep_wait();
 }
 
 }  // namespace mxg

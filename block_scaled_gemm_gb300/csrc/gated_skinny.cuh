@@ -216,13 +216,13 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
       int t, k;
       if (lane < 8) {
         step_at(lane >> 1, t, k);
-        nb = __ldg((lane & 1 ? p.u_scale : p.b_scale) + t * p.bs_n + k * p.bs_k);
+        nb = __ldcg((lane & 1 ? p.u_scale : p.b_scale) + t * p.bs_n + k * p.bs_k);
       }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int i = lane + 32 * j, m = i % ROWS;
         step_at(i / ROWS, t, k);
-        na[j] = m < rows ? __ldg(p.a_scale + static_cast<int64_t>(row0 + m) * kb + k) : 0.f;
+        na[j] = m < rows ? __ldcg(p.a_scale + static_cast<int64_t>(row0 + m) * kb + k) : 0.f;
       }
       step_at(4, gt, gk);
     };
