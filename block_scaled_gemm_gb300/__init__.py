@@ -33,7 +33,7 @@ __all__ = [
     "mxgemm_noalloc_set_option", "mxgemm_run_block128", "mxgemm_quantize_block128", "BLOCK_ROWS", "BLOCK_COLS",
     "BLOCK_TILES", "Cache", "mxgemm_cache_append", "mxgemm_cache_attention", "OUT_E4M3", "ACT_SILU", "ACT_GELU_TANH",
     "mxgemm_run_gated_block128", "mxgemm_gated_backward", "mxgemm_norm_rope", "mxgemm_norm_rope_backward",
-    "mxgemm_rope_frequencies", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS", "mxgemm_cache_attention_shared",
+    "mxgemm_rope_frequencies", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS", "mxgemm_cache_attention_shared", "OPT_SHARED_KEYS",
 ]
 
 OUT_F32 = 0
@@ -50,6 +50,7 @@ OPT_B_FORMAT = 7
 OPT_SCALE_LAYOUT = 8
 OPT_ELEMENT_LAYOUT = 10
 OPT_B_MAJOR = 11
+OPT_SHARED_KEYS = 12
 B_K_BY_N = 0
 B_N_BY_K = 1
 ELEMS_BYTE = 0

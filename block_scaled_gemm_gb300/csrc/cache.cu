@@ -219,19 +219,35 @@ int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &
   return launch_attention<D, mxg::kAllKeys>(v, p, a, stream);
 }
 
-// Parts of the shared keys for each of `tiles` row tiles, in key tiles' time: a CTA
-// takes its own and about five more, and each part costs the next launch a twentieth.
-int shared_parts(int64_t tiles, int64_t key_tiles, int64_t sms) {
-  int best = 1;
-  double least = 1e300;
+// Parts of the shared keys for each of `tiles` row tiles, and the time (us) of a launch
+// over them: a key tile takes a CTA 1.65 us, its start and end about as long as five,
+// and each part costs the launch that joins a twentieth.
+struct SharedPlan {
+  int parts;
+  double us;
+};
+SharedPlan plan_shared(int64_t tiles, int64_t key_tiles, int64_t sms) {
+  SharedPlan best{1, 1e300};
   for (int64_t n = 1; n <= std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4)); ++n) {
-    const double cost = static_cast<double>((tiles * n + sms - 1) / sms) * (static_cast<double>((key_tiles + n - 1) / n) + 5) + 0.05 * n;
-    if (cost < least) {
-      least = cost;
-      best = static_cast<int>(n);
-    }
+    const double us = 1.65 * (static_cast<double>((tiles * n + sms - 1) / sms) * (static_cast<double>((key_tiles + n - 1) / n) + 5) + 0.05 * n);
+    if (us < best.us) best = SharedPlan{static_cast<int>(n), us};
   }
   return best;
+}
+
+// Time (us) that the shared keys take where each sequence reads them with its own: by
+// the kernel for few rows 5 TB/s, once for each 8 or 16 rows; by the one for prompts
+// its key tiles.  (32/8 heads, 256 keys of their own, together and apart: 4 sequences
+// behind 8192 keys 19.9 and 28.5 us, 8 33 and 29.8, 16 58 and 31.5; 16 behind 2048 24
+// and 26, 64 62 and 31.)
+template <int D>
+double apart_us(const mxg::HandleView &v, const mxg::AttnParams &p) {
+  mxg::AttnParams all = p;
+  all.shared = 0;
+  const int64_t key_tiles = (p.shared + 127) / 128;
+  if (takes_prompt(v, all)) return 1.65 * static_cast<double>(equal_row_tiles(all) * key_tiles) / v.sm_count;
+  const int64_t rows = takes_two(all) ? 16 : 8, passes = (p.b.tokens * p.group + rows * p.b.batch - 1) / (rows * p.b.batch);
+  return static_cast<double>(passes * p.b.batch * p.shared) * p.c.kv_heads * 2 * D / 5e6;
 }
 
 // Each sequence's own keys, then the shared ones for all tokens, then both joined.
@@ -240,7 +256,12 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   using S = mxg::PromptCfg<D>;
   p.left_tiles = static_cast<int>((p.b.tokens * p.group + S::ROWS - 1) / S::ROWS);
   const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
-  p.left_parts = shared_parts(items, (p.shared + S::KT - 1) / S::KT, v.sm_count);
+  const SharedPlan plan = plan_shared(items, (p.shared + S::KT - 1) / S::KT, v.sm_count);
+  if (!v.shared_keys && plan.us > apart_us<D>(v, p)) {
+    p.shared = 0;
+    return run_attention<D>(h, v, p, stream);
+  }
+  p.left_parts = plan.parts;
   const int64_t left = items * p.left_parts * S::PARTIAL * static_cast<int64_t>(sizeof(float));
   const int64_t rows = p.b.tokens * p.heads, own = rows * (D + 4) * static_cast<int64_t>(sizeof(float));
   const int64_t blocks = (p.b.tokens * p.group + mxg::JoinCfg<D>::ROWS - 1) / mxg::JoinCfg<D>::ROWS;

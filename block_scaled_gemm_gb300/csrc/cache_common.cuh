@@ -37,18 +37,28 @@ struct Sequence {
   int n;      // how many new tokens (queries)
 };
 
+// A load, from L2 where FRESH: by a kernel that has not itself waited for the launch
+// that wrote the value (another launch between them has), so that no line that an SM
+// held before is taken.
+template <bool FRESH, typename T>
+__device__ __forceinline__ T load_value(const T *p) {
+  if constexpr (FRESH) return __ldcg(p);
+  else return *p;
+}
+
 // Sequence b with values that stay in bounds whatever the arrays hold: a
 // length that does not fit the page table counts as 0, rows are clamped to
 // [0, tokens].
+template <bool FRESH = false>
 __device__ __forceinline__ Sequence load_sequence(const BatchView &bv, const CacheView &c, int b) {
   Sequence s;
-  s.len = bv.kv_len[b];
+  s.len = load_value<FRESH>(bv.kv_len + b);
   if (s.len < 0 || s.len > bv.table_pitch * c.page_size) {
     cache_invalid(bv, 0x21);
     s.len = 0;
   }
   if (bv.q_start) {
-    const int64_t s0 = bv.q_start[b], s1 = bv.q_start[b + 1];
+    const int64_t s0 = load_value<FRESH>(bv.q_start + b), s1 = load_value<FRESH>(bv.q_start + b + 1);
     if (s0 < 0 || s1 < s0 || s1 > bv.tokens) {
       cache_invalid(bv, 0x22);
       s.first = s.n = 0;
@@ -64,8 +74,9 @@ __device__ __forceinline__ Sequence load_sequence(const BatchView &bv, const Cac
 }
 
 // Page number of page slot `i` of sequence b, or -1 when it names none.
+template <bool FRESH = false>
 __device__ __forceinline__ int load_page(const BatchView &bv, const CacheView &c, int b, int64_t i) {
-  const int pg = bv.table[b * bv.table_pitch + i];
+  const int pg = load_value<FRESH>(bv.table + b * bv.table_pitch + i);
   if (pg < 0 || pg >= c.num_pages) {
     cache_invalid(bv, 0x23);
     return -1;

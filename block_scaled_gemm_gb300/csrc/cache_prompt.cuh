@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     int most = 0;
     b = 0;
     for (int i = lane; i < p.b.batch; i += 32) {
-      const int len = load_sequence(p.b, p.c, i).len;
+      const int len = load_sequence<true>(p.b, p.c, i).len;
       if (len > most) {
         most = len;
         b = i;
@@ -248,12 +248,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         // their page (a window may have passed it)
         int pg = -1;
         const int k0 = key0 + 16 * lane, page0 = k0 >> lg << lg;
-        if (lane < 8 && k0 < end && (page0 + (1 << lg) > win_lo || page0 < p.sinks)) pg = load_page(p.b, p.c, b, k0 >> lg);
+        if (lane < 8 && k0 < end && (page0 + (1 << lg) > win_lo || page0 < p.sinks)) pg = load_page<MODE == kSharedKeys>(p.b, p.c, b, k0 >> lg);
         float ks = 1.f, vs = 1.f;
         if (pg >= 0) {
           const int64_t cell = static_cast<int64_t>(pg) * p.c.kv_heads + h;
-          ks = p.c.K_scale[cell];
-          vs = fmaxf(p.c.V_scale[cell], kScaleFloor);
+          ks = load_value<MODE == kSharedKeys>(p.c.K_scale + cell);
+          vs = fmaxf(load_value<MODE == kSharedKeys>(p.c.V_scale + cell), kScaleFloor);
         }
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
         // lane i < npg: page i of the tile
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int n = 0; n < 32 / kRows; ++n) {
           const int from = kRows * n + sub;
           const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, from);
-          x[n] = 128 * i + 32 * qd + from < rows ? *reinterpret_cast<const uint4 *>(p.Q + at + 8 * unit) : make_uint4(0, 0, 0, 0);
+          x[n] = 128 * i + 32 * qd + from < rows ? load_value<MODE == kSharedKeys>(reinterpret_cast<const uint4 *>(p.Q + at + 8 * unit)) : make_uint4(0, 0, 0, 0);
         }
         float top = 0.f;  // of this thread's row
         const uint32_t dst = base + S::OFF_Q + i * S::TILE16 + (unit >> 3) * 16384;
@@ -465,13 +465,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         if (p.b.q_start) {
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (p.b.q_start[mid] <= tok) lo = mid;
+            if (load_value<true>(p.b.q_start + mid) <= tok) lo = mid;
             else hi = mid;
           }
         } else {
           lo = tok;
         }
-        const Sequence own = load_sequence(p.b, p.c, lo);
+        const Sequence own = load_sequence<true>(p.b, p.c, lo);
         const int at = tok - own.first;
         no_query = at < 0 || at >= own.n;
         row_to = no_query ? 0 : max(0, min(end, p.causal ? own.len - own.n + at + 1 : own.len));

@@ -19,6 +19,7 @@ struct HandleView {
   int stall_producer;
   int a_fmt, b_fmt;  // mxgemm_format_t
   int b_major;       // mxgemm_b_major_t
+  int shared_keys;   // MXGEMM_OPT_SHARED_KEYS
   int64_t *launches;
   cudaEvent_t prof_before, prof_after;
   PFN_cuTensorMapEncodeTiled_v12000 encode;

@@ -126,6 +126,7 @@ struct mxgemm_ctx {
   int scale_layout = MXGEMM_SCALES_ROW_MAJOR;
   int elem_layout = MXGEMM_ELEMS_BYTE;
   int b_major = MXGEMM_B_K_BY_N;
+  int shared_keys = 0;
   bool attr_set[3][16] = {};
   bool swap_attr[4][4] = {};
   cudaEvent_t prof_before = nullptr;
@@ -729,6 +730,10 @@ int mxgemm_set_option(mxgemm_handle_t h, int option, int64_t value) {
       if (value != MXGEMM_B_K_BY_N && value != MXGEMM_B_N_BY_K) return MXGEMM_ERR_INVALID_VALUE;
       h->b_major = static_cast<int>(value);
       return MXGEMM_OK;
+    case MXGEMM_OPT_SHARED_KEYS:
+      if (value != 0 && value != 1) return MXGEMM_ERR_INVALID_VALUE;
+      h->shared_keys = static_cast<int>(value);
+      return MXGEMM_OK;
     default:
       return MXGEMM_ERR_INVALID_VALUE;
   }
@@ -955,7 +960,7 @@ namespace mxg {
 HandleView handle_view(mxgemm_handle_t h) {
   return HandleView{h->device,   h->sm_count,    h->d_status, static_cast<unsigned long long>(h->timeout_ns),
                     h->stall_producer, h->a_fmt, h->b_fmt,    h->b_major,
-                    &h->launches, h->prof_before, h->prof_after, h->encode,
+                    h->shared_keys, &h->launches, h->prof_before, h->prof_after, h->encode,
                     h->counters};
 }
 

@@ -143,7 +143,11 @@ typedef enum {
    * formats. */
   MXGEMM_OPT_ELEMENT_LAYOUT = 10,
   /* Layout of B, an mxgemm_b_major_t; default MXGEMM_B_K_BY_N. */
-  MXGEMM_OPT_B_MAJOR = 11
+  MXGEMM_OPT_B_MAJOR = 11,
+  /* mxgemm_cache_attention_shared: 0 (default) reads the shared keys apart where
+   * that is estimated to take less time than reading them with each sequence's own;
+   * 1: always. */
+  MXGEMM_OPT_SHARED_KEYS = 12
 } mxgemm_option_t;
 
 /* Layouts of B (B_scale is N x (K/32) either way).

@@ -15,7 +15,9 @@ pytestmark = pytest.mark.gpu
 
 @pytest.fixture(scope="module")
 def h():
+    """A handle that reads the shared keys apart whatever their number."""
     h = mx.mxgemm_create(0)
+    mx.mxgemm_set_option(h, mx.OPT_SHARED_KEYS, 1)
     yield h
     mx.mxgemm_destroy(h)
 
@@ -96,6 +98,31 @@ def test_as_without_sharing(h):
     _, _, mag, size = plain64.attention(plain64.value(m.K), m.sK, plain64.value(m.V), m.sV, m.table, lens, [0, 1, 2, 3], q, 128 ** -0.5)
     assert ((O.double() - O0.cpu().double()).abs() <= 2.0 ** -7 * O.double().abs() + 2.0 ** -9 * mag).all()
     assert ((L.double() - L0.cpu().double()).abs() <= 2.0 ** -18 * (1 + size)).all()
+
+
+def test_chosen_by_the_library():
+    """Few shared keys are read with each sequence's own, as the call without sharing
+    does it (equal bits, one launch); many apart (three launches)."""
+    h = mx.mxgemm_create(0)
+    with pytest.raises(mx.MxgemmError):
+        mx.mxgemm_set_option(h, mx.OPT_SHARED_KEYS, 2)
+    m = made([200, 190], 2, 128, 16, 128)
+    q = queries(m, 2, 8)
+    n = mx.mxgemm_get_launch_count(h)
+    O, L = attend(h, m, q, None, 128)
+    assert mx.mxgemm_get_launch_count(h) == n + 1
+    O0, L0 = torch.empty(2, 8, 128, dtype=torch.bfloat16, device=DEV), torch.empty(2, 8, device=DEV)
+    mx.mxgemm_cache_attention(h, m.cache(), m.table_tensor(), torch.tensor(m.kv_len, dtype=torch.int32, device=DEV), q.to(DEV), O0, lse=L0)
+    torch.cuda.synchronize()
+    assert torch.equal(O, O0.cpu()) and torch.equal(L, L0.cpu())
+    m = made([4100 + i for i in range(96)], 2, 128, 64, 4096)
+    q = queries(m, 96, 4)
+    n = mx.mxgemm_get_launch_count(h)
+    O, L = attend(h, m, q, None, 4096)
+    assert mx.mxgemm_get_launch_count(h) == n + 3
+    check(m, q, [1] * 96, O, L)
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
+    mx.mxgemm_destroy(h)
 
 
 @pytest.mark.parametrize("f,scale", [(2.0 ** 20, 0.08), (2.0 ** -40, 0.08), (1.0, -0.1)])
@@ -186,6 +213,7 @@ def test_graph_with_growing_sequences(h):
 @pytest.mark.parametrize("new", [1, 40])
 def test_a_call_that_gives_up_leaves_nothing(new):
     h = mx.mxgemm_create(0)
+    mx.mxgemm_set_option(h, mx.OPT_SHARED_KEYS, 1)
     lens, news = [700, 650, 600], [new] * 3
     m = made(lens, 2, 128, 16, 512)
     q = queries(m, 3 * new, 16)
@@ -204,6 +232,7 @@ def test_a_call_that_gives_up_leaves_nothing(new):
 def test_two_handles_on_two_streams(h):
     """The same batch on two streams at once, each with its handle: equal bits."""
     other = mx.mxgemm_create(0)
+    mx.mxgemm_set_option(other, mx.OPT_SHARED_KEYS, 1)
     m = made([3000] * 8, 2, 128, 64, 2560)
     q = queries(m, 8, 16).to(DEV)
     want, _ = attend(h, m, q, None, 2560)
