@@ -96,8 +96,8 @@ template <typename T, int D>
 int run_forward(mxg::RopeParams &p, cudaStream_t stream) {
   // as many blocks as the SMs hold, no more warps than steps
   using C = mxg::RopeCfg<T, D, false>;
-  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), 8), (sizeof(T) == 4 ? 3 : 4) * 152);
-  return mxg::launch(mxg::norm_rope_kernel<T, D>, dim3(static_cast<unsigned>(grid)), 256, C::SMEM_BYTES, 1, stream, p);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), C::WARPS), C::BLOCKS * 152);
+  return mxg::launch(mxg::norm_rope_kernel<T, D>, dim3(static_cast<unsigned>(grid)), 32 * C::WARPS, C::SMEM_BYTES, 1, stream, p);
 }
 
 template <typename T, int D>
@@ -107,7 +107,7 @@ int run_backward(mxgemm_handle_t h, const mxg::HandleView &v, mxg::RopeParams &p
   const int64_t all = count_steps<C>(p);
   int blocks = 0, rows = 0;
   for (mxg::RopeTensor &t : p.t) {
-    t.blocks = t.heads ? static_cast<int>(std::min(cdiv(p.tokens * t.steps, 8), std::max<int64_t>(1, (sizeof(T) == 4 ? 1 : 2) * v.sm_count * t.steps / all))) : 0;
+    t.blocks = t.heads ? static_cast<int>(std::min(cdiv(p.tokens * t.steps, C::WARPS), std::max<int64_t>(1, C::BLOCKS * v.sm_count * t.steps / all))) : 0;
     const int g = mxg::rope_group(t.blocks);
     blocks += t.blocks;
     rows += t.blocks + (t.blocks + g - 1) / g;
@@ -118,7 +118,7 @@ int run_backward(mxgemm_handle_t h, const mxg::HandleView &v, mxg::RopeParams &p
     p.partials = reinterpret_cast<float *>(ws);
     p.counters = v.counters;
   }
-  return mxg::launch(mxg::norm_rope_backward_kernel<T, D>, dim3(blocks), 256, C::SMEM_BYTES, 1, stream, p);
+  return mxg::launch(mxg::norm_rope_backward_kernel<T, D>, dim3(blocks), 32 * C::WARPS, C::SMEM_BYTES, 1, stream, p);
 }
 
 }  // namespace

@@ -18,7 +18,7 @@
 // rotated values and run s of the second), so that a rotation needs no exchange
 // between lanes.  All tokens' heads, four or eight at a time, are cut into equal
 // ranges for the warps, each of which works by itself: its lanes copy what they will
-// read themselves into a ring in shared memory, three steps ahead (cp.async: what is
+// read themselves into a ring in shared memory, some steps ahead (cp.async: what is
 // on its way takes no registers), and it computes a token's cosines and sines once
 // for all of that token's heads in its range.
 #pragma once
@@ -108,13 +108,16 @@ struct RopeCfg {
   static constexpr int LANES = D / 16, HEADS = 32 / LANES;  // lanes of a head, heads of a warp
   static constexpr int WORDS = sizeof(T) / 2;               // 16-byte words of a run
   static constexpr int PIECES = (BACK ? 4 : 2) * WORDS;     // words of a lane: dy and x, or x
-  static constexpr int STAGES = 4;
+  // Warps of a block, blocks of an SM, and loads of a warp on their way plus one.  The
+  // gradient's registers allow 16 warps without spills: 8192 tokens, 32/8 heads, 53 us
+  // so, 56 with four stages, 62 with two, 60 with 20 warps, 63 with 8.
+  static constexpr int WARPS = 8, BLOCKS = BACK ? (sizeof(T) == 4 ? 1 : 2) : sizeof(T) == 4 ? 3 : 4, STAGES = BACK ? 3 : 4;
   static constexpr int OFF_TURN = 0;                        // [D / 2] turns a position
   static constexpr int OFF_W = OFF_TURN + D / 2 * 8;        // [2][runs a, b][D / 2] weights
-  static constexpr int OFF_CS = OFF_W + 2 * D * 4;          // [8 warps][cosines, sines][D / 2]
-  static constexpr int OFF_POS = OFF_CS + 8 * D / 2 * 8;    // [8 warps][STAGES] positions
-  static constexpr int OFF_RING = OFF_POS + 8 * STAGES * 4;  // [8 warps][STAGES][PIECES][32 lanes]
-  static constexpr int SMEM_BYTES = OFF_RING + 8 * STAGES * PIECES * 512;
+  static constexpr int OFF_CS = OFF_W + 2 * D * 4;          // [warps][cosines, sines][D / 2]
+  static constexpr int OFF_POS = OFF_CS + WARPS * D / 2 * 8;  // [warps][STAGES] positions
+  static constexpr int OFF_RING = (OFF_POS + WARPS * STAGES * 4 + 15) / 16 * 16;  // [warps][STAGES][PIECES][32 lanes]
+  static constexpr int SMEM_BYTES = OFF_RING + WARPS * STAGES * PIECES * 512;
   static_assert(OFF_RING % 16 == 0, "alignment");
 };
 
@@ -332,8 +335,8 @@ struct RopeWalk {
 template <typename T, int D, bool BACK>
 __device__ __forceinline__ void rope_tables(const RopeParams &p, uint8_t *sm) {
   using C = RopeCfg<T, D, BACK>;
-  for (int j = threadIdx.x; j < p.rot >> 1; j += 256) reinterpret_cast<uint64_t *>(sm + C::OFF_TURN)[j] = turn_of(p.freqs[j]);
-  for (int i = threadIdx.x; i < 2 * D; i += 256) {
+  for (int j = threadIdx.x; j < p.rot >> 1; j += 32 * C::WARPS) reinterpret_cast<uint64_t *>(sm + C::OFF_TURN)[j] = turn_of(p.freqs[j]);
+  for (int i = threadIdx.x; i < 2 * D; i += 32 * C::WARPS) {
     // value e of run `run` of lane `sub`, of tensor i / D
     const int run = i / 8 % 2, sub = i % D / 16, e = i % 8;
     const Runs r = runs_of<D>(sub, p.rot);
@@ -346,12 +349,13 @@ __device__ __forceinline__ void rope_tables(const RopeParams &p, uint8_t *sm) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * RopeCfg<T, D, false>::WARPS, RopeCfg<T, D, false>::BLOCKS) norm_rope_kernel(const RopeParams p) {
   using C = RopeCfg<T, D, false>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   griddep_launch_dependents();
   griddep_wait();
-  RopeWalk<T, D, false> walk(p, smem_u32(rope_smem), static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * 8, 0);
+  RopeWalk<T, D, false> walk(p, smem_u32(rope_smem), static_cast<int64_t>(blockIdx.x) * C::WARPS + (threadIdx.x >> 5),
+                                static_cast<int64_t>(gridDim.x) * C::WARPS, 0);
   rope_tables<T, D, false>(p, rope_smem);
   __syncthreads();
   for (; walk.more(); walk.advance()) {
@@ -374,15 +378,15 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(
   }
 }
 
-// Sum of `rows` rows of D partials by 256 threads into `to`, in a fixed order.
+// Sum of `rows` rows of D partials by a block's first 256 threads into `to`, in a fixed order.
 template <int D>
 __device__ __forceinline__ void sum_rows(const float *from, int rows, float *to, float *part) {
   constexpr int PARTS = 256 / D;
   const int col = threadIdx.x % D, first = threadIdx.x / D;
   float s = 0.f;
 #pragma unroll 8
-  for (int i = first; i < rows; i += PARTS) s += __ldcg(from + static_cast<int64_t>(i) * D + col);
-  part[threadIdx.x] = s;
+  for (int i = first; i < rows && first < PARTS; i += PARTS) s += __ldcg(from + static_cast<int64_t>(i) * D + col);
+  if (first < PARTS) part[threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.x < D) {
     s = part[threadIdx.x];
@@ -399,16 +403,16 @@ __host__ __device__ constexpr int rope_group(int blocks) {
   return g;
 }
 
-// The gradient: blocks of eight warps that stay for further tokens.  dw is summed in registers over a thread's tokens and
+// The gradient: blocks that stay for further tokens.  dw is summed in registers over a thread's tokens and
 // heads, then over the block, and the blocks' sums are added by the block that
 // arrives last, first in groups and then over the groups: no float atomics, so that
 // equal calls give equal bits, and 25 rows to add at most where 608 would take one
 // block longer than the rest of the call.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) norm_rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * RopeCfg<T, D, true>::WARPS, RopeCfg<T, D, true>::BLOCKS) norm_rope_backward_kernel(const RopeParams p) {
   using C = RopeCfg<T, D, true>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
-  __shared__ float sums[8][D];
+  __shared__ float sums[C::WARPS][D];
   __shared__ int last;
   griddep_launch_dependents();
   griddep_wait();
@@ -416,7 +420,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) norm_rope_backwar
   const int which = static_cast<int>(blockIdx.x) < p.t[0].blocks ? 0 : 1;
   const RopeTensor &t = p.t[which];
   const int block = blockIdx.x - (which ? p.t[0].blocks : 0);
-  RopeWalk<T, D, true> walk(p, smem_u32(rope_smem), static_cast<int64_t>(block) * 8 + warp, static_cast<int64_t>(t.blocks) * 8, which);
+  RopeWalk<T, D, true> walk(p, smem_u32(rope_smem), static_cast<int64_t>(block) * C::WARPS + warp, static_cast<int64_t>(t.blocks) * C::WARPS,
+                               which);
   rope_tables<T, D, true>(p, rope_smem);
   __syncthreads();
   F8 da{}, db{};
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) norm_rope_backwar
   if (threadIdx.x < D) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += sums[w][threadIdx.x];
+    for (int w = 0; w < C::WARPS; ++w) s += sums[w][threadIdx.x];
     rows[static_cast<int64_t>(block) * D + threadIdx.x] = s;
   }
   // the last block of a group adds its rows, and the last group of the tensor the groups'
