@@ -470,12 +470,24 @@ def mxgemm_cache_attention_shared(h, cache: Cache, page_table, kv_len, shared, Q
     return st
 
 
+def _bfloat16(**tensors):
+    """The entry points that write BF16 through plain addresses: tensors of another type are refused."""
+    for name, t in tensors.items():
+        if getattr(t, "dtype", None) is not None and str(t.dtype) != "torch.bfloat16":
+            raise ValueError(f"{name}: bfloat16, not {t.dtype}")
+
+
 def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H, H_scale=None, act=ACT_SILU,
                               out_dtype=OUT_BF16, gate=None, up=None, stream=None, check: bool = True) -> int:
     """H = act(A.G) * (A.U) with the operands of mxgemm_run_block128 (both weights as the
     handle's OPT_B_MAJOR says): float32, bfloat16, or OUT_E4M3 codes with H_scale
     (M x ceil(N/128)), the operand of the next product.  gate and up (M x N bfloat16)
     receive A.G and A.U for mxgemm_gated_backward."""
+    if gate is not None or up is not None:
+        _bfloat16(gate=gate, up=up)
+    size = getattr(H, "element_size", None)
+    if size is not None and size() != {OUT_F32: 4, OUT_BF16: 2, OUT_E4M3: 1}.get(out_dtype):
+        raise ValueError("H: of out_dtype (codes of one byte for OUT_E4M3)")
     st = library().mxgemm_run_gated_block128(h, int(M), int(N), int(K), _ptr(A), _ptr(A_scale), _ptr(G), _ptr(G_scale),
                                              _ptr(U), _ptr(U_scale), int(act), _ptr(H), _ptr(H_scale), int(out_dtype),
                                              _ptr(gate), _ptr(up), _stream(stream))
@@ -493,6 +505,7 @@ def mxgemm_gated_backward(gate, up, dH, R, C, dgate=None, dup=None, dgate_rows=N
     left out."""
     if x_dtype is None:
         x_dtype = _in_dtype(dH)
+    _bfloat16(gate=gate, up=up, dgate=dgate, dup=dup)
     pairs = [p if p is not None else (None, None) for p in (dgate_rows, dup_rows, dgate_cols, dup_cols, hidden_cols)]
     out = _GRADS_STRUCT.pack(*(_ptr(x) or 0 for x in (dgate, dup, *(y for p in pairs for y in p))))
     st = library().mxgemm_gated_backward(_ptr(gate), _ptr(up), _ptr(dH), int(x_dtype), int(R), int(C), int(act), out,

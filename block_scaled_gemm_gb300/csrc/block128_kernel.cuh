@@ -683,31 +683,31 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
         }
       };
       if constexpr (kGated) {
-        // acc: 64 values of the gate, then 64 of the other product
-        if (p.gate && row0 < p.M && col0 < p.N) {
+        // acc: 64 values of the gate, then 64 of the other product.  The gate is on its
+        // way out while the activation is computed, the other product while the rows'
+        // largest values are exchanged.
+        const bool keep = p.gate && row0 < p.M && col0 < p.N;
+        auto keep_half = [&](int c) {
           if (p.tma_keep) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (lane == 0) bulk_wait_read_all();
-              __syncwarp();
-              stage_bf16(c);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_2d(c ? &tm.up : &tm.gate, stg, col0, row0);
-                bulk_commit_group();
-              }
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+            stage_bf16(c);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(c ? &tm.up : &tm.gate, stg, col0, row0);
+              bulk_commit_group();
             }
           } else {
             if (lane == 0) bulk_wait_read_all();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int h = 0; h < 2; ++h) {
               __syncwarp();
-              stage_f32(c);
+              stage_f32(2 * c + h);
               __syncwarp();
-              const int col = col0 + (c & 1) * 32 + lane, rows = min(32, p.M - row0);
+              const int col = col0 + h * 32 + lane, rows = min(32, p.M - row0);
               const float *from = reinterpret_cast<const float *>(sm + (stg - base));
-              __nv_bfloat16 *to = c < 2 ? p.gate : p.up;
+              __nv_bfloat16 *to = c ? p.up : p.gate;
               if (col < p.N)
                 for (int r = 0; r < rows; ++r)
                   to[static_cast<int64_t>(row0 + r) * p.N + col] =
@@ -715,9 +715,11 @@ __global__ void __launch_bounds__(PairCfg<V>::THREADS, 1)
             }
             __syncwarp();
           }
-        }
+        };
+        if (keep) keep_half(0);
 #pragma unroll
         for (int j = 0; j < 64; ++j) acc[j] = gated(acc[j], acc[64 + j], p.act);
+        if (keep) keep_half(1);
       }
       if constexpr (kCodes) {
         float top = 0.f;

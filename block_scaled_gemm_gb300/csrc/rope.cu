@@ -34,7 +34,7 @@ int tensor_args(const mxgemm_heads_t *a, int64_t tokens, int64_t head_dim, int w
   if ((need_x && !a->x) || !a->out || (back && !a->dy)) return MXGEMM_ERR_INVALID_VALUE;
   const size_t w_al = w_dtype == MXGEMM_IN_F32 ? 4 : 2;
   if ((need_x && (!aligned(a->x, 16) || a->x_pitch % 8 != 0)) || !aligned(a->out, 16) || a->out_pitch % 8 != 0 ||
-      (back && (!aligned(a->dy, 16) || a->dy_pitch % 8 != 0)) || (a->weight && !aligned(a->weight, 8 * w_al)) ||
+      (back && (!aligned(a->dy, 16) || a->dy_pitch % 8 != 0)) || (a->weight && !aligned(a->weight, w_al)) ||
       !aligned(a->dweight, 4))
     return MXGEMM_ERR_MISALIGNED;
   t->x = need_x ? a->x : nullptr;

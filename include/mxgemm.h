@@ -491,7 +491,8 @@ typedef enum {
  *   H    : M x N: MXGEMM_OUT_F32, MXGEMM_OUT_BF16 (H_scale NULL), or
  *          MXGEMM_OUT_E4M3: codes with H_scale M x ceil(N/128) float, as
  *          mxgemm_quantize_block128 makes them by MXGEMM_BLOCK_ROWS (the operand
- *          of the down-projection).
+ *          of the down-projection; E4M3 whatever the operands' formats are).
+ *          g, u and H must be finite then.
  *   gate, up : M x N bfloat16 that receive g and u for mxgemm_gated_backward, or
  *          both NULL.
  * Alignment, ranges of the scales, formats and options as for
@@ -574,8 +575,7 @@ typedef struct {
  * 2^31, heads < 65536.  FP32 throughout, rounded once; the angles are exact to
  * 2^-24 of half a turn at any position (the frequencies' products with positions are
  * reduced in 64 bits).  mean x^2 is to be in FP32's range.  x, dy and out 16-byte
- * aligned with pitches that are multiples of 8, weights aligned to 8 of their
- * elements (MXGEMM_ERR_MISALIGNED).  Runs on the current device, needs no handle and
+ * aligned with pitches that are multiples of 8 (MXGEMM_ERR_MISALIGNED).  Runs on the current device, needs no handle and
  * allocates nothing; errors as for mxgemm_quantize. */
 int mxgemm_norm_rope(const mxgemm_heads_t *q, const mxgemm_heads_t *k, int64_t tokens,
                      int64_t head_dim, int x_dtype, int w_dtype, float eps,

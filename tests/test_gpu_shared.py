@@ -178,6 +178,30 @@ def test_rows_of_padding(h):
     assert mx.mxgemm_get_device_status(h) == (0, 0)
 
 
+@pytest.mark.parametrize("new", [1, 3])
+def test_more_shared_tokens_than_any_sequence_has(h, new):
+    """All sequences within the shared tokens: nothing of their own is left, and a
+    length past all of them is no longer than the table."""
+    m = made([200, 130, 64], 2, 128, 16, 10 ** 6)
+    q = queries(m, 3 * new, 8)
+    for shared in (208, 10 ** 6, 2 ** 40):
+        O, L = attend(h, m, q, [new] * 3, shared)
+        check(m, q, [new] * 3, O, L)
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
+
+
+def test_refusals(h):
+    m = made([64, 64], 1, 64, 16, 32)
+    cache, table, lens = m.cache(), m.table_tensor(), torch.tensor([64, 64], dtype=torch.int32, device=DEV)
+    q = queries(m, 2, 3).to(DEV)
+    O = torch.empty_like(q)
+    call = lambda shared, **kw: mx.mxgemm_cache_attention_shared(h, cache, table, lens, shared, q, O, check=False, **kw)  # noqa: E731
+    assert call(-1) == mx.ERR_INVALID_VALUE
+    assert call(32, scale=math.nan) == mx.ERR_INVALID_VALUE
+    assert call(32) == mx.OK
+    torch.cuda.synchronize()
+
+
 def test_rows_behind_the_last_sequence_stay(h):
     m = made([200, 190], 1, 128, 16, 128)
     q = queries(m, 6, 4)

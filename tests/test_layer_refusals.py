@@ -38,6 +38,21 @@ def test_gated_backward_refuses():
             grads(x=dtype, dgate=bf)
 
 
+def test_gated_binding_refuses():
+    f, b, c = torch.zeros(16, 16), torch.zeros(16, 16, dtype=torch.bfloat16), torch.zeros(16, 16, dtype=torch.uint8)
+    call = lambda H, **kw: mx.mxgemm_run_gated_block128(None, 16, 16, 16, c, f, c, f, c, f, H, check=False, **kw)  # noqa: E731
+    for H, out in ((b, mx.OUT_F32), (f, mx.OUT_BF16), (b, mx.OUT_E4M3), (c, mx.OUT_BF16), (b, 7)):
+        with pytest.raises(ValueError):
+            call(H, out_dtype=out)
+    for kw in (dict(gate=f, up=b), dict(gate=b, up=c), dict(gate=b.half(), up=b)):
+        with pytest.raises(ValueError):
+            call(b, **kw)
+    assert call(b, gate=b, up=b) == call(c, out_dtype=mx.OUT_E4M3, H_scale=f) == mx.ERR_INVALID_VALUE  # no handle
+    for wrong in (dict(gate=f, up=b, dgate=b), dict(gate=b, up=b.half(), dgate=b), dict(gate=b, up=b, dgate=f), dict(gate=b, up=b, dup=c)):
+        with pytest.raises(ValueError):
+            mx.mxgemm_gated_backward(wrong.pop("gate"), wrong.pop("up"), b, 16, 16, check=False, **wrong)
+
+
 def rope(q=None, k=None, **kw):
     q = torch.zeros(3, 2, 64) if q is None else q
     return mx.mxgemm_norm_rope(q, k, torch.zeros(q.shape, dtype=q.dtype), None if k is None else torch.zeros_like(k), check=False, **kw)
