@@ -29,6 +29,10 @@
 // first codes arrive 3 us after the start).  The warps' chains of dependent
 // instructions bound it: issue slots are used to 46 %.
 //
+// Behind shared tokens (kOwnKeys) the ranges are of warps and not of CTAs, and what they
+// leave is added by the launch that joins: 64 sequences of 100-982 own keys, 64/8 heads,
+// 22-24 us where all keys by ranges of CTAs take 36.
+//
 // Work: an item is one sequence, key/value head and ROWS query rows; all
 // items' tiles, laid end to end, are cut into equal ranges, one per CTA, or,
 // where items are few, each one's into parts for CTAs of its own.  An item

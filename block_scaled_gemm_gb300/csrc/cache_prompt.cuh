@@ -31,6 +31,11 @@
 // them, each one's keys are cut into parts for several CTAs; they leave FP32
 // partials in the workspace, and the one that arrives last adds them in order.
 //
+// Shared tokens' keys (kSharedKeys): the rows of all sequences together, each cut for
+// as many CTAs as the SMs allow, which leave partials for the launch that joins.  512
+// rows of 8 key/value heads over 8192 keys, eight tiles a CTA: 27 us, of which 2.3 are
+// set-up, 4 until the first scores and 4 the first tile's softmax (0.9 later).
+//
 // Warps (512 threads): 0 TMA loads of the pages' codes, and the scales;
 // 1 MMAs; 4-7 convert codes to FP16 in the MMA's layout (128-byte swizzle);
 // 8-11 and 12-15 the softmax of the two Q tiles.

@@ -11,6 +11,12 @@
 // of 128 x 128, computes the three values once, keeps them in registers until its
 // rows' and its columns' largest are known, and stores the columns' codes through
 // shared memory.
+//
+// Measured: 4096 x 28672, BF16 dH, to five quantized operands 240 us (5.4 TB/s, 0.79 of
+// the measured copy rate; with one tile a block and its loads in registers 501 us, with
+// scalar operations and a division for each row by all lanes 321 us): issue slots are
+// used to half, and loads wait while a tile's values are formed.  1741 x 7000, FP32 dH,
+// to BF16 17.9 us with inputs in L2.
 #pragma once
 #include "gated_math.cuh"
 #include "quantize128.cuh"

@@ -11,6 +11,12 @@
 // partials in the workspace, and the CTA that arrives last adds them, in order, and
 // finishes it: nobody waits for another CTA.
 //
+// Measured: 16 x 28672 x 8192 to codes 79 us on the same buffers again and again and
+// 83 us with others each time (5.9 and 5.7 TB/s, 0.87 and 0.83 of the measured copy
+// rate), 1 x 4096 x 4096 10.8 us with the weights in L2, 64 x 8192 x 8192 39 us.  The
+// rest is the start (3-4 us before the first loads land) and, where column blocks are
+// shared by several CTAs, their join (some 3 us).
+//
 // Waits are bounded as in the other kernels.  The epilogue's warps go on to the end
 // after a wait that gave up, without waiting again: their barrier and the arrivals
 // at shared column blocks stay whole, and the counters are left at zero.

@@ -21,6 +21,13 @@
 // read themselves into a ring in shared memory, some steps ahead (cp.async: what is
 // on its way takes no registers), and it computes a token's cosines and sines once
 // for all of that token's heads in its range.
+//
+// Measured: 8192 tokens, 32/8 heads of 128 in BF16, half of each rotated: 29.3 us (5.7
+// TB/s, 0.84 of the measured copy rate; with blocks of tokens and their loads in
+// registers 40 us, ranges of a tensor's parity 46, halves of sectors where values
+// pass 35); 64 tokens 3.4 us.  The gradient, all of each head rotated: 53 us (4.7 TB/s;
+// 105 us with loads in registers), bound by issue slots and dependent
+// instructions at the 16 warps an SM that its registers allow.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
