@@ -257,7 +257,8 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   p.left_tiles = static_cast<int>((p.b.tokens * p.group + S::ROWS - 1) / S::ROWS);
   const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
   const SharedPlan plan = plan_shared(items, (p.shared + S::KT - 1) / S::KT, v.sm_count);
-  if (!v.shared_keys && plan.us > apart_us<D>(v, p)) {
+  // (four more for the launches that share what one does otherwise)
+  if (!v.shared_keys && plan.us + 4 > apart_us<D>(v, p)) {
     p.shared = 0;
     return run_attention<D>(h, v, p, stream);
   }

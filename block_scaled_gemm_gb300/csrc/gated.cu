@@ -23,7 +23,25 @@ using mxg::cdiv;
 using mxg::encode;
 using mxg::kLim;
 
-// M <= 64 by one CTA an SM, its range of the steps four at least.
+// CTAs for each column block where those are fewer than the SMs, in us: a K block takes
+// 0.3, a join 3 and its sums 0.25 for each part, or 0.8 with 32 rows a warp.
+int block_parts(int64_t blocks, int64_t kb, int64_t sms, double each) {
+  int best = 1;
+  double least = 0.3 * static_cast<double>(kb);
+  for (int64_t n = 2; n * blocks <= sms && n <= kb; ++n) {
+    const double us = 0.3 * static_cast<double>(cdiv(kb, n)) + 3 + each * static_cast<double>(n);
+    if (us < least) {
+      least = us;
+      best = static_cast<int>(n);
+    }
+  }
+  return best;
+}
+
+// M <= 64 by one CTA an SM at most.  Fewer column blocks than SMs: each is cut into
+// whole CTAs' parts, so that no CTA ends two blocks' parts (30 x 4096 x 4096 19.5 -> 14
+// us with 128 CTAs of eight K blocks and not 152 of six or seven).  More: all K blocks
+// are cut into equal ranges (224 blocks on 152 SMs would take two rounds).
 template <int NT, bool KM>
 int run_skinny(mxgemm_handle_t h, const mxg::HandleView &v, mxg::GatedSkinnyParams &gp, const void *A, const void *G, const void *U,
                cudaStream_t stream) {
@@ -34,7 +52,8 @@ int run_skinny(mxgemm_handle_t h, const mxg::HandleView &v, mxg::GatedSkinnyPara
   p.idesc_fmt = mxg::fmt_bits(v.b_fmt, v.a_fmt);
   gp.n_tiles = static_cast<int>(cdiv(p.N, 128));
   gp.total = static_cast<int64_t>(gp.n_tiles) * p.kb;
-  const int grid = static_cast<int>(std::min<int64_t>(std::min(v.sm_count, mxg::kCounters), std::max<int64_t>(1, gp.total / 4)));
+  const int sms = std::min(v.sm_count, mxg::kCounters);
+  const int grid = gp.n_tiles <= sms ? gp.n_tiles * block_parts(gp.n_tiles, p.kb, sms, S::ROWS >= 32 ? 0.8 : 0.25) : sms;
   uint8_t *ws = nullptr;
   if (int st = mxg::handle_workspace(h, static_cast<size_t>(grid) * 2 * S::PARTIAL * sizeof(float), stream, &ws)) return st;
   gp.partials = reinterpret_cast<float *>(ws);
