@@ -7,9 +7,12 @@
 // as its N.  A step of the ring is one K block of one column block: 16 KB of each
 // weight and A's rows.  All steps of all column blocks, laid end to end, are cut
 // into equal ranges, one for each CTA, so that no SM waits for a last wave and the
-// loads go on across column blocks.  A column block that spans CTAs leaves FP32
-// partials in the workspace, and the CTA that arrives last adds them, in order, and
-// finishes it: nobody waits for another CTA.
+// loads go on across column blocks.  A CTA leaves its FP32 sums of a column block in the
+// workspace, and the one that arrives last there adds them, in order, and finishes
+// the block: nobody waits for another CTA.  It does so from the workspace, also where
+// the block is its own alone, with a warp for each row: sums lie in registers by
+// columns, and the end of a block from there (64 rows: 32 values of each of two sums a
+// thread, in code that runs once) took 5 us, a row's largest value a reduction each.
 //
 // Measured: 16 x 28672 x 8192 to codes 79 us on the same buffers again and again and
 // 83 us with others each time (5.9 and 5.7 TB/s, 0.87 and 0.83 of the measured copy
@@ -29,7 +32,7 @@ struct GatedSkinnyParams {
   B128Params b;
   int n_tiles;
   int64_t total;       // steps: column blocks x K blocks
-  float *partials;     // two slots a CTA: [sets][2][ROWS / 4][128 columns] of four
+  float *partials;     // two slots a CTA: [2][NT rows][128 columns]
   unsigned *counters;  // of the CTA with a shared column block's first step
   int h_type;          // mxgemm_out_dtype_t
 };
@@ -41,16 +44,11 @@ struct GatedSkinnyCfg {
   static constexpr int STAGES = NT <= 32 ? 6 : 5;
   static constexpr int BUFS = 4;  // accumulators, each of both products
   // Epilogue warps: four for the 128 columns, and from 32 rows on two sets of them
-  // with half the rows each (one set: 64 x 8192 x 8192 78 us, most of it in the
-  // sums of parts and the end of column blocks).
+  // with half the rows each.
   static constexpr int SETS = NT >= 32 ? 2 : 1, ROWS = NT / SETS, EPI_WARPS = 4 * SETS;
-  static constexpr int PARTS = ROWS >= 32 ? 1 : 4;  // whose loads are on their way at a time when parts are added
   // scales of A, for each epilogue warp [2 groups][4 steps][ROWS]
   static constexpr int OFF_CS = STAGES * STAGE;
-  // codes: rows' largest values, [2][4 warps of columns][NT], and their reciprocals [2][NT]
-  static constexpr int OFF_TOP = OFF_CS + EPI_WARPS * 2 * 4 * ROWS * 4;
-  static constexpr int OFF_INV = OFF_TOP + 2 * 4 * NT * 4;
-  static constexpr int OFF_BAR = OFF_INV + 2 * NT * 4;
+  static constexpr int OFF_BAR = OFF_CS + EPI_WARPS * 2 * 4 * ROWS * 4;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -60,6 +58,108 @@ struct GatedSkinnyCfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(STAGE % 1024 == 0 && OFF_BAR % 8 == 0 && TM_COLS <= 512, "layout");
 };
+
+// The end of a column block: rows warp, warp + EPI_WARPS, ... by this warp, a lane four
+// columns, from the parts of CTAs c0 .. c1.  Four rows' loads of two parts at a time.
+template <int NT, typename Slot>
+__device__ __forceinline__ void gated_skinny_rows(const GatedSkinnyParams &gp, Slot slot, int64_t c0, int64_t c1, int tile, int warp, int lane) {
+  constexpr int kStep = GatedSkinnyCfg<NT>::EPI_WARPS, kRows = 4, kParts = 2;
+  const B128Params &p = gp.b;
+  const int col = tile * 128 + 4 * lane, there = p.N - col;  // columns from here on (0 or fewer: none)
+  const bool whole = there >= 4 && p.N % 4 == 0;              // four, and aligned
+#pragma unroll 1
+  for (int r0 = warp; r0 < p.M; r0 += kRows * kStep) {
+    float4 s[kRows][2];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s[i][0] = s[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int64_t c = c0; c <= c1; c += kParts) {
+      float4 o[kParts][kRows][2];
+#pragma unroll
+      for (int n = 0; n < kParts; ++n)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int r = r0 + i * kStep;
+            o[n][i][w] = c + n <= c1 && r < p.M ? __ldcg(reinterpret_cast<const float4 *>(slot(c + n) + (w * NT + r) * 128) + lane)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+      for (int n = 0; n < kParts; ++n)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            s[i][w].x += o[n][i][w].x;
+            s[i][w].y += o[n][i][w].y;
+            s[i][w].z += o[n][i][w].z;
+            s[i][w].w += o[n][i][w].w;
+          }
+    }
+    auto pack = [](float a, float b) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      return *reinterpret_cast<const uint32_t *>(&h);
+    };
+    auto store_bf16 = [&](__nv_bfloat16 *to, float4 v) {
+      if (whole) {
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
+      } else {
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < there) to[e] = __float2bfloat16_rn(x[e]);
+      }
+    };
+    // (step by step for all rows together: one row after the other takes 0.32 us each)
+    float4 h[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float4 g = s[i][0], u = s[i][1];
+      h[i] = make_float4(gated(g.x, u.x, p.act), gated(g.y, u.y, p.act), gated(g.z, u.z, p.act), gated(g.w, u.w, p.act));
+    }
+    float top[kRows], inv[kRows];
+    if (gp.h_type == 2) {  // MXGEMM_OUT_E4M3 (columns past the last are 0)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float most = fmaxf(fmaxf(fabsf(h[i].x), fabsf(h[i].y)), fmaxf(fabsf(h[i].z), fabsf(h[i].w)));
+        top[i] = fmaxf(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most))), kQ128Least);
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) inv[i] = __fdiv_rn(448.0f, top[i]);
+      if (lane < kRows && r0 + lane * kStep < p.M) {
+        float mine = top[0];
+#pragma unroll
+        for (int i = 1; i < kRows; ++i) mine = lane == i ? top[i] : mine;
+        p.h_scale[static_cast<int64_t>(r0 + lane * kStep) * p.bs_cols + tile] = __fdiv_rn(mine, 448.0f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = r0 + i * kStep;
+      if (r >= p.M) continue;
+      const int64_t at = static_cast<int64_t>(r) * p.N + col;
+      if (p.gate) {
+        store_bf16(p.gate + at, s[i][0]);
+        store_bf16(p.up + at, s[i][1]);
+      }
+      if (gp.h_type == 2) {
+        if (there > 0)
+          *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.C) + at) =
+              mx_e4m3x2(h[i].x * inv[i], h[i].y * inv[i]) | (mx_e4m3x2(h[i].z * inv[i], h[i].w * inv[i]) << 16);
+      } else if (gp.h_type == 1) {
+        store_bf16(static_cast<__nv_bfloat16 *>(p.C) + at, h[i]);
+      } else if (whole) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = h[i];
+      } else {
+        const float x[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < there) static_cast<float *>(p.C)[at + e] = x[e];
+      }
+    }
+  }
+}
 
 template <int NT, bool kKM>
 __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
@@ -198,7 +298,6 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
     const int rows = min(ROWS, p.M - row0);                   // that there are (0 or fewer: none)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + row0;
     float *cs = reinterpret_cast<float *>(sm + S::OFF_CS) + (warp - 2) * 8 * ROWS;
-    float *tops = reinterpret_cast<float *>(sm + S::OFF_TOP), *invs = reinterpret_cast<float *>(sm + S::OFF_INV);
     auto all_warps = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * S::EPI_WARPS) : "memory"); };  // of the epilogue
     float acc[2][ROWS];
 #pragma unroll
@@ -234,7 +333,7 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
     };
     fetch();
     bool have = true;
-    int tile = tile0, k = k0, begin = k0, ends = 0;
+    int tile = tile0, k = k0, begin = k0;
     for (int i = 0; i < steps; ++i) {
       if ((i & 3) == 0) {
         sb = nb;
@@ -275,21 +374,24 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
       if (++k < kb && i + 1 < steps) continue;
       // -------------------------------------------------------- the end of this
       // CTA's part [begin, k) of the column block
-      bool finish = true;
-      if (begin > 0 || k < kb) {
+      const bool split = begin > 0 || k < kb;
+      int64_t c0 = blockIdx.x, c1 = blockIdx.x;  // the CTAs that share the block
+      if (split) {
         const int64_t first = static_cast<int64_t>(tile) * kb, end = first + kb;
-        const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = (end * ctas - 1) / total;  // the CTAs that share it
-        auto slot = [&](int64_t c) {
-          return reinterpret_cast<float4 *>(gp.partials + (2 * c + (c == c0)) * S::PARTIAL) + set * (ROWS / 2) * 128 + n;
-        };
-        float4 *to = slot(blockIdx.x);
+        c0 = ((first + 1) * ctas - 1) / total;
+        c1 = (end * ctas - 1) / total;
+      }
+      auto slot = [&](int64_t c) { return gp.partials + (2 * c + (c == c0)) * S::PARTIAL; };
+      float *to = slot(blockIdx.x) + row0 * 128 + n;
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int j = 0; j < ROWS / 4; ++j)
-            if (4 * j < rows) to[(w * (ROWS / 4) + j) * 128] = make_float4(acc[w][4 * j], acc[w][4 * j + 1], acc[w][4 * j + 2], acc[w][4 * j + 3]);
-        __threadfence();
-        all_warps();
+        for (int m = 0; m < ROWS; ++m)
+          if (m < rows) to[(w * NT + m) * 128] = acc[w][m];
+      if (split) __threadfence();
+      all_warps();
+      bool finish = true;
+      if (split) {
         if (threadIdx.x == 64) {
           const bool mine = atomicAdd(gp.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
           if (mine) gp.counters[c0] = 0;  // for the next launch
@@ -297,79 +399,10 @@ __global__ void __launch_bounds__(GatedSkinnyCfg<NT>::THREADS, 1)
         }
         all_warps();
         finish = *last != 0;
-        if (finish) {
-          __threadfence();
-#pragma unroll
-          for (int m = 0; m < ROWS; ++m) acc[0][m] = acc[1][m] = 0.f;
-#pragma unroll 1
-          for (int64_t c = c0; c <= c1; c += S::PARTS) {
-            float4 o[S::PARTS][2][ROWS / 4];
-#pragma unroll
-            for (int i = 0; i < S::PARTS; ++i)
-#pragma unroll
-              for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int j = 0; j < ROWS / 4; ++j)
-                  o[i][w][j] = c + i <= c1 && 4 * j < rows ? __ldcg(slot(c + i) + (w * (ROWS / 4) + j) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < S::PARTS; ++i)
-#pragma unroll
-              for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int j = 0; j < ROWS / 4; ++j) {
-                  acc[w][4 * j] += o[i][w][j].x;
-                  acc[w][4 * j + 1] += o[i][w][j].y;
-                  acc[w][4 * j + 2] += o[i][w][j].z;
-                  acc[w][4 * j + 3] += o[i][w][j].w;
-                }
-          }
-        }
+        if (finish) __threadfence();
       }
-      if (finish) {
-        const int col = tile * 128 + n;
-        const bool live = col < p.N && have;
-        if (p.gate && live) {
-#pragma unroll
-          for (int m = 0; m < ROWS; ++m)
-            if (m < rows) {
-              p.gate[static_cast<int64_t>(row0 + m) * p.N + col] = __float2bfloat16_rn(acc[0][m]);
-              p.up[static_cast<int64_t>(row0 + m) * p.N + col] = __float2bfloat16_rn(acc[1][m]);
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < ROWS; ++m)
-          if (m < rows) acc[0][m] = gated(acc[0][m], acc[1][m], p.act);
-        if (gp.h_type == 2) {  // MXGEMM_OUT_E4M3
-          float *mine = tops + (ends & 1) * 4 * NT, *inv = invs + (ends & 1) * NT;
-#pragma unroll
-          for (int m = 0; m < ROWS; ++m)
-            if (m < rows) {
-              const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(acc[0][m])));
-              if (lane == m) mine[q * NT + row0 + m] = __uint_as_float(t);
-            }
-          all_warps();
-          const int row = threadIdx.x - 64;
-          if (row < p.M) {
-            const float t = fmaxf(fmaxf(fmaxf(mine[row], mine[NT + row]), fmaxf(mine[2 * NT + row], mine[3 * NT + row])), kQ128Least);
-            inv[row] = __fdiv_rn(448.0f, t);
-            if (have) p.h_scale[static_cast<int64_t>(row) * p.bs_cols + tile] = __fdiv_rn(t, 448.0f);
-          }
-          all_warps();
-#pragma unroll
-          for (int m = 0; m < ROWS; ++m)
-            if (m < rows && live)
-              static_cast<uint8_t *>(p.C)[static_cast<int64_t>(row0 + m) * p.N + col] = static_cast<uint8_t>(mx_e4m3(acc[0][m] * inv[row0 + m]));
-          ++ends;
-        } else if (live) {
-#pragma unroll
-          for (int m = 0; m < ROWS; ++m)
-            if (m < rows) {
-              const int64_t at = static_cast<int64_t>(row0 + m) * p.N + col;
-              if (gp.h_type == 1) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(acc[0][m]);
-              else static_cast<float *>(p.C)[at] = acc[0][m];
-            }
-        }
-      }
+      if (finish && have) gated_skinny_rows<NT>(gp, slot, c0, c1, tile, warp - 2, lane);
+      all_warps();  // the slot has been read
 #pragma unroll
       for (int m = 0; m < ROWS; ++m) acc[0][m] = acc[1][m] = 0.f;
       ++tile;
