@@ -573,8 +573,10 @@ def _rope(positions, freqs, interleaved, factor, tokens):
 def _rope_call(name, handle, q, k, positions, freqs, interleaved, factor, eps, stream, check):
     """q and k: (values, result, weight, dy, dweight) each, k's result None for none."""
     y = q[1]
-    if y.dim() != 3:
+    if y is None or y.dim() != 3:
         raise ValueError("q: tokens x heads x head dim")
+    if k[1] is None and (k[0] is not None or k[3] is not None or k[4] is not None):
+        raise ValueError("k: without a result nothing of it would be computed")
     tokens, _, d = y.shape
     dtype = y.dtype
     types = _type_codes()

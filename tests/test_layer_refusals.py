@@ -102,6 +102,18 @@ def test_rope_binding_refuses():
         mx.mxgemm_norm_rope_backward(None, q, None, q.clone(), None, q=q, dq_weight=torch.ones(64))
 
 
+def test_keys_without_a_result_are_refused():
+    q, k, w = torch.zeros(3, 2, 64), torch.zeros(3, 1, 64), torch.ones(64)
+    for args, kw in (((q, k, q, None), {}), ((q, None, None, None), {})):
+        with pytest.raises(ValueError):
+            mx.mxgemm_norm_rope(*args, **kw)
+    for args, kw in (((q, k, q, None), {}), ((q, None, q, None), dict(k=k)), ((q, None, q, None), dict(dk_weight=w)), ((q, None, None, None), {})):
+        with pytest.raises(ValueError):
+            mx.mxgemm_norm_rope_backward(None, *args, **kw)
+    # a weight alone asks for nothing
+    assert mx.mxgemm_norm_rope(q[:0], None, q[:0], None, k_weight=w) == mx.OK
+
+
 def test_handles_are_needed():
     q = torch.zeros(3, 2, 64)
     assert mx.mxgemm_norm_rope_backward(None, q, None, q.clone(), None, check=False) == mx.ERR_INVALID_VALUE
