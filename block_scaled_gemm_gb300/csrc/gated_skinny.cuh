@@ -5,20 +5,22 @@
 // Bound by reading both weights once.  Transposed, as the single product's kernel
 // for few rows: 128 columns of a weight on the MMA's 128-row side and the rows of A
 // as its N.  A step of the ring is one K block of one column block: 16 KB of each
-// weight and A's rows.  All steps of all column blocks, laid end to end, are cut
-// into equal ranges, one for each CTA, so that no SM waits for a last wave and the
-// loads go on across column blocks.  A CTA leaves its FP32 sums of a column block in the
-// workspace, and the one that arrives last there adds them, in order, and finishes
-// the block: nobody waits for another CTA.  It does so from the workspace, also where
+// weight and A's rows.  More column blocks than SMs: all their steps, laid end to end,
+// are cut into equal ranges, one for each CTA, so that no SM waits for a last wave and
+// the loads go on across column blocks.  Fewer: each is cut into whole CTAs' parts.  A
+// CTA leaves its FP32 sums of a column block in the workspace, and the one that arrives
+// last there adds them, in order, and finishes the block: nobody waits for another CTA.
+// It does so from the workspace, also where
 // the block is its own alone, with a warp for each row: sums lie in registers by
 // columns, and the end of a block from there (64 rows: 32 values of each of two sums a
 // thread, in code that runs once) took 5 us, a row's largest value a reduction each.
 //
-// Measured: 16 x 28672 x 8192 to codes 79 us on the same buffers again and again and
-// 83 us with others each time (5.9 and 5.7 TB/s, 0.87 and 0.83 of the measured copy
-// rate), 1 x 4096 x 4096 10.8 us with the weights in L2, 64 x 8192 x 8192 39 us.  The
+// Measured: 16 x 28672 x 8192 to codes 80.5 us on the same buffers again and again and
+// 82 us with others each time (5.8 and 5.7 TB/s, 0.86 and 0.84 of the measured copy
+// rate), 1 x 4096 x 4096 10 us with the weights in L2, 64 x 8192 x 8192 38 us.  The
 // rest is the start (3-4 us before the first loads land) and, where column blocks are
-// shared by several CTAs, their join (some 3 us).
+// shared by several CTAs, their join (some 3 us: sums to L2 1, counted 1, read and
+// added 1, and the rows).
 //
 // Waits are bounded as in the other kernels.  The epilogue's warps go on to the end
 // after a wait that gave up, without waiting again: their barrier and the arrivals
