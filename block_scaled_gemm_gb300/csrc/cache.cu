@@ -149,7 +149,8 @@ int64_t plan_prompt(const mxg::HandleView &v, mxg::AttnParams &p) {
 template <int D, int MODE>
 int launch_prompt(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::PromptCfg<D>;
-  const int grid = p.whole + (p.items - p.whole) * p.parts;
+  // (behind shared tokens one CTA more waits for the launch over the shared keys)
+  const int grid = p.whole + (p.items - p.whole) * p.parts + (MODE == mxg::kOwnKeys ? 1 : 0);
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, p.c.page_size, false, &tK, &tV)) return st;
   return mxg::launch(mxg::cache_prompt_kernel<D, MODE>, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, 1, stream,
@@ -157,22 +158,22 @@ int launch_prompt(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t str
 }
 
 template <int D, int NT>
-int decode_grid(const mxg::HandleView &v) {
-  return std::min(mxg::DecodeCfg<D, NT>::CTAS * v.sm_count, mxg::kCounters / 4);
+int decode_grid(int sms) {
+  return std::min(mxg::DecodeCfg<D, NT>::CTAS * sms, mxg::kCounters / 4);
 }
 template <int D, int NT>
-int64_t decode_bytes(const mxg::HandleView &v, const mxg::AttnParams &p) {
+int64_t decode_bytes(const mxg::AttnParams &p, int sms) {
   // two slots a CTA, or, behind shared tokens, a warp
-  return static_cast<int64_t>(decode_grid<D, NT>(v)) * (p.shared ? 8 : 2) * mxg::DecodeCfg<D, NT>::PARTIAL * sizeof(float);
+  return static_cast<int64_t>(decode_grid<D, NT>(sms)) * (p.shared ? 8 : 2) * mxg::DecodeCfg<D, NT>::PARTIAL * sizeof(float);
 }
 
 template <int D, int NT, int MODE>
-int launch_decode(const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
+int launch_decode(const mxg::HandleView &v, mxg::AttnParams &p, int sms, cudaStream_t stream) {
   using S = mxg::DecodeCfg<D, NT>;
   CUtensorMap tK, tV;
   if (int st = encode_cache(v, p.c, D, std::min(p.c.page_size, 32), true, &tK, &tV)) return st;
-  return mxg::launch(mxg::cache_decode_kernel<D, NT, MODE>, dim3(static_cast<unsigned>(decode_grid<D, NT>(v))), 128, S::SMEM_BYTES, 1,
-                     stream, tK, tV, p);
+  const int grid = decode_grid<D, NT>(sms) + (MODE == mxg::kOwnKeys ? 1 : 0);
+  return mxg::launch(mxg::cache_decode_kernel<D, NT, MODE>, dim3(static_cast<unsigned>(grid)), 128, S::SMEM_BYTES, 1, stream, tK, tV, p);
 }
 
 // Rows (query tokens x heads of a group) of an ordinary sequence decide: many
@@ -190,26 +191,28 @@ bool takes_prompt(const mxg::HandleView &v, const mxg::AttnParams &p) {
 // (of the kernel for few rows: items of 16)
 bool takes_two(const mxg::AttnParams &p) { return p.b.tokens * p.group > 8 * p.b.batch; }
 
-// How an attention runs, and the bytes of its partials (-1: too many row tiles).
+// How an attention runs: by which kernel, on how many SMs (that for few rows), and the
+// bytes of its partials (-1: too many row tiles).
 struct AttnPlan {
   bool prompt, two;
+  int sms;
   int64_t bytes;
 };
 template <int D>
-AttnPlan plan_attention(const mxg::HandleView &v, mxg::AttnParams &p) {
-  AttnPlan a{takes_prompt(v, p), takes_two(p), 0};
-  a.bytes = a.prompt ? plan_prompt<D>(v, p) : a.two ? decode_bytes<D, 2>(v, p) : decode_bytes<D, 1>(v, p);
+AttnPlan plan_attention(const mxg::HandleView &v, mxg::AttnParams &p, int sms) {
+  AttnPlan a{takes_prompt(v, p), takes_two(p), sms, 0};
+  a.bytes = a.prompt ? plan_prompt<D>(v, p) : a.two ? decode_bytes<D, 2>(p, sms) : decode_bytes<D, 1>(p, sms);
   return a;
 }
 template <int D, int MODE>
 int launch_attention(const mxg::HandleView &v, mxg::AttnParams &p, const AttnPlan &a, cudaStream_t stream) {
   if (a.prompt) return launch_prompt<D, MODE>(v, p, stream);
-  return a.two ? launch_decode<D, 2, MODE>(v, p, stream) : launch_decode<D, 1, MODE>(v, p, stream);
+  return a.two ? launch_decode<D, 2, MODE>(v, p, a.sms, stream) : launch_decode<D, 1, MODE>(v, p, a.sms, stream);
 }
 
 template <int D>
 int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
-  const AttnPlan a = plan_attention<D>(v, p);
+  const AttnPlan a = plan_attention<D>(v, p, v.sm_count);
   if (a.bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
   if (a.bytes > 0) {
     uint8_t *ws = nullptr;
@@ -219,46 +222,64 @@ int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &
   return launch_attention<D, mxg::kAllKeys>(v, p, a, stream);
 }
 
-// Parts of the shared keys for each of `tiles` row tiles, and the time (us) of a launch
-// over them: a key tile takes a CTA 1.65 us, its start and end about as long as five,
-// and each part costs the launch that joins a twentieth.
+// Time (us) of an attention over `keys` keys of each sequence on `sms` SMs: start and
+// end, and 1.65 us for a row tile's 128 keys, or the codes at the rate of an SM, once for
+// each 8 or 16 rows.  Fitted to 2-128 sequences of 1-64 tokens, 512-65536 keys; the
+// kernel for few rows without the join of its parts where only own keys are its.
+double attention_us(const mxg::HandleView &v, const mxg::AttnParams &p, double keys, int sms, int d) {
+  if (takes_prompt(v, p)) return 13 + 1.65 * static_cast<double>(equal_row_tiles(p)) * keys / 128 / sms;
+  const int64_t rows = takes_two(p) ? 16 : 8, passes = (p.b.tokens * p.group + rows * p.b.batch - 1) / (rows * p.b.batch);
+  const double rate = p.shared ? (rows == 16 ? 30e3 : 36e3) : (rows == 16 ? 22e3 : 42e3);  // bytes a us
+  return (p.shared ? 6 : 12) + static_cast<double>(passes * p.b.batch * p.c.kv_heads * 2 * d) * keys / (rate * sms);
+}
+
+// How the shared keys and the sequences' own are computed apart: parts of the shared
+// keys for each of `tiles` row tiles (a CTA each), the SMs for the own keys, and the time
+// (us).  A key tile takes a CTA 1.65 us, its start and end as long as five or (more than
+// 128 rows) seven, and the launch that joins 3 us and its reads.  Where the
+// first launch leaves SMs, the second runs there beside it, in one wave: 64 tokens of
+// 64/8 heads behind 8192 keys, 100-1000 of their own: 43.7 us with 5 parts and 72 SMs
+// for the own keys (4 and 88: 48.7, 6 and 56: 49.6; two waves on 72 SMs 50), and one
+// launch after the other with 8 parts 56.  How many keys sequences have of their own is
+// known to the device alone; an estimate that is too high must not make the shared
+// keys' launch much longer than it could be.
 struct SharedPlan {
-  int parts;
+  int parts, sms;
   double us;
 };
-SharedPlan plan_shared(int64_t tiles, int64_t key_tiles, int64_t sms) {
-  SharedPlan best{1, 1e300};
-  for (int64_t n = 1; n <= std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4)); ++n) {
-    const double us = 1.65 * (static_cast<double>((tiles * n + sms - 1) / sms) * (static_cast<double>((key_tiles + n - 1) / n) + 5) + 0.05 * n);
-    if (us < best.us) best = SharedPlan{static_cast<int>(n), us};
+SharedPlan plan_shared(const mxg::HandleView &v, const mxg::AttnParams &p, int64_t tiles, double own_keys, int d) {
+  const int64_t rows = p.b.tokens * p.group, key_tiles = (p.shared + 127) / 128, most = std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4));
+  auto shared_us = [&](int64_t n) {
+    return 1.65 * static_cast<double>((tiles * n + v.sm_count - 1) / v.sm_count) * (static_cast<double>((key_tiles + n - 1) / n) + (rows > 128 ? 7 : 5));
+  };
+  double least = 1e300;
+  for (int64_t n = 1; n <= most; ++n) least = std::min(least, shared_us(n));
+  SharedPlan best{1, v.sm_count, 1e300};
+  for (int64_t n = 1; n <= most; ++n) {
+    const double shared = shared_us(n), join = 3 + static_cast<double>(rows * p.c.kv_heads * (n + 2)) * 1e-4;
+    const double after = shared + attention_us(v, p, own_keys, v.sm_count, d) + join;
+    if (after < best.us) best = SharedPlan{static_cast<int>(n), v.sm_count, after};
+    if (tiles * n < v.sm_count && shared <= 1.4 * least && !takes_prompt(v, p)) {
+      const int left = v.sm_count - static_cast<int>(tiles * n);
+      const double beside = std::max(shared, attention_us(v, p, own_keys, left, d)) + join;
+      if (beside < best.us) best = SharedPlan{static_cast<int>(n), left, beside};
+    }
   }
   return best;
 }
 
-// Time (us) that the shared keys take where each sequence reads them with its own: by
-// the kernel for few rows 5 TB/s, once for each 8 or 16 rows; by the one for prompts
-// its key tiles.  (32/8 heads, 256 keys of their own, together and apart: 4 sequences
-// behind 8192 keys 19.9 and 28.5 us, 8 33 and 29.8, 16 58 and 31.5; 16 behind 2048 24
-// and 26, 64 62 and 31.)
-template <int D>
-double apart_us(const mxg::HandleView &v, const mxg::AttnParams &p) {
-  mxg::AttnParams all = p;
-  all.shared = 0;
-  const int64_t key_tiles = (p.shared + 127) / 128;
-  if (takes_prompt(v, all)) return 1.65 * static_cast<double>(equal_row_tiles(all) * key_tiles) / v.sm_count;
-  const int64_t rows = takes_two(all) ? 16 : 8, passes = (p.b.tokens * p.group + rows * p.b.batch - 1) / (rows * p.b.batch);
-  return static_cast<double>(passes * p.b.batch * p.shared) * p.c.kv_heads * 2 * D / 5e6;
-}
-
-// Each sequence's own keys, then the shared ones for all tokens, then both joined.
+// The shared keys for all tokens, then each sequence's own, then both joined.
 template <int D>
 int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, cudaStream_t stream) {
   using S = mxg::PromptCfg<D>;
   p.left_tiles = static_cast<int>((p.b.tokens * p.group + S::ROWS - 1) / S::ROWS);
   const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
-  const SharedPlan plan = plan_shared(items, (p.shared + S::KT - 1) / S::KT, v.sm_count);
-  // (four more for the launches that share what one does otherwise)
-  if (!v.shared_keys && plan.us + 4 > apart_us<D>(v, p)) {
+  // (half of the page table's room)
+  const double own_keys = 0.5 * static_cast<double>(p.b.table_pitch * p.c.page_size - p.shared);
+  const SharedPlan plan = plan_shared(v, p, items, own_keys, D);
+  mxg::AttnParams all = p;
+  all.shared = 0;
+  if (!v.shared_keys && plan.us > attention_us(v, all, p.shared + own_keys, v.sm_count, D)) {
     p.shared = 0;
     return run_attention<D>(h, v, p, stream);
   }
@@ -267,7 +288,7 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   const int64_t rows = p.b.tokens * p.heads, own = rows * (D + 4) * static_cast<int64_t>(sizeof(float));
   const int64_t blocks = (p.b.tokens * p.group + mxg::JoinCfg<D>::ROWS - 1) / mxg::JoinCfg<D>::ROWS;
   mxg::AttnParams first = p;
-  const AttnPlan a = plan_attention<D>(v, p);
+  const AttnPlan a = plan_attention<D>(v, p, plan.sms);
   if (items * p.left_parts >= kLim || a.bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
   uint8_t *ws = nullptr;
   if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + (own + 15) / 16 * 16 + a.bytes), stream, &ws)) return st;
@@ -280,9 +301,9 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   first.items = static_cast<int>(items);
   first.whole = 0;
   first.parts = first.left_parts;
-  if (int st = launch_attention<D, mxg::kOwnKeys>(v, p, a, stream)) return st;
-  ++*v.launches;
   if (int st = launch_prompt<D, mxg::kSharedKeys>(v, first, stream)) return st;
+  ++*v.launches;
+  if (int st = launch_attention<D, mxg::kOwnKeys>(v, p, a, stream)) return st;
   ++*v.launches;
   return mxg::launch(mxg::cache_join_kernel<D>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.c.kv_heads)), 256, 0, 1, stream, p);
 }

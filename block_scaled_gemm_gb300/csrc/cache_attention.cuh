@@ -31,7 +31,8 @@
 //
 // Behind shared tokens (kOwnKeys) the ranges are of warps and not of CTAs, and what they
 // leave is added by the launch that joins: 64 sequences of 100-982 own keys, 64/8 heads,
-// 22-24 us where all keys by ranges of CTAs take 36.
+// 22-24 us where all keys by ranges of CTAs take 36, and 34 us on the 72 SMs that the
+// launch over the shared keys leaves.
 //
 // Work: an item is one sequence, key/value head and ROWS query rows; all
 // items' tiles, laid end to end, are cut into equal ranges, one per CTA, or,
@@ -86,6 +87,16 @@ constexpr int kTilePartial = kTileRows * (D + 2);
 
 // What a launch computes: all keys; the shared ones for all tokens; the others.
 constexpr int kAllKeys = 0, kSharedKeys = 1, kOwnKeys = 2;
+
+// Before a launch reads global memory.  The one over the own keys comes behind the one
+// over the shared keys, needs nothing of it and does not wait for it: that one has
+// itself waited for what came before when it lets this one begin.  Lines that an SM
+// held before that are not to be read: the fence drops them, and most loads are from L2.
+template <int MODE>
+__device__ __forceinline__ void start_after() {
+  if (MODE == kOwnKeys) __threadfence();
+  else griddep_wait();
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -229,7 +240,7 @@ struct Cursor {
     }
   }
   __device__ void enter(const AttnParams &p, int rows) {
-    s = load_sequence(p.b, p.c, b);
+    s = load_sequence<MODE == kOwnKeys>(p.b, p.c, b);
     k = key_tiles<MODE>(p, s);
     items = item_count(p, s, rows);
   }
@@ -245,7 +256,7 @@ template <int MODE>
 __device__ __forceinline__ int64_t sequence_items(const AttnParams &p, int rows, int b, int &tiles) {
   tiles = 1;
   if (b >= p.b.batch) return 0;
-  const Sequence s = load_sequence(p.b, p.c, b);
+  const Sequence s = load_sequence<MODE == kOwnKeys>(p.b, p.c, b);
   tiles = key_tiles<MODE>(p, s).tiles;
   return item_count(p, s, rows);
 }
@@ -305,8 +316,15 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   // units of a CTA, 4.5 us of them an item's end).  Else a unit is a CTA.
   constexpr bool kWarps = MODE == kOwnKeys;
   constexpr int kStep = kWarps ? 1 : 4;  // from a warp's tile to its next
-  const int64_t unit = kWarps ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x : blockIdx.x;
-  const int64_t units_most = kWarps ? 4ll * gridDim.x : gridDim.x;
+  // (its last CTA does nothing but wait for the launch over the shared keys, so that
+  // the launch that joins need not)
+  if (MODE == kOwnKeys && blockIdx.x == gridDim.x - 1) {
+    griddep_wait();
+    return;
+  }
+  const int64_t blocks = gridDim.x - (MODE == kOwnKeys ? 1 : 0);
+  const int64_t unit = kWarps ? warp * blocks + blockIdx.x : blockIdx.x;
+  const int64_t units_most = kWarps ? 4 * blocks : blocks;
   // how tiles are cut: all of them and the units that share them, or 0 and the
   // first and the last unit of this one's item; then the range's first tile
   // (kept here: registers are short)
@@ -319,11 +337,8 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     fence_proxy_async_smem();
   }
   __syncwarp();
-  // (behind shared tokens the next launch does not need this one's results, and
-  // does not wait for them at its start: it may begin once this one has waited)
-  if (MODE != kOwnKeys) griddep_launch_dependents();
-  griddep_wait();
-  if (MODE == kOwnKeys) griddep_launch_dependents();
+  if (MODE != kOwnKeys) griddep_launch_dependents();  // (the launch that joins is kept away: see there)
+  start_after<MODE>();
   // All tiles (each warp counts for itself, 32 sequences at a time), and this
   // CTA's range of them: ranges of four tiles at least.
   int mt;
@@ -415,7 +430,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     int pg = -1;
     // (a page of which no query sees a key is left alone: a window may have passed it)
     const int k0 = key0 + 16 * lane;
-    if (lane < per && k0 < in.k.end && (k0 + 32 / per > in.k.win_lo || k0 < p.sinks)) pg = load_page(p.b, p.c, in.b, k0 >> lg);
+    if (lane < per && k0 < in.k.end && (k0 + 32 / per > in.k.win_lo || k0 < p.sinks)) pg = load_page<MODE == kOwnKeys>(p.b, p.c, in.b, k0 >> lg);
     const uint32_t bar = bars + 8 * st;
     const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
     if (lane < per) {
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + static_cast<int64_t>(at.s.first + tok) * p.q_pitch +
                                                          static_cast<int64_t>(hd) * D + t * (D / 4));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) qraw[n][i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < D / 32; ++i) qraw[n][i] = live ? (MODE == kOwnKeys ? __ldcg(src + i) : __ldg(src + i)) : make_uint4(0, 0, 0, 0);
     }
   };
   load_q();

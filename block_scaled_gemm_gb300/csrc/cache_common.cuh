@@ -37,9 +37,8 @@ struct Sequence {
   int n;      // how many new tokens (queries)
 };
 
-// A load, from L2 where FRESH: by a kernel that has not itself waited for the launch
-// that wrote the value (another launch between them has), so that no line that an SM
-// held before is taken.
+// A load, from L2 where FRESH: by the launch that has not itself waited for the one that
+// wrote the value (start_after).
 template <bool FRESH, typename T>
 __device__ __forceinline__ T load_value(const T *p) {
   if constexpr (FRESH) return __ldcg(p);

@@ -4,9 +4,13 @@
 //   top = max over parts of m,  o = sum 2^(m - top) o_part / (2^7 sum 2^(m - top) l_part)
 //
 // In a launch of its own, by all SMs: 64 tokens of 64 heads behind 8192 shared ones
-// are some 40 MB of partials from L2, 8.6 us.  Joined by the CTA that arrives last in the
+// are some 30 MB of partials from L2, 7 us.  Joined by the CTA that arrives last in the
 // launch over the shared keys they took 22 us for its row tile, and by the launch over
 // the own keys, at the end of each of its items, 30 us.
+// It begins when the launch before it has ended, and lets the next one begin when it has
+// ended itself: its blocks waiting on freed SMs slowed those that still computed
+// (the own keys' last 44 -> 52 us), and a next launch that comes while some are left
+// finds SMs in no order, the two launches' CTAs crowded together (50 -> 43.7 us in all).
 #pragma once
 #include "cache_attention.cuh"
 
@@ -20,7 +24,6 @@ struct JoinCfg {
 
 template <int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p) {
-  griddep_launch_dependents();
   griddep_wait();
   const int d4 = threadIdx.x / JoinCfg<D>::ROWS, h = blockIdx.y;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * JoinCfg<D>::ROWS + threadIdx.x % JoinCfg<D>::ROWS;  // token x head of the group

@@ -32,9 +32,10 @@
 // partials in the workspace, and the one that arrives last adds them in order.
 //
 // Shared tokens' keys (kSharedKeys): the rows of all sequences together, each cut for
-// as many CTAs as the SMs allow, which leave partials for the launch that joins.  512
-// rows of 8 key/value heads over 8192 keys, eight tiles a CTA: 27 us, of which 2.3 are
-// set-up, 4 until the first scores and 4 the first tile's softmax (0.9 later).
+// CTAs that leave partials for the launch that joins.  512 rows of 8 key/value heads
+// over 8192 keys, eight tiles a CTA on 128 SMs: 27 us, of which 2.3 are set-up, 4 until
+// the first scores and 4 the first tile's softmax (0.9 later); thirteen tiles a CTA on 80
+// SMs, beside the own keys on the others, 35 us.
 //
 // Warps (512 threads): 0 TMA loads of the pages' codes, and the scales;
 // 1 MMAs; 4-7 convert codes to FP16 in the MMA's layout (128-byte swizzle);
@@ -121,12 +122,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   uint8_t *sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // (the launch over the own keys comes before the one over the shared, which needs
-  // nothing of it: the first lets the second begin once it has itself waited for what
-  // came before, and the second waits for it at its end, for the launch that joins)
-  if (MODE != kOwnKeys) griddep_launch_dependents();
-  if (MODE != kSharedKeys) griddep_wait();
-  if (MODE == kOwnKeys) griddep_launch_dependents();
+  if (MODE == kOwnKeys && blockIdx.x == gridDim.x - 1) {  // waits for the shared keys', for the launch that joins
+    griddep_wait();
+    return;
+  }
+  if (MODE == kAllKeys) griddep_launch_dependents();
+  start_after<MODE>();
+  if (MODE == kSharedKeys) griddep_launch_dependents();  // (the launch over the own keys: see there)
   // ------------------------------------------------------------ this CTA's rows
   // Sequence b's row tiles are numbered from f(b) = floor(q_start group / 256) + b
   // (room for all of them); the last tiles, which see most keys, come first.
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const int h = static_cast<int>(item % p.c.kv_heads);
   const int64_t id = p.items / p.c.kv_heads - 1 - item / p.c.kv_heads;
   auto f = [&](int b) -> int64_t {
-    const int64_t q = p.b.q_start ? p.b.q_start[b] : b;
+    const int64_t q = p.b.q_start ? load_value<MODE == kOwnKeys>(p.b.q_start + b) : b;
     return q * p.group / S::ROWS + b;
   };
   int b;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     int most = 0;
     b = 0;
     for (int i = lane; i < p.b.batch; i += 32) {
-      const int len = load_sequence<true>(p.b, p.c, i).len;
+      const int len = load_sequence(p.b, p.c, i).len;
       if (len > most) {
         most = len;
         b = i;
@@ -157,14 +159,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     s = Sequence{min(p.shared, longest), 0, static_cast<int>(p.b.tokens)};
   } else {
     b = warp_find(p.b.batch, f, id);
-    s = load_sequence(p.b, p.c, b);
+    s = load_sequence<MODE == kOwnKeys>(p.b, p.c, b);
   }
   const int64_t row_first = (MODE == kSharedKeys ? id : id - f(b)) * S::ROWS;
   const int64_t row_count = static_cast<int64_t>(s.n) * p.group;
-  if (row_first < 0 || row_first >= row_count) {
-    if (MODE == kSharedKeys) griddep_wait();
-    return;
-  }
+  if (row_first < 0 || row_first >= row_count) return;
   const int row0 = static_cast<int>(row_first);
   const int rows = static_cast<int>(min(static_cast<int64_t>(S::ROWS), row_count - row_first));
   const int nq = rows > 128 ? 2 : 1;
@@ -185,10 +184,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       slot[threadIdx.x] = threadIdx.x < S::ROWS ? -INFINITY : 0.f;
     }
   }
-  if (part >= parts) {
-    if (MODE == kSharedKeys) griddep_wait();
-    return;
-  }
+  if (part >= parts) return;
   const int tile0 = static_cast<int>(static_cast<int64_t>(part) * all_tiles / parts);
   const int tiles = static_cast<int>(static_cast<int64_t>(part + 1) * all_tiles / parts) - tile0;
   auto tile_key = [&](int j) { return (j + tile0 < ns ? j + tile0 : lo + j + tile0 - ns) * 128; };
@@ -253,12 +249,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         // their page (a window may have passed it)
         int pg = -1;
         const int k0 = key0 + 16 * lane, page0 = k0 >> lg << lg;
-        if (lane < 8 && k0 < end && (page0 + (1 << lg) > win_lo || page0 < p.sinks)) pg = load_page<MODE == kSharedKeys>(p.b, p.c, b, k0 >> lg);
+        if (lane < 8 && k0 < end && (page0 + (1 << lg) > win_lo || page0 < p.sinks)) pg = load_page<MODE == kOwnKeys>(p.b, p.c, b, k0 >> lg);
         float ks = 1.f, vs = 1.f;
         if (pg >= 0) {
           const int64_t cell = static_cast<int64_t>(pg) * p.c.kv_heads + h;
-          ks = load_value<MODE == kSharedKeys>(p.c.K_scale + cell);
-          vs = fmaxf(load_value<MODE == kSharedKeys>(p.c.V_scale + cell), kScaleFloor);
+          ks = load_value<MODE == kOwnKeys>(p.c.K_scale + cell);
+          vs = fmaxf(load_value<MODE == kOwnKeys>(p.c.V_scale + cell), kScaleFloor);
         }
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, pg >= 0);
         // lane i < npg: page i of the tile
@@ -424,7 +420,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int n = 0; n < 32 / kRows; ++n) {
           const int from = kRows * n + sub;
           const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, from);
-          x[n] = 128 * i + 32 * qd + from < rows ? load_value<MODE == kSharedKeys>(reinterpret_cast<const uint4 *>(p.Q + at + 8 * unit)) : make_uint4(0, 0, 0, 0);
+          x[n] = 128 * i + 32 * qd + from < rows ? load_value<MODE == kOwnKeys>(reinterpret_cast<const uint4 *>(p.Q + at + 8 * unit)) : make_uint4(0, 0, 0, 0);
         }
         float top = 0.f;  // of this thread's row
         const uint32_t dst = base + S::OFF_Q + i * S::TILE16 + (unit >> 3) * 16384;
@@ -710,7 +706,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc<1>(tmem, 512);
-  if (MODE == kSharedKeys) griddep_wait();
 }
 
 }  // namespace mxg

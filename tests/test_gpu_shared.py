@@ -234,6 +234,50 @@ def test_graph_with_growing_sequences(h):
     assert mx.mxgemm_get_device_status(h) == (0, 0)
 
 
+@pytest.mark.parametrize("new", [1, 16])
+@pytest.mark.parametrize("graph", [False, True])
+def test_reads_what_was_appended_just_before(h, new, graph):
+    """The launch over the own keys does not wait for the one before it: steps in a row,
+    in which the pages' codes and scales, the lengths and the queries change, give what
+    they give with the device idle between any two calls, to the bit."""
+    batch, steps, kv, group, d, page, common = 24, 8, 2, 4, 128, 16, 512
+    m = made([common + 20 + steps * new + i for i in range(batch)], kv, d, page, common, seed=3)
+    table = m.table_tensor()
+    g = torch.Generator().manual_seed(4)
+    K, V = ((torch.randn(steps, batch * new, kv, d, generator=g) * 1.5 ** torch.arange(steps).view(-1, 1, 1, 1)).bfloat16().to(DEV) for _ in range(2))
+    Q = torch.randn(steps, batch * new, kv * group, d, generator=g).bfloat16().to(DEV)
+    lens = torch.tensor([[n - (steps - 1 - i) * new for n in m.kv_len] for i in range(steps)], dtype=torch.int32, device=DEV)
+    starts = torch.arange(batch + 1, dtype=torch.int32, device=DEV) * new if new > 1 else None
+
+    def run(cache, q, k, v, n, O, wait):
+        for i in range(steps):
+            for to, what in ((q, Q), (k, K), (v, V), (n, lens)):
+                to.copy_(what[i])
+            wait()
+            mx.mxgemm_cache_append(h, cache, table, n, k, v, q_start=starts, stream=torch.cuda.current_stream())
+            wait()
+            mx.mxgemm_cache_attention_shared(h, cache, table, n, common, q, O[i], q_start=starts, stream=torch.cuda.current_stream())
+            wait()
+
+    def buffers():
+        return (m.cache(), *(torch.empty_like(x[0]) for x in (Q, K, V, lens)), torch.full_like(Q, math.nan))
+
+    want = buffers()
+    run(*want, torch.cuda.synchronize)
+    got = buffers()
+    if graph:
+        torch.cuda.synchronize()
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            run(*got, lambda: None)
+        cg.replay()
+    else:
+        run(*got, lambda: None)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want[5].float()).all() and torch.equal(got[5], want[5])
+    assert mx.mxgemm_get_device_status(h) == (0, 0)
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_a_call_that_gives_up_leaves_nothing(new):
     h = mx.mxgemm_create(0)
