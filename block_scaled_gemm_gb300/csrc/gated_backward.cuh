@@ -12,11 +12,11 @@
 // rows' and its columns' largest are known, and stores the columns' codes through
 // shared memory.
 //
-// Measured: 4096 x 28672, BF16 dH, to five quantized operands 240 us (5.4 TB/s, 0.79 of
+// Measured: 4096 x 28672, BF16 dH, to five quantized operands 226 us (5.8 TB/s, 0.86 of
 // the measured copy rate; with one tile a block and its loads in registers 501 us, with
-// scalar operations and a division for each row by all lanes 321 us): issue slots are
-// used to half, and loads wait while a tile's values are formed.  1741 x 7000, FP32 dH,
-// to BF16 17.9 us with inputs in L2.
+// scalar operations and a division for each row by all lanes 321 us, with the next
+// tile's loads after the first barrier 240 us): issue slots are used to half.  1741 x
+// 7000, FP32 dH, to BF16 17.9 us with inputs in L2.
 #pragma once
 #include "gated_math.cuh"
 #include "quantize128.cuh"
@@ -99,8 +99,8 @@ __device__ __forceinline__ float abs_max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return mx_e4m3x2(a, b) | (mx_e4m3x2(c, d) << 16); }
 
 // One block of 512 threads an SM, which goes from tile to tile and copies the next
-// one's values to shared memory while it stores this one's codes (each thread copies
-// what it will read itself).  Thread (ty, tx) has rows 4 ty .. +3 of columns 8 tx ..
+// one's values to shared memory, a row as soon as this tile's has been read from there
+// (each thread copies what it will read itself).  Thread (ty, tx) has rows 4 ty .. +3 of columns 8 tx ..
 // +7, so that the four rows' codes of a column are one word of the transposed tile.
 // Issue slots are as short as bandwidth: operations go in pairs, and a row's largest
 // values are exchanged so that each lane ends with one of them and divides once.
@@ -116,29 +116,36 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const uint32_t in = smem_u32(smem + S::OFF_IN) + threadIdx.x * 16;
   const uint32_t tiles = static_cast<uint32_t>(p.rb * p.cb), cb = static_cast<uint32_t>(p.cb);
-  auto load = [&](uint32_t t) {
+  // a tile's place in the matrices, for this thread, and how many of its rows are there
+  auto place = [&](uint32_t t, int64_t &at) {
     const uint32_t rblock = t / cb, cblock = t - rblock * cb;
     const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128 + 8 * tx;
-    const int rows = t < tiles && c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;  // that are there
-    int64_t at = r0 * p.C + c0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i, at += p.C) {
-      const int64_t from = i < rows ? at : 0;
-      const uint32_t to = in + i * S::WORDS * 8192;
-      grad_copy16(to, p.gate + from, i < rows);
-      grad_copy16(to + 8192, p.up + from, i < rows);
-#pragma unroll
-      for (int w = 0; w < S::WORDS - 2; ++w)
-        grad_copy16(to + (2 + w) * 8192, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dH) + from) + w, i < rows);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    at = r0 * p.C + c0;
+    return t < tiles && c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;
   };
-  load(blockIdx.x);
+  auto load = [&](int i, int rows, int64_t at) {  // row i of a tile
+    const int64_t from = i < rows ? at + i * p.C : 0;
+    const uint32_t to = in + i * S::WORDS * 8192;
+    grad_copy16(to, p.gate + from, i < rows);
+    grad_copy16(to + 8192, p.up + from, i < rows);
+#pragma unroll
+    for (int w = 0; w < S::WORDS - 2; ++w)
+      grad_copy16(to + (2 + w) * 8192, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dH) + from) + w, i < rows);
+  };
+  {
+    int64_t at;
+    const int rows = place(blockIdx.x, at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load(i, rows, at);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const uint32_t rblock = t / cb, cblock = t - rblock * cb;
     const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128 + 8 * tx;
     const int rows = c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;
     float2 v[3][4][4];  // dgate, dup, h: [row][columns 2 e, + 1]
+    int64_t next_at;
+    const int next_rows = place(t + gridDim.x, next_at);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -156,7 +163,9 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
         v[1][i][e] = x.du;
         v[2][i][e] = x.h;
       }
+      load(i, next_rows, next_at);  // into what this thread has just read
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     // columns' largest of this thread's rows
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
@@ -171,7 +180,6 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
       to[1] = make_float4(c[4], c[5], c[6], c[7]);
     }
     __syncthreads();
-    load(t + gridDim.x);
     // the columns' reciprocals and scales
     if (threadIdx.x < 384) {
       const int m = threadIdx.x >> 7, c = threadIdx.x & 127;
