@@ -229,7 +229,8 @@ int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &
 double attention_us(const mxg::HandleView &v, const mxg::AttnParams &p, double keys, int sms, int d) {
   if (takes_prompt(v, p)) return 13 + 1.65 * static_cast<double>(equal_row_tiles(p)) * keys / 128 / sms;
   const int64_t rows = takes_two(p) ? 16 : 8, passes = (p.b.tokens * p.group + rows * p.b.batch - 1) / (rows * p.b.batch);
-  const double rate = p.shared ? (rows == 16 ? 30e3 : 36e3) : (rows == 16 ? 22e3 : 42e3);  // bytes a us
+  // bytes a us (heads of 64: 1.4 times the keys)
+  const double rate = (p.shared ? (rows == 16 ? 30e3 : 36e3) : (rows == 16 ? 22e3 : 42e3)) * (d == 64 ? 0.72 : 1);
   return (p.shared ? 6 : 12) + static_cast<double>(passes * p.b.batch * p.c.kv_heads * 2 * d) * keys / (rate * sms);
 }
 
@@ -274,8 +275,8 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   using S = mxg::PromptCfg<D>;
   p.left_tiles = static_cast<int>((p.b.tokens * p.group + S::ROWS - 1) / S::ROWS);
   const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
-  // (half of the page table's room)
-  const double own_keys = 0.5 * static_cast<double>(p.b.table_pitch * p.c.page_size - p.shared);
+  // (tables are about as wide as the longest sequence needs: three quarters of it)
+  const double own_keys = 0.75 * static_cast<double>(p.b.table_pitch * p.c.page_size - p.shared);
   const SharedPlan plan = plan_shared(v, p, items, own_keys, D);
   mxg::AttnParams all = p;
   all.shared = 0;
