@@ -235,11 +235,13 @@ def test_graph_with_growing_sequences(h):
 
 
 @pytest.mark.parametrize("new", [1, 16])
+@pytest.mark.parametrize("copies", [False, True])
 @pytest.mark.parametrize("graph", [False, True])
-def test_reads_what_was_appended_just_before(h, new, graph):
+def test_reads_what_was_appended_just_before(h, new, graph, copies):
     """The launch over the own keys does not wait for the one before it: steps in a row,
     in which the pages' codes and scales, the lengths and the queries change, give what
-    they give with the device idle between any two calls, to the bit."""
+    they give with the device idle between any two calls, to the bit.  With the steps'
+    inputs in buffers of their own, or copied into the same ones."""
     batch, steps, kv, group, d, page, common = 24, 8, 2, 4, 128, 16, 512
     m = made([common + 20 + steps * new + i for i in range(batch)], kv, d, page, common, seed=3)
     table = m.table_tensor()
@@ -251,8 +253,11 @@ def test_reads_what_was_appended_just_before(h, new, graph):
 
     def run(cache, q, k, v, n, O, wait):
         for i in range(steps):
-            for to, what in ((q, Q), (k, K), (v, V), (n, lens)):
-                to.copy_(what[i])
+            if copies:
+                for to, what in ((q, Q), (k, K), (v, V), (n, lens)):
+                    to.copy_(what[i])
+            else:
+                q, k, v, n = Q[i], K[i], V[i], lens[i]
             wait()
             mx.mxgemm_cache_append(h, cache, table, n, k, v, q_start=starts, stream=torch.cuda.current_stream())
             wait()
