@@ -470,11 +470,22 @@ def mxgemm_cache_attention_shared(h, cache: Cache, page_table, kv_len, shared, Q
     return st
 
 
+_codes = {}  # IN_F32 and IN_BF16 by torch's types, once torch is there
+
+
+def _type_codes():
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: IN_F32, torch.bfloat16: IN_BF16})
+    return _codes
+
+
 def _bfloat16(**tensors):
     """The entry points that write BF16 through plain addresses: tensors of another type are refused."""
     for name, t in tensors.items():
-        if getattr(t, "dtype", None) is not None and str(t.dtype) != "torch.bfloat16":
-            raise ValueError(f"{name}: bfloat16, not {t.dtype}")
+        dtype = getattr(t, "dtype", None)
+        if dtype is not None and _type_codes().get(dtype) != IN_BF16:
+            raise ValueError(f"{name}: bfloat16, not {dtype}")
 
 
 def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H, H_scale=None, act=ACT_SILU,
@@ -515,30 +526,25 @@ def mxgemm_gated_backward(gate, up, dH, R, C, dgate=None, dup=None, dgate_rows=N
     return st
 
 
-_codes = {}  # IN_F32 and IN_BF16 by torch's types, once torch is there
-
-
-def _type_codes():
-    if not _codes:
-        import torch
-        _codes.update({torch.float32: IN_F32, torch.bfloat16: IN_BF16})
-    return _codes
+def _rows(name, t, shape, dtype):
+    """Address and pitch of a tensor of (tokens, heads, d) values."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name}: tokens x heads x head dim, all tensors of one type")
+    pitch, head, step = t.stride()
+    tokens, heads, d = shape
+    if step != 1 or (head != d and heads > 1):
+        raise ValueError(f"{name}: tokens x heads x head dim, each token dense")
+    return t.data_ptr(), pitch if tokens > 1 else heads * d
 
 
 def _heads(name, tokens, d, dtype, x, y, weight, dy, dweight):
     """mxgemm_heads_t of a tensor's values, result and gradient, each (tokens, heads, d) of one type."""
-    at, heads = [], y.shape[1] if y.dim() == 3 else -1
-    for t in (x, dy, y):
-        if t is None:
-            at += (0, 0)
-            continue
-        shape = t.shape
-        if shape != (tokens, heads, d) or t.dtype is not dtype:
-            raise ValueError(f"{name}: tokens x heads x head dim, all tensors of one type")
-        step = t.stride()
-        if step[2] != 1 or (heads > 1 and step[1] != d):
-            raise ValueError(f"{name}: tokens x heads x head dim, each token dense")
-        at += (t.data_ptr(), step[0] if tokens > 1 else heads * d)
+    shape = y.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != d:
+        raise ValueError(f"{name}: tokens x heads x head dim, all tensors of one type")
+    out, out_pitch = _rows(name, y, shape, dtype)
+    at, pitch = (0, 0) if x is None else _rows(name, x, shape, dtype)
+    g, g_pitch = (0, 0) if dy is None else _rows(name, dy, shape, dtype)
     w = dw = 0
     if weight is not None:
         if x is None:
@@ -550,7 +556,7 @@ def _heads(name, tokens, d, dtype, x, y, weight, dy, dweight):
         if weight is None or _type_codes().get(dweight.dtype) != IN_F32 or dweight.shape != (d,) or not dweight.is_contiguous():
             raise ValueError(f"{name}'s weight's gradient: head dim float32 values, of a weight")
         dw = dweight.data_ptr()
-    return _HEADS_STRUCT.pack(*at, w, dw, heads)
+    return _HEADS_STRUCT.pack(at, pitch, g, g_pitch, out, out_pitch, w, dw, shape[1])
 
 
 _rope_types = {}  # the types of positions and frequencies
