@@ -13,11 +13,11 @@
 // product where FP64 would be far slower on this GPU.
 //
 // Bound by HBM: each value is read once and written once, and everything between
-// happens in registers.  A head is D / 16 lanes, each with two runs of eight
-// values that hold whole pairs in either layout (run s of the first half of the
-// rotated values and run s of the second), so that a rotation needs no exchange
-// between lanes.  All tokens' heads, four or eight at a time, are cut into equal
-// ranges for the warps, each of which works by itself: its lanes copy what they will
+// happens in registers.  A lane has two runs of 16 bytes of a head (eight values in
+// BF16, four in FP32) that hold whole pairs in either layout (run s of the first half of
+// the rotated values and run s of the second), so that a rotation needs no exchange
+// between lanes.  All tokens' heads, as many at a time as a warp has lanes for, are cut
+// into equal ranges for the warps, each of which works by itself: its lanes copy what they will
 // read themselves into a ring in shared memory, some steps ahead (cp.async: what is
 // on its way takes no registers), and it computes a token's cosines and sines once
 // for all of that token's heads in its range.
@@ -27,7 +27,10 @@
 // registers 40 us, ranges of a tensor's parity 46, halves of sectors where values
 // pass 35); 64 tokens 3.4 us.  The gradient, all of each head rotated: 53 us (4.7 TB/s;
 // 105 us with loads in registers), bound by issue slots and dependent
-// instructions at the 16 warps an SM that its registers allow.
+// instructions at the 16 warps an SM that its registers allow (runs of four values
+// and 24 warps: 59 us).  In FP32 4112 tokens, all of each head rotated: 28.7 us (5.9
+// TB/s; with runs of eight values, of which a copy takes every other 16 bytes,
+// 40.6), the gradient 51.8 (69.6).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -60,26 +63,25 @@ struct RopeParams {
   unsigned *counters;  // backward: one for each tensor, then groups of queries, groups of keys
 };
 
-// Eight consecutive values in FP32, in pairs.
-struct F8 {
-  float2 v[4];
+// R consecutive values (a run: 16 bytes as they lie) in FP32, in pairs.
+template <int R>
+struct Run {
+  float2 v[R / 2];
 };
-__device__ __forceinline__ F8 floats_of(const uint4 (&w)[2], float) {
-  return F8{{make_float2(__uint_as_float(w[0].x), __uint_as_float(w[0].y)), make_float2(__uint_as_float(w[0].z), __uint_as_float(w[0].w)),
-             make_float2(__uint_as_float(w[1].x), __uint_as_float(w[1].y)), make_float2(__uint_as_float(w[1].z), __uint_as_float(w[1].w))}};
+__device__ __forceinline__ Run<4> floats_of(uint4 w, float) {
+  return Run<4>{{make_float2(__uint_as_float(w.x), __uint_as_float(w.y)), make_float2(__uint_as_float(w.z), __uint_as_float(w.w))}};
 }
-__device__ __forceinline__ F8 floats_of(const uint4 (&w)[1], __nv_bfloat16) {
-  const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-  F8 r;
+__device__ __forceinline__ Run<8> floats_of(uint4 w, __nv_bfloat16) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  Run<8> r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r.v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
   return r;
 }
-__device__ __forceinline__ void store8(float *p, const F8 &a) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+__device__ __forceinline__ void store_run(float *p, const Run<4> &a) {
+  *reinterpret_cast<float4 *>(p) = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const F8 &a) {
+__device__ __forceinline__ void store_run(__nv_bfloat16 *p, const Run<8> &a) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -88,13 +90,19 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const F8 &a) {
   }
   *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-// A lane's eight values of a table in shared memory whose values 4 k .. + 3 are at
+// A lane's R values of a table in shared memory whose values 4 k .. + 3 are at
 // [k][lane of the head]: 16-byte loads of a head's lanes lie side by side.
-template <int LANES>
-__device__ __forceinline__ F8 shared_run(uint32_t at, int sub) {
+template <int R, int LANES>
+__device__ __forceinline__ Run<R> shared_run(uint32_t at, int sub) {
   at += sub * 16;
-  const uint4 a[2] = {ld_shared_v4(at), ld_shared_v4(at + LANES * 16)};
-  return floats_of(a, 0.f);
+  Run<R> r;
+#pragma unroll
+  for (int k = 0; k < R / 4; ++k) {
+    const Run<4> four = floats_of(ld_shared_v4(at + k * LANES * 16), 0.f);
+    r.v[2 * k] = four.v[0];
+    r.v[2 * k + 1] = four.v[1];
+  }
+  return r;
 }
 
 // A frequency (radians a position) as a fraction of a turn, times 2^64.
@@ -112,18 +120,18 @@ __device__ __forceinline__ float2 angle_at(uint64_t turn, int pos, float factor)
 
 template <typename T, int D, bool BACK>
 struct RopeCfg {
-  static constexpr int LANES = D / 16, HEADS = 32 / LANES;  // lanes of a head, heads of a warp
-  static constexpr int WORDS = sizeof(T) / 2;               // 16-byte words of a run
-  static constexpr int PIECES = (BACK ? 4 : 2) * WORDS;     // words of a lane: dy and x, or x
+  static constexpr int RUN = 16 / sizeof(T);                       // values of a run
+  static constexpr int LANES = D / (2 * RUN), HEADS = 32 / LANES;  // lanes of a head, heads of a warp
+  static constexpr int PIECES = BACK ? 4 : 2;                      // runs of a lane: dy and x, or x
   // Warps of a block, blocks of an SM, and loads of a warp on their way plus one.  The
-  // gradient's registers allow 16 warps without spills: 8192 tokens, 32/8 heads, 53 us
-  // so, 56 with four stages, 62 with two, 60 with 20 warps, 63 with 8.
-  static constexpr int WARPS = 8, BLOCKS = BACK ? (sizeof(T) == 4 ? 1 : 2) : sizeof(T) == 4 ? 3 : 4, STAGES = BACK ? 3 : 4;
+  // gradient's registers in BF16 allow 16 warps without spills: 8192 tokens, 32/8 heads, 53
+  // us so, 56 with four stages, 62 with two, 60 with 20 warps, 63 with 8.
+  static constexpr int WARPS = 8, BLOCKS = BACK ? 2 : 4, STAGES = BACK ? 3 : 4;
   static constexpr int OFF_TURN = 0;                        // [D / 2] turns a position
   static constexpr int OFF_W = OFF_TURN + D / 2 * 8;        // [2][runs a, b][D / 2] weights
   static constexpr int OFF_CS = OFF_W + 2 * D * 4;          // [warps][cosines, sines][D / 2]
   static constexpr int OFF_POS = OFF_CS + WARPS * D / 2 * 8;  // [warps][STAGES] positions
-  static constexpr int OFF_RING = (OFF_POS + WARPS * STAGES * 4 + 15) / 16 * 16;  // [warps][STAGES][PIECES][32 lanes]
+  static constexpr int OFF_RING = (OFF_POS + WARPS * STAGES * 4 + 15) / 16 * 16;  // [warps][STAGES][PIECES][32 lanes] runs
   static constexpr int SMEM_BYTES = OFF_RING + WARPS * STAGES * PIECES * 512;
   static_assert(OFF_RING % 16 == 0, "alignment");
 };
@@ -134,20 +142,25 @@ struct Runs {
   bool turned;
 };
 // (the lanes' first runs lie side by side, and so do the second)
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ Runs runs_of(int sub, int rot) {
-  const int n = rot >> 4;
-  if (sub < n) return Runs{8 * sub, (rot >> 1) + 8 * sub, true};
-  const int at = rot + 8 * (sub - n);
+  const int n = rot / (2 * R);
+  if (sub < n) return Runs{R * sub, (rot >> 1) + R * sub, true};
+  const int at = rot + R * (sub - n);
   return Runs{at, at + ((D - rot) >> 1), false};
 }
 
 // Where pair j of a token's rot / 2 is in such a table of cosines (or sines).
-template <int LANES>
+template <int R, int LANES>
 __device__ __forceinline__ int pair_place(int j, int rot, int interleaved) {
-  const int k = interleaved ? j >= rot >> 2 : (j >> 2) & 1;
-  const int sub = interleaved ? (j - (k ? rot >> 2 : 0)) >> 2 : j >> 3;
-  return (k * LANES + sub) * 4 + (j & 3);
+  int sub = j / R, e = j % R;
+  if (interleaved) {  // a lane has R / 2 pairs in each run
+    const bool second = j >= rot >> 2;
+    if (second) j -= rot >> 2;
+    sub = j / (R / 2);
+    e = j % (R / 2) + (second ? R / 2 : 0);
+  }
+  return ((e >> 2) * LANES + sub) * 4 + (e & 3);
 }
 __device__ __forceinline__ uint32_t rope_shared_word(uint32_t at) {
   uint32_t v;
@@ -158,18 +171,18 @@ __device__ __forceinline__ void rope_store_word(uint32_t at, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 // A lane's pairs turned forward, or back, by its cosines and sines.
-template <bool BACK>
-__device__ __forceinline__ void turn(F8 &a, F8 &b, const F8 &c, const F8 &s, int interleaved) {
+template <bool BACK, int R>
+__device__ __forceinline__ void turn(Run<R> &a, Run<R> &b, const Run<R> &c, const Run<R> &s, int interleaved) {
   if (interleaved) {  // (x, y) -> (x, y) c + (y, x) (-s, s)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float2 &x = e < 4 ? a.v[e] : b.v[e - 4];
+    for (int e = 0; e < R; ++e) {
+      float2 &x = e < R / 2 ? a.v[e] : b.v[e - R / 2];
       const float cc = e & 1 ? c.v[e >> 1].y : c.v[e >> 1].x, ss = e & 1 ? s.v[e >> 1].y : s.v[e >> 1].x, t = BACK ? -ss : ss;
       x = fma2(make_float2(x.y, x.x), make_float2(-t, t), mul2(x, make_float2(cc, cc)));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < R / 2; ++e) {
       const float2 t = BACK ? make_float2(-s.v[e].x, -s.v[e].y) : s.v[e], u = a.v[e], v = b.v[e];
       a.v[e] = fma2(v, make_float2(-t.x, -t.y), mul2(u, c.v[e]));
       b.v[e] = fma2(u, t, mul2(v, c.v[e]));
@@ -206,6 +219,7 @@ struct RopeAt {
 template <typename T, int D, bool BACK>
 struct RopeWalk {
   using C = RopeCfg<T, D, BACK>;
+  using F = Run<C::RUN>;
   const RopeParams &p;
   const int only;  // backward: the one tensor
   uint32_t sm;     // the block's shared memory
@@ -217,7 +231,7 @@ struct RopeWalk {
   // warp `w` of `warps`
   __device__ RopeWalk(const RopeParams &p_, uint32_t sm_, int64_t w, int64_t warps, int which)
       : p(p_), only(which), sm(sm_), sub(threadIdx.x % C::LANES), stage(0), filled(0), angles_of(-1) {
-    const Runs r = runs_of<D>(sub, p.rot);
+    const Runs r = runs_of<D, C::RUN>(sub, p.rot);
     apart = r.b - r.a;
     const int64_t all = p.tokens * of_token(), u0 = w * all / warps;
     at.token = static_cast<int>(u0 / of_token());
@@ -243,7 +257,7 @@ struct RopeWalk {
   __device__ void enter(RopeAt<T> &a) const {
     const RopeTensor &t = p.t[which(a)];
     a.h = (a.j - (!BACK && which(a) ? first() : 0)) * C::HEADS + (threadIdx.x & 31) / C::LANES;
-    const int64_t in_row = static_cast<int64_t>(a.h) * D + runs_of<D>(sub, p.rot).a, token = a.token;
+    const int64_t in_row = static_cast<int64_t>(a.h) * D + runs_of<D, C::RUN>(sub, p.rot).a, token = a.token;
     if (LOADS) {
       a.a = static_cast<T *>(const_cast<void *>(BACK ? t.dy : t.x)) + token * (BACK ? t.dy_pitch : t.x_pitch) + in_row;
       if (BACK) a.b = static_cast<T *>(const_cast<void *>(t.x)) + token * t.x_pitch + in_row;
@@ -279,11 +293,8 @@ struct RopeWalk {
         for (int k = 0; k < (BACK ? 2 : 1); ++k) {  // dy, then x
           if (k == 1 && !p.t[only].w) continue;
           const T *from = k ? ahead.b : ahead.a;
-#pragma unroll
-          for (int i = 0; i < C::WORDS; ++i) {
-            rope_copy16(to + (k * 2 * C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from) + i);
-            rope_copy16(to + (k * 2 * C::WORDS + C::WORDS + i) * 512, reinterpret_cast<const uint4 *>(from + apart) + i);
-          }
+          rope_copy16(to + k * 1024, from);
+          rope_copy16(to + k * 1024 + 512, from + apart);
         }
       }
       if ((threadIdx.x & 31) == 0 && p.rot) rope_copy4(position(filled), p.positions + ahead.token);
@@ -303,7 +314,7 @@ struct RopeWalk {
         uint64_t turns;
         asm volatile("ld.shared.b64 %0, [%1];" : "=l"(turns) : "r"(sm + C::OFF_TURN + j * 8) : "memory");
         const float2 a = angle_at(turns, pos, p.factor);
-        const uint32_t to = angles() + pair_place<C::LANES>(j, p.rot, p.interleaved) * 4;
+        const uint32_t to = angles() + pair_place<C::RUN, C::LANES>(j, p.rot, p.interleaved) * 4;
         rope_store_word(to, __float_as_uint(a.x));
         rope_store_word(to + D * 2, __float_as_uint(a.y));
       }
@@ -311,22 +322,20 @@ struct RopeWalk {
     }
   }
   template <bool BACKWARD>
-  __device__ void turned(F8 &a, F8 &b) const {
-    if (sub < p.rot >> 4) turn<BACKWARD>(a, b, shared_run<C::LANES>(angles(), sub), shared_run<C::LANES>(angles() + D * 2, sub), p.interleaved);
+  __device__ void turned(F &a, F &b) const {
+    if (sub < p.rot / (2 * C::RUN))
+      turn<BACKWARD>(a, b, shared_run<C::RUN, C::LANES>(angles(), sub), shared_run<C::RUN, C::LANES>(angles() + D * 2, sub), p.interleaved);
   }
   // This lane's weights of the tensor's run `i`.
-  __device__ F8 weights(int i) const { return shared_run<C::LANES>(sm + C::OFF_W + (2 * which(at) + i) * (D * 2), sub); }
+  __device__ F weights(int i) const { return shared_run<C::RUN, C::LANES>(sm + C::OFF_W + (2 * which(at) + i) * (D * 2), sub); }
   // Run `i` (0, 1) of tensor k (0: dy where there is one, 1: then x).
-  __device__ F8 run(int k, int i) const {
-    uint4 w[C::WORDS];
-#pragma unroll
-    for (int n = 0; n < C::WORDS; ++n) w[n] = ld_shared_v4(ring(stage) + ((k * 2 + i) * C::WORDS + n) * 512);
-    return floats_of(w, T{});
+  __device__ F run(int k, int i) const {
+    return floats_of(ld_shared_v4(ring(stage) + (k * 2 + i) * 512), T{});
   }
-  __device__ void store(const F8 &a, const F8 &b) const {
+  __device__ void store(const F &a, const F &b) const {
     if (live()) {
-      store8(at.a, a);
-      store8(at.a + apart, b);
+      store_run(at.a, a);
+      store_run(at.a + apart, b);
     }
   }
   // Past this place: its stage has been read by this lane (and, positions, by the warp).
@@ -345,8 +354,8 @@ __device__ __forceinline__ void rope_tables(const RopeParams &p, uint8_t *sm) {
   for (int j = threadIdx.x; j < p.rot >> 1; j += 32 * C::WARPS) reinterpret_cast<uint64_t *>(sm + C::OFF_TURN)[j] = turn_of(p.freqs[j]);
   for (int i = threadIdx.x; i < 2 * D; i += 32 * C::WARPS) {
     // value e of run `run` of lane `sub`, of tensor i / D
-    const int run = i / 8 % 2, sub = i % D / 16, e = i % 8;
-    const Runs r = runs_of<D>(sub, p.rot);
+    const int run = i / C::RUN % 2, sub = i % D / (2 * C::RUN), e = i % C::RUN;
+    const Runs r = runs_of<D, C::RUN>(sub, p.rot);
     const int from = (run ? r.b : r.a) + e;
     const void *w = p.t[i / D].w;
     if (w)
@@ -367,15 +376,15 @@ __global__ void __launch_bounds__(32 * RopeCfg<T, D, false>::WARPS, RopeCfg<T, D
   __syncthreads();
   for (; walk.more(); walk.advance()) {
     walk.arrive();
-    F8 a = walk.run(0, 0), b = walk.run(0, 1);
+    Run<C::RUN> a = walk.run(0, 0), b = walk.run(0, 1);
     if (walk.norm()) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum = fma2(a.v[e], a.v[e], fma2(b.v[e], b.v[e], sum));
+      for (int e = 0; e < C::RUN / 2; ++e) sum = fma2(a.v[e], a.v[e], fma2(b.v[e], b.v[e], sum));
       const float inv = rsqrtf(fmaf(head_sum<C::LANES>(sum.x + sum.y), 1.f / D, p.eps));
-      const F8 wa = walk.weights(0), wb = walk.weights(1);
+      const Run<C::RUN> wa = walk.weights(0), wb = walk.weights(1);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < C::RUN / 2; ++e) {
         a.v[e] = mul2(mul2(a.v[e], make_float2(inv, inv)), wa.v[e]);
         b.v[e] = mul2(mul2(b.v[e], make_float2(inv, inv)), wb.v[e]);
       }
@@ -431,19 +440,20 @@ __global__ void __launch_bounds__(32 * RopeCfg<T, D, true>::WARPS, RopeCfg<T, D,
                                which);
   rope_tables<T, D, true>(p, rope_smem);
   __syncthreads();
-  F8 da{}, db{};
+  using F = Run<C::RUN>;
+  F da{}, db{};
   for (; walk.more(); walk.advance()) {
     walk.arrive();
-    F8 ga = walk.run(0, 0), gb = walk.run(0, 1);
+    F ga = walk.run(0, 0), gb = walk.run(0, 1);
     walk.template turned<true>(ga, gb);
     if (t.w) {
       // (values and weights are read twice from shared memory, not held)
       float2 ss = make_float2(0.f, 0.f), sd = ss;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const F8 &g = i ? gb : ga, x = walk.run(1, i), w = walk.weights(i);
+        const F &g = i ? gb : ga, x = walk.run(1, i), w = walk.weights(i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < C::RUN / 2; ++e) {
           ss = fma2(x.v[e], x.v[e], ss);
           sd = fma2(mul2(g.v[e], w.v[e]), x.v[e], sd);
         }
@@ -454,10 +464,10 @@ __global__ void __launch_bounds__(32 * RopeCfg<T, D, true>::WARPS, RopeCfg<T, D,
       const bool live = walk.live();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        F8 &g = i ? gb : ga, &d = i ? db : da;
-        const F8 x = walk.run(1, i), w = walk.weights(i);
+        F &g = i ? gb : ga, &d = i ? db : da;
+        const F x = walk.run(1, i), w = walk.weights(i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < C::RUN / 2; ++e) {
           const float2 r = mul2(g.v[e], make_float2(inv, inv));
           if (live) d.v[e] = fma2(r, x.v[e], d.v[e]);
           g.v[e] = fma2(r, w.v[e], mul2(x.v[e], make_float2(m, m)));
@@ -468,9 +478,9 @@ __global__ void __launch_bounds__(32 * RopeCfg<T, D, true>::WARPS, RopeCfg<T, D,
   }
   if (!t.dw) return;
   // this block's row of dw: its warps' heads, then its warps
-  const Runs r = runs_of<D>(lane % C::LANES, p.rot);
+  const Runs r = runs_of<D, C::RUN>(lane % C::LANES, p.rot);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < C::RUN; ++e) {
     float a = e & 1 ? da.v[e >> 1].y : da.v[e >> 1].x, b = e & 1 ? db.v[e >> 1].y : db.v[e >> 1].x;
 #pragma unroll
     for (int o = C::LANES; o < 32; o <<= 1) {
