@@ -15,8 +15,9 @@
 // Measured: 4096 x 28672, BF16 dH, to five quantized operands 226 us (5.8 TB/s, 0.86 of
 // the measured copy rate; with one tile a block and its loads in registers 501 us, with
 // scalar operations and a division for each row by all lanes 321 us, with the next
-// tile's loads after the first barrier 240 us): issue slots are used to half.  1741 x
-// 7000, FP32 dH, to BF16 17.9 us with inputs in L2.
+// tile's loads after the first barrier 240 us): issue slots are used to half.  4096 x
+// 14336, FP32 dH, 124 us (6.2 TB/s; with each thread copying its own 32 bytes 146).
+// 1741 x 7000, FP32 dH, to BF16 17.9 us with inputs in L2.
 #pragma once
 #include "gated_math.cuh"
 #include "quantize128.cuh"
@@ -100,7 +101,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // One block of 512 threads an SM, which goes from tile to tile and copies the next
 // one's values to shared memory, a row as soon as this tile's has been read from there
-// (each thread copies what it will read itself).  Thread (ty, tx) has rows 4 ty .. +3 of columns 8 tx ..
+// (each thread copies what it, or a lane beside it, will read).  Thread (ty, tx) has rows 4 ty .. +3 of columns 8 tx ..
 // +7, so that the four rows' codes of a column are one word of the transposed tile.
 // Issue slots are as short as bandwidth: operations go in pairs, and a row's largest
 // values are exchanged so that each lane ends with one of them and divides once.
@@ -116,27 +117,43 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const uint32_t in = smem_u32(smem + S::OFF_IN) + threadIdx.x * 16;
   const uint32_t tiles = static_cast<uint32_t>(p.rb * p.cb), cb = static_cast<uint32_t>(p.cb);
-  // a tile's place in the matrices, for this thread, and how many of its rows are there
-  auto place = [&](uint32_t t, int64_t &at) {
-    const uint32_t rblock = t / cb, cblock = t - rblock * cb;
-    const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128 + 8 * tx;
-    at = r0 * p.C + c0;
-    return t < tiles && c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;
+  // a tile's place in the matrices, for this thread: how many of its rows are there, and
+  // columns of the tile
+  struct Place {
+    int64_t at;
+    int rows, cols;
   };
-  auto load = [&](int i, int rows, int64_t at) {  // row i of a tile
-    const int64_t from = i < rows ? at + i * p.C : 0;
+  auto place = [&](uint32_t t) {
+    const uint32_t rblock = t / cb, cblock = t - rblock * cb;
+    const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128;
+    return Place{r0 * p.C + c0 + 8 * tx, t < tiles ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0,
+                 static_cast<int>(min(static_cast<int64_t>(128), p.C - c0))};
+  };
+  // Row i of a tile.  A row's FP32 dH is 32 copies by 16 lanes: lane tx takes those of
+  // columns 4 tx and 64 + 4 tx, so that copies lie side by side, and reads 8 tx and
+  // 8 tx + 4, copies of its neighbours (the warp meets before it reads, and before the
+  // next copies).
+  auto load = [&](int i, const Place &a) {
+    const bool row = i < a.rows, there = row && 8 * tx < a.cols;
+    const int64_t from = there ? a.at + i * p.C : 0;
     const uint32_t to = in + i * S::WORDS * 8192;
-    grad_copy16(to, p.gate + from, i < rows);
-    grad_copy16(to + 8192, p.up + from, i < rows);
+    grad_copy16(to, p.gate + from, there);
+    grad_copy16(to + 8192, p.up + from, there);
+    if constexpr (sizeof(T) == 4) {
+      __syncwarp();
 #pragma unroll
-    for (int w = 0; w < S::WORDS - 2; ++w)
-      grad_copy16(to + (2 + w) * 8192, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dH) + from) + w, i < rows);
+      for (int w = 0; w < 2; ++w) {
+        const bool four = row && 64 * w + 4 * tx < a.cols;
+        grad_copy16(to + (2 + w) * 8192, static_cast<const T *>(p.dH) + (four ? a.at + i * p.C + 64 * w - 4 * tx : 0), four);
+      }
+    } else {
+      grad_copy16(to + 16384, static_cast<const T *>(p.dH) + from, there);
+    }
   };
   {
-    int64_t at;
-    const int rows = place(blockIdx.x, at);
+    const Place first = place(blockIdx.x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load(i, rows, at);
+    for (int i = 0; i < 4; ++i) load(i, first);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -144,9 +161,9 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
     const int64_t r0 = static_cast<int64_t>(rblock) * 128 + 4 * ty, c0 = static_cast<int64_t>(cblock) * 128 + 8 * tx;
     const int rows = c0 < p.C ? static_cast<int>(min(static_cast<int64_t>(4), p.R - r0)) : 0;
     float2 v[3][4][4];  // dgate, dup, h: [row][columns 2 e, + 1]
-    int64_t next_at;
-    const int next_rows = place(t + gridDim.x, next_at);
+    const Place next = place(t + gridDim.x);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (sizeof(T) == 4) __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       Eight<__nv_bfloat16> g, u;
@@ -154,8 +171,13 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
       const uint32_t from = in + i * S::WORDS * 8192;
       g.w[0] = ld_shared_v4(from);
       u.w[0] = ld_shared_v4(from + 8192);
-#pragma unroll
-      for (int w = 0; w < S::WORDS - 2; ++w) d.w[w] = ld_shared_v4(from + (2 + w) * 8192);
+      if constexpr (sizeof(T) == 4) {
+        const uint32_t two = from + 16384 + (tx >> 3) * 8192 + (((2 * tx) & 15) - tx) * 16;
+        d.w[0] = ld_shared_v4(two);
+        d.w[1] = ld_shared_v4(two + 16);
+      } else {
+        d.w[0] = ld_shared_v4(from + 16384);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const GatedGrad2 x = gated_grad<ACT>(two_of(g, e), two_of(u, e), two_of(d, e));
@@ -163,7 +185,7 @@ __global__ void __launch_bounds__(512, 1) gated_grad_tile_kernel(const GatedGrad
         v[1][i][e] = x.du;
         v[2][i][e] = x.h;
       }
-      load(i, next_rows, next_at);  // into what this thread has just read
+      load(i, next);  // into what has just been read
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     // columns' largest of this thread's rows
