@@ -32,11 +32,16 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p) {
   const float *left = p.left + ((p.left_tiles - 1 - tile) * p.c.kv_heads + h) * p.left_parts * kTilePartial<D>;
   const int r = static_cast<int>(row % kTileRows);
   const int64_t at = row / p.group * p.heads + h * p.group + row % p.group;  // token x head
+  // A row that is no sequence's (before the first one, behind the last one, of one whose
+  // start was refused) has a negative sum in the first part, always, and nothing else of
+  // it is set: `own_at` holds what the workspace held, and is not followed.
+  const float whose = __ldcg(left + kTileRows * D + kTileRows + r);
+  const int2 where = p.own_at ? __ldcg(p.own_at + at) : make_int2(-1, 0);
+  if (whose < 0.f) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float top = -INFINITY, sum = 0.f;
   // the shared keys' parts, then the own keys' sums or parts: eight loads of each
   // kind at once, then their sums in order, over the maximum so far
-  const int2 where = p.own_at ? __ldcg(p.own_at + at) : make_int2(-1, 0);
   const int rows = p.own_rows, size = rows * (D + 2), rr = where.y & 15, parts = p.left_parts + (where.x < 0 ? 0 : where.y >> 4) + 1;
   for (int v = 0; v < parts; v += 8) {
     float m[8], l[8];
@@ -69,7 +74,6 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p) {
       l[i] = __ldcg(ml + apart);
       b[i] = __ldcg(reinterpret_cast<const float4 *>(o));
     }
-    if (v == 0 && l[0] < 0.f) return;  // a row that is no sequence's
     float most = top;
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = fmaxf(most, m[i]);

@@ -571,6 +571,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         }
       }
       if (ok) ok = wait(o_done + 8 * i, (tiles - 1) & 1, 0x4F);
+      if (MODE == kSharedKeys && !ok) {
+        // a partial without any key, and whether the row is a sequence's: what joins relies on that
+        float *slot = p.left + (static_cast<int64_t>(item) * p.left_parts + part) * S::PARTIAL + S::ROWS * D;
+        slot[r] = -INFINITY;
+        slot[S::ROWS + r] = no_query ? -1.f : 0.f;
+      }
       if (ok) {
         tc_fence_after();
         const int at = (s.first + tok) * p.heads + head;

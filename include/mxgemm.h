@@ -644,9 +644,13 @@ typedef struct {
  *   page_table : batch x table_pitch int32 (above)
  *   kv_len     : batch int32, each sequence's length WITH the new tokens (the
  *                array that mxgemm_cache_attention takes next)
- *   q_start    : batch + 1 int32, ascending from 0 to `tokens`: sequence b's
- *                new tokens are rows q_start[b] .. q_start[b+1] - 1.  NULL: one
- *                token each (tokens == batch).
+ *   q_start    : batch + 1 int32, ascending, in [0, tokens]: sequence b's
+ *                new tokens are rows q_start[b] .. q_start[b+1] - 1.  Rows before
+ *                the first and behind the last one's (padding) are neither read
+ *                nor written.  NULL: one token each (tokens == batch).  A start that
+ *                is out of range or below the one before it is not followed:
+ *                MXGEMM_ERR_INVALID_VALUE is recorded in the device status word,
+ *                and rows of this and of other sequences may be left out.
  *   new_K, new_V : tokens rows of kv_heads x head_dim values, `pitch`
  *                elements from row to row (slices of a projection's output);
  *                x_dtype as for mxgemm_quantize.  Finite.
