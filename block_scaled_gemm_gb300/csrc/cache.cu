@@ -336,6 +336,7 @@ int attention_args(const mxg::HandleView &v, const mxgemm_cache_t *cache, int64_
   p->O = static_cast<__nv_bfloat16 *>(O);
   p->lse = lse;
   p->counters = v.counters;
+  p->begun = v.counters + mxg::kCounters;
   p->timeout_ns = v.timeout_ns;
   p->stall_producer = v.stall_producer;
   p->shared = p->left_parts = p->left_tiles = 0;

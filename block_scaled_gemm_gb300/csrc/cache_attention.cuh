@@ -76,6 +76,7 @@ struct AttnParams {
   float2 *own_ml;
   int2 *own_at;
   int own_rows;  // of a partial
+  unsigned *begun;  // set by the first launch while the second runs
   int left_parts, left_tiles;  // parts of a row tile, row tiles of a key/value head
 };
 
@@ -89,13 +90,36 @@ constexpr int kTilePartial = kTileRows * (D + 2);
 constexpr int kAllKeys = 0, kSharedKeys = 1, kOwnKeys = 2;
 
 // Before a launch reads global memory.  The one over the own keys comes behind the one
-// over the shared keys, needs nothing of it and does not wait for it: that one has
-// itself waited for what came before when it lets this one begin.  Lines that an SM
-// held before that are not to be read: the fence drops them, and most loads are from L2.
+// over the shared keys, needs nothing of it and does not wait for it to end.  What came
+// before both is in order for it by a word of the handle: a thread of the first launch,
+// which has waited, sets it with a release, and every thread of this one reads it with
+// an acquire, behind which no older line of the SM's is read; the fence carries that
+// over to the codes' copies.  (The first launch sets it before it lets this one begin,
+// but for its block's other warps: a wait of some ns, bounded as the others are.  The
+// launch that joins clears it.)
 template <int MODE>
-__device__ __forceinline__ void start_after() {
-  if (MODE == kOwnKeys) __threadfence();
-  else griddep_wait();
+__device__ __forceinline__ void start_after(const AttnParams &p) {
+  if constexpr (MODE == kOwnKeys) {
+    auto begun = [&]() {
+      unsigned v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.begun) : "memory");
+      return v != 0;
+    };
+    if (!begun()) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!begun())
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+          if (atomicCAS(p.b.status, 0, 6) == 0) atomicExch(p.b.status + 1, 0x32);
+          break;
+        }
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    __syncwarp();
+  } else {
+    griddep_wait();
+    if (MODE == kSharedKeys && blockIdx.x == 0 && threadIdx.x == 0)
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.begun), "r"(1u) : "memory");
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -338,7 +362,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
   }
   __syncwarp();
   if (MODE != kOwnKeys) griddep_launch_dependents();  // (the launch that joins is kept away: see there)
-  start_after<MODE>();
+  start_after<MODE>(p);
   // All tiles (each warp counts for itself, 32 sequences at a time), and this
   // CTA's range of them: ranges of four tiles at least.
   int mt;

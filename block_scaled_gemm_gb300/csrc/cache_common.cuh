@@ -38,7 +38,7 @@ struct Sequence {
 };
 
 // A load, from L2 where FRESH: by the launch that has not itself waited for the one that
-// wrote the value (start_after).
+// wrote the value (start_after puts it in order behind that).
 template <bool FRESH, typename T>
 __device__ __forceinline__ T load_value(const T *p) {
   if constexpr (FRESH) return __ldcg(p);

@@ -25,6 +25,7 @@ struct JoinCfg {
 template <int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p) {
   griddep_wait();
+  if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) *p.begun = 0;  // for the next call
   const int d4 = threadIdx.x / JoinCfg<D>::ROWS, h = blockIdx.y;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * JoinCfg<D>::ROWS + threadIdx.x % JoinCfg<D>::ROWS;  // token x head of the group
   if (row >= p.b.tokens * p.group) return;

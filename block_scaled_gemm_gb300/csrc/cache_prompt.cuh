@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     return;
   }
   if (MODE == kAllKeys) griddep_launch_dependents();
-  start_after<MODE>();
+  start_after<MODE>(p);
   if (MODE == kSharedKeys) griddep_launch_dependents();  // (the launch over the own keys: see there)
   // ------------------------------------------------------------ this CTA's rows
   // Sequence b's row tiles are numbered from f(b) = floor(q_start group / 256) + b

@@ -23,7 +23,7 @@ struct HandleView {
   int64_t *launches;
   cudaEvent_t prof_before, prof_after;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
-  unsigned *counters;  // kCounters words, zero between launches
+  unsigned *counters;  // kCounters words, zero between launches, and one more: AttnParams::begun
 };
 
 // Counters of a handle: the arrivals of work split over CTAs, each taken by

@@ -113,7 +113,7 @@ struct mxgemm_ctx {
   // captured one has them zeroed before it
   unsigned *flags = nullptr;
   unsigned epoch = 0;
-  unsigned *counters = nullptr;  // mxg::kCounters words, zero between launches
+  unsigned *counters = nullptr;  // mxg::kCounters words and one more (context.h), zero between launches
   Workspace ws;
   Outgrown *outgrown = nullptr;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -668,7 +668,7 @@ int mxgemm_create(mxgemm_handle_t *out, int device) {
   // a flag slot per epilogue warp of every CTA a grid can have
   // (and, behind them, the counters of work split over CTAs)
   const size_t flag_bytes = flag_words(h) * sizeof(unsigned);
-  const size_t counter_bytes = mxg::kCounters * sizeof(unsigned);
+  const size_t counter_bytes = (mxg::kCounters + 1) * sizeof(unsigned);
   if (cudaMalloc(&h->flags, flag_bytes + counter_bytes) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->d_status);

@@ -331,7 +331,8 @@ int mxgemm_set_option(mxgemm_handle_t h, int option, int64_t value);
  * 0x09 scale loader (free stage), 0x0A scale loader (staged scale rows), in
  * mxgemm_run_block128 epilogue (scales), 0x0B scale loader (staging load at exit),
  * 0x0C producer (scale loader's first staging load), 0x0E epilogue (C's old
- * values), 0x11 producer (drain at exit); attention of few query rows: 0x31 (codes);
+ * values), 0x11 producer (drain at exit); attention of few query rows: 0x31 (codes), 0x32
+ * (behind shared tokens: the launch before);
  * of many: 0x41 / 0x42 loader (free place for K / V), 0x43 loader (drain at exit),
  * 0x44 to 0x48 MMA issuer (Q, K, V, weights, final commit), 0x49 / 0x4B converters
  * (codes of K / V), 0x4A / 0x4C converters (free place for K / V), 0x4D softmax
