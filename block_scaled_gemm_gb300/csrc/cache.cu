@@ -226,12 +226,16 @@ int run_attention(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &
 // end, and 1.65 us for a row tile's 128 keys, or the codes at the rate of an SM, once for
 // each 8 or 16 rows.  Fitted to 2-128 sequences of 1-64 tokens, 512-65536 keys; the
 // kernel for few rows without the join of its parts where only own keys are its.
-double attention_us(const mxg::HandleView &v, const mxg::AttnParams &p, double keys, int sms, int d) {
-  if (takes_prompt(v, p)) return 13 + 1.65 * static_cast<double>(equal_row_tiles(p)) * keys / 128 / sms;
+struct AttnTime {
+  double start, key, tile;  // key: on one SM; tile: 32 keys of an item of the kernel for few rows, on one SM
+  double us(double keys, int sms) const { return start + key * keys / sms; }
+};
+AttnTime attention_time(const mxg::AttnParams &p, bool prompt, bool own, int d) {
+  if (prompt) return AttnTime{13, 1.65 * static_cast<double>(equal_row_tiles(p)) / 128, 0};
   const int64_t rows = takes_two(p) ? 16 : 8, passes = (p.b.tokens * p.group + rows * p.b.batch - 1) / (rows * p.b.batch);
   // bytes a us (heads of 64: 1.4 times the keys)
-  const double rate = (p.shared ? (rows == 16 ? 30e3 : 36e3) : (rows == 16 ? 22e3 : 42e3)) * (d == 64 ? 0.72 : 1);
-  return (p.shared ? 6 : 12) + static_cast<double>(passes * p.b.batch * p.c.kv_heads * 2 * d) * keys / (rate * sms);
+  const double rate = (own ? (rows == 16 ? 30e3 : 36e3) : (rows == 16 ? 22e3 : 42e3)) * (d == 64 ? 0.72 : 1);
+  return AttnTime{own ? 6.0 : 12.0, static_cast<double>(passes * p.b.batch * p.c.kv_heads * 2 * d) / rate, 64 * d / rate};
 }
 
 // How the shared keys and the sequences' own are computed apart: parts of the shared
@@ -241,29 +245,45 @@ double attention_us(const mxg::HandleView &v, const mxg::AttnParams &p, double k
 // first launch leaves SMs, the second runs there beside it, in one wave: 64 tokens of
 // 64/8 heads behind 8192 keys, 100-1000 of their own: 43.7 us with 5 parts and 72 SMs
 // for the own keys (4 and 88: 48.7, 6 and 56: 49.6; two waves on 72 SMs 50), and one
-// launch after the other with 8 parts 56.  How many keys sequences have of their own is
-// known to the device alone; an estimate that is too high must not make the shared
-// keys' launch much longer than it could be.
+// launch after the other with 8 parts 56.
+// How many keys sequences have of their own is known to the device alone.  The host
+// knows the table's room, of which three quarters are taken where tables are about as wide
+// as the longest sequence needs, but no more than kOwnMost: a table for the greatest length
+// there can be says nothing.  So the second launch has CTAs for all SMs, and on the device
+// those beside the first one alone work where that takes no longer than 1.3 times the
+// first (`beside_tiles`); else all, and those that find no place begin when the first one's end.
+// The same 64 tokens with tables of 16384 to 131072: 44.7 us; by the table's room alone
+// 59.7, and from 65536 on, where the own keys' two estimates differ by more than the
+// shared keys cost, not apart at all, 162.  16 x 4 tokens behind 65536, 1000-2000 of
+// their own: 79 (with a kOwnMost of 1024 84.5); 8 tokens behind 8192, 50-500 of their own:
+// 20.2, and 22.3 with wider tables (of 2048: 23.6).
+constexpr double kOwnMost = 1536;
 struct SharedPlan {
-  int parts, sms;
-  double us;
+  int parts, sms;        // sms: beside the first launch
+  double us, keys;       // keys: of each sequence's own, as estimated
+  int64_t beside_tiles;  // -1: the launches come one after the other
 };
-SharedPlan plan_shared(const mxg::HandleView &v, const mxg::AttnParams &p, int64_t tiles, double own_keys, int d) {
+SharedPlan plan_shared(const mxg::HandleView &v, const mxg::AttnParams &p, int64_t tiles, int d) {
   const int64_t rows = p.b.tokens * p.group, key_tiles = (p.shared + 127) / 128, most = std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4));
   auto shared_us = [&](int64_t n) {
     return 1.65 * static_cast<double>((tiles * n + v.sm_count - 1) / v.sm_count) * (static_cast<double>((key_tiles + n - 1) / n) + (rows > 128 ? 7 : 5));
   };
   double least = 1e300;
   for (int64_t n = 1; n <= most; ++n) least = std::min(least, shared_us(n));
-  SharedPlan best{1, v.sm_count, 1e300};
+  const bool prompt = takes_prompt(v, p);
+  const AttnTime own = attention_time(p, prompt, true, d);
+  const double keys = std::min(0.75 * static_cast<double>(p.b.table_pitch * p.c.page_size - p.shared), kOwnMost);
+  SharedPlan best{1, v.sm_count, 1e300, keys, -1};
   for (int64_t n = 1; n <= most; ++n) {
     const double shared = shared_us(n), join = 3 + static_cast<double>(rows * p.c.kv_heads * (n + 2)) * 1e-4;
-    const double after = shared + attention_us(v, p, own_keys, v.sm_count, d) + join;
-    if (after < best.us) best = SharedPlan{static_cast<int>(n), v.sm_count, after};
-    if (tiles * n < v.sm_count && shared <= 1.4 * least && !takes_prompt(v, p)) {
-      const int left = v.sm_count - static_cast<int>(tiles * n);
-      const double beside = std::max(shared, attention_us(v, p, own_keys, left, d)) + join;
-      if (beside < best.us) best = SharedPlan{static_cast<int>(n), left, beside};
+    const double after = shared + own.us(keys, v.sm_count) + join;
+    if (after < best.us) best = SharedPlan{static_cast<int>(n), v.sm_count, after, keys, -1};
+    // (a shared launch made longer than it need be has to pay whatever own keys there are)
+    if (tiles * n < v.sm_count && shared <= 1.4 * least && !prompt) {
+      const int busy = static_cast<int>(tiles * n), left = v.sm_count - busy;
+      const double limit = 1.3 * shared, one = own.us(keys, left), all = own.us(keys, v.sm_count) + shared * busy / v.sm_count;
+      const double beside = std::max(shared, one <= limit ? one : all) + join;
+      if (beside < best.us) best = SharedPlan{static_cast<int>(n), left, beside, keys, static_cast<int64_t>((limit - own.start) * left / own.tile)};
     }
   }
   return best;
@@ -275,12 +295,10 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   using S = mxg::PromptCfg<D>;
   p.left_tiles = static_cast<int>((p.b.tokens * p.group + S::ROWS - 1) / S::ROWS);
   const int64_t items = static_cast<int64_t>(p.left_tiles) * p.c.kv_heads;
-  // (tables are about as wide as the longest sequence needs: three quarters of it)
-  const double own_keys = 0.75 * static_cast<double>(p.b.table_pitch * p.c.page_size - p.shared);
-  const SharedPlan plan = plan_shared(v, p, items, own_keys, D);
+  const SharedPlan plan = plan_shared(v, p, items, D);
   mxg::AttnParams all = p;
   all.shared = 0;
-  if (!v.shared_keys && plan.us > attention_us(v, all, p.shared + own_keys, v.sm_count, D)) {
+  if (!v.shared_keys && plan.us > attention_time(all, takes_prompt(v, all), false, D).us(p.shared + plan.keys, v.sm_count)) {
     p.shared = 0;
     return run_attention<D>(h, v, p, stream);
   }
@@ -289,7 +307,9 @@ int run_shared(mxgemm_handle_t h, const mxg::HandleView &v, mxg::AttnParams &p, 
   const int64_t rows = p.b.tokens * p.heads, own = rows * (D + 4) * static_cast<int64_t>(sizeof(float));
   const int64_t blocks = (p.b.tokens * p.group + mxg::JoinCfg<D>::ROWS - 1) / mxg::JoinCfg<D>::ROWS;
   mxg::AttnParams first = p;
-  const AttnPlan a = plan_attention<D>(v, p, plan.sms);
+  const AttnPlan a = plan_attention<D>(v, p, plan.beside_tiles < 0 ? plan.sms : v.sm_count);
+  p.beside_tiles = plan.beside_tiles;
+  p.beside_blocks = a.two ? decode_grid<D, 2>(plan.sms) : decode_grid<D, 1>(plan.sms);
   if (items * p.left_parts >= kLim || a.bytes < 0) return MXGEMM_ERR_INVALID_VALUE;
   uint8_t *ws = nullptr;
   if (int st = mxg::handle_workspace(h, static_cast<size_t>(left + (own + 15) / 16 * 16 + a.bytes), stream, &ws)) return st;
@@ -343,7 +363,8 @@ int attention_args(const mxg::HandleView &v, const mxgemm_cache_t *cache, int64_
   p->left = p->own = nullptr;
   p->own_ml = nullptr;
   p->own_at = nullptr;
-  p->own_rows = 0;
+  p->own_rows = p->beside_blocks = 0;
+  p->beside_tiles = -1;
   return MXGEMM_OK;
 }
 

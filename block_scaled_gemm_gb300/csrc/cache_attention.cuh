@@ -76,6 +76,8 @@ struct AttnParams {
   float2 *own_ml;
   int2 *own_at;
   int own_rows;  // of a partial
+  int beside_blocks;     // CTAs of the second launch that work where there are few own keys:
+  int64_t beside_tiles;  // `beside_tiles` tiles of 32 or fewer (-1: all always work)
   unsigned *begun;  // set by the first launch while the second runs
   int left_parts, left_tiles;  // parts of a row tile, row tiles of a key/value head
 };
@@ -346,9 +348,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     griddep_wait();
     return;
   }
-  const int64_t blocks = gridDim.x - (MODE == kOwnKeys ? 1 : 0);
-  const int64_t unit = kWarps ? warp * blocks + blockIdx.x : blockIdx.x;
-  const int64_t units_most = kWarps ? 4 * blocks : blocks;
+  int64_t blocks = gridDim.x - (MODE == kOwnKeys ? 1 : 0);
   // how tiles are cut: all of them and the units that share them, or 0 and the
   // first and the last unit of this one's item; then the range's first tile
   // (kept here: registers are short)
@@ -376,6 +376,14 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, NT>::CTAS)
     total += __shfl_sync(0xFFFFFFFFu, warp_prefix(items * tiles), 31);
     all_items += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(items));
   }
+  // (no more keys than the SMs beside the launch over the shared keys take in its time:
+  // by the CTAs that start there, and the others have none)
+  if (MODE == kOwnKeys && total <= p.beside_tiles) {
+    blocks = p.beside_blocks;
+    if (blockIdx.x >= blocks) return;
+  }
+  const int64_t unit = kWarps ? warp * blocks + blockIdx.x : blockIdx.x;
+  const int64_t units_most = kWarps ? 4 * blocks : blocks;
   // the sequence of the range's first tile, and where its tiles begin
   int b0 = 0;
   int64_t base_b = 0, x0, x1;
