@@ -8,9 +8,10 @@
 // R turns the pairs of a head's first `rot` values, pair j by the angle pos f_j;
 // the others pass.  The angle of a far position has to be reduced to one turn
 // before it is rounded to FP32: f_j / (2 pi) is held as a fixed-point fraction of
-// a turn in 64 bits, and its product with the position, modulo 2^64, is the
-// angle's fraction of a turn, exact but for the fraction's own 2^-53.  An integer
-// product where FP64 would be far slower on this GPU.
+// a turn in 64 bits, rounded once (the quotient by 2 pi is formed as a sum of two
+// doubles), and its product with the position, modulo 2^64, is the angle's fraction of a
+// turn, off by 2^-64 a position: 2^-33 of a turn at position 2^31, whatever the frequency
+// is.  An integer product where FP64 would be far slower on this GPU.
 //
 // Bound by HBM: each value is read once and written once, and everything between
 // happens in registers.  A lane has two runs of 16 bytes of a head (eight values in
@@ -105,10 +106,14 @@ __device__ __forceinline__ Run<R> shared_run(uint32_t at, int sub) {
   return r;
 }
 
-// A frequency (radians a position) as a fraction of a turn, times 2^64.
+// A frequency (radians a position, below 2^50) as a fraction of a turn, times 2^64.
+// 1 / (2 pi) is two doubles, and the product's own rounding is added to the smaller part:
+// one double alone would be off by 2^-53 of itself, more than FP32's angle from a product
+// with the position of some 2^28 on.
 __device__ __forceinline__ uint64_t turn_of(double freq) {
-  const double t = freq * 0.15915494309189533577;  // 1 / (2 pi)
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  constexpr double kHigh = 0.15915494309189533577, kLow = -9.839338337591243e-18;
+  const double t = freq * kHigh, rest = fma(freq, kLow, fma(freq, kHigh, -t));
+  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0) + static_cast<uint64_t>(__double2ll_rn(rest * 18446744073709551616.0));
 }
 // Cosine and sine of the angle at a position, times the factor.
 __device__ __forceinline__ float2 angle_at(uint64_t turn, int pos, float factor) {

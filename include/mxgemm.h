@@ -574,8 +574,8 @@ typedef struct {
  * same pitch, else outputs overlap nothing.  x, dy and out float or bfloat16
  * (x_dtype), weights float or bfloat16 (w_dtype).  head_dim 64 or 128; tokens * heads <
  * 2^31, heads < 65536.  FP32 throughout, rounded once; the angles are exact to
- * 2^-24 of half a turn at any position (the frequencies' products with positions are
- * reduced in 64 bits).  mean x^2 is to be in FP32's range.  x, dy and out 16-byte
+ * 2^-24 of half a turn at any position for frequencies below 2^50 (the frequencies'
+ * products with positions are reduced in 64 bits).  mean x^2 is to be in FP32's range.  x, dy and out 16-byte
  * aligned with pitches that are multiples of 8 (MXGEMM_ERR_MISALIGNED).  Runs on the current device, needs no handle and
  * allocates nothing; errors as for mxgemm_quantize. */
 int mxgemm_norm_rope(const mxgemm_heads_t *q, const mxgemm_heads_t *k, int64_t tokens,
