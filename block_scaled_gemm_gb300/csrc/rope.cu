@@ -93,10 +93,15 @@ int64_t count_steps(mxg::RopeParams &p) {
 }
 
 template <typename T, int D>
-int run_forward(mxg::RopeParams &p, cudaStream_t stream) {
+int run_forward(mxg::RopeParams &p, int device, cudaStream_t stream) {
   // as many blocks as the SMs hold, no more warps than steps
   using C = mxg::RopeCfg<T, D, false>;
-  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), C::WARPS), C::BLOCKS * 152);
+  int sms = 1;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    cudaGetLastError();
+    return MXGEMM_ERR_CUDA;
+  }
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * count_steps<C>(p), C::WARPS), static_cast<int64_t>(C::BLOCKS) * sms);
   return mxg::launch(mxg::norm_rope_kernel<T, D>, dim3(static_cast<unsigned>(grid)), 32 * C::WARPS, C::SMEM_BYTES, 1, stream, p);
 }
 
@@ -135,8 +140,8 @@ extern "C" int mxgemm_norm_rope(const mxgemm_heads_t *q, const mxgemm_heads_t *k
   if (tokens == 0 || p.t[0].heads + p.t[1].heads == 0) return MXGEMM_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const bool f32 = x_dtype == MXGEMM_IN_F32;
-  return head_dim == 128 ? (f32 ? run_forward<float, 128>(p, stream) : run_forward<__nv_bfloat16, 128>(p, stream))
-                         : (f32 ? run_forward<float, 64>(p, stream) : run_forward<__nv_bfloat16, 64>(p, stream));
+  return head_dim == 128 ? (f32 ? run_forward<float, 128>(p, device, stream) : run_forward<__nv_bfloat16, 128>(p, device, stream))
+                         : (f32 ? run_forward<float, 64>(p, device, stream) : run_forward<__nv_bfloat16, 64>(p, device, stream));
 }
 
 extern "C" int mxgemm_norm_rope_backward(mxgemm_handle_t h, const mxgemm_heads_t *q, const mxgemm_heads_t *k, int64_t tokens,
