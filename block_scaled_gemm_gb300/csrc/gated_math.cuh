@@ -2,8 +2,12 @@
 //
 // Both are g times a logistic function: SiLU g / (1 + e^-g), and the tanh form of
 // GELU, g (1 + tanh z) / 2 = g / (1 + e^-2z) with z = sqrt(2/pi) (g + 0.044715 g^3).
-// e^x is ex2.approx of x log2 e, whose argument's rounding makes it off by 2^-24 |x|
-// of itself beside the approximation's 2^-22; the reciprocal is off by 2^-23.
+// e^x is ex2.approx of t, x log2 e rounded, times 1 + (x - t ln 2): what the rounding left
+// of x, up to 2^-24 |x|, goes in to first order, and 2^-22 is left beside the
+// approximation's 2^-22; the reciprocal is off by 2^-23, and below -87.3 the function is 0.
+// The products take no longer than they spread (with expf 1-2 %).  The gradient, whose
+// results are BF16 or codes (2^-8 or 2^-4 of themselves), leaves the first order out and
+// is off by 2^-24 |x| more (with expf 226 -> 255 us).
 #pragma once
 #include <cstdint>
 
@@ -16,8 +20,10 @@ constexpr float kGeluTwo = 1.59576912160573071176f, kGeluCube = 0.044715f;  // 2
 
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float logistic(float x) {
+  const float y = fminf(fmaxf(-x, -88.f), 88.f), t = y * 1.44269504088896340736f;
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504088896340736f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  e = fmaf(e, fmaf(t, -0.69314718055994530942f, y), e);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }

@@ -486,7 +486,9 @@ typedef enum {
  * with the products of mxgemm_run_block128 (b_block = 128), whose arguments these
  * are: A M x K with A_scale; G and U the two weights with their scales, both N x K
  * or both K x N as MXGEMM_OPT_B_MAJOR says.  g, u and H stay in FP32 until H is
- * rounded once.
+ * rounded once;
+ * the activation is exact to 2^-20 of itself (GELU: and 2^-22 |z| for its e^z), and 0
+ * where its logistic function's argument is below -87.3.
  *   M, N : each in [0, 2^31 - 512];  K in [16, 2^31 - 512], K % 16 == 0;  N % 16 == 0
  *          with K x N weights or MXGEMM_OUT_E4M3.  M == 0 or N == 0 is a no-op.
  *   H    : M x N: MXGEMM_OUT_F32, MXGEMM_OUT_BF16 (H_scale NULL), or
