@@ -125,7 +125,8 @@ __device__ __forceinline__ void gated_skinny_rows(const GatedSkinnyParams &gp, S
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const float most = fmaxf(fmaxf(fabsf(h[i].x), fabsf(h[i].y)), fmaxf(fabsf(h[i].z), fabsf(h[i].w)));
-        top[i] = fmaxf(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most))), kQ128Least);
+        // (NaN is passed over, as the quantizer does; four of them would win as bits)
+        top[i] = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(most, kQ128Least))));
       }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) inv[i] = __fdiv_rn(448.0f, top[i]);
