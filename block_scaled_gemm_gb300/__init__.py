@@ -480,12 +480,30 @@ def _type_codes():
     return _codes
 
 
-def _bfloat16(**tensors):
-    """The entry points that write BF16 through plain addresses: tensors of another type are refused."""
-    for name, t in tensors.items():
-        dtype = getattr(t, "dtype", None)
-        if dtype is not None and _type_codes().get(dtype) != IN_BF16:
-            raise ValueError(f"{name}: bfloat16, not {dtype}")
+_kinds = {}  # torch's types of what is passed on as plain addresses, by IN_F32, IN_BF16 and (None) one byte a value
+
+
+def _type_sets():
+    if not _kinds:
+        import torch
+        one = (x for x in vars(torch).values() if isinstance(x, torch.dtype) and x.itemsize == 1)
+        _kinds.update({IN_F32: {torch.float32}, IN_BF16: {torch.bfloat16}, None: set(one)})
+    return _kinds
+
+
+def _addresses(names, *tensors):
+    """Addresses of (tensor, its types, n) each, refused unless it is of one of the types and
+    dense with n values or more.  (Addresses and None are taken as they are.)"""
+    out = []
+    for t, types, n in tensors:
+        if t is not None and t.__class__ is not int:
+            if t.dtype not in types:
+                raise ValueError(f"{names.split()[len(out)]}: {'one byte a value' if len(types) > 1 else ' or '.join(map(str, types)) or 'of out_dtype'}, not {t.dtype}")
+            if not t.is_contiguous() or t.numel() < n:
+                raise ValueError(f"{names.split()[len(out)]}: a dense tensor of {n} values, not {tuple(t.shape)} with strides {t.stride()}")
+            t = t.data_ptr()
+        out.append(t)
+    return out
 
 
 def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H, H_scale=None, act=ACT_SILU,
@@ -493,15 +511,18 @@ def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H,
     """H = act(A.G) * (A.U) with the operands of mxgemm_run_block128 (both weights as the
     handle's OPT_B_MAJOR says): float32, bfloat16, or OUT_E4M3 codes with H_scale
     (M x ceil(N/128)), the operand of the next product.  gate and up (M x N bfloat16)
-    receive A.G and A.U for mxgemm_gated_backward."""
+    receive A.G and A.U for mxgemm_gated_backward.  All tensors dense; scales float32."""
+    M, N, K = int(M), int(N), int(K)
+    kb, nb, w, n = -(-K // 128), -(-N // 128), N * K, M * N
+    types = _type_sets()
+    one, f32, bf16 = types[None], types[IN_F32], types[IN_BF16]
+    of_h = one if out_dtype == OUT_E4M3 else types.get(out_dtype, ())
+    a, sa, g, sg, u, su, x, sx = _addresses(
+        "A A_scale G G_scale U U_scale H H_scale", (A, one, M * K), (A_scale, f32, M * kb), (G, one, w), (G_scale, f32, nb * kb), (U, one, w),
+        (U_scale, f32, nb * kb), (H, of_h, n), (H_scale, f32, M * nb))
     if gate is not None or up is not None:
-        _bfloat16(gate=gate, up=up)
-    size = getattr(H, "element_size", None)
-    if size is not None and size() != {OUT_F32: 4, OUT_BF16: 2, OUT_E4M3: 1}.get(out_dtype):
-        raise ValueError("H: of out_dtype (codes of one byte for OUT_E4M3)")
-    st = library().mxgemm_run_gated_block128(h, int(M), int(N), int(K), _ptr(A), _ptr(A_scale), _ptr(G), _ptr(G_scale),
-                                             _ptr(U), _ptr(U_scale), int(act), _ptr(H), _ptr(H_scale), int(out_dtype),
-                                             _ptr(gate), _ptr(up), _stream(stream))
+        gate, up = _addresses("gate up", (gate, bf16, n), (up, bf16, n))
+    st = library().mxgemm_run_gated_block128(h, M, N, K, a, sa, g, sg, u, su, int(act), x, sx, int(out_dtype), gate, up, _stream(stream))
     if check:
         _check(st, "mxgemm_run_gated_block128")
     return st
@@ -512,14 +533,25 @@ def mxgemm_gated_backward(gate, up, dH, R, C, dgate=None, dup=None, dgate_rows=N
                           check: bool = True) -> int:
     """The gradient of act(gate) * up (R x C bfloat16) for dH (float32 or bfloat16).
     dgate, dup: R x C bfloat16; the others pairs (codes, scales) as
-    mxgemm_quantize_block128 makes them, by rows or by columns.  What is None is
-    left out."""
+    mxgemm_quantize_block128 makes them, by rows or by columns.  All tensors dense.
+    What is None is left out."""
     if x_dtype is None:
         x_dtype = _in_dtype(dH)
-    _bfloat16(gate=gate, up=up, dgate=dgate, dup=dup)
+    R, C = int(R), int(C)
+    n = R * C
+    types = _type_sets()
+    one, f32, bf16 = types[None], types[IN_F32], types[IN_BF16]
+    g, u, dg, du = _addresses("gate up dgate dup", (gate, bf16, n), (up, bf16, n), (dgate, bf16, n), (dup, bf16, n))
+    # (another x_dtype is the library's to refuse)
+    dh, = _addresses("dH", (dH, types[x_dtype], n)) if x_dtype in (IN_F32, IN_BF16) else (_ptr(dH),)
     pairs = [p if p is not None else (None, None) for p in (dgate_rows, dup_rows, dgate_cols, dup_cols, hidden_cols)]
-    out = _GRADS_STRUCT.pack(*(_ptr(x) or 0 for x in (dgate, dup, *(y for p in pairs for y in p))))
-    st = library().mxgemm_gated_backward(_ptr(gate), _ptr(up), _ptr(dH), int(x_dtype), int(R), int(C), int(act), out,
+    if C % 16 == 0:  # (else the library refuses quantized outputs)
+        rows, cols = (n, R * -(-C // 128)), (C * (-(-R // 16) * 16), C * -(-R // 128))
+        for name, (codes, scales), of in zip(("dgate_rows", "dup_rows", "dgate_cols", "dup_cols", "hidden_cols"), pairs, (rows, rows, cols, cols, cols)):
+            if hasattr(codes, "dtype") and hasattr(scales, "dtype"):
+                _addresses(f"{name}[0] {name}[1]", (codes, one, of[0]), (scales, f32, of[1]))
+    out = _GRADS_STRUCT.pack(dg or 0, du or 0, *(_ptr(y) or 0 for p in pairs for y in p))
+    st = library().mxgemm_gated_backward(g, u, dh, int(x_dtype), R, C, int(act), out,
                                          _stream(stream))
     if check:
         _check(st, "mxgemm_gated_backward")
