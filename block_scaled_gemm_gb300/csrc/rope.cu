@@ -189,6 +189,7 @@ extern "C" int mxgemm_rope_frequencies(int64_t rot, double base, int scaling, do
     return MXGEMM_ERR_INVALID_VALUE;
   if (scaling == MXGEMM_ROPE_BASE && rot > 2)
     base *= std::pow(scale, static_cast<double>(rot) / static_cast<double>(rot - 2));
+  if (!std::isfinite(base)) return MXGEMM_ERR_INVALID_VALUE;
   for (int64_t j = 0; j < rot / 2; ++j) {
     double f = std::pow(base, -2.0 * static_cast<double>(j) / static_cast<double>(rot));
     if (scaling == MXGEMM_ROPE_LINEAR) f /= scale;

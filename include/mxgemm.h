@@ -329,7 +329,8 @@ int mxgemm_set_option(mxgemm_handle_t h, int option, int64_t value);
  * issuer (final commit), 0x05 epilogue (full accumulator), 0x06 epilogue (stream-K
  * partials), 0x07 / 0x08 cluster-launch-control response / free slot,
  * 0x09 scale loader (free stage), 0x0A scale loader (staged scale rows), in
- * mxgemm_run_block128 epilogue (scales), 0x0B scale loader (staging load at exit),
+ * mxgemm_run_block128 epilogue (scales), 0x0B scale loader (staging load at exit), in
+ * mxgemm_run_gated_block128 epilogue (the halves of a row of H as codes),
  * 0x0C producer (scale loader's first staging load), 0x0E epilogue (C's old
  * values), 0x11 producer (drain at exit); attention of few query rows: 0x31 (codes), 0x32
  * (behind shared tokens: the launch before);
@@ -612,6 +613,7 @@ typedef enum {
 
 /* Frequencies for mxgemm_rope_t, in HOST memory: rot / 2 doubles (copy them to the
  * device once).  rot even and >= 0; base > 0; scale >= 1; for
+ * MXGEMM_ROPE_BASE rot > 2 unless scale is 1, and the stretched base finite; for
  * MXGEMM_ROPE_BY_PARTS trained > 0 and 0 < slow < fast.  Touches no GPU. */
 int mxgemm_rope_frequencies(int64_t rot, double base, int scaling, double scale,
                             double trained, double slow, double fast, double *freqs);
