@@ -23,13 +23,17 @@ using mxg::cdiv;
 using mxg::encode;
 using mxg::kLim;
 
-// CTAs for each column block where those are fewer than the SMs, in us: a K block takes
-// 0.3, a join 3 and its sums 0.25 for each part, or 0.8 with 32 rows a warp.
-int block_parts(int64_t blocks, int64_t kb, int64_t sms, double each) {
+// CTAs for each column block where those are fewer than the SMs.  What their number
+// changes, in us: a K block takes 0.3 with up to 16 rows, 0.41 with up to 32 and 0.55
+// with 64, a join 1 and 0.25 for each part, or 0.8 with 32 rows a warp.  Some 10 us of start
+// and end, whatever the number, are left out.  Measured with each number of parts: 8 x
+// 1024 x 8192 30.4 us with one, 12.9 with four, 10.8 with eight (the choice), 12.7 with 19;
+// 64 x 1024 x 8192 45.8, 21.9, 20.5 (the choice), 28.4.
+int block_parts(int64_t blocks, int64_t kb, int64_t sms, double k_block, double part) {
   int best = 1;
-  double least = 0.3 * static_cast<double>(kb);
+  double least = k_block * static_cast<double>(kb);
   for (int64_t n = 2; n * blocks <= sms && n <= kb; ++n) {
-    const double us = 0.3 * static_cast<double>(cdiv(kb, n)) + 3 + each * static_cast<double>(n);
+    const double us = k_block * static_cast<double>(cdiv(kb, n)) + 1 + part * static_cast<double>(n);
     if (us < least) {
       least = us;
       best = static_cast<int>(n);
@@ -53,7 +57,7 @@ int run_skinny(mxgemm_handle_t h, const mxg::HandleView &v, mxg::GatedSkinnyPara
   gp.n_tiles = static_cast<int>(cdiv(p.N, 128));
   gp.total = static_cast<int64_t>(gp.n_tiles) * p.kb;
   const int sms = std::min(v.sm_count, mxg::kCounters);
-  const int grid = gp.n_tiles <= sms ? gp.n_tiles * block_parts(gp.n_tiles, p.kb, sms, S::ROWS >= 32 ? 0.8 : 0.25) : sms;
+  const int grid = gp.n_tiles <= sms ? gp.n_tiles * block_parts(gp.n_tiles, p.kb, sms, NT == 16 ? 0.3 : NT == 32 ? 0.41 : 0.55, S::ROWS >= 32 ? 0.8 : 0.25) : sms;
   uint8_t *ws = nullptr;
   if (int st = mxg::handle_workspace(h, static_cast<size_t>(grid) * 2 * S::PARTIAL * sizeof(float), stream, &ws)) return st;
   gp.partials = reinterpret_cast<float *>(ws);
