@@ -491,19 +491,15 @@ def _type_sets():
     return _kinds
 
 
-def _addresses(names, *tensors):
-    """Addresses of (tensor, its types, n) each, refused unless it is of one of the types and
-    dense with n values or more.  (Addresses and None are taken as they are.)"""
-    out = []
-    for t, types, n in tensors:
-        if t is not None and t.__class__ is not int:
-            if t.dtype not in types:
-                raise ValueError(f"{names.split()[len(out)]}: {'one byte a value' if len(types) > 1 else ' or '.join(map(str, types)) or 'of out_dtype'}, not {t.dtype}")
-            if not t.is_contiguous() or t.numel() < n:
-                raise ValueError(f"{names.split()[len(out)]}: a dense tensor of {n} values, not {tuple(t.shape)} with strides {t.stride()}")
-            t = t.data_ptr()
-        out.append(t)
-    return out
+def _address(name, t, types, n):
+    """The address of a tensor, refused unless it is of one of the types and dense with n
+    values or more.  (An address and None are taken as they are.)"""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype in types and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    of = "one byte a value" if len(types) > 1 else "".join(map(str, types)) or "of out_dtype"
+    raise ValueError(f"{name}: a dense tensor of {n} values, {of}; not {t.dtype}, {tuple(t.shape)} with strides {t.stride()}")
 
 
 def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H, H_scale=None, act=ACT_SILU,
@@ -517,12 +513,11 @@ def mxgemm_run_gated_block128(h, M, N, K, A, A_scale, G, G_scale, U, U_scale, H,
     types = _type_sets()
     one, f32, bf16 = types[None], types[IN_F32], types[IN_BF16]
     of_h = one if out_dtype == OUT_E4M3 else types.get(out_dtype, ())
-    a, sa, g, sg, u, su, x, sx = _addresses(
-        "A A_scale G G_scale U U_scale H H_scale", (A, one, M * K), (A_scale, f32, M * kb), (G, one, w), (G_scale, f32, nb * kb), (U, one, w),
-        (U_scale, f32, nb * kb), (H, of_h, n), (H_scale, f32, M * nb))
-    if gate is not None or up is not None:
-        gate, up = _addresses("gate up", (gate, bf16, n), (up, bf16, n))
-    st = library().mxgemm_run_gated_block128(h, M, N, K, a, sa, g, sg, u, su, int(act), x, sx, int(out_dtype), gate, up, _stream(stream))
+    st = library().mxgemm_run_gated_block128(
+        h, M, N, K, _address("A", A, one, M * K), _address("A_scale", A_scale, f32, M * kb), _address("G", G, one, w),
+        _address("G_scale", G_scale, f32, nb * kb), _address("U", U, one, w), _address("U_scale", U_scale, f32, nb * kb), int(act),
+        _address("H", H, of_h, n), _address("H_scale", H_scale, f32, M * nb), int(out_dtype), _address("gate", gate, bf16, n),
+        _address("up", up, bf16, n), _stream(stream))
     if check:
         _check(st, "mxgemm_run_gated_block128")
     return st
@@ -541,18 +536,19 @@ def mxgemm_gated_backward(gate, up, dH, R, C, dgate=None, dup=None, dgate_rows=N
     n = R * C
     types = _type_sets()
     one, f32, bf16 = types[None], types[IN_F32], types[IN_BF16]
-    g, u, dg, du = _addresses("gate up dgate dup", (gate, bf16, n), (up, bf16, n), (dgate, bf16, n), (dup, bf16, n))
+    dgate, dup = _address("dgate", dgate, bf16, n), _address("dup", dup, bf16, n)
     # (another x_dtype is the library's to refuse)
-    dh, = _addresses("dH", (dH, types[x_dtype], n)) if x_dtype in (IN_F32, IN_BF16) else (_ptr(dH),)
+    dh = _address("dH", dH, types[x_dtype], n) if x_dtype in (IN_F32, IN_BF16) else _ptr(dH)
     pairs = [p if p is not None else (None, None) for p in (dgate_rows, dup_rows, dgate_cols, dup_cols, hidden_cols)]
     if C % 16 == 0:  # (else the library refuses quantized outputs)
         rows, cols = (n, R * -(-C // 128)), (C * (-(-R // 16) * 16), C * -(-R // 128))
         for name, (codes, scales), of in zip(("dgate_rows", "dup_rows", "dgate_cols", "dup_cols", "hidden_cols"), pairs, (rows, rows, cols, cols, cols)):
             if hasattr(codes, "dtype") and hasattr(scales, "dtype"):
-                _addresses(f"{name}[0] {name}[1]", (codes, one, of[0]), (scales, f32, of[1]))
-    out = _GRADS_STRUCT.pack(dg or 0, du or 0, *(_ptr(y) or 0 for p in pairs for y in p))
-    st = library().mxgemm_gated_backward(g, u, dh, int(x_dtype), R, C, int(act), out,
-                                         _stream(stream))
+                _address(name + "' codes", codes, one, of[0])
+                _address(name + "' scales", scales, f32, of[1])
+    out = _GRADS_STRUCT.pack(dgate or 0, dup or 0, *(_ptr(y) or 0 for p in pairs for y in p))
+    st = library().mxgemm_gated_backward(_address("gate", gate, bf16, n), _address("up", up, bf16, n), dh, int(x_dtype), R, C, int(act),
+                                         out, _stream(stream))
     if check:
         _check(st, "mxgemm_gated_backward")
     return st
