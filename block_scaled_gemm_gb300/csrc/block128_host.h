@@ -11,11 +11,6 @@
 
 namespace mxg {
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-constexpr int64_t kLim = int64_t(1) << 31;
-
 // 2-D tensor map of bytes (or of C's elements): dims {inner, outer}, row pitch in
 // bytes, box.
 inline int encode(const HandleView &v, CUtensorMap *tm, CUtensorMapDataType dt, const void *base, int64_t inner, int64_t outer,

@@ -18,9 +18,8 @@
 
 namespace {
 
-inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-constexpr int64_t kLim = int64_t(1) << 31;
+using mxg::aligned;
+using mxg::kLim;
 
 // The checks that both entry points share; fills the kernels' views.
 int cache_args(const mxg::HandleView &v, const mxgemm_cache_t *c, int64_t batch, const int32_t *table,

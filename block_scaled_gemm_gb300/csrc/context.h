@@ -11,6 +11,11 @@
 
 namespace mxg {
 
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+constexpr int64_t kLim = int64_t(1) << 31;
+
 struct HandleView {
   int device;
   int sm_count;

@@ -15,10 +15,9 @@
 
 namespace {
 
-inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-constexpr int64_t kLim = int64_t(1) << 31;
+using mxg::aligned;
+using mxg::cdiv;
+using mxg::kLim;
 
 // One tensor's checks but for its pointers' device, and the kernels' view of it.
 int tensor_args(const mxgemm_heads_t *a, int64_t tokens, int64_t head_dim, int w_dtype, bool back, mxg::RopeTensor *t) {

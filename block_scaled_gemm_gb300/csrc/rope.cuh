@@ -26,12 +26,12 @@
 // Measured: 8192 tokens, 32/8 heads of 128 in BF16, half of each rotated: 29.3 us (5.7
 // TB/s, 0.84 of the measured copy rate; with blocks of tokens and their loads in
 // registers 40 us, ranges of a tensor's parity 46, halves of sectors where values
-// pass 35); 64 tokens 3.4 us.  The gradient, all of each head rotated: 53 us (4.7 TB/s;
-// 105 us with loads in registers), bound by issue slots and dependent
-// instructions at the 16 warps an SM that its registers allow (runs of four values
+// pass 35); 64 tokens 3.7 us.  The gradient, all of each head rotated: 53 us (4.7 TB/s;
+// 105 us with loads in registers), bound by dependent instructions at the 16 warps an SM
+// that its registers allow, with issue slots used to 51 % (runs of four values
 // and 24 warps: 59 us).  In FP32 4112 tokens, all of each head rotated: 28.7 us (5.9
 // TB/s; with runs of eight values, of which a copy takes every other 16 bytes,
-// 40.6), the gradient 51.8 (69.6).
+// 40.6), the gradient 51.8 (69.6), whose 90 registers a thread leave 16 warps an SM too.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
