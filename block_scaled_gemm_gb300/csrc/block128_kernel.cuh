@@ -18,8 +18,8 @@
 // the other's, so that an epilogue warp holds both products of 64 columns and forms H
 // in registers.  H as codes needs a row's largest value over 128 columns: the two
 // warps that share it exchange theirs.  4096 x 28672 x 8192 to codes with both
-// products kept: 1.38 ms at 2 GHz, 1.46-1.52 under the power limit (2.5-2.8 PFLOP/s, as
-// the single product of as many operations); 1741 x 7000 x 4112 99-105 us.
+// products kept: 1.38 ms at 2 GHz, 1.46-1.55 under the power limit (2.5 PFLOP/s in a
+// program, as the single product of as many operations); 1741 x 7000 x 4112 99-105 us.
 //
 // Two kernels:
 //   b128_pair_kernel    M > 64: CTA pairs (cta_group::2), 256 x 256 tiles,

@@ -17,7 +17,7 @@
 //
 // Measured: 16 x 28672 x 8192 to codes 80.5 us on the same buffers again and again and
 // 82 us with others each time (5.8 and 5.7 TB/s, 0.86 and 0.84 of the measured copy
-// rate), 1 x 4096 x 4096 10 us with the weights in L2, 64 x 8192 x 8192 38 us.  The
+// rate), 1 x 4096 x 4096 9.8 us with the weights in L2, 64 x 8192 x 8192 38 us.  The
 // rest is the start (3-4 us before the first loads land) and, where column blocks are
 // shared by several CTAs, their join (some 3 us: sums to L2 1, counted 1, read and
 // added 1, and the rows).
