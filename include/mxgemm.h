@@ -530,8 +530,8 @@ typedef struct {
  *   dgate = dH * up * act'(gate),   dup = dH * act(gate)
  *
  * of R x C matrices: gate and up bfloat16 (as mxgemm_run_gated_block128 keeps
- * them), dH float (MXGEMM_IN_F32) or bfloat16 (MXGEMM_IN_BF16).  Formed in FP32 and
- * rounded once to each output; the quantized ones are what
+ * them), dH float (MXGEMM_IN_F32) or bfloat16 (MXGEMM_IN_BF16).  Formed in FP32 (e^x
+ * of the activation to 2^-22 + 2^-24 |x| of itself, 0 below -87.3) and rounded once to each output; the quantized ones are what
  * mxgemm_quantize_block128 makes of the FP32 values.  Values must be finite.
  * R, C in [0, 2^31 - 128); C % 16 == 0 where an output is quantized.  At least one
  * output.  All matrices and codes 16-byte aligned, scales 4-byte; outputs overlap
